@@ -1,0 +1,148 @@
+/*
+ * mccb_ssm.h -- the operators around the causal depthwise convolution in a selective state space
+ * block, on AMD Instinct MI355X (gfx950): the convolution with its bias, activation and carried
+ * rows, the selective scan, and the matrix product with its epilogue; each with its backward, and
+ * the first two with their single-token form.
+ *
+ * Conventions are those of mccb.h: raw device pointers, caller-owned buffers, a
+ * ..._get_workspace_size call (host only, no HIP call) before each call that needs a workspace,
+ * status codes, work enqueued on `stream` (a hipStream_t; NULL = the default stream) without
+ * waiting. All checks run on the host before any HIP call, and on an error nothing is enqueued:
+ * NULL pointers (MCCB_ERR_PARAM_NULLPTR), dtype, activation, strides, alignment, overlap and
+ * workspace (MCCB_ERR_PARAM_INVALID), sizes (MCCB_ERR_SHAPE); MCCB_ERR_RUNTIME reports a failed
+ * launch. Nothing is allocated and nothing is kept between calls, so every call can be recorded
+ * into a HIP graph. Results are the same bits on every call with the same inputs.
+ *
+ * Data tensors are time-major, [S,B,...], as in mccb.h, and are read through element strides
+ * (>= 0; 0 repeats). Element strides are in the tensor's own elements. Outputs are contiguous, are
+ * overwritten, and overlap no other buffer. 16-bit buffers are 2-byte, 32-bit ones 4-byte aligned,
+ * workspaces and `saved` 16-byte.
+ *
+ * lengths: optional int64 [B] on the device, clamped to [0, S]; NULL = all S. Rows at or past a
+ * sequence's length are not computed with, whatever they hold (also infinities and NaN): outputs
+ * and gradients there are zero, and states are those after the last row before it. A length of
+ * zero hands the initial state on.
+ */
+#ifndef MCCB_SSM_H
+#define MCCB_SSM_H
+
+#include <stdint.h>
+
+#include "mccb.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* Activations. gelu is the tanh form: v/2 (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3))). */
+typedef enum {
+    MCCB_ACT_NONE = 0,
+    MCCB_ACT_RELU = 1,
+    MCCB_ACT_SILU = 2,
+    MCCB_ACT_GELU = 3,
+    MCCB_ACT_SOFTPLUS = 4
+} mccb_act_t;
+
+/* ------------------------------------------------------------------------------------------------
+ * Causal depthwise convolution with bias, activation and carried rows.
+ *
+ *   y[t,b,h] = act(bias[h] + sum_{k<W} weight[k,h] x[t-W+1+k,b,h]),
+ *
+ * rows before the first taken from `state` (state[r] is row r-W+1), or zero without one. Products
+ * of two 16-bit values are exact in fp32; the sum, the activation and the gradients are fp32 (the
+ * sums over rows and batches fp64 from one strip of rows to the next), rounded once.
+ *
+ * B in [1, 65535], S in [0, 2^31), H in [1, 2^24], W in 1..4; activation none or silu.
+ * -----------------------------------------------------------------------------------------------*/
+typedef struct {
+    int64_t S, B, H, W;
+    int32_t dtype, activation;
+    const void *x;           /* [S,B,H] */
+    int64_t x_stride[3];     /* along S, B, H */
+    const void *weight;      /* [W,H] contiguous */
+    const void *bias;        /* [H] or NULL */
+    const int64_t *lengths;  /* [B] or NULL */
+    const void *state;       /* [W-1,B,H] contiguous: the rows before the first; NULL = zeros */
+} mccb_conv_t;
+
+/* y [S,B,H]; final_state [W-1,B,H] or NULL: the last W-1 rows before each sequence's length (from
+ * `state` where the sequence is shorter). No workspace. */
+int mccb_conv_act_forward(const mccb_conv_t *args, void *y, void *final_state, void *stream);
+
+/* The gradients, from the same arguments as the forward and
+ *   gradY [S,B,H] (strides gy_stride), gradFinalState [W-1,B,H] contiguous or NULL.
+ * gradX [S,B,H] and gradWeight [W,H] are required, gradBias [H] and gradState [W-1,B,H] optional.
+ * The pre-activation is computed again from x. */
+int mccb_conv_act_backward_get_workspace_size(const mccb_conv_t *args, uint64_t *workspace_size);
+int mccb_conv_act_backward(const mccb_conv_t *args, const void *gradY, const int64_t *gy_stride,
+                           const void *gradFinalState, void *gradX, void *gradWeight,
+                           void *gradBias, void *gradState, void *workspace,
+                           uint64_t workspace_size, void *stream);
+
+/* One token: x and y [B,H] (args->S = 1, x_stride[0] unused); `state` [W-1,B,H] is read and then
+ * shifted up by one row in place. args->state and args->lengths are NULL. */
+int mccb_conv_act_step(const mccb_conv_t *args, void *state, void *y, void *stream);
+
+/* ------------------------------------------------------------------------------------------------
+ * Selective state space scan. For every channel h of group g = h / (H/G) and state n < N:
+ *
+ *   d[t]   = softplus(dt[t,b,h] + dt_bias[h])        (without softplus: the sum itself)
+ *   s[t,n] = exp(d[t] A[n,h]) s[t-1,n] + d[t] Bm[t,b,g,n] x[t,b,h]
+ *   y[t]   = sum_n Cm[t,b,g,n] s[t,n] + D[h] x[t]
+ *   out[t] = y[t] silu(z[t])                         (without z: y[t])
+ *
+ * x, dt, z, out, Bm and Cm have the dtype, A, D, dt_bias and the states are fp32; everything is
+ * computed in fp32 and rounded once (sums over rows, batches and channels go on in fp64 or in a
+ * fixed order of fp32 partial sums).
+ *
+ * B in [1, 65535], S in [0, 2^31), H in [1, 2^24] and a multiple of G, N in 1..32.
+ * -----------------------------------------------------------------------------------------------*/
+typedef struct {
+    int64_t S, B, H, N, G;
+    int32_t dtype, softplus;  /* softplus: nonzero = applied */
+    const void *x, *dt;       /* [S,B,H] */
+    const void *z;            /* [S,B,H] or NULL */
+    const void *Bm, *Cm;      /* [S,B,G,N] */
+    int64_t x_stride[3], dt_stride[3], z_stride[3]; /* along S, B, H */
+    int64_t b_stride[4], c_stride[4];               /* along S, B, G, N */
+    const float *A;           /* [N,H] contiguous */
+    const float *D;           /* [H] or NULL (zero) */
+    const float *dt_bias;     /* [H] or NULL (zero) */
+    const int64_t *lengths;   /* [B] or NULL */
+    const float *state;       /* [B,N,H] contiguous, the state before the first row; NULL = zeros */
+} mccb_scan_t;
+
+/* out [S,B,H]; final_state [B,N,H] or NULL; saved: NULL, or mccb_scan_saved_size bytes that the
+ * backward reads (the state before every 16th row). */
+int mccb_scan_saved_size(const mccb_scan_t *args, uint64_t *bytes);
+int mccb_scan_forward_get_workspace_size(const mccb_scan_t *args, uint64_t *workspace_size);
+int mccb_scan_forward(const mccb_scan_t *args, void *out, float *final_state, void *saved,
+                      void *workspace, uint64_t workspace_size, void *stream);
+
+/* Gradients. gradOut has strides gout_stride; gradFinalState may be NULL (zero). The [S,B,H] and
+ * [S,B,G,N] outputs are contiguous and required, except gradZ (required with z, else NULL); gradA is
+ * required, gradD, gradDtBias and gradState are optional. */
+typedef struct {
+    const void *gradOut;          /* [S,B,H] */
+    int64_t gout_stride[3];       /* along S, B, H */
+    const float *gradFinalState;  /* [B,N,H] or NULL */
+    void *gradX, *gradDt, *gradZ; /* [S,B,H] */
+    void *gradB, *gradC;          /* [S,B,G,N] */
+    float *gradA;                 /* [N,H] */
+    float *gradD, *gradDtBias;    /* [H] or NULL */
+    float *gradState;             /* [B,N,H] or NULL */
+} mccb_scan_grads_t;
+
+int mccb_scan_backward_get_workspace_size(const mccb_scan_t *args, uint64_t *workspace_size);
+int mccb_scan_backward(const mccb_scan_t *args, const mccb_scan_grads_t *grads, const void *saved,
+                       void *workspace, uint64_t workspace_size, void *stream);
+
+/* One token: x, dt, z and out [B,H], Bm and Cm [B,G,N] (args->S = 1, the strides along S unused);
+ * `state` [B,N,H] is updated in place. args->state and args->lengths are NULL. */
+int mccb_scan_step(const mccb_scan_t *args, float *state, void *out, void *stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* MCCB_SSM_H */

@@ -32,15 +32,20 @@ class Strides(ctypes.Structure):
                 ("weight", ctypes.c_int64 * 2), ("mask", ctypes.c_int64 * 2)]
 
 
+def load(path: str, env: str, build) -> ctypes.CDLL:
+    """The library at `path`, built first if there is none (unless `env` named the path)."""
+    if not os.path.exists(path):
+        if os.environ.get(env):
+            raise OSError(f"{env}={path} does not exist")
+        build()
+    return ctypes.CDLL(path)
+
+
 def lib() -> ctypes.CDLL:
     """The loaded library, building it first if no build exists."""
     global _lib
     if _lib is None:
-        if not os.path.exists(_build.LIB):
-            if os.environ.get("MCCB_LIBRARY"):
-                raise OSError(f"MCCB_LIBRARY={_build.LIB} does not exist")
-            _build.build_library()
-        L = ctypes.CDLL(_build.LIB)
+        L = load(_build.LIB, "MCCB_LIBRARY", _build.build_library)
         i64, u64, vp = ctypes.c_int64, ctypes.c_uint64, ctypes.c_void_p
         L.mccb_get_workspace_size.argtypes = [i64, i64, i64, ctypes.c_int, ctypes.POINTER(u64)]
         L.mccb_get_workspace_size.restype = ctypes.c_int

@@ -1,8 +1,9 @@
-"""Compile the HIP library (libmccb.so) for gfx950 in-tree."""
+"""Compile the HIP libraries (libmccb.so, libmccb_ssm.so) for gfx950 in-tree."""
 from __future__ import annotations
 
 import os
 import subprocess
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -11,6 +12,9 @@ SRC = os.path.join(PKG, "csrc", "mccb.hip")
 # build); it is loaded as given and never built.
 LIB = os.environ.get("MCCB_LIBRARY") or os.path.join(PKG, "libmccb.so")
 INCLUDE = os.path.join(ROOT, "include")
+# the state space block's operators; MCCB_SSM_LIBRARY as above
+SSM_SRCS = [os.path.join(PKG, "csrc", f) for f in ("ssm_conv.hip", "ssm_scan.hip")]
+SSM_LIB = os.environ.get("MCCB_SSM_LIBRARY") or os.path.join(PKG, "libmccb_ssm.so")
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-shared", "-fPIC",
@@ -31,5 +35,38 @@ def build_library(out: str = LIB, extra: list[str] | None = None, verbose: bool 
     return out
 
 
+def build_ssm_library(out: str = SSM_LIB, extra: list[str] | None = None,
+                      verbose: bool = False) -> str:
+    """One object a source, compiled side by side, then linked."""
+    hipcc = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
+
+    def run(cmd):
+        res = subprocess.run(cmd, capture_output=True, text=True)
+        if res.returncode != 0:
+            raise RuntimeError(f"hipcc failed ({res.returncode}):\n{res.stderr}")
+        if verbose:
+            print(res.stderr)
+
+    flags = [f for f in HIPCC_FLAGS if f != "-shared"] + (extra or [])
+    objects = [f"{out}.{os.path.basename(src)}.o" for src in SSM_SRCS]
+    try:
+        with ThreadPoolExecutor(len(SSM_SRCS)) as pool:
+            list(pool.map(lambda so: run([hipcc, *flags, "-I", INCLUDE, "-c", so[0], "-o", so[1]]),
+                          zip(SSM_SRCS, objects)))
+        run([hipcc, *HIPCC_FLAGS, *(extra or []), *objects, "-o", out + ".tmp"])
+    finally:
+        for o in objects:
+            if os.path.exists(o):
+                os.remove(o)
+    os.replace(out + ".tmp", out)
+    return out
+
+
+def build_all() -> list[str]:
+    """Both libraries, side by side."""
+    with ThreadPoolExecutor(2) as pool:
+        return [f.result() for f in (pool.submit(build_library), pool.submit(build_ssm_library))]
+
+
 if __name__ == "__main__":
-    print(build_library())
+    print(*build_all())

@@ -1,0 +1,186 @@
+// ssm_common.h -- what the kernels of the state space block share: 16-bit formats, activations in
+// fp32, and the host's argument checks.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <stddef.h>
+#include <stdint.h>
+
+#include "mccb_ssm.h"
+
+namespace ssm {
+
+constexpr int kWave = 64;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// ---------------------------------------------------------------------------------------------
+// 16-bit formats. Conversions to 16 bits round to nearest, ties to even.
+// ---------------------------------------------------------------------------------------------
+template <int DT>
+struct F16;
+template <>
+struct F16<MCCB_BF16> {
+    typedef __bf16 elem;
+    __device__ static inline float to_f32(uint16_t u) { return __uint_as_float((uint32_t)u << 16); }
+};
+template <>
+struct F16<MCCB_FP16> {
+    typedef _Float16 elem;
+    __device__ static inline float to_f32(uint16_t u) {
+        return (float)__builtin_bit_cast(_Float16, u);
+    }
+};
+template <int DT>
+__device__ static inline float to_f32(uint16_t u) {
+    return F16<DT>::to_f32(u);
+}
+template <int DT>
+__device__ static inline uint16_t from_f32(float f) {
+    return __builtin_bit_cast(uint16_t, (typename F16<DT>::elem)f);
+}
+
+// V 16-bit values in one load. Global memory takes vectors at any 2-byte address on this target,
+// so the type carries the elements' alignment: rows of odd lengths keep their wide loads.
+template <int V>
+struct HVec {
+    typedef uint16_t t __attribute__((ext_vector_type(V), aligned(2)));
+};
+template <>
+struct HVec<1> {
+    struct t {
+        uint16_t v;
+        __device__ uint16_t &operator[](int) { return v; }
+        __device__ uint16_t operator[](int) const { return v; }
+    };
+};
+
+// ---------------------------------------------------------------------------------------------
+// fp32 functions. exp2, log and the reciprocal are the hardware's (about 1 ulp).
+// ---------------------------------------------------------------------------------------------
+__device__ static inline float exp2_f(float v) { return __builtin_amdgcn_exp2f(v); }
+__device__ static inline float exp_f(float v) { return exp2_f(v * kLog2e); }
+__device__ static inline float rcp_f(float v) { return __builtin_amdgcn_rcpf(v); }
+
+// 1/(1+exp(-v)): exp(-v) overflows to infinity below v = -88 and its reciprocal is 0, the limit.
+__device__ static inline float sigmoid_f(float v) { return rcp_f(1.0f + exp_f(-v)); }
+
+// log(1+e) for e in [0,1]: 2 atanh(s) with s = e/(2+e) in [0,1/3], and atanh(s)/s = 1 + s^2 P(s^2)
+// with P of degree 3, fitted at Chebyshev nodes over s^2 in [0,1/9] (relative error 1.5e-8). Keeps
+// the relative precision of small e, which log(1+e) loses: step sizes of 1e-3 come from e = 1e-3.
+__device__ static inline float log1p_unit(float e) {
+    const float q = 2.0f + e;
+    float r = rcp_f(q);
+    r = __builtin_fmaf(__builtin_fmaf(-q, r, 1.0f), r, r);
+    const float s = e * r, s2 = s * s;
+    float p = __builtin_fmaf(s2, 0.13433775305747986f, 0.14116978645324707f);
+    p = __builtin_fmaf(s2, p, 0.2000383585691452f);
+    p = __builtin_fmaf(s2, p, 0.33333319425582886f);
+    return 2.0f * __builtin_fmaf(s * s2, p, s);
+}
+
+// softplus(v) = max(v,0) + log(1 + exp(-|v|)); `slope` gets its derivative, the logistic function.
+__device__ static inline float softplus_f(float v, float &slope) {
+    const float e = exp_f(-__builtin_fabsf(v));
+    const float r = rcp_f(1.0f + e);
+    slope = v >= 0.0f ? r : e * r;
+    // a NaN stays one (max alone would drop it)
+    return (v != v ? v : __builtin_fmaxf(v, 0.0f)) + log1p_unit(e);
+}
+__device__ static inline float softplus_f(float v) {
+    float unused;
+    return softplus_f(v, unused);
+}
+
+__device__ static inline float silu_f(float v) { return v * sigmoid_f(v); }
+__device__ static inline float silu_slope_f(float v) {
+    const float g = sigmoid_f(v);
+    return g * __builtin_fmaf(v, 1.0f - g, 1.0f);
+}
+
+// tanh-form gelu: 0.5 (1 + tanh u) is the logistic function of 2u, u = c (v + 0.044715 v^3).
+constexpr float kGelu2c = 1.5957691216057308f;  // 2 sqrt(2/pi)
+__device__ static inline float act_f(float v, int act) {
+    switch (act) {
+        case MCCB_ACT_RELU: return v < 0.0f ? 0.0f : v;
+        case MCCB_ACT_SILU: return silu_f(v);
+        case MCCB_ACT_GELU:
+            return v * sigmoid_f(kGelu2c * v * __builtin_fmaf(0.044715f * v, v, 1.0f));
+        case MCCB_ACT_SOFTPLUS: return softplus_f(v);
+        default: return v;
+    }
+}
+__device__ static inline float act_slope_f(float v, int act) {
+    switch (act) {
+        case MCCB_ACT_RELU: return v > 0.0f ? 1.0f : 0.0f;
+        case MCCB_ACT_SILU: return silu_slope_f(v);
+        case MCCB_ACT_GELU: {
+            const float g = sigmoid_f(kGelu2c * v * __builtin_fmaf(0.044715f * v, v, 1.0f));
+            const float du = kGelu2c * __builtin_fmaf(0.134145f * v, v, 1.0f);
+            return __builtin_fmaf(v * g * (1.0f - g), du, g);
+        }
+        case MCCB_ACT_SOFTPLUS: return sigmoid_f(v);
+        default: return 1.0f;
+    }
+}
+
+// ---------------------------------------------------------------------------------------------
+// Host side: checks shared by the entry points. Nothing here allocates or throws.
+// ---------------------------------------------------------------------------------------------
+constexpr int64_t kMaxBatch = 65535, kMaxRows = (int64_t)1 << 31, kMaxWidth = (int64_t)1 << 24;
+
+inline uint64_t align16(uint64_t v) { return (v + 15u) & ~(uint64_t)15u; }
+
+struct Span {
+    const void *p;
+    uint64_t bytes;
+};
+
+// Bytes from the base to one past the last element of a strided tensor (0 for an empty one); false
+// if a stride is negative or the extent does not fit in 2^62 bytes.
+inline bool extent(int n, const int64_t *size, const int64_t *stride, int64_t esz, uint64_t *out) {
+    unsigned __int128 last = 0;
+    for (int i = 0; i < n; ++i) {
+        if (stride[i] < 0) return false;
+        if (size[i] == 0) {
+            *out = 0;
+            return true;
+        }
+        last += (unsigned __int128)(uint64_t)(size[i] - 1) * (uint64_t)stride[i];
+    }
+    const unsigned __int128 bytes = (last + 1) * (uint64_t)esz;
+    if (bytes >> 62) return false;
+    *out = (uint64_t)bytes;
+    return true;
+}
+
+inline bool overlap(const Span &a, const Span &b) {
+    if (!a.p || !b.p || !a.bytes || !b.bytes) return false;
+    const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
+    return x < y + b.bytes && y < x + a.bytes;
+}
+
+// No output may overlap an input or another output.
+inline bool outputs_clash(const Span *in, int n_in, const Span *out, int n_out) {
+    for (int o = 0; o < n_out; ++o) {
+        for (int i = 0; i < n_in; ++i)
+            if (overlap(out[o], in[i])) return true;
+        for (int q = 0; q < o; ++q)
+            if (overlap(out[o], out[q])) return true;
+    }
+    return false;
+}
+
+inline bool misaligned(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) != 0; }
+
+inline int launched() { return hipGetLastError() == hipSuccess ? MCCB_OK : MCCB_ERR_RUNTIME; }
+
+// A workspace argument against the size needed.
+inline int check_workspace(const void *ws, uint64_t have, uint64_t need) {
+    if (need == 0) return MCCB_OK;
+    if (!ws) return MCCB_ERR_PARAM_NULLPTR;
+    return have < need || misaligned(ws, 16) ? MCCB_ERR_PARAM_INVALID : MCCB_OK;
+}
+
+}  // namespace ssm
