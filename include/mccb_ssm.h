@@ -141,6 +141,44 @@ int mccb_scan_backward(const mccb_scan_t *args, const mccb_scan_grads_t *grads, 
  * `state` [B,N,H] is updated in place. args->state and args->lengths are NULL. */
 int mccb_scan_step(const mccb_scan_t *args, float *state, void *out, void *stream);
 
+/* ------------------------------------------------------------------------------------------------
+ * Matrix product with bias, activation and residual in its epilogue:
+ *
+ *   pre = x weight^T + bias,  out = act(pre) + residual
+ *
+ * x [M,K] and weight [N,K] have contiguous rows x_ld and weight_ld elements apart; bias [N],
+ * residual [M,N] (rows residual_ld apart) and everything else have the same dtype. Products are
+ * accumulated in fp32; bias, activation and residual are applied in fp32 and the result is rounded
+ * once.
+ *
+ * M in [0, 2^22 - 64], N and K in [1, 2^22 - 64].
+ * -----------------------------------------------------------------------------------------------*/
+typedef struct {
+    int64_t M, K, N;
+    int32_t dtype, activation;
+    const void *x;      /* [M,K] */
+    const void *weight; /* [N,K] */
+    const void *bias;   /* [N] or NULL */
+    int64_t x_ld, weight_ld;
+} mccb_linear_t;
+
+/* out [M,N] contiguous; pre [M,N] contiguous or NULL: the pre-activation, for the backward;
+ * residual may be NULL. */
+int mccb_linear_forward_get_workspace_size(const mccb_linear_t *args, uint64_t *workspace_size);
+int mccb_linear_forward(const mccb_linear_t *args, const void *residual, int64_t residual_ld,
+                        void *out, void *pre, void *workspace, uint64_t workspace_size,
+                        void *stream);
+
+/* With g = gradOut act'(pre) (rounded to the dtype once, since the matrix instructions take 16-bit
+ * operands; gradBias sums it before that rounding): gradX = g weight [M,K], gradWeight = g^T x
+ * [N,K], gradBias = column sums [N]. Each may be NULL and is then not computed; gradient of the
+ * residual is gradOut itself. pre is needed unless the activation is none. gradOut's rows are
+ * gout_ld elements apart. */
+int mccb_linear_backward_get_workspace_size(const mccb_linear_t *args, uint64_t *workspace_size);
+int mccb_linear_backward(const mccb_linear_t *args, const void *gradOut, int64_t gout_ld,
+                         const void *pre, void *gradX, void *gradWeight, void *gradBias,
+                         void *workspace, uint64_t workspace_size, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -16,8 +16,9 @@ import ctypes
 import torch
 
 from ._lib import MccbError, Plan, Strides, lib, status_string  # noqa: F401
-from .ssm import (ACTIVATIONS, ConvGrads, ScanGrads, conv_act_backward,  # noqa: F401
-                  conv_act_forward, conv_act_step, scan_backward, scan_forward, scan_step, ssm_lib)
+from .ssm import (ACTIVATIONS, ConvGrads, LinearGrads, ScanGrads,  # noqa: F401
+                  conv_act_backward, conv_act_forward, conv_act_step, linear_backward,
+                  linear_forward, scan_backward, scan_forward, scan_step, ssm_lib)
 
 MCCB_BF16, MCCB_FP16 = 0, 1
 MCCB_OK = 0

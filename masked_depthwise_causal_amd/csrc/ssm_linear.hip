@@ -1,0 +1,783 @@
+// ssm_linear.hip -- matrix product with bias, activation and residual in its epilogue, and its
+// backward, for MI355X (gfx950) (mccb_ssm.h).
+//
+//   out[m,n] = act(sum_k x[m,k] w[n,k] + bias[n]) + residual[m,n]
+//   g = gout act'(pre),  gx[m,k] = sum_n g[m,n] w[n,k],  gw[n,k] = sum_m g[m,n] x[m,k]
+//
+// Three kernels carry the products, all of the form C = P Q^T with both operands' rows contiguous
+// along the contraction:
+//   tiles   (M above 64): a block computes a BM x BN tile with 32x32x16 matrix instructions from two
+//           LDS buffers that are filled by loads straight to LDS, 64 of the contraction at a time.
+//           Few tiles and a long contraction: the contraction is split over blocks, which leave fp32
+//           partial tiles for `finish` to add in a fixed order.
+//   skinny  (M up to 64): bound by reading w once. A wave takes 16 rows of w and every WAVES-th
+//           part of the contraction, straight from memory into 16x16x32 matrix instructions.
+// The epilogue works on fp32 sums staged through LDS, so that bias, residual, pre and out are read
+// and written as whole rows.
+//
+// Operands that the direct-to-LDS loads cannot take (rows not 16-byte aligned) are first copied into
+// the workspace with rows padded by zeros. The backward needs w, x and g with the other dimension
+// contiguous; those are transposed into the workspace first.
+#include "ssm_common.h"
+
+using namespace ssm;
+
+namespace {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
+
+template <int DT>
+__device__ static inline f32x16 mfma32(u16x8 a, u16x8 b, f32x16 c) {
+    if constexpr (DT == MCCB_BF16)
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
+                                                       __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a),
+                                                      __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+}
+template <int DT>
+__device__ static inline f32x4 mfma16(u16x8 a, u16x8 b, f32x4 c) {
+    if constexpr (DT == MCCB_BF16)
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
+                                                       __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a),
+                                                      __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+}
+
+constexpr int kBK = 64;  // contraction a tile step takes: a row's 128 bytes, eight 16-byte chunks
+
+__device__ __align__(16) const uint32_t zero_chunk[4] = {0, 0, 0, 0};
+
+// What happens to a finished sum of out[m, n].
+struct Epilogue {
+    const uint16_t *bias, *residual;
+    uint16_t *out, *pre;
+    int64_t residual_ld, N;
+    int act;
+};
+
+template <int ACT>
+__device__ static inline void act8(float (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = act_f(v[i], ACT);
+}
+
+// Eight adjacent columns of row m from column n (`count` of them inside the matrix).
+template <int DT>
+__device__ static inline void finish8(const Epilogue &e, int64_t m, int64_t n, int count, float (&v)[8]) {
+    typedef HVec<8>::t vec;
+    auto get = [&](const uint16_t *p, float (&f)[8]) {
+        if (count == 8) {
+            const vec q = *(const vec *)p;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] = to_f32<DT>(q[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] = i < count ? to_f32<DT>(p[i]) : 0.0f;
+        }
+    };
+    auto put = [&](uint16_t *p) {
+        if (count == 8) {
+            vec q;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) q[i] = from_f32<DT>(v[i]);
+            *(vec *)p = q;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i < count) p[i] = from_f32<DT>(v[i]);
+        }
+    };
+    float f[8];
+    if (e.bias) {
+        get(e.bias + n, f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] += f[i];
+    }
+    if (e.pre) put(e.pre + m * e.N + n);
+    switch (e.act) {
+        case MCCB_ACT_RELU: act8<MCCB_ACT_RELU>(v); break;
+        case MCCB_ACT_SILU: act8<MCCB_ACT_SILU>(v); break;
+        case MCCB_ACT_GELU: act8<MCCB_ACT_GELU>(v); break;
+        case MCCB_ACT_SOFTPLUS: act8<MCCB_ACT_SOFTPLUS>(v); break;
+        default: break;
+    }
+    if (e.residual) {
+        get(e.residual + m * e.residual_ld + n, f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] += f[i];
+    }
+    put(e.out + m * e.N + n);
+}
+
+// Two operands whose rows run along the contraction: P [M,K] and Q [N,K], 16-byte aligned rows.
+struct Product {
+    const uint16_t *p, *q;
+    int64_t p_ld, q_ld;
+    int64_t M, N, K;
+    int tiles_m, tiles_n, splits, steps_per_split;  // steps of kBK
+    float *partial;                                 // [splits][M][N] where splits > 1
+};
+
+// A block's tile: consecutive blocks go to different XCDs, so each XCD gets a run of tiles, and a
+// run walks columns of eight tile rows, whose operands its L2 then holds.
+__device__ static inline void tile_of(const Product &g, int &tm, int &tn) {
+    constexpr int kXcd = 8, kGroup = 8;
+    const int n = g.tiles_m * g.tiles_n, id = blockIdx.x;
+    const int full = n / kXcd * kXcd;
+    const int t = id < full ? id % kXcd * (n / kXcd) + id / kXcd : id;
+    const int per = kGroup * g.tiles_n, grp = t / per, first = grp * kGroup;
+    const int rows = g.tiles_m - first < kGroup ? g.tiles_m - first : kGroup;
+    const int r = t - grp * per;
+    tm = first + r % rows;
+    tn = r / rows;
+}
+
+template <int DT, int BM, int BN, int WM, int WN>
+__global__ void __launch_bounds__(WM *WN *kWave)
+    product_tiles(Product g, Epilogue e) {
+    constexpr int kWaves = WM * WN, kThreads = kWaves * kWave;
+    constexpr int TM = BM / WM / 32, TN = BN / WN / 32;      // a wave's 32x32 tiles
+    constexpr int kRows = BM + BN, kLoads = kRows / 8 / kWaves;  // a wave's load takes 8 rows
+    constexpr int kBuf = kRows * kBK;                        // 16-bit values of a buffer
+    constexpr int kStage = BN + 4;                           // fp32 row of the epilogue's staging
+    constexpr int kRound = BM / WM;                          // rows it stages at a time
+    constexpr size_t kBytes = sizeof(uint16_t) * 2 * kBuf > sizeof(float) * kRound * kStage
+                                  ? sizeof(uint16_t) * 2 * kBuf
+                                  : sizeof(float) * kRound * kStage;
+    __shared__ __align__(16) uint8_t smem[kBytes];
+    uint16_t *lds = (uint16_t *)smem;
+    const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int wm = wave / WN, wn = wave % WN;
+    int tm, tn;
+    tile_of(g, tm, tn);
+    const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
+    const int all_steps = (int)((g.K + kBK - 1) / kBK);
+    const int s0 = blockIdx.y * g.steps_per_split;
+    const int s1 = s0 + g.steps_per_split < all_steps ? s0 + g.steps_per_split : all_steps;
+
+    // Row r of a buffer (P's rows, then Q's) holds its eight chunks in the order c ^ (r % 8), so
+    // that reading one chunk of 32 rows spreads over the banks. A load's lane i fills place i % 8 of
+    // row i / 8 of the wave's eight rows. Rows past the matrix repeat its last row.
+    const uint16_t *src[kLoads];
+    int chunk = (lane % 8) ^ (lane / 8);
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+        const int r = (wave * kLoads + i) * 8 + lane / 8;
+        if (r < BM) {
+            const int64_t m = m0 + r < g.M ? m0 + r : g.M - 1;
+            src[i] = g.p + m * g.p_ld + chunk * 8;
+        } else {
+            const int64_t n = n0 + r - BM < g.N ? n0 + r - BM : g.N - 1;
+            src[i] = g.q + n * g.q_ld + chunk * 8;
+        }
+    }
+    typedef __attribute__((address_space(1))) const uint32_t gmem;
+    typedef __attribute__((address_space(3))) uint32_t lmem;
+    auto fill = [&](int step, int buf) {
+        const int64_t k = (int64_t)step * kBK;
+        const bool past = k + chunk * 8 >= g.K;  // rows are padded to whole chunks
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const uint16_t *s = past ? (const uint16_t *)zero_chunk : src[i] + k;
+            __builtin_amdgcn_global_load_lds(
+                (gmem *)s, (lmem *)(lds + buf * kBuf + (wave * kLoads + i) * 8 * kBK), 16, 0, 0);
+        }
+    };
+    f32x16 acc[TN][TM];
+#pragma unroll
+    for (int i = 0; i < TN; ++i)
+#pragma unroll
+        for (int j = 0; j < TM; ++j)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
+
+    fill(s0, 0);
+    for (int s = s0; s < s1; ++s) {
+        const int buf = (s - s0) & 1;
+        // this step's loads have landed, and every wave is done with the other buffer
+        __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
+        __syncthreads();
+        if (s + 1 < s1) fill(s + 1, buf ^ 1);
+        const uint16_t *base = lds + buf * kBuf;
+#pragma unroll
+        for (int ks = 0; ks < kBK / 16; ++ks) {
+            const int c = (ks * 2 + lane / 32) ^ (lane % 8);  // rows below are lane % 8 modulo 8
+            u16x8 a[TN], b[TM];
+#pragma unroll
+            for (int i = 0; i < TN; ++i) {
+                const int r = BM + (wn * TN + i) * 32 + lane % 32;
+                a[i] = *(const u16x8 *)(base + r * kBK + c * 8);
+            }
+#pragma unroll
+            for (int j = 0; j < TM; ++j) {
+                const int r = (wm * TM + j) * 32 + lane % 32;
+                b[j] = *(const u16x8 *)(base + r * kBK + c * 8);
+            }
+#pragma unroll
+            for (int i = 0; i < TN; ++i)
+#pragma unroll
+                for (int j = 0; j < TM; ++j) acc[i][j] = mfma32<DT>(a[i], b[j], acc[i][j]);
+        }
+    }
+    // Epilogue, kRound rows at a time. A lane's 16 sums of a 32x32 tile are column lane % 32 (a row
+    // of P) and rows 8 (v / 4) + 4 (lane / 32) + v % 4 (rows of Q, columns of the output).
+    float *stage = (float *)smem;
+#pragma unroll
+    for (int round = 0; round < WM; ++round) {
+        __syncthreads();
+        if (wm == round) {
+#pragma unroll
+            for (int i = 0; i < TN; ++i)
+#pragma unroll
+                for (int j = 0; j < TM; ++j)
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) {
+                        const int m = j * 32 + lane % 32;
+                        const int n = (wn * TN + i) * 32 + 8 * v + 4 * (lane / 32);
+                        *(f32x4 *)(stage + m * kStage + n) =
+                            f32x4{acc[i][j][4 * v], acc[i][j][4 * v + 1], acc[i][j][4 * v + 2],
+                                  acc[i][j][4 * v + 3]};
+                    }
+        }
+        __syncthreads();
+        constexpr int kAcross = BN / 8, kDown = kThreads / kAcross;
+        const int n = threadIdx.x % kAcross * 8;
+        const int64_t left = g.N - n0 - n;
+        if (left <= 0) continue;
+        for (int r = threadIdx.x / kAcross; r < kRound; r += kDown) {
+            const int64_t m = m0 + round * kRound + r;
+            if (m >= g.M) break;
+            float v[8];
+            const f32x4 lo = *(const f32x4 *)(stage + r * kStage + n);
+            const f32x4 hi = *(const f32x4 *)(stage + r * kStage + n + 4);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = lo[i], v[4 + i] = hi[i];
+            const int count = left < 8 ? (int)left : 8;
+            if (g.partial) {
+                float *q = g.partial + ((int64_t)blockIdx.y * g.M + m) * g.N + n0 + n;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (i < count) q[i] = v[i];
+            } else {
+                finish8<DT>(e, m, n0 + n, count, v);
+            }
+        }
+    }
+}
+
+// The split contraction's partial sums, added in order, through the epilogue.
+template <int DT>
+__global__ void __launch_bounds__(256)
+    finish(Product g, Epilogue e) {
+    const int64_t across = (g.N + 7) / 8;
+    const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t m = id / across, n = id % across * 8;
+    if (m >= g.M) return;
+    const int count = g.N - n < 8 ? (int)(g.N - n) : 8;
+    float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    for (int s = 0; s < g.splits; ++s) {
+        const float *p = g.partial + ((int64_t)s * g.M + m) * g.N + n;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < count) v[i] += p[i];
+    }
+    finish8<DT>(e, m, n, count, v);
+}
+
+// M up to 16 MB: a block has 16 rows of Q; its waves take chunks of 32 of the contraction in turn and
+// add their sums in LDS. Loads are 16 bytes at any 2-byte address, so nothing is packed.
+template <int DT, int MB, int WAVES>
+__global__ void __launch_bounds__(WAVES *kWave)
+    product_skinny(Product g, Epilogue e) {
+    __shared__ float part[WAVES][MB * 16][16 + 4];
+    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+    const int64_t n0 = (int64_t)blockIdx.x * 16;
+    const int64_t n = n0 + lane % 16 < g.N ? n0 + lane % 16 : g.N - 1;
+    const uint16_t *qp = g.q + n * g.q_ld, *pp[MB];
+#pragma unroll
+    for (int b = 0; b < MB; ++b) {
+        const int64_t m = b * 16 + lane % 16;
+        pp[b] = g.p + (m < g.M ? m : g.M - 1) * g.p_ld;
+    }
+    f32x4 acc[MB];
+#pragma unroll
+    for (int b = 0; b < MB; ++b) acc[b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    auto chunk = [&](const uint16_t *p, int64_t k) {
+        u16x8 v;
+        if (k + 8 <= g.K) {
+            v = *(const HVec<8>::t *)(p + k);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = k + i < g.K ? p[k + i] : 0;
+        }
+        return v;
+    };
+    // the whole part without a bounds check: eight steps' loads in flight
+    constexpr int kAhead = 8;
+    const int64_t own = (lane / 16) * 8, stride = WAVES * 32;
+    int64_t k = wave * 32;
+    for (; k + (kAhead - 1) * stride + 32 <= g.K; k += kAhead * stride) {
+        u16x8 q[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) q[i] = *(const HVec<8>::t *)(qp + k + i * stride + own);
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+            for (int b = 0; b < MB; ++b) {
+                const u16x8 p = *(const HVec<8>::t *)(pp[b] + k + i * stride + own);
+                acc[b] = mfma16<DT>(q[i], p, acc[b]);
+            }
+    }
+    for (; k < g.K; k += stride) {
+        const u16x8 q = chunk(qp, k + own);
+#pragma unroll
+        for (int b = 0; b < MB; ++b) acc[b] = mfma16<DT>(q, chunk(pp[b], k + own), acc[b]);
+    }
+    // a lane's four sums: row lane % 16 of P, rows 4 (lane / 16) + 0..3 of Q
+#pragma unroll
+    for (int b = 0; b < MB; ++b)
+        *(f32x4 *)&part[wave][b * 16 + lane % 16][lane / 16 * 4] = acc[b];
+    __syncthreads();
+    for (int id = threadIdx.x; id < MB * 16 * 2; id += WAVES * kWave) {
+        const int64_t m = id / 2, c = id % 2 * 8, left = g.N - n0 - c;
+        if (m >= g.M || left <= 0) continue;
+        float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] += part[w][m][c + i];
+        finish8<DT>(e, m, n0 + c, left < 8 ? (int)left : 8, v);
+    }
+}
+
+// ---------------------------------------------------------------------------------------------
+// Operands laid out for the products
+// ---------------------------------------------------------------------------------------------
+// dst [R, Cp] = src [R, C], zeros past C.
+__global__ void __launch_bounds__(256)
+    pack_rows(const uint16_t *__restrict__ src, int64_t ld, int64_t R, int64_t C, int64_t Cp,
+              uint16_t *__restrict__ dst) {
+    const int64_t id = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
+    if (id >= R * Cp) return;
+    const int64_t r = id / Cp, c = id % Cp;  // Cp is a multiple of 8
+    u16x8 v;
+    if (c + 8 <= C) {
+        v = *(const HVec<8>::t *)(src + r * ld + c);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = c + i < C ? src[r * ld + c + i] : 0;
+    }
+    *(u16x8 *)(dst + id) = v;
+}
+
+// What the backward makes of gout (or of a plain matrix, without `pre`): g = gout act'(pre), kept by
+// rows and / or by columns, and the column sums of 64 rows. One 64x64 tile a block.
+struct Turn {
+    const uint16_t *src, *pre;
+    int64_t ld, R, C;
+    uint16_t *rows;     // [R, rows_ld] or NULL
+    uint16_t *columns;  // [C, columns_ld] or NULL, zeros past R
+    float *sums;        // [row tiles][C] or NULL
+    int64_t rows_ld, columns_ld;
+    int act;
+};
+
+template <int DT>
+__global__ void __launch_bounds__(256)
+    turn(Turn t) {
+    __shared__ uint16_t tile[64][64 + 2];
+    __shared__ float sum[32][64];
+    const int64_t r0 = (int64_t)blockIdx.y * 64, c0 = (int64_t)blockIdx.x * 64;
+    const int c = threadIdx.x % 8 * 8, rr = threadIdx.x / 8;  // eight columns, rows rr and rr + 32
+    float s[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    const int64_t left = t.C - c0 - c;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        const int r = rr + half * 32;
+        u16x8 v = {0, 0, 0, 0, 0, 0, 0, 0};
+        if (r0 + r < t.R && left > 0) {
+            const uint16_t *p = t.src + (r0 + r) * t.ld + c0 + c;
+            const uint16_t *z = t.pre ? t.pre + (r0 + r) * t.C + c0 + c : nullptr;
+            u16x8 q = {0, 0, 0, 0, 0, 0, 0, 0};
+            if (left >= 8) {
+                v = *(const HVec<8>::t *)p;
+                if (z) q = *(const HVec<8>::t *)z;
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (i < left) {
+                        v[i] = p[i];
+                        if (z) q[i] = z[i];
+                    }
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                float f = to_f32<DT>(v[i]);
+                if (z) {
+                    f *= act_slope_f(to_f32<DT>(q[i]), t.act);
+                    v[i] = from_f32<DT>(f);
+                }
+                s[i] += f;
+            }
+            if (t.rows) {
+                // rows are padded to whole vectors, with zeros past C
+                u16x8 w = v;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (i >= left) w[i] = 0;
+                *(u16x8 *)(t.rows + (r0 + r) * t.rows_ld + c0 + c) = w;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) tile[r][c + i] = v[i];
+    }
+    if (t.sums) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum[rr][c + i] = s[i];
+    }
+    __syncthreads();
+    if (t.sums && threadIdx.x < 64 && c0 + threadIdx.x < t.C) {
+        float a = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) a += sum[i][threadIdx.x];
+        t.sums[(int64_t)blockIdx.y * t.C + c0 + threadIdx.x] = a;
+    }
+    if (!t.columns) return;
+    // column cc, rows r .. r + 7 of the tile as one vector
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        const int cc = rr + half * 32, r = c;
+        if (c0 + cc >= t.C || r0 + r >= t.columns_ld) continue;
+        u16x8 v;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = tile[r + i][cc];
+        *(u16x8 *)(t.columns + (c0 + cc) * t.columns_ld + r0 + r) = v;
+    }
+}
+
+// bias gradient: [P][N] over P, in fp64.
+template <int DT>
+__global__ void __launch_bounds__(256)
+    sum_columns(const float *__restrict__ sums, int64_t P, int64_t N, uint16_t *__restrict__ gb) {
+    __shared__ double part[4][64];
+    const int lane = threadIdx.x % 64, w = threadIdx.x / 64;
+    const int64_t c = (int64_t)blockIdx.x * 64 + lane;
+    double s = 0.0;
+    if (c < N) {
+#pragma unroll 8
+        for (int64_t p = w; p < P; p += 4) s += (double)sums[p * N + c];
+    }
+    part[w][lane] = s;
+    __syncthreads();
+    if (w == 0 && c < N)
+        gb[c] = from_f32<DT>((float)((part[0][lane] + part[1][lane]) + (part[2][lane] + part[3][lane])));
+}
+
+// ---------------------------------------------------------------------------------------------
+// Host
+// ---------------------------------------------------------------------------------------------
+int64_t up8(int64_t v) { return (v + 7) & ~(int64_t)7; }
+uint64_t area(int64_t rows, int64_t ld) { return align16((uint64_t)rows * (uint64_t)ld * 2); }
+
+bool direct_rows(const void *p, int64_t ld, int64_t K) {
+    return !misaligned(p, 16) && ld % 8 == 0 && K % 8 == 0;
+}
+
+// How a product is cut; a function of its sizes alone.
+struct Cut {
+    bool skinny, large;
+    int splits, steps_per_split;
+    int64_t tiles_m, tiles_n;
+    uint64_t partial;  // workspace bytes
+};
+
+Cut cut_of(int64_t M, int64_t N, int64_t K) {
+    Cut c{};
+    c.skinny = M <= 64;
+    c.splits = 1;
+    if (c.skinny) return c;
+    // 256x256 tiles read half as much of LDS and L2 a product as 128x128 ones, which in turn fill the
+    // 256 compute units from a quarter of the output.
+    const int64_t big = ((M + 255) / 256) * ((N + 255) / 256);
+    c.large = big >= 200;
+    const int64_t b = c.large ? 256 : 128;
+    c.tiles_m = (M + b - 1) / b, c.tiles_n = (N + b - 1) / b;
+    const int64_t tiles = c.tiles_m * c.tiles_n, steps = (K + kBK - 1) / kBK;
+    int64_t splits = 1;
+    if (tiles < 256) {  // fewer blocks than compute units
+        splits = 512 / tiles;
+        if (splits > steps / 4) splits = steps / 4;
+        if (splits > 32) splits = 32;
+        if (splits < 2) splits = 1;
+    }
+    const int64_t per = (steps + splits - 1) / splits;
+    c.steps_per_split = (int)per;
+    c.splits = (int)((steps + per - 1) / per);
+    if (c.splits > 1) c.partial = (uint64_t)c.splits * (uint64_t)M * (uint64_t)N * 4;
+    return c;
+}
+
+template <int DT>
+int launch_product(const uint16_t *p, int64_t p_ld, const uint16_t *q, int64_t q_ld, int64_t M,
+                   int64_t N, int64_t K, const Epilogue &e, void *partial, hipStream_t st) {
+    const Cut c = cut_of(M, N, K);
+    Product g{p, q, p_ld, q_ld, M, N, K, (int)c.tiles_m, (int)c.tiles_n, c.splits, c.steps_per_split,
+              c.splits > 1 ? (float *)partial : nullptr};
+    if (c.skinny) {
+        const dim3 grid((unsigned)((N + 15) / 16));
+        if (M <= 16)
+            hipLaunchKernelGGL((product_skinny<DT, 1, 8>), grid, dim3(512), 0, st, g, e);
+        else if (M <= 32)
+            hipLaunchKernelGGL((product_skinny<DT, 2, 8>), grid, dim3(512), 0, st, g, e);
+        else
+            hipLaunchKernelGGL((product_skinny<DT, 4, 8>), grid, dim3(512), 0, st, g, e);
+        return launched();
+    }
+    const dim3 grid((unsigned)(c.tiles_m * c.tiles_n), (unsigned)c.splits);
+    if (c.large)
+        hipLaunchKernelGGL((product_tiles<DT, 256, 256, 2, 4>), grid, dim3(512), 0, st, g, e);
+    else
+        hipLaunchKernelGGL((product_tiles<DT, 128, 128, 2, 2>), grid, dim3(256), 0, st, g, e);
+    const int rc = launched();
+    if (rc != MCCB_OK || c.splits == 1) return rc;
+    const int64_t ids = M * ((N + 7) / 8);
+    hipLaunchKernelGGL((finish<DT>), dim3((unsigned)((ids + 255) / 256)), dim3(256), 0, st, g, e);
+    return launched();
+}
+
+int pack(const void *src, int64_t ld, int64_t R, int64_t C, void *dst, hipStream_t st) {
+    const int64_t n = R * up8(C) / 8;
+    hipLaunchKernelGGL(pack_rows, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st,
+                       (const uint16_t *)src, ld, R, C, up8(C), (uint16_t *)dst);
+    return launched();
+}
+
+template <int DT>
+int launch_turn(const Turn &t, hipStream_t st) {
+    const dim3 grid((unsigned)((t.C + 63) / 64), (unsigned)((t.R + 63) / 64));
+    hipLaunchKernelGGL((turn<DT>), grid, dim3(256), 0, st, t);
+    return launched();
+}
+
+int check_linear(const mccb_linear_t *a) {
+    if (!a) return MCCB_ERR_PARAM_NULLPTR;
+    if (a->dtype != MCCB_BF16 && a->dtype != MCCB_FP16) return MCCB_ERR_PARAM_INVALID;
+    if (a->activation < MCCB_ACT_NONE || a->activation > MCCB_ACT_SOFTPLUS)
+        return MCCB_ERR_PARAM_INVALID;
+    // tiles of 64 rows and columns are counted in a grid's 65535 rows
+    if (a->M < 0 || a->M > ((int64_t)1 << 22) - 64 || a->N < 1 || a->N > ((int64_t)1 << 22) - 64 ||
+        a->K < 1 || a->K > ((int64_t)1 << 22) - 64)
+        return MCCB_ERR_SHAPE;
+    return MCCB_OK;
+}
+
+int check_linear_inputs(const mccb_linear_t *a, Span *in) {
+    if (!a->weight || (!a->x && a->M > 0)) return MCCB_ERR_PARAM_NULLPTR;
+    const int64_t xs[2] = {a->M, a->K}, ws[2] = {a->N, a->K};
+    const int64_t xst[2] = {a->x_ld, 1}, wst[2] = {a->weight_ld, 1};
+    uint64_t x, w;
+    if (!extent(2, xs, xst, 2, &x) || !extent(2, ws, wst, 2, &w) || misaligned(a->x, 2) ||
+        misaligned(a->weight, 2) || misaligned(a->bias, 2))
+        return MCCB_ERR_PARAM_INVALID;
+    in[0] = {a->x, x};
+    in[1] = {a->weight, w};
+    in[2] = {a->bias, (uint64_t)a->N * 2};
+    return MCCB_OK;
+}
+
+struct FwdLayout {
+    bool pack_x, pack_w;
+    uint64_t x, w, partial, total;  // offsets, and the size
+};
+
+FwdLayout fwd_layout(const mccb_linear_t *a) {
+    FwdLayout l{};
+    const Cut c = cut_of(a->M, a->N, a->K);
+    uint64_t at = 0;
+    if (!c.skinny) {
+        l.pack_x = !direct_rows(a->x, a->x_ld, a->K);
+        l.pack_w = !direct_rows(a->weight, a->weight_ld, a->K);
+        l.x = at;
+        if (l.pack_x) at += area(a->M, up8(a->K));
+        l.w = at;
+        if (l.pack_w) at += area(a->N, up8(a->K));
+    }
+    l.partial = at;
+    l.total = at + c.partial;
+    return l;
+}
+
+// The backward's: g by rows and by columns, x and w by columns, the column sums, and the larger of
+// the two products' partial sums.
+struct BwdLayout {
+    uint64_t g_rows, g_cols, x_cols, w_cols, sums, partial, total;
+};
+
+BwdLayout bwd_layout(const mccb_linear_t *a) {
+    BwdLayout l{};
+    const int64_t Mp = up8(a->M), Np = up8(a->N);
+    const Cut cx = cut_of(a->M, a->K, a->N), cw = cut_of(a->N, a->K, a->M);
+    uint64_t at = 0;
+    l.g_rows = at, at += area(a->M, Np);
+    l.g_cols = at, at += area(a->N, Mp);
+    l.x_cols = at, at += area(a->K, Mp);
+    l.w_cols = at, at += area(a->K, Np);
+    l.sums = at, at += align16((uint64_t)((a->M + 63) / 64) * (uint64_t)a->N * 4);
+    l.partial = at, at += cx.partial > cw.partial ? cx.partial : cw.partial;
+    l.total = at;
+    return l;
+}
+
+template <typename F>
+int by_dtype(int dtype, F f) {
+    return dtype == MCCB_BF16 ? f(std::integral_constant<int, MCCB_BF16>{})
+                              : f(std::integral_constant<int, MCCB_FP16>{});
+}
+
+// Zeros for a gradient that sums no rows.
+__global__ void __launch_bounds__(256) fill_zero(uint16_t *p, int64_t n) {
+    const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (id < n) p[id] = 0;
+}
+int zero(void *p, int64_t n, hipStream_t st) {
+    if (!p) return MCCB_OK;
+    hipLaunchKernelGGL(fill_zero, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, (uint16_t *)p, n);
+    return launched();
+}
+
+}  // namespace
+
+extern "C" {
+
+int mccb_linear_forward_get_workspace_size(const mccb_linear_t *a, uint64_t *size) {
+    if (!size) return MCCB_ERR_PARAM_NULLPTR;
+    const int rc = check_linear(a);
+    if (rc != MCCB_OK) return rc;
+    *size = fwd_layout(a).total;
+    return MCCB_OK;
+}
+
+int mccb_linear_forward(const mccb_linear_t *a, const void *residual, int64_t residual_ld, void *out,
+                        void *pre, void *ws, uint64_t ws_size, void *stream) {
+    int rc = check_linear(a);
+    if (rc != MCCB_OK) return rc;
+    if (!out && a->M > 0) return MCCB_ERR_PARAM_NULLPTR;
+    Span in[4];
+    rc = check_linear_inputs(a, in);
+    if (rc != MCCB_OK) return rc;
+    const int64_t size[2] = {a->M, a->N}, stride[2] = {residual_ld, 1};
+    uint64_t r_bytes = 0;
+    if (residual && (!extent(2, size, stride, 2, &r_bytes) || misaligned(residual, 2)))
+        return MCCB_ERR_PARAM_INVALID;
+    const FwdLayout l = fwd_layout(a);
+    rc = check_workspace(ws, ws_size, l.total);
+    if (rc != MCCB_OK) return rc;
+    in[3] = {residual, r_bytes};
+    const uint64_t n_out = (uint64_t)a->M * (uint64_t)a->N * 2;
+    const Span outs[3] = {{out, n_out}, {pre, n_out}, {ws, l.total}};
+    if (misaligned(out, 2) || misaligned(pre, 2) || outputs_clash(in, 4, outs, 3))
+        return MCCB_ERR_PARAM_INVALID;
+    if (a->M == 0) return MCCB_OK;
+    const hipStream_t st = (hipStream_t)stream;
+    uint8_t *at = (uint8_t *)ws;
+    const void *x = a->x, *w = a->weight;
+    int64_t x_ld = a->x_ld, w_ld = a->weight_ld;
+    if (l.pack_x) {
+        rc = pack(x, x_ld, a->M, a->K, at + l.x, st);
+        if (rc != MCCB_OK) return rc;
+        x = at + l.x, x_ld = up8(a->K);
+    }
+    if (l.pack_w) {
+        rc = pack(w, w_ld, a->N, a->K, at + l.w, st);
+        if (rc != MCCB_OK) return rc;
+        w = at + l.w, w_ld = up8(a->K);
+    }
+    const Epilogue e{(const uint16_t *)a->bias, (const uint16_t *)residual, (uint16_t *)out,
+                     (uint16_t *)pre, residual_ld, a->N, a->activation};
+    return by_dtype(a->dtype, [&](auto dt) {
+        return launch_product<decltype(dt)::value>((const uint16_t *)x, x_ld, (const uint16_t *)w, w_ld,
+                                                   a->M, a->N, a->K, e, at + l.partial, st);
+    });
+}
+
+int mccb_linear_backward_get_workspace_size(const mccb_linear_t *a, uint64_t *size) {
+    if (!size) return MCCB_ERR_PARAM_NULLPTR;
+    const int rc = check_linear(a);
+    if (rc != MCCB_OK) return rc;
+    *size = a->M > 0 ? bwd_layout(a).total : 0;
+    return MCCB_OK;
+}
+
+int mccb_linear_backward(const mccb_linear_t *a, const void *gout, int64_t gout_ld, const void *pre,
+                         void *gx, void *gw, void *gb, void *ws, uint64_t ws_size, void *stream) {
+    int rc = check_linear(a);
+    if (rc != MCCB_OK) return rc;
+    if (a->M > 0 && (!gout || (a->activation != MCCB_ACT_NONE && !pre))) return MCCB_ERR_PARAM_NULLPTR;
+    Span in[5];
+    rc = check_linear_inputs(a, in);
+    if (rc != MCCB_OK) return rc;
+    const int64_t size[2] = {a->M, a->N}, stride[2] = {gout_ld, 1};
+    uint64_t g_bytes = 0, need = 0;
+    if (!extent(2, size, stride, 2, &g_bytes) || misaligned(gout, 2) || misaligned(pre, 2))
+        return MCCB_ERR_PARAM_INVALID;
+    mccb_linear_backward_get_workspace_size(a, &need);
+    rc = check_workspace(ws, ws_size, need);
+    if (rc != MCCB_OK) return rc;
+    in[3] = {gout, g_bytes};
+    in[4] = {pre, (uint64_t)a->M * (uint64_t)a->N * 2};
+    const Span outs[4] = {{gx, (uint64_t)a->M * (uint64_t)a->K * 2},
+                          {gw, (uint64_t)a->N * (uint64_t)a->K * 2},
+                          {gb, (uint64_t)a->N * 2},
+                          {ws, need}};
+    if (misaligned(gx, 2) || misaligned(gw, 2) || misaligned(gb, 2) || outputs_clash(in, 5, outs, 4))
+        return MCCB_ERR_PARAM_INVALID;
+    const hipStream_t st = (hipStream_t)stream;
+    if (a->M == 0) {
+        rc = zero(gw, a->N * a->K, st);
+        return rc != MCCB_OK ? rc : zero(gb, a->N, st);
+    }
+    const BwdLayout l = bwd_layout(a);
+    uint8_t *at = (uint8_t *)ws;
+    const int64_t Mp = up8(a->M), Np = up8(a->N);
+    uint16_t *g_rows = (uint16_t *)(at + l.g_rows), *g_cols = (uint16_t *)(at + l.g_cols);
+    uint16_t *x_cols = (uint16_t *)(at + l.x_cols), *w_cols = (uint16_t *)(at + l.w_cols);
+    float *sums = (float *)(at + l.sums);
+    return by_dtype(a->dtype, [&](auto dt) {
+        constexpr int DT = decltype(dt)::value;
+        const bool slope = a->activation != MCCB_ACT_NONE;
+        const Turn tg{(const uint16_t *)gout, slope ? (const uint16_t *)pre : nullptr,
+                      gout_ld, a->M, a->N, gx ? g_rows : nullptr, gw ? g_cols : nullptr,
+                      gb ? sums : nullptr, Np, Mp, a->activation};
+        int r = gx || gw || gb ? launch_turn<DT>(tg, st) : MCCB_OK;
+        if (r == MCCB_OK && gb) {
+            hipLaunchKernelGGL((sum_columns<DT>), dim3((unsigned)((a->N + 63) / 64)), dim3(256), 0, st,
+                               sums, (a->M + 63) / 64, a->N, (uint16_t *)gb);
+            r = launched();
+        }
+        if (r == MCCB_OK && gx) {
+            const Turn tw{(const uint16_t *)a->weight, nullptr, a->weight_ld, a->N, a->K,
+                          nullptr, w_cols, nullptr, 0, Np, MCCB_ACT_NONE};
+            r = launch_turn<DT>(tw, st);
+            const Epilogue e{nullptr, nullptr, (uint16_t *)gx, nullptr, 0, a->K, MCCB_ACT_NONE};
+            if (r == MCCB_OK)
+                r = launch_product<DT>(g_rows, Np, w_cols, Np, a->M, a->K, a->N, e, at + l.partial, st);
+        }
+        if (r == MCCB_OK && gw) {
+            const Turn tx{(const uint16_t *)a->x, nullptr, a->x_ld, a->M, a->K,
+                          nullptr, x_cols, nullptr, 0, Mp, MCCB_ACT_NONE};
+            r = launch_turn<DT>(tx, st);
+            const Epilogue e{nullptr, nullptr, (uint16_t *)gw, nullptr, 0, a->K, MCCB_ACT_NONE};
+            if (r == MCCB_OK)
+                r = launch_product<DT>(g_cols, Mp, x_cols, Mp, a->N, a->K, a->M, e, at + l.partial, st);
+        }
+        return r;
+    });
+}
+
+}  // extern "C"

@@ -56,6 +56,11 @@ class ScanGradArgs(ctypes.Structure):
                        "gradC gradA gradD gradDtBias gradState")
 
 
+class LinearArgs(ctypes.Structure):
+    """mccb_linear_t."""
+    _fields_ = _fields("i: M K N; w: dtype activation; p: x weight bias; i: x_ld weight_ld")
+
+
 _SIGNATURES = {
     "mccb_conv_act_forward": (ConvArgs, _vp, _vp, _vp),
     "mccb_conv_act_backward_get_workspace_size": (ConvArgs, _vp),
@@ -67,6 +72,10 @@ _SIGNATURES = {
     "mccb_scan_backward_get_workspace_size": (ScanArgs, _vp),
     "mccb_scan_backward": (ScanArgs, _vp, _vp, _vp, _u64, _vp),
     "mccb_scan_step": (ScanArgs, _vp, _vp, _vp),
+    "mccb_linear_forward_get_workspace_size": (LinearArgs, _vp),
+    "mccb_linear_forward": (LinearArgs, _vp, _i64, _vp, _vp, _vp, _u64, _vp),
+    "mccb_linear_backward_get_workspace_size": (LinearArgs, _vp),
+    "mccb_linear_backward": (LinearArgs, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _u64, _vp),
 }
 
 _lib = None
@@ -386,3 +395,83 @@ def scan_step(state, x, dt, A, B, C, D=None, z=None, dt_bias=None, softplus=True
         _check("out", out, (Bn, H), kind, dev, True)
     _run("mccb_scan_step", args, state.data_ptr(), out.data_ptr(), _handle(stream, dev))
     return out
+
+
+# -- matrix product with its epilogue ----------------------------------------------------------------
+class LinearGrads(NamedTuple):
+    x: Optional[torch.Tensor]
+    weight: Optional[torch.Tensor]
+    bias: Optional[torch.Tensor]
+
+
+def _rows2(name, t):
+    """A [..., C] tensor as [R, C] with evenly spaced, contiguous rows, and the rows' spacing."""
+    if t.dim() != 2:
+        try:
+            t = t.view(-1, t.shape[-1])
+        except RuntimeError:
+            raise ValueError(f"{name}'s rows are not evenly spaced: make it contiguous") from None
+    R, C = t.shape
+    if C > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    return t, t.stride(0) if R > 1 else C
+
+
+def _linear_args(x, weight, bias, activation):
+    if not isinstance(x, torch.Tensor) or x.dim() < 2:
+        raise ValueError("x must be a [...,K] tensor of at least two dimensions")
+    x2, x_ld = _rows2("x", x)
+    code, dev = _data("x", x2, "MK")
+    M, K = x2.shape
+    if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
+        raise ValueError("weight must be a [N,K] tensor")
+    N = weight.shape[0]
+    _check("weight", weight, (N, K), x.dtype, dev)
+    weight, w_ld = _rows2("weight", weight)
+    if bias is not None:
+        _check("bias", bias, (N,), x.dtype, dev, True)
+    return LinearArgs(M, K, N, code, _activation(activation, (0, 1, 2, 3, 4)), x2.data_ptr(),
+                      weight.data_ptr(), _ptr(bias), x_ld, w_ld), (M, K, N, x.dtype, dev)
+
+
+def linear_forward(x, weight, bias=None, activation=None, residual=None, return_pre=False, out=None,
+                   stream=None):
+    """out [...,N] = activation(x weight^T + bias) + residual; x [...,K], weight [N,K], bias [N],
+    residual [...,N], activation None, "relu", "silu", "gelu" (tanh form) or "softplus". With
+    `return_pre` the result is (out, pre), pre = x weight^T + bias as linear_backward needs it."""
+    args, (M, K, N, kind, dev) = _linear_args(x, weight, bias, activation)
+    shape = (*x.shape[:-1], N)
+    res, res_ld = None, 0
+    if residual is not None:
+        _check("residual", residual, shape, kind, dev)
+        res, res_ld = _rows2("residual", residual)
+    with _On(stream):
+        if out is None:
+            out = torch.empty(shape, dtype=kind, device=dev)
+        else:
+            _check("out", out, shape, kind, dev, True)
+        pre = torch.empty(shape, dtype=kind, device=dev) if return_pre else None
+        ws, n = _workspace("mccb_linear_forward_get_workspace_size", args, dev)
+    _run("mccb_linear_forward", args, _ptr(res), res_ld, out.data_ptr(), _ptr(pre), _ptr(ws), n,
+         _handle(stream, dev))
+    return (out, pre) if return_pre else out
+
+
+def linear_backward(gradOut, x, weight, pre=None, activation=None, grad_x=True, grad_weight=True,
+                    grad_bias=True, stream=None) -> LinearGrads:
+    """Gradients of linear_forward for gradOut [...,N]: of x, weight and bias, as asked for. `pre` is
+    linear_forward's (not needed without an activation). The residual's gradient is gradOut."""
+    args, (M, K, N, kind, dev) = _linear_args(x, weight, None, activation)
+    shape = (*x.shape[:-1], N)
+    _check("gradOut", gradOut, shape, kind, dev)
+    go, go_ld = _rows2("gradOut", gradOut)
+    if pre is not None:
+        _check("pre", pre, shape, kind, dev, True)
+    with _On(stream):
+        g = LinearGrads(torch.empty(x.shape, dtype=kind, device=dev) if grad_x else None,
+                        torch.empty((N, K), dtype=kind, device=dev) if grad_weight else None,
+                        torch.empty(N, dtype=kind, device=dev) if grad_bias else None)
+        ws, n = _workspace("mccb_linear_backward_get_workspace_size", args, dev)
+    _run("mccb_linear_backward", args, go.data_ptr(), go_ld, _ptr(pre), _ptr(g.x), _ptr(g.weight),
+         _ptr(g.bias), _ptr(ws), n, _handle(stream, dev))
+    return g
