@@ -56,6 +56,10 @@ struct HVec<1> {
     };
 };
 
+// A barrier for data in LDS: this wave's LDS accesses are done, its global loads and stores may stay
+// in flight (__syncthreads waits for those too, which ends every prefetch at the barrier).
+__device__ static inline void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
 // ---------------------------------------------------------------------------------------------
 // fp32 functions. exp2, log and the reciprocal are the hardware's (about 1 ulp).
 // ---------------------------------------------------------------------------------------------
@@ -66,27 +70,21 @@ __device__ static inline float rcp_f(float v) { return __builtin_amdgcn_rcpf(v);
 // 1/(1+exp(-v)): exp(-v) overflows to infinity below v = -88 and its reciprocal is 0, the limit.
 __device__ static inline float sigmoid_f(float v) { return rcp_f(1.0f + exp_f(-v)); }
 
-// log(1+e) for e in [0,1]: 2 atanh(s) with s = e/(2+e) in [0,1/3], and atanh(s)/s = 1 + s^2 P(s^2)
-// with P of degree 3, fitted at Chebyshev nodes over s^2 in [0,1/9] (relative error 1.5e-8). Keeps
-// the relative precision of small e, which log(1+e) loses: step sizes of 1e-3 come from e = 1e-3.
+// log(1+e) for e in [0,1] to 2e-7 of itself: with u = 1+e rounded, log(1+e) = log(u) + (e-(u-1))/u,
+// whose last term (below 2^-24, its division by u below 2^-25) matters where e is small and u near
+// 1. Step sizes of 1e-3 come from e = 1e-3, of which log(1+e) alone keeps four digits.
 __device__ static inline float log1p_unit(float e) {
-    const float q = 2.0f + e;
-    float r = rcp_f(q);
-    r = __builtin_fmaf(__builtin_fmaf(-q, r, 1.0f), r, r);
-    const float s = e * r, s2 = s * s;
-    float p = __builtin_fmaf(s2, 0.13433775305747986f, 0.14116978645324707f);
-    p = __builtin_fmaf(s2, p, 0.2000383585691452f);
-    p = __builtin_fmaf(s2, p, 0.33333319425582886f);
-    return 2.0f * __builtin_fmaf(s * s2, p, s);
+    const float u = 1.0f + e;
+    return __builtin_fmaf(__builtin_amdgcn_logf(u), kLn2, e - (u - 1.0f));
 }
 
-// softplus(v) = max(v,0) + log(1 + exp(-|v|)); `slope` gets its derivative, the logistic function.
+// softplus(v) = max(v,0) + log(1 + exp(-|v|)) (NaN through the second term); `slope` gets its
+// derivative, the logistic function.
 __device__ static inline float softplus_f(float v, float &slope) {
     const float e = exp_f(-__builtin_fabsf(v));
     const float r = rcp_f(1.0f + e);
     slope = v >= 0.0f ? r : e * r;
-    // a NaN stays one (max alone would drop it)
-    return (v != v ? v : __builtin_fmaxf(v, 0.0f)) + log1p_unit(e);
+    return __builtin_fmaxf(v, 0.0f) + log1p_unit(e);
 }
 __device__ static inline float softplus_f(float v) {
     float unused;

@@ -52,23 +52,36 @@ struct ScanIn {
     int64_t chunk_rows;  // whole tiles
 };
 
-// What a block works on.
+// What a block works on. Its threads have two roles: in the recurrence a lane has one channel and its
+// wave four states; in preparing and finishing a tile a thread has JR = 16 / NW adjacent channels
+// of one of the 16 rows, so that rows are read and written by wide loads and stores.
 struct Place {
     int lane, wave;
     int64_t b, h;  // batch; the lane's channel, clamped into the group
     int g;
-    bool on;  // whether the lane has a channel of its own
+    bool on;              // whether the lane has a channel of its own
+    int row, c;           // the thread's row of a tile and its first channel of the block
+    int64_t h0;           // the block's first channel
+    int channels;         // of the block
     int64_t r0, r1, end;  // the chunk's rows, and where its live rows end
 };
 
+template <int NW, bool WIDE>
 __device__ static inline Place place(const ScanIn &a) {
+    constexpr int JR = kTile / NW;
     Place p;
     p.lane = threadIdx.x % kWave;
     p.wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     p.g = blockIdx.x / a.per_group;
-    const int64_t k = (int64_t)(blockIdx.x % a.per_group) * kWave + p.lane;
-    p.on = k < a.K;
-    p.h = p.g * a.K + (p.on ? k : a.K - 1);
+    const int64_t k0 = (int64_t)(blockIdx.x % a.per_group) * kWave;
+    p.channels = a.K - k0 < kWave ? (int)(a.K - k0) : kWave;
+    p.on = p.lane < p.channels;
+    p.h0 = p.g * a.K + k0;
+    p.h = p.h0 + (p.on ? p.lane : p.channels - 1);
+    p.row = threadIdx.x / (kWave / JR);
+    p.c = threadIdx.x % (kWave / JR) * JR;
+    // in a block with fewer channels the last threads take the last JR, twice
+    if (WIDE && p.c > p.channels - JR) p.c = p.channels - JR;
     p.b = blockIdx.y;
     int64_t len = a.S;
     if (a.lengths) {
@@ -81,9 +94,20 @@ __device__ static inline Place place(const ScanIn &a) {
     return p;
 }
 
-__device__ static inline float step_size(const ScanIn &a, float v, float &slope) {
-    slope = 1.0f;
-    return a.softplus ? softplus_f(v, slope) : v;
+// Step sizes d of v = dt + dt_bias, and (SLOPE) their derivatives by v.
+template <bool SLOPE, int JR>
+__device__ static inline void step_sizes(const ScanIn &a, const float (&v)[JR], float (&d)[JR],
+                                         float (&slope)[JR]) {
+    if (a.softplus) {
+#pragma unroll
+        for (int j = 0; j < JR; ++j) {
+            if (SLOPE) d[j] = softplus_f(v[j], slope[j]);
+            else d[j] = softplus_f(v[j]);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < JR; ++j) d[j] = v[j], slope[j] = 1.0f;
+    }
 }
 
 // A [N,H] times log2(e), so that the decay is one exp2; zero for states past N, which then stay 0.
@@ -130,32 +154,114 @@ __device__ static inline void fold_chunks(const float *ends, const float *dsum, 
     }
 }
 
-// One value of B and of C for each of the block's threads: 16 rows of NW*4 states.
+// A thread's way through a [S,B,H] tensor, tile by tile from one that is whole or the chunk's last:
+// JR channels of its row. WIDE: channels are adjacent and every block has JR, one load. Else one by
+// one, channels past the group's last repeating it.
+template <int NW, bool WIDE>
+struct Walk {
+    static constexpr int JR = kTile / NW;
+    typedef typename HVec<JR>::t vec;
+    const uint16_t *p;  // the thread's row of the tile
+    int64_t step, s, h;
+    __device__ inline Walk(const Rows &r, const Place &q, int64_t row, int dir)
+        : p(r.p ? r.p + (row + q.row) * r.s + q.b * r.b + q.h0 * r.h + (WIDE ? q.c : 0) : nullptr),
+          step(dir * kTile * r.s), s(r.s), h(r.h) {}
+    // The tile's values. `last`: its last live row; rows past it repeat it
+    __device__ inline vec fetch(const Place &q, int last) const {
+        const uint16_t *at = p;
+        if (last < kTile - 1) at -= (q.row > last ? q.row - last : 0) * s;
+        if (WIDE) return *(const vec *)at;
+        vec v;
+#pragma unroll
+        for (int i = 0; i < JR; ++i) {
+            const int c = q.c + i < q.channels ? q.c + i : q.channels - 1;
+            v[i] = at[c * h];
+        }
+        return v;
+    }
+    __device__ inline void move(bool on) { p += on ? step : 0; }
+};
+
+// The same channels of the thread's row to a contiguous [S,B,H] output.
+template <bool WIDE, int JR>
+__device__ static inline void store_rows(uint16_t *p, const Place &q, const typename HVec<JR>::t v) {
+    if (WIDE) {
+        *(typename HVec<JR>::t *)p = v;
+    } else {
+#pragma unroll
+        for (int i = 0; i < JR; ++i)
+            if (q.c + i < q.channels) p[i] = v[i];
+    }
+}
+
+// JR adjacent floats of LDS.
+template <int JR>
+__device__ static inline void load_floats(const float *p, float (&f)[JR]) {
+    if constexpr (JR == 2) {
+        const float2 q = *(const float2 *)p;
+        f[0] = q.x, f[1] = q.y;
+    } else {
+#pragma unroll
+        for (int i = 0; i < JR; i += 4) {
+            const float4 q = *(const float4 *)(p + i);
+            f[i] = q.x, f[i + 1] = q.y, f[i + 2] = q.z, f[i + 3] = q.w;
+        }
+    }
+}
+template <int JR>
+__device__ static inline void store_floats(float *p, const float (&f)[JR]) {
+    if constexpr (JR == 2) {
+        *(float2 *)p = make_float2(f[0], f[1]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < JR; i += 4) *(float4 *)(p + i) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
+    }
+}
+// A per-channel fp32 parameter (or zeros) of the thread's channels.
+template <int JR>
+__device__ static inline void load_param(const float *v, const Place &q, float (&f)[JR]) {
+#pragma unroll
+    for (int i = 0; i < JR; ++i) {
+        const int c = q.c + i < q.channels ? q.c + i : q.channels - 1;
+        f[i] = v ? v[q.h0 + c] : 0.0f;
+    }
+}
+
+// The same for B and C: each of the block's threads has one value of 16 rows of NW*4 states.
 template <int DT, int NW>
-struct CoefTile {
+struct CoefWalk {
     int n, t;
-    const uint16_t *bp, *cp;
+    const uint16_t *bp, *cp;  // the thread's row of the tile
+    int64_t bs, cs;
+    int dir;
     bool has;
     uint16_t bv, cv;
-    __device__ inline CoefTile(const ScanIn &a, const Place &p) {
+    __device__ inline CoefWalk(const ScanIn &a, const Place &p, int64_t row, int d)
+        : bs(a.B.s), cs(a.C.s), dir(d * kTile) {
         n = threadIdx.x % (NW * kPer);
         t = threadIdx.x / (NW * kPer);
         has = n < a.N;
         const int nc = has ? n : 0;
-        bp = a.B.p + p.b * a.B.b + p.g * a.B.g + nc * a.B.n;
-        cp = a.C.p + p.b * a.C.b + p.g * a.C.g + nc * a.C.n;
+        bp = a.B.p + p.b * a.B.b + p.g * a.B.g + nc * a.B.n + (row + t) * bs;
+        cp = a.C.p + p.b * a.C.b + p.g * a.C.g + nc * a.C.n + (row + t) * cs;
     }
-    __device__ inline void fetch(const ScanIn &a, int64_t t0, int64_t end) {
-        const int64_t r = t0 + t < end ? t0 + t : end - 1;
-        bv = bp[r * a.B.s];
-        cv = cp[r * a.C.s];
+    template <bool USE_B, bool USE_C>
+    __device__ inline void fetch(int last) {
+        const uint16_t *b = bp, *c = cp;
+        if (last < kTile - 1) {
+            const int over = t > last ? t - last : 0;
+            b -= over * bs;
+            c -= over * cs;
+        }
+        if (USE_B) bv = *b;
+        if (USE_C) cv = *c;
     }
-    __device__ inline float b(int64_t t0, int64_t end) const {
-        return has && t0 + t < end ? to_f32<DT>(bv) : 0.0f;
+    __device__ inline void move(bool on) {
+        bp += on ? dir * bs : 0;
+        cp += on ? dir * cs : 0;
     }
-    __device__ inline float c(int64_t t0, int64_t end) const {
-        return has && t0 + t < end ? to_f32<DT>(cv) : 0.0f;
-    }
+    __device__ inline float b(int last) const { return has && t <= last ? to_f32<DT>(bv) : 0.0f; }
+    __device__ inline float c(int last) const { return has && t <= last ? to_f32<DT>(cv) : 0.0f; }
 };
 
 __device__ static inline void load4(const float *p, float (&f)[kPer]) {
@@ -164,89 +270,157 @@ __device__ static inline void load4(const float *p, float (&f)[kPer]) {
 }
 
 // Forward. ENDS: only the end state of each chunk from a zero state, and its sum of d (the last
-// chunk's is not needed).
-template <int DT, int NW, bool ENDS>
+// chunk's is not needed). One barrier a tile: while the waves scan tile k, whose operands one half
+// of the LDS buffers holds, tile k+1 is prepared in the other half.
+template <int DT, int NW, bool ENDS, bool GATE, bool WIDE>
 __global__ void __launch_bounds__(NW *kWave)
     scan_fwd(ScanIn a, uint16_t *__restrict__ out, float *__restrict__ final_state,
              float *__restrict__ saved, float *__restrict__ ends, float *__restrict__ dsum) {
     constexpr int NP = NW * kPer, JR = kTile / NW;
-    __shared__ float2 sd[kTile][kWave];  // d, d x
-    __shared__ __align__(16) float sB[kTile][NP], sC[kTile][NP];
-    __shared__ float sy[ENDS ? 1 : NW][ENDS ? 1 : kTile][kWave];
-    const Place p = place(a);
+    typedef typename HVec<JR>::t vec;
+    __shared__ __align__(16) float sd[2][kTile][2][kWave];  // d, d x
+    __shared__ __align__(16) float sB[2][kTile][NP], sC[ENDS ? 1 : 2][kTile][NP];
+    __shared__ __align__(16) float sy[ENDS ? 1 : 2][ENDS ? 1 : NW][ENDS ? 1 : kTile][kWave];
+    const Place p = place<NW, WIDE>(a);
     float A2[kPer], s[kPer], total = 0.0f;
     load_rates(a, p, A2);
     load_state(ENDS ? nullptr : a.state, a, p, s);
     if (!ENDS) fold_chunks(ends, dsum, a, p, 0, 1, blockIdx.z, A2, s);
-    const float bias = a.bias ? a.bias[p.h] : 0.0f, D = a.D ? a.D[p.h] : 0.0f;
-    const uint16_t *xp = a.x.p + p.b * a.x.b + p.h * a.x.h;
-    const uint16_t *dp = a.dt.p + p.b * a.dt.b + p.h * a.dt.h;
-    const uint16_t *zp = a.z.p ? a.z.p + p.b * a.z.b + p.h * a.z.h : nullptr;
-    CoefTile<DT, NW> coef(a, p);
-    uint16_t xr[JR], dr[JR], zr[JR];
-    auto fetch = [&](int64_t t0) {
-#pragma unroll
-        for (int j = 0; j < JR; ++j) {
-            const int64_t t = t0 + p.wave + NW * j, r = t < p.end ? t : p.end - 1;
-            xr[j] = xp[r * a.x.s];
-            dr[j] = dp[r * a.dt.s];
-            if (!ENDS && zp) zr[j] = zp[r * a.z.s];
-        }
-        coef.fetch(a, t0, p.end);
+    float bias[JR], D[JR];
+    load_param(a.bias, p, bias);
+    load_param(ENDS ? nullptr : a.D, p, D);
+    Walk<NW, WIDE> xw(a.x, p, p.r0, 1), dw(a.dt, p, p.r0, 1), zw(a.z, p, p.r0, 1);
+    CoefWalk<DT, NW> coef(a, p, p.r0, 1);
+    const int64_t BH = a.nb * a.H, states = BH * a.N;
+    uint16_t *op = ENDS ? nullptr : out + (p.r0 + p.row) * BH + p.b * a.H + p.h0 + p.c;
+    float *kept = saved ? saved + p.r0 / kTile * states + (p.b * a.N + p.wave * kPer) * a.H + p.h : nullptr;
+    // fetched values; the next tile's, and the last one's, that finishing them needs
+    vec xr, dr, zr, xn, zn, xc, zc;
+    const int64_t live_rows = p.end - p.r0;
+    const int tiles = live_rows > 0 ? (int)((live_rows + kTile - 1) / kTile) : 0;
+    const int tail = (int)(live_rows - (int64_t)(tiles - 1) * kTile) - 1;  // the last tile's last row
+    auto fetch = [&](int k) {
+        const int last = k + 1 < tiles ? kTile - 1 : tail;
+        xr = xw.fetch(p, last);
+        dr = dw.fetch(p, last);
+        if (GATE) zr = zw.fetch(p, last);
+        coef.template fetch<true, !ENDS>(last);
+        const bool more = k + 1 < tiles;  // the last tile is fetched again instead of one past it
+        xw.move(more), dw.move(more), coef.move(more);
+        if (GATE) zw.move(more);
     };
-    int64_t t0 = p.r0;
-    if (t0 < p.end) fetch(t0);
-    for (; t0 < p.end; t0 += kTile) {
-        float xf[JR], zf[JR];
+    auto prepare = [&](int k) {
+        const int at = k & 1, last = k + 1 < tiles ? kTile - 1 : tail;
+        float v[JR], d[JR], dx[JR], slope[JR];
 #pragma unroll
-        for (int j = 0; j < JR; ++j) {
-            const int t = p.wave + NW * j;
-            const bool live = t0 + t < p.end;
-            float slope;
-            const float d = live ? step_size(a, to_f32<DT>(dr[j]) + bias, slope) : 0.0f;
-            xf[j] = live ? to_f32<DT>(xr[j]) : 0.0f;
-            zf[j] = to_f32<DT>(zr[j]);
-            sd[t][p.lane] = make_float2(d, d * xf[j]);
+        for (int j = 0; j < JR; ++j) v[j] = to_f32<DT>(dr[j]) + bias[j];
+        step_sizes<false>(a, v, d, slope);
+#pragma unroll
+        for (int j = 0; j < JR; ++j) dx[j] = d[j] * to_f32<DT>(xr[j]);
+        if (p.row > last) {  // past the length: d = 0 leaves the state alone
+#pragma unroll
+            for (int j = 0; j < JR; ++j) d[j] = dx[j] = 0.0f;
         }
-        sB[coef.t][coef.n] = coef.b(t0, p.end);
-        if (!ENDS) sC[coef.t][coef.n] = coef.c(t0, p.end);
-        __syncthreads();
-        if (t0 + kTile < p.end) fetch(t0 + kTile);
-        if (!ENDS && saved) store_state(saved + t0 / kTile * a.nb * a.N * a.H, a, p, s);
+        store_floats(&sd[at][p.row][0][p.c], d);
+        store_floats(&sd[at][p.row][1][p.c], dx);
+        sB[at][coef.t][coef.n] = coef.b(last);
+        if (!ENDS) sC[at][coef.t][coef.n] = coef.c(last);
+    };
+    // Tile k's output, from the sums its waves left in LDS.
+    auto finish = [&](int k) {
+        float y[JR];
 #pragma unroll
-        for (int t = 0; t < kTile; ++t) {
-            const float2 dd = sd[t][p.lane];
-            float Bt[kPer], Ct[kPer], y = 0.0f;
-            load4(&sB[t][p.wave * kPer], Bt);
-            if (!ENDS) load4(&sC[t][p.wave * kPer], Ct);
+        for (int j = 0; j < JR; ++j) y[j] = D[j] * to_f32<DT>(xc[j]);
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                s[i] = __builtin_fmaf(exp2_f(dd.x * A2[i]), s[i], dd.y * Bt[i]);
-                if (!ENDS) y = __builtin_fmaf(Ct[i], s[i], y);
-            }
-            if (ENDS) total += dd.x;
-            else sy[p.wave][t][p.lane] = y;
+        for (int w = 0; w < NW; ++w) {
+            float f[JR];
+            load_floats(&sy[k & 1][w][p.row][p.c], f);
+#pragma unroll
+            for (int j = 0; j < JR; ++j) y[j] += f[j];
         }
-        __syncthreads();
-        if (ENDS) continue;
+        vec v;
 #pragma unroll
-        for (int j = 0; j < JR; ++j) {
-            const int t = p.wave + NW * j;
-            float y = D * xf[j];
-#pragma unroll
-            for (int w = 0; w < NW; ++w) y += sy[w][t][p.lane];
-            if (zp) y *= silu_f(zf[j]);
-            if (p.on && t0 + t < p.r1)
-                out[((t0 + t) * a.nb + p.b) * a.H + p.h] = t0 + t < p.end ? from_f32<DT>(y) : 0;
-        }
+        for (int j = 0; j < JR; ++j)
+            v[j] = from_f32<DT>(GATE ? y[j] * silu_f(to_f32<DT>(zc[j])) : y[j]);
+        if (p.row <= (k + 1 < tiles ? kTile - 1 : tail)) store_rows<WIDE, JR>(op, p, v);
+        op += kTile * BH;
+    };
+    if (WIDE && p.channels < kWave) {  // columns that no thread writes
+        for (int r = p.wave; r < 2 * kTile * 2; r += NW)
+            if (!p.on) (&sd[0][0][0][0])[r * kWave + p.lane] = 0.0f;
     }
+    if (tiles > 0) {
+        fetch(0);
+        prepare(0);
+        xn = xr, zn = zr;
+        fetch(tiles > 1 ? 1 : 0);
+        lds_barrier();
+    }
+    // The order matters: a wave's wait counts take loads and stores in order, and a store or load
+    // under a condition makes the wait for an older one wait for it as well. So the loads are issued
+    // last, without a condition, a whole tile before they are waited for (measured at S=16384
+    // H=4096: 418 us with the stores after the loads, 371 us so).
+    for (int k = 0; k < tiles; ++k) {
+        const int half = k & 1;
+        const vec xk = xn, zk = zn;
+        xn = xr, zn = zr;
+        if (k + 1 < tiles) prepare(k + 1);
+        if (!ENDS && k > 0) finish(k - 1);
+        xc = xk, zc = zk;
+        if (!ENDS && kept) {
+            if (p.on) {
+#pragma unroll
+                for (int i = 0; i < kPer; ++i)
+                    if (p.wave * kPer + i < a.N) kept[i * a.H] = s[i];
+            }
+            kept += states;
+        }
+        fetch(k + 2 < tiles ? k + 2 : tiles - 1);
+        // Rows by groups, with the next group's operands on their way from LDS while this one's are
+        // used.
+        constexpr int kGroup = 4;
+        float dd[2][kGroup], dx[2][kGroup];
+        float Bt[2][kGroup][kPer], Ct[2][kGroup][kPer];
+        auto operands = [&](int g, int to) {
+#pragma unroll
+            for (int r = 0; r < kGroup; ++r) {
+                const int t = g * kGroup + r;
+                dd[to][r] = sd[half][t][0][p.lane];
+                dx[to][r] = sd[half][t][1][p.lane];
+                load4(&sB[half][t][p.wave * kPer], Bt[to][r]);
+                if (!ENDS) load4(&sC[half][t][p.wave * kPer], Ct[to][r]);
+            }
+        };
+        operands(0, 0);
+#pragma unroll
+        for (int g = 0; g < kTile / kGroup; ++g) {
+            const int at = g & 1;
+            if (g + 1 < kTile / kGroup) operands(g + 1, at ^ 1);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int r = 0; r < kGroup; ++r) {
+                float y = 0.0f;
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) {
+                    s[i] = __builtin_fmaf(exp2_f(dd[at][r] * A2[i]), s[i], dx[at][r] * Bt[at][r][i]);
+                    if (!ENDS) y = __builtin_fmaf(Ct[at][r][i], s[i], y);
+                }
+                if (ENDS) total += dd[at][r];
+                else sy[half][p.wave][g * kGroup + r][p.lane] = y;
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        lds_barrier();
+    }
+    if (!ENDS && tiles > 0) finish(tiles - 1);
     if (ENDS) {
         store_state(ends + (int64_t)blockIdx.z * a.nb * a.N * a.H, a, p, s);
         if (p.wave == 0 && p.on) dsum[((int64_t)blockIdx.z * a.nb + p.b) * a.H + p.h] = total;
         return;
     }
-    if (p.on)
-        for (int64_t t = t0 + p.wave; t < p.r1; t += NW) out[(t * a.nb + p.b) * a.H + p.h] = 0;
+    if (p.on)  // rows past the length
+        for (int64_t t = (p.end > p.r0 ? p.end : p.r0) + p.wave; t < p.r1; t += NW)
+            out[(t * a.nb + p.b) * a.H + p.h] = 0;
     if (final_state && (int)blockIdx.z == a.chunks - 1) store_state(final_state, a, p, s);
 }
 
@@ -258,7 +432,8 @@ struct ScanGrad {
     const float *gfinal, *saved;
     uint16_t *gx, *gdt, *gz;
     float *gstate;
-    float *pbc;     // [block of channels][S][B][2][NP]: sums over the block's channels
+    float *pbc;     // [block of channels][pbc_rows][B][2][NP]: sums over the block's channels
+    int64_t pbc_rows;  // S in whole tiles
     double *pa;     // [chunk][B][(N+2) H]: gA, gD, gdt_bias of a chunk
     float *ends, *dsum;
 };
@@ -285,244 +460,349 @@ __device__ static inline float join(float a, float b, bool second) {
 }
 
 // Carry of a chunk from a zero gradient behind it: gs a at its first row, and its sum of d.
-template <int DT, int NW>
+template <int DT, int NW, bool GATE, bool WIDE>
 __global__ void __launch_bounds__(NW *kWave)
     scan_bwd_ends(ScanIn a, ScanGrad q) {
     constexpr int NP = NW * kPer, JR = kTile / NW;
-    __shared__ float2 sd[kTile][kWave];  // d, gy
-    __shared__ __align__(16) float sC[kTile][NP];
-    const Place p = place(a);
-    float A2[kPer], carry[kPer] = {0.0f, 0.0f, 0.0f, 0.0f}, total = 0.0f;
+    typedef typename HVec<JR>::t vec;
+    __shared__ __align__(16) float sd[2][kTile][2][kWave];  // d, gy
+    __shared__ __align__(16) float sC[2][kTile][NP];
+    const Place p = place<NW, WIDE>(a);
+    float A2[kPer], carry[kPer] = {0.0f, 0.0f, 0.0f, 0.0f}, total = 0.0f, bias[JR];
     load_rates(a, p, A2);
-    const float bias = a.bias ? a.bias[p.h] : 0.0f;
-    const uint16_t *dp = a.dt.p + p.b * a.dt.b + p.h * a.dt.h;
-    const uint16_t *zp = a.z.p ? a.z.p + p.b * a.z.b + p.h * a.z.h : nullptr;
-    const uint16_t *gp = q.go.p + p.b * q.go.b + p.h * q.go.h;
-    CoefTile<DT, NW> coef(a, p);
-    uint16_t dr[JR], zr[JR], gr[JR];
-    auto fetch = [&](int64_t t0) {
-#pragma unroll
-        for (int j = 0; j < JR; ++j) {
-            const int64_t t = t0 + p.wave + NW * j, r = t < p.end ? t : p.end - 1;
-            dr[j] = dp[r * a.dt.s];
-            gr[j] = gp[r * q.go.s];
-            if (zp) zr[j] = zp[r * a.z.s];
-        }
-        coef.fetch(a, t0, p.end);
+    load_param(a.bias, p, bias);
+    const int tiles = p.end > p.r0 ? (int)((p.end - p.r0 + kTile - 1) / kTile) : 0;
+    const int64_t t0 = p.r0 + (int64_t)(tiles - 1) * kTile;
+    Walk<NW, WIDE> dw(a.dt, p, t0, -1), zw(a.z, p, t0, -1), gw(q.go, p, t0, -1);
+    CoefWalk<DT, NW> coef(a, p, t0, -1);
+    const int tail = (int)(p.end - t0) - 1;  // the last tile may be partial, the others are whole
+    vec dr, zr, gr;
+    auto fetch = [&](int k) {
+        const int last = k + 1 < tiles ? kTile - 1 : tail;
+        dr = dw.fetch(p, last);
+        gr = gw.fetch(p, last);
+        if (GATE) zr = zw.fetch(p, last);
+        coef.template fetch<false, true>(last);
+        const bool more = k > 0;
+        dw.move(more), gw.move(more), coef.move(more);
+        if (GATE) zw.move(more);
     };
-    const int64_t tiles = p.end > p.r0 ? (p.end - p.r0 + kTile - 1) / kTile : 0;
-    if (tiles) fetch(p.r0 + (tiles - 1) * kTile);
-    for (int64_t k = tiles - 1; k >= 0; --k) {
-        const int64_t t0 = p.r0 + k * kTile;
+    auto prepare = [&](int k) {
+        const int at = k & 1, last = k + 1 < tiles ? kTile - 1 : tail;
+        float v[JR], d[JR], gy[JR], slope[JR];
+#pragma unroll
+        for (int j = 0; j < JR; ++j) v[j] = to_f32<DT>(dr[j]) + bias[j];
+        step_sizes<false>(a, v, d, slope);
 #pragma unroll
         for (int j = 0; j < JR; ++j) {
-            const int t = p.wave + NW * j;
-            const bool live = t0 + t < p.end;
-            float slope;
-            const float d = live ? step_size(a, to_f32<DT>(dr[j]) + bias, slope) : 0.0f;
-            float gy = to_f32<DT>(gr[j]);
-            if (zp) gy *= silu_f(to_f32<DT>(zr[j]));
-            sd[t][p.lane] = make_float2(d, live ? gy : 0.0f);
+            gy[j] = to_f32<DT>(gr[j]);
+            if (GATE) gy[j] *= silu_f(to_f32<DT>(zr[j]));
         }
-        sC[coef.t][coef.n] = coef.c(t0, p.end);
-        __syncthreads();
-        if (k > 0) fetch(t0 - kTile);
+        if (p.row > last) {
 #pragma unroll
-        for (int t = kTile - 1; t >= 0; --t) {
-            const float2 dd = sd[t][p.lane];
-            float Ct[kPer];
-            load4(&sC[t][p.wave * kPer], Ct);
-#pragma unroll
-            for (int i = 0; i < kPer; ++i)
-                carry[i] = __builtin_fmaf(Ct[i], dd.y, carry[i]) * exp2_f(dd.x * A2[i]);
-            total += dd.x;
+            for (int j = 0; j < JR; ++j) d[j] = gy[j] = 0.0f;
         }
-        __syncthreads();
+        store_floats(&sd[at][p.row][0][p.c], d);
+        store_floats(&sd[at][p.row][1][p.c], gy);
+        sC[at][coef.t][coef.n] = coef.c(last);
+    };
+    if (WIDE && p.channels < kWave) {
+        for (int r = p.wave; r < 2 * kTile * 2; r += NW)
+            if (!p.on) (&sd[0][0][0][0])[r * kWave + p.lane] = 0.0f;
+    }
+    if (tiles > 0) {
+        fetch(tiles - 1);
+        prepare(tiles - 1);
+        fetch(tiles > 1 ? tiles - 2 : 0);
+        lds_barrier();
+    }
+    for (int k = tiles - 1; k >= 0; --k) {
+        const int half = k & 1;
+        if (k > 0) prepare(k - 1);
+        fetch(k > 1 ? k - 2 : 0);
+        constexpr int kGroup = 4;  // as in the forward
+        float dd[2][kGroup], gy[2][kGroup];
+        float Ct[2][kGroup][kPer];
+        auto operands = [&](int g, int to) {
+#pragma unroll
+            for (int r = 0; r < kGroup; ++r) {
+                const int t = g * kGroup + r;
+                dd[to][r] = sd[half][t][0][p.lane];
+                gy[to][r] = sd[half][t][1][p.lane];
+                load4(&sC[half][t][p.wave * kPer], Ct[to][r]);
+            }
+        };
+        operands(kTile / kGroup - 1, (kTile / kGroup - 1) & 1);
+#pragma unroll
+        for (int g = kTile / kGroup - 1; g >= 0; --g) {
+            const int at = g & 1;
+            if (g > 0) operands(g - 1, at ^ 1);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int r = kGroup - 1; r >= 0; --r) {
+#pragma unroll
+                for (int i = 0; i < kPer; ++i)
+                    carry[i] = __builtin_fmaf(Ct[at][r][i], gy[at][r], carry[i]) *
+                               exp2_f(dd[at][r] * A2[i]);
+                total += dd[at][r];
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        lds_barrier();
     }
     store_state(q.ends + (int64_t)blockIdx.z * a.nb * a.N * a.H, a, p, carry);
     if (p.wave == 0 && p.on) q.dsum[((int64_t)blockIdx.z * a.nb + p.b) * a.H + p.h] = total;
 }
 
-template <int DT, int NW, bool GATE>
-__global__ void __launch_bounds__(NW *kWave)
+// Two waves a SIMD: a single one issues an fp32 instruction every five cycles, two together one every
+// two and a half. The tile's history takes 128 registers of the 256 that leaves.
+template <int DT, int NW, bool GATE, bool WIDE>
+__global__ void __launch_bounds__(NW *kWave, 2)
     scan_bwd(ScanIn a, ScanGrad q) {
     constexpr int NP = NW * kPer, JR = kTile / NW;
-    __shared__ float2 sd[kTile][kWave];  // d, d x
-    __shared__ float sg[kTile][kWave];   // gy
+    typedef typename HVec<JR>::t vec;
+    __shared__ __align__(16) float sd[kTile][3][kWave];  // d, d x, gy
     __shared__ __align__(16) float sB[kTile][NP], sC[kTile][NP];
-    __shared__ float su[NW][kTile][kWave], sq[NW][kTile][kWave];  // sums over a wave's states
-    __shared__ float sy[GATE ? NW : 1][GATE ? kTile : 1][kWave];
-    const Place p = place(a);
+    // sums over a wave's states: u, w and (with a gate) y
+    __shared__ __align__(16) float su[NW][kTile][kWave], sw[NW][kTile][kWave];
+    __shared__ __align__(16) float sy[GATE ? NW : 1][GATE ? kTile : 1][kWave];
+    const Place p = place<NW, WIDE>(a);
     float A2[kPer], carry[kPer];
-    double gA[kPer] = {0.0, 0.0, 0.0, 0.0}, gD = 0.0, gbias = 0.0;
+    double gA[kPer] = {0.0, 0.0, 0.0, 0.0};
     load_rates(a, p, A2);
     load_state(q.gfinal, a, p, carry);
     fold_chunks(q.ends, q.dsum, a, p, a.chunks - 1, -1, a.chunks - 1 - (int)blockIdx.z, A2, carry);
-    const float bias = a.bias ? a.bias[p.h] : 0.0f, D = a.D ? a.D[p.h] : 0.0f;
-    const uint16_t *xp = a.x.p + p.b * a.x.b + p.h * a.x.h;
-    const uint16_t *dp = a.dt.p + p.b * a.dt.b + p.h * a.dt.h;
-    const uint16_t *zp = GATE ? a.z.p + p.b * a.z.b + p.h * a.z.h : nullptr;
-    const uint16_t *gp = q.go.p + p.b * q.go.b + p.h * q.go.h;
-    CoefTile<DT, NW> coef(a, p);
-    uint16_t xr[JR], dr[JR], zr[JR], gr[JR];
+    // gD and gdt_bias of the thread's channels: fp32 sums of 32 rows, and of those sums
+    float gD[2][JR], gb[2][JR];
+#pragma unroll
+    for (int j = 0; j < JR; ++j) gD[0][j] = gD[1][j] = gb[0][j] = gb[1][j] = 0.0f;
+    const int tiles = p.end > p.r0 ? (int)((p.end - p.r0 + kTile - 1) / kTile) : 0;
+    const int64_t t0 = p.r0 + (int64_t)(tiles - 1) * kTile;
+    const int tail = (int)(p.end - t0) - 1;  // the last tile may be partial, the others are whole
+    const int64_t BH = a.nb * a.H, states = BH * a.N;
+    if (p.on)  // rows past the length
+        for (int64_t t = (p.end > p.r0 ? p.end : p.r0) + p.wave; t < p.r1; t += NW) {
+            const int64_t o = t * BH + p.b * a.H + p.h;
+            q.gx[o] = 0;
+            q.gdt[o] = 0;
+            if (GATE) q.gz[o] = 0;
+        }
+    Walk<NW, WIDE> xw(a.x, p, t0, -1), dw(a.dt, p, t0, -1), zw(a.z, p, t0, -1), gw(q.go, p, t0, -1);
+    CoefWalk<DT, NW> coef(a, p, t0, -1);
+    // the lane's state n before the tile at kept[n H]
+    const float *kept = q.saved + t0 / kTile * states + (p.b * a.N + p.wave * kPer) * a.H + p.h;
+    int64_t to = (t0 + p.row) * BH + p.b * a.H + p.h0 + p.c;  // where the thread's row goes
+    const int64_t pbc_row = a.nb * 2 * NP;
+    // the sums over channels that this lane ends up with (see below): value n of B or C, row sum_t
+    // of a half tile
+    const int sum_t = ((p.lane >> 2) & 1) + (p.lane & 2) + (p.lane & 1) * 4;
+    float *pbc = q.pbc + (((int64_t)blockIdx.x * q.pbc_rows + t0 + sum_t) * a.nb + p.b) * 2 * NP +
+                 ((p.lane >> 3) & 1) * NP + p.wave * kPer + (p.lane >> 5) + ((p.lane >> 4) & 1) * 2;
+    vec xr, dr, zr, gr;  // fetched; then the tile's and the last one's, which finishing it needs
+    vec xc, zc, gc;
     float first[kPer];  // the state before the tile
-    auto fetch = [&](int64_t t0) {
+    float slope[JR];
+    auto fetch = [&](int k) {
+        const int last = k + 1 < tiles ? kTile - 1 : tail;
+        xr = xw.fetch(p, last);
+        dr = dw.fetch(p, last);
+        gr = gw.fetch(p, last);
+        if (GATE) zr = zw.fetch(p, last);
+        coef.template fetch<true, true>(last);
+        // states past N have no place: the first of the wave's (or of all) is read and not used
 #pragma unroll
-        for (int j = 0; j < JR; ++j) {
-            const int64_t t = t0 + p.wave + NW * j, r = t < p.end ? t : p.end - 1;
-            xr[j] = xp[r * a.x.s];
-            dr[j] = dp[r * a.dt.s];
-            gr[j] = gp[r * q.go.s];
-            if (GATE) zr[j] = zp[r * a.z.s];
-        }
-        coef.fetch(a, t0, p.end);
-        load_state(q.saved + t0 / kTile * a.nb * a.N * a.H, a, p, first);
+        for (int i = 0; i < kPer; ++i)
+            first[i] = kept[p.wave * kPer + i < a.N ? i * a.H : p.wave * kPer < a.N ? 0 : -(int64_t)(p.wave * kPer) * a.H];
+        const bool more = k > 0;
+        xw.move(more), dw.move(more), gw.move(more), coef.move(more);
+        if (GATE) zw.move(more);
+        kept -= more ? states : 0;
     };
-    // rows past the length
-    const int64_t tiles = p.end > p.r0 ? (p.end - p.r0 + kTile - 1) / kTile : 0;
-    const int64_t at = p.b * a.H + p.h, BH = a.nb * a.H;
-    if (p.on)
-        for (int64_t t = p.r0 + tiles * kTile + p.wave; t < p.r1; t += NW) {
-            q.gx[t * BH + at] = 0;
-            q.gdt[t * BH + at] = 0;
-            if (GATE) q.gz[t * BH + at] = 0;
-        }
-    if (tiles) fetch(p.r0 + (tiles - 1) * kTile);
-    for (int64_t k = tiles - 1; k >= 0; --k) {
-        const int64_t t0 = p.r0 + k * kTile;
-        float xf[JR], df[JR], slope[JR], gf[JR], zf[JR], gyf[JR];
+    // Tile k's operands in LDS.
+    auto prepare = [&](int k) {
+        const int last = k + 1 < tiles ? kTile - 1 : tail;
+        float v[JR], d[JR], dx[JR], gy[JR];
+        load_param(a.bias, p, v);
+#pragma unroll
+        for (int j = 0; j < JR; ++j) v[j] += to_f32<DT>(dr[j]);
+        step_sizes<true>(a, v, d, slope);
 #pragma unroll
         for (int j = 0; j < JR; ++j) {
-            const int t = p.wave + NW * j;
-            const bool live = p.on && t0 + t < p.end;
-            const float d = step_size(a, to_f32<DT>(dr[j]) + bias, slope[j]);
-            df[j] = live ? d : 0.0f;
-            xf[j] = live ? to_f32<DT>(xr[j]) : 0.0f;
-            gf[j] = live ? to_f32<DT>(gr[j]) : 0.0f;
-            zf[j] = GATE && live ? to_f32<DT>(zr[j]) : 0.0f;
-            gyf[j] = GATE ? gf[j] * silu_f(zf[j]) : gf[j];
-            sd[t][p.lane] = make_float2(df[j], df[j] * xf[j]);
-            sg[t][p.lane] = gyf[j];
+            dx[j] = d[j] * to_f32<DT>(xr[j]);
+            gy[j] = to_f32<DT>(gr[j]);
+            if (GATE) gy[j] *= silu_f(to_f32<DT>(zr[j]));
         }
-        sB[coef.t][coef.n] = coef.b(t0, p.end);
-        sC[coef.t][coef.n] = coef.c(t0, p.end);
-        float s0[kPer];
+        if (p.row > last || (!WIDE && p.channels < kWave)) {
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) s0[i] = first[i];
-        __syncthreads();
-        if (k > 0) fetch(t0 - kTile);
+            for (int j = 0; j < JR; ++j)
+                if (p.row > last || p.c + j >= p.channels) d[j] = dx[j] = gy[j] = 0.0f;
+        }
+        store_floats(&sd[p.row][0][p.c], d);
+        store_floats(&sd[p.row][1][p.c], dx);
+        store_floats(&sd[p.row][2][p.c], gy);
+        sB[coef.t][coef.n] = coef.b(last);
+        sC[coef.t][coef.n] = coef.c(last);
+    };
+    // Tile k's gradients, from the sums its waves left in LDS; d and gy are its rows', read before
+    // the next tile's took their place.
+    auto finish = [&](int k, const float (&d)[JR], const float (&gy)[JR], const float (&slope)[JR]) {
+        float D[JR], u[JR], w[JR], y[JR], f[JR];
+        load_param(a.D, p, D);
+        load_floats(&su[0][p.row][p.c], u);
+        load_floats(&sw[0][p.row][p.c], w);
+        if (GATE) load_floats(&sy[0][p.row][p.c], y);
+#pragma unroll
+        for (int i = 1; i < NW; ++i) {
+            load_floats(&su[i][p.row][p.c], f);
+#pragma unroll
+            for (int j = 0; j < JR; ++j) u[j] += f[j];
+            load_floats(&sw[i][p.row][p.c], f);
+#pragma unroll
+            for (int j = 0; j < JR; ++j) w[j] += f[j];
+            if (GATE) {
+                load_floats(&sy[i][p.row][p.c], f);
+#pragma unroll
+                for (int j = 0; j < JR; ++j) y[j] += f[j];
+            }
+        }
+        if (p.row <= (k + 1 < tiles ? kTile - 1 : tail)) {
+            vec gx, gdt, gz;
+#pragma unroll
+            for (int j = 0; j < JR; ++j) {
+                const float x = to_f32<DT>(xc[j]);
+                const float gd = __builtin_fmaf(w[j], kLn2, u[j] * x) * slope[j];
+                gx[j] = from_f32<DT>(__builtin_fmaf(u[j], d[j], D[j] * gy[j]));
+                gdt[j] = from_f32<DT>(gd);
+                gD[0][j] = __builtin_fmaf(gy[j], x, gD[0][j]);
+                gb[0][j] += gd;
+                if (GATE)
+                    gz[j] = from_f32<DT>(to_f32<DT>(gc[j]) * __builtin_fmaf(D[j], x, y[j]) *
+                                         silu_slope_f(to_f32<DT>(zc[j])));
+            }
+            store_rows<WIDE, JR>(q.gx + to, p, gx);
+            store_rows<WIDE, JR>(q.gdt + to, p, gdt);
+            if (GATE) store_rows<WIDE, JR>(q.gz + to, p, gz);
+        }
+        to -= kTile * BH;
+        if (k % 32 == 0) {
+#pragma unroll
+            for (int j = 0; j < JR; ++j) {
+                gD[1][j] += gD[0][j], gD[0][j] = 0.0f;
+                gb[1][j] += gb[0][j], gb[0][j] = 0.0f;
+            }
+        }
+    };
+    if (WIDE && p.channels < kWave) {  // columns that no thread writes add nothing to the sums
+        for (int r = p.wave; r < kTile * 3; r += NW)
+            if (!p.on) (&sd[0][0][0])[r * kWave + p.lane] = 0.0f;
+    }
+    if (tiles > 0) fetch(tiles - 1);
+    for (int k = tiles - 1; k >= 0; --k) {
+        float d[JR], gy[JR], last_slope[JR], s0[kPer];
+        load_floats(&sd[p.row][0][p.c], d);
+        load_floats(&sd[p.row][2][p.c], gy);
+#pragma unroll
+        for (int j = 0; j < JR; ++j) last_slope[j] = slope[j];
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) s0[i] = p.wave * kPer + i < a.N ? first[i] : 0.0f;
+        prepare(k);  // waits for the tile's loads, so before any store (see the forward)
+        if (k + 1 < tiles) finish(k + 1, d, gy, last_slope);
+        xc = xr, zc = zr, gc = gr;
+        fetch(k > 0 ? k - 1 : 0);
+        lds_barrier();
         // the tile's states and decays again, kept in registers
         float S[kTile][kPer], E[kTile][kPer];
 #pragma unroll
         for (int t = 0; t < kTile; ++t) {
-            const float2 dd = sd[t][p.lane];
+            const float dd = sd[t][0][p.lane], dx = sd[t][1][p.lane];
             float Bt[kPer], Ct[kPer], y = 0.0f;
             load4(&sB[t][p.wave * kPer], Bt);
             if (GATE) load4(&sC[t][p.wave * kPer], Ct);
 #pragma unroll
             for (int i = 0; i < kPer; ++i) {
-                E[t][i] = exp2_f(dd.x * A2[i]);
-                S[t][i] = __builtin_fmaf(E[t][i], t ? S[t - 1][i] : s0[i], dd.y * Bt[i]);
+                E[t][i] = exp2_f(dd * A2[i]);
+                S[t][i] = __builtin_fmaf(E[t][i], t ? S[t - 1][i] : s0[i], dx * Bt[i]);
                 if (GATE) y = __builtin_fmaf(Ct[i], S[t][i], y);
             }
             if (GATE) sy[p.wave][t][p.lane] = y;
+            // keep the reads of later rows from being taken up front: registers are what is short
+            if (t % 4 == 3) __builtin_amdgcn_sched_barrier(0);
         }
         float tA[kPer] = {0.0f, 0.0f, 0.0f, 0.0f};
-        float part[kTile];  // a row's eight sums, each over eight lanes
+        // Sums over the wave's channels. A row has eight values (four of gB, four of gC) in 64 lanes:
+        // halving the values while adding lanes 32, 16 and 8 apart leaves a register a row, and eight
+        // rows' registers join the same way over the last eight lanes. Value v of row t ends in lane
+        // bits 5, 4, 3 = v's bits 0, 1, 2 and lane bits 2, 1, 0 = t's bits 0, 1, 2.
+        float part[kTile / 2];
 #pragma unroll
         for (int t = kTile - 1; t >= 0; --t) {
-            const float2 dd = sd[t][p.lane];
-            const float gy = sg[t][p.lane];
+            const float dd = sd[t][0][p.lane], dx = sd[t][1][p.lane], gy = sd[t][2][p.lane];
             float Bt[kPer], Ct[kPer], u = 0.0f, w = 0.0f, v[2 * kPer];
             load4(&sB[t][p.wave * kPer], Bt);
             load4(&sC[t][p.wave * kPer], Ct);
 #pragma unroll
             for (int i = 0; i < kPer; ++i) {
                 const float gs = __builtin_fmaf(Ct[i], gy, carry[i]);
-                v[i] = gs * dd.y;
+                v[i] = gs * dx;
                 v[kPer + i] = gy * S[t][i];
                 u = __builtin_fmaf(gs, Bt[i], u);
                 carry[i] = gs * E[t][i];
                 const float g = carry[i] * (t ? S[t - 1][i] : s0[i]);
                 w = __builtin_fmaf(g, A2[i], w);
-                tA[i] = __builtin_fmaf(g, dd.x, tA[i]);
+                tA[i] = __builtin_fmaf(g, dd, tA[i]);
             }
             su[p.wave][t][p.lane] = u;
-            sq[p.wave][t][p.lane] = w;
+            sw[p.wave][t][p.lane] = w;
             float r4[4], r2[2];
 #pragma unroll
             for (int i = 0; i < 4; ++i) r4[i] = swap_add32(v[2 * i], v[2 * i + 1]);
 #pragma unroll
             for (int i = 0; i < 2; ++i) r2[i] = swap_add16(r4[2 * i], r4[2 * i + 1]);
-            part[t] = join<kRor8>(r2[0], r2[1], p.lane & 8);
+            part[t % 8] = join<kRor8>(r2[0], r2[1], p.lane & 8);
+            if (t % 8 == 0) {
+                float h[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    h[i] = join<kHalfMirror>(part[2 * i], part[2 * i + 1], p.lane & 4);
+                const float m0 = join<kXor2>(h[0], h[1], p.lane & 2);
+                const float m1 = join<kXor2>(h[2], h[3], p.lane & 2);
+                const float m = join<kXor1>(m0, m1, p.lane & 1);
+                pbc[t * pbc_row] = m;  // rows past the length too: their place is never read
+            }
+            if (t % 2 == 0) __builtin_amdgcn_sched_barrier(0);
         }
+        pbc -= kTile * pbc_row;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) gA[i] += (double)tA[i];
-        // 16 rows of 8 sums over 8 lanes: two values a lane. Value v of row t ends in lane bits
-        // 5, 4, 3 = v's bits 0, 1, 2 and lane bits 2, 1, 0 = t's bits 0, 1, 2; t's bit 3 is `half`.
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            float r[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                r[i] = join<kHalfMirror>(part[half * 8 + 2 * i], part[half * 8 + 2 * i + 1], p.lane & 4);
-            const float m0 = join<kXor2>(r[0], r[1], p.lane & 2), m1 = join<kXor2>(r[2], r[3], p.lane & 2);
-            const float m = join<kXor1>(m0, m1, p.lane & 1);
-            const int l = p.lane;
-            const int t = half * 8 + ((l >> 2) & 1) + (l & 2) + (l & 1) * 4;
-            const int n = (l >> 5) + ((l >> 4) & 1) * 2, which = (l >> 3) & 1;
-            if (t0 + t < p.end)
-                q.pbc[((((int64_t)blockIdx.x * a.S + t0 + t) * a.nb + p.b) * 2 + which) * NP +
-                      p.wave * kPer + n] = m;
-        }
-        __syncthreads();
-        float tD = 0.0f, tb = 0.0f;
-#pragma unroll
-        for (int j = 0; j < JR; ++j) {
-            const int t = p.wave + NW * j;
-            float u = 0.0f, w = 0.0f, y = D * xf[j];
-#pragma unroll
-            for (int i = 0; i < NW; ++i) {
-                u += su[i][t][p.lane];
-                w += sq[i][t][p.lane];
-                if (GATE) y += sy[i][t][p.lane];
-            }
-            const float gd = __builtin_fmaf(w, kLn2, u * xf[j]) * slope[j];
-            const bool live = p.on && t0 + t < p.end;
-            tD = __builtin_fmaf(gyf[j], xf[j], tD);
-            tb += live ? gd : 0.0f;
-            if (p.on && t0 + t < p.r1) {
-                const int64_t o = (t0 + t) * BH + at;
-                q.gx[o] = live ? from_f32<DT>(__builtin_fmaf(u, df[j], D * gyf[j])) : 0;
-                q.gdt[o] = live ? from_f32<DT>(gd) : 0;
-                if (GATE) q.gz[o] = live ? from_f32<DT>(gf[j] * y * silu_slope_f(zf[j])) : 0;
-            }
-        }
-        gD += (double)tD;
-        gbias += (double)tb;
+        lds_barrier();
+    }
+    if (tiles > 0) {
+        float d[JR], gy[JR];
+        load_floats(&sd[p.row][0][p.c], d);
+        load_floats(&sd[p.row][2][p.c], gy);
+        finish(0, d, gy, slope);
+        lds_barrier();  // the sums below take the place of what finish read
     }
     if (blockIdx.z == 0 && q.gstate) store_state(q.gstate, a, p, carry);
-    double *pa = q.pa + ((int64_t)blockIdx.z * a.nb + p.b) * (a.N + 2) * a.H + p.h;
-    __syncthreads();
-    double *sums = (double *)&su[0][0][0];  // [NW][2][64] doubles: 1 KiB a wave, of its 4 KiB
-    sums[(p.wave * 2 + 0) * kWave + p.lane] = gD;
-    sums[(p.wave * 2 + 1) * kWave + p.lane] = gbias;
-    __syncthreads();
+    double *pa = q.pa + ((int64_t)blockIdx.z * a.nb + p.b) * (a.N + 2) * a.H;
+    store_floats(&su[0][p.row][p.c], gD[1]);
+    store_floats(&sw[0][p.row][p.c], gb[1]);
+    lds_barrier();
     if (!p.on) return;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         const int n = p.wave * kPer + i;
-        if (n < a.N) pa[(int64_t)n * a.H] = gA[i];
+        if (n < a.N) pa[(int64_t)n * a.H + p.h] = gA[i];
     }
     if (p.wave == 0) {
         double d = 0.0, b = 0.0;
 #pragma unroll
-        for (int w = 0; w < NW; ++w) {
-            d += sums[(w * 2 + 0) * kWave + p.lane];
-            b += sums[(w * 2 + 1) * kWave + p.lane];
+        for (int t = 0; t < kTile; ++t) {
+            d += (double)su[0][t][p.lane];
+            b += (double)sw[0][t][p.lane];
         }
-        pa[(int64_t)a.N * a.H] = d;
-        pa[(int64_t)(a.N + 1) * a.H] = b;
+        pa[(int64_t)a.N * a.H + p.h] = d;
+        pa[(int64_t)(a.N + 1) * a.H + p.h] = b;
     }
 }
 
@@ -531,7 +811,7 @@ __global__ void __launch_bounds__(NW *kWave)
 template <int DT>
 __global__ void __launch_bounds__(256)
     scan_sum_bc(const float *__restrict__ pbc, const int64_t *__restrict__ lengths, int64_t S,
-                int64_t nb, int N, int NP, int G, int per_group, uint16_t *__restrict__ gB,
+                int64_t pbc_rows, int64_t nb, int N, int NP, int G, int per_group, uint16_t *__restrict__ gB,
                 uint16_t *__restrict__ gC) {
     const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
     const int64_t rows = S * nb;
@@ -542,9 +822,10 @@ __global__ void __launch_bounds__(256)
     const int64_t t = row / nb, b = row - t * nb;
     float s = 0.0f;
     if (!lengths || t < lengths[b]) {
-        const float *p = pbc + ((g * per_group * rows + row) * 2 + which) * NP + n;
+        const int64_t block = pbc_rows * nb;
+        const float *p = pbc + ((g * per_group * block + row) * 2 + which) * NP + n;
 #pragma unroll 8
-        for (int i = 0; i < per_group; ++i) s += p[(int64_t)i * rows * 2 * NP];
+        for (int i = 0; i < per_group; ++i) s += p[(int64_t)i * block * 2 * NP];
     }
     (which ? gC : gB)[(row * G + g) * N + n] = from_f32<DT>(s);
 }
@@ -586,9 +867,8 @@ __global__ void __launch_bounds__(kWave)
     const int64_t g = h / a.K;
     const uint16_t *bp = a.B.p + b * a.B.b + g * a.B.g, *cp = a.C.p + b * a.C.b + g * a.C.g;
     const float x = to_f32<DT>(a.x.p[b * a.x.b + h * a.x.h]);
-    float slope;
-    const float d = step_size(
-        a, to_f32<DT>(a.dt.p[b * a.dt.b + h * a.dt.h]) + (a.bias ? a.bias[h] : 0.0f), slope);
+    const float v = to_f32<DT>(a.dt.p[b * a.dt.b + h * a.dt.h]) + (a.bias ? a.bias[h] : 0.0f);
+    const float d = a.softplus ? softplus_f(v) : v;
     float y = a.D ? a.D[h] * x : 0.0f;
     const float dx = d * x, d2 = d * kLog2e;
 #pragma unroll
@@ -654,7 +934,7 @@ struct ScanPlan {
 
 ScanPlan plan_of(const mccb_scan_t *a) {
     ScanPlan p;
-    p.waves = a->N <= 4 ? 1 : a->N <= 8 ? 2 : a->N <= 16 ? 4 : 8;
+    p.waves = a->N <= 8 ? 2 : a->N <= 16 ? 4 : 8;
     const int64_t K = a->H / a->G;
     p.per_group = (K + kWave - 1) / kWave;
     p.blocks = p.per_group * a->G;
@@ -694,6 +974,14 @@ ScanIn device_args(const mccb_scan_t *a, const ScanPlan &p) {
     return in;
 }
 
+// Whether a block's threads can take their channels of a row by one load: adjacent channels, and in
+// every block as many as a thread takes.
+bool wide(const mccb_scan_t *a, const ScanPlan &p) {
+    const int64_t K = a->H / a->G, JR = kTile / p.waves, tail = K % kWave;
+    return a->x_stride[2] == 1 && a->dt_stride[2] == 1 && (!a->z || a->z_stride[2] == 1) &&
+           (tail == 0 || tail >= JR);
+}
+
 // Workspace for handing states between chunks.
 uint64_t chunk_bytes(const mccb_scan_t *a, const ScanPlan &p) {
     if (p.chunks == 1) return 0;
@@ -701,7 +989,8 @@ uint64_t chunk_bytes(const mccb_scan_t *a, const ScanPlan &p) {
 }
 
 uint64_t pbc_bytes(const mccb_scan_t *a, const ScanPlan &p) {
-    return (uint64_t)p.blocks * (uint64_t)a->S * (uint64_t)a->B * (2 * p.waves * kPer) * 4;
+    const uint64_t rows = (uint64_t)((a->S + kTile - 1) / kTile * kTile);
+    return (uint64_t)p.blocks * rows * (uint64_t)a->B * (2 * p.waves * kPer) * 4;
 }
 uint64_t pa_bytes(const mccb_scan_t *a, const ScanPlan &p) {
     return (uint64_t)p.chunks * (uint64_t)a->B * (uint64_t)((a->N + 2) * a->H) * 8;
@@ -710,11 +999,14 @@ uint64_t pa_bytes(const mccb_scan_t *a, const ScanPlan &p) {
 template <typename F>
 int by_waves(int waves, F f) {
     switch (waves) {
-        case 1: return f(std::integral_constant<int, 1>{});
         case 2: return f(std::integral_constant<int, 2>{});
         case 4: return f(std::integral_constant<int, 4>{});
         default: return f(std::integral_constant<int, 8>{});
     }
+}
+template <typename F>
+int by_flag(bool v, F f) {
+    return v ? f(std::true_type{}) : f(std::false_type{});
 }
 template <typename F>
 int by_dtype(int dtype, F f) {
@@ -773,17 +1065,24 @@ int mccb_scan_forward(const mccb_scan_t *a, void *out, float *final_state, void 
     const hipStream_t st = (hipStream_t)stream;
     return by_dtype(a->dtype, [&](auto dt) {
         return by_waves(p.waves, [&](auto nw) {
-            constexpr int DT = decltype(dt)::value, NW = decltype(nw)::value;
-            if (p.chunks > 1) {
-                hipLaunchKernelGGL((scan_fwd<DT, NW, true>), first, dim3(NW * kWave), 0, st, da,
-                                   (uint16_t *)nullptr, (float *)nullptr, (float *)nullptr, ends,
-                                   dsum);
-                const int r = launched();
-                if (r != MCCB_OK) return r;
-            }
-            hipLaunchKernelGGL((scan_fwd<DT, NW, false>), grid, dim3(NW * kWave), 0, st, da,
-                               (uint16_t *)out, final_state, (float *)saved, ends, dsum);
-            return launched();
+            return by_flag(wide(a, p), [&](auto wd) {
+                constexpr int DT = decltype(dt)::value, NW = decltype(nw)::value;
+                constexpr bool W = decltype(wd)::value;
+                const dim3 block(NW * kWave);
+                if (p.chunks > 1) {
+                    hipLaunchKernelGGL((scan_fwd<DT, NW, true, false, W>), first, block, 0, st, da,
+                                       (uint16_t *)nullptr, (float *)nullptr, (float *)nullptr, ends,
+                                       dsum);
+                    const int r = launched();
+                    if (r != MCCB_OK) return r;
+                }
+                return by_flag(a->z != nullptr, [&](auto gate) {
+                    hipLaunchKernelGGL((scan_fwd<DT, NW, false, decltype(gate)::value, W>), grid, block,
+                                       0, st, da, (uint16_t *)out, final_state, (float *)saved, ends,
+                                       dsum);
+                    return launched();
+                });
+            });
         });
     });
 }
@@ -843,6 +1142,7 @@ int mccb_scan_backward(const mccb_scan_t *a, const mccb_scan_grads_t *g, const v
     q.pa = (double *)at;
     at += pa_bytes(a, p);
     q.pbc = (float *)at;
+    q.pbc_rows = (a->S + kTile - 1) / kTile * kTile;
     at += align16(pbc_bytes(a, p));
     q.ends = p.chunks > 1 ? (float *)at : nullptr;
     q.dsum = p.chunks > 1 ? q.ends + (uint64_t)p.chunks * (uint64_t)(a->B * a->N * a->H) : nullptr;
@@ -852,20 +1152,23 @@ int mccb_scan_backward(const mccb_scan_t *a, const mccb_scan_grads_t *g, const v
         return by_waves(p.waves, [&](auto nw) {
             constexpr int DT = decltype(dt)::value, NW = decltype(nw)::value;
             const dim3 block(NW * kWave);
-            if (p.chunks > 1) {
-                hipLaunchKernelGGL((scan_bwd_ends<DT, NW>), grid, block, 0, st, da, q);
-                const int e = launched();
-                if (e != MCCB_OK) return e;
-            }
-            if (a->z)
-                hipLaunchKernelGGL((scan_bwd<DT, NW, true>), grid, block, 0, st, da, q);
-            else
-                hipLaunchKernelGGL((scan_bwd<DT, NW, false>), grid, block, 0, st, da, q);
-            int e = launched();
+            const bool w = wide(a, p) && g->gout_stride[2] == 1;
+            int e = by_flag(w, [&](auto wd) {
+                return by_flag(a->z != nullptr, [&](auto gate) {
+                    constexpr bool W = decltype(wd)::value, GATE = decltype(gate)::value;
+                    if (p.chunks > 1) {
+                        hipLaunchKernelGGL((scan_bwd_ends<DT, NW, GATE, W>), grid, block, 0, st, da, q);
+                        const int r = launched();
+                        if (r != MCCB_OK) return r;
+                    }
+                    hipLaunchKernelGGL((scan_bwd<DT, NW, GATE, W>), grid, block, 0, st, da, q);
+                    return launched();
+                });
+            });
             if (e != MCCB_OK || a->S == 0) return e;
             const int64_t ids = a->S * a->B * a->G * 2 * NW * kPer;
             hipLaunchKernelGGL((scan_sum_bc<DT>), dim3((unsigned)((ids + 255) / 256)), dim3(256), 0,
-                               st, q.pbc, a->lengths, a->S, a->B, (int)a->N, NW * kPer, (int)a->G,
+                               st, q.pbc, a->lengths, a->S, q.pbc_rows, a->B, (int)a->N, NW * kPer, (int)a->G,
                                (int)p.per_group, (uint16_t *)g->gradB, (uint16_t *)g->gradC);
             return launched();
         });
