@@ -566,7 +566,12 @@ __global__ void __launch_bounds__(NW *kWave, 2)
     // sums over a wave's states: u, w and (with a gate) y
     __shared__ __align__(16) float su[NW][kTile][kWave], sw[NW][kTile][kWave];
     __shared__ __align__(16) float sy[GATE ? NW : 1][GATE ? kTile : 1][kWave];
+    __shared__ __align__(16) float sparam[2][kWave];  // dt_bias, D
     const Place p = place<NW, WIDE>(a);
+    if (p.wave == 0) {
+        sparam[0][p.lane] = a.bias ? a.bias[p.h] : 0.0f;
+        sparam[1][p.lane] = a.D ? a.D[p.h] : 0.0f;
+    }
     float A2[kPer], carry[kPer];
     double gA[kPer] = {0.0, 0.0, 0.0, 0.0};
     load_rates(a, p, A2);
@@ -602,8 +607,7 @@ __global__ void __launch_bounds__(NW *kWave, 2)
     vec xc, zc, gc;
     float first[kPer];  // the state before the tile
     float slope[JR];
-    auto fetch = [&](int k) {
-        const int last = k + 1 < tiles ? kTile - 1 : tail;
+    auto fetch = [&](int k, int last) {
         xr = xw.fetch(p, last);
         dr = dw.fetch(p, last);
         gr = gw.fetch(p, last);
@@ -622,7 +626,7 @@ __global__ void __launch_bounds__(NW *kWave, 2)
     auto prepare = [&](int k) {
         const int last = k + 1 < tiles ? kTile - 1 : tail;
         float v[JR], d[JR], dx[JR], gy[JR];
-        load_param(a.bias, p, v);
+        load_floats(&sparam[0][p.c], v);
 #pragma unroll
         for (int j = 0; j < JR; ++j) v[j] += to_f32<DT>(dr[j]);
         step_sizes<true>(a, v, d, slope);
@@ -647,7 +651,7 @@ __global__ void __launch_bounds__(NW *kWave, 2)
     // the next tile's took their place.
     auto finish = [&](int k, const float (&d)[JR], const float (&gy)[JR], const float (&slope)[JR]) {
         float D[JR], u[JR], w[JR], y[JR], f[JR];
-        load_param(a.D, p, D);
+        load_floats(&sparam[1][p.c], D);
         load_floats(&su[0][p.row][p.c], u);
         load_floats(&sw[0][p.row][p.c], w);
         if (GATE) load_floats(&sy[0][p.row][p.c], y);
@@ -696,7 +700,8 @@ __global__ void __launch_bounds__(NW *kWave, 2)
         for (int r = p.wave; r < kTile * 3; r += NW)
             if (!p.on) (&sd[0][0][0])[r * kWave + p.lane] = 0.0f;
     }
-    if (tiles > 0) fetch(tiles - 1);
+    if (tiles > 0) fetch(tiles - 1, tail);
+    lds_barrier();
     for (int k = tiles - 1; k >= 0; --k) {
         float d[JR], gy[JR], last_slope[JR], s0[kPer];
         load_floats(&sd[p.row][0][p.c], d);
@@ -708,7 +713,7 @@ __global__ void __launch_bounds__(NW *kWave, 2)
         prepare(k);  // waits for the tile's loads, so before any store (see the forward)
         if (k + 1 < tiles) finish(k + 1, d, gy, last_slope);
         xc = xr, zc = zr, gc = gr;
-        fetch(k > 0 ? k - 1 : 0);
+        if (k > 0) fetch(k - 1, kTile - 1);
         lds_barrier();
         // the tile's states and decays again, kept in registers
         float S[kTile][kPer], E[kTile][kPer];
