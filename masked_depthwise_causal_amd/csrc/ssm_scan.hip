@@ -66,6 +66,16 @@ struct Place {
     int64_t r0, r1, end;  // the chunk's rows, and where its live rows end
 };
 
+// Two blocks share a compute unit, and the older one's waves win every issue slot that both want: it
+// ends a quarter earlier and leaves the other alone at half of the rate. So blocks take the higher
+// wave priority in turn, four tiles each, blocks a whole round of the 256 compute units apart in
+// opposite turns (S=2048 B=8 H=4096: backward 941 -> 905 us, forward unchanged within its noise).
+__device__ static inline void take_turn(int tile) {
+    const uint32_t block = blockIdx.x + gridDim.x * (blockIdx.y + gridDim.y * blockIdx.z);
+    if (((tile >> 2) + (block >> 8)) & 1) __builtin_amdgcn_s_setprio(1);
+    else __builtin_amdgcn_s_setprio(0);
+}
+
 template <int NW, bool WIDE>
 __device__ static inline Place place(const ScanIn &a) {
     constexpr int JR = kTile / NW;
@@ -144,13 +154,22 @@ __device__ static inline void fold_chunks(const float *ends, const float *dsum, 
                                           const Place &p, int first, int dir, int n,
                                           const float (&A2)[kPer], float (&s)[kPer]) {
     const int64_t states = a.nb * a.N * a.H;
-    for (int j = 0; j < n; ++j) {
-        const int c = first + dir * j;
-        const float d = dsum[((int64_t)c * a.nb + p.b) * a.H + p.h];
-        float e[kPer];
-        load_state(ends + c * states, a, p, e);
+    constexpr int kAhead = 8;  // chunks whose values are loaded together; missing ones change nothing
+    for (int j0 = 0; j0 < n; j0 += kAhead) {
+        float d[kAhead], e[kAhead][kPer];
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) s[i] = __builtin_fmaf(exp2_f(d * A2[i]), s[i], e[i]);
+        for (int j = 0; j < kAhead; ++j) {
+            const int c = first + dir * (j0 + j < n ? j0 + j : n - 1);
+            d[j] = dsum[((int64_t)c * a.nb + p.b) * a.H + p.h];
+            load_state(ends + c * states, a, p, e[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            if (j0 + j >= n) break;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+                s[i] = __builtin_fmaf(exp2_f(d[j] * A2[i]), s[i], e[j][i]);
+        }
     }
 }
 
@@ -362,6 +381,7 @@ __global__ void __launch_bounds__(NW *kWave)
     // H=4096: 418 us with the stores after the loads, 371 us so).
     for (int k = 0; k < tiles; ++k) {
         const int half = k & 1;
+        take_turn(k);
         const vec xk = xn, zk = zn;
         xn = xr, zn = zr;
         if (k + 1 < tiles) prepare(k + 1);
@@ -517,6 +537,7 @@ __global__ void __launch_bounds__(NW *kWave)
         lds_barrier();
     }
     for (int k = tiles - 1; k >= 0; --k) {
+        take_turn(k);
         const int half = k & 1;
         if (k > 0) prepare(k - 1);
         fetch(k > 1 ? k - 2 : 0);
@@ -703,6 +724,7 @@ __global__ void __launch_bounds__(NW *kWave, 2)
     if (tiles > 0) fetch(tiles - 1, tail);
     lds_barrier();
     for (int k = tiles - 1; k >= 0; --k) {
+        take_turn(k);
         float d[JR], gy[JR], last_slope[JR], s0[kPer];
         load_floats(&sd[p.row][0][p.c], d);
         load_floats(&sd[p.row][2][p.c], gy);
@@ -854,37 +876,63 @@ __global__ void __launch_bounds__(256)
 }
 
 // ---------------------------------------------------------------------------------------------
-// Single token: a lane has a channel of one batch and all its states; the state is read and
-// written once, a wave's 64 channels at a time.
+// Single token: a lane has a channel of one batch and all its states; the state is read and written
+// once, by rows of 64 channels (two channels a lane were slower: 10.5 us against 9.5 for B=64 H=5120
+// N=16, 4.4 TB/s). Where the wave's channels are of one group its lanes load all of B and C at once,
+// a value each (N is at most 32), and hand them round (12.5 us with a load a value).
 // ---------------------------------------------------------------------------------------------
 template <int DT, int NMAX>
 __global__ void __launch_bounds__(kWave)
     scan_one(ScanIn a, float *__restrict__ state, uint16_t *__restrict__ out) {
-    const int64_t h = (int64_t)blockIdx.x * kWave + threadIdx.x, b = blockIdx.y;
-    if (h >= a.H) return;
+    const int64_t b = blockIdx.y, h0 = (int64_t)blockIdx.x * kWave;
+    const bool on = h0 + threadIdx.x < a.H;
+    const int64_t h = on ? h0 + threadIdx.x : a.H - 1;
+    const int64_t g0 = h0 / a.K, last = h0 + kWave < a.H ? h0 + kWave - 1 : a.H - 1;
+    const bool one_group = g0 == last / a.K;
     float s[NMAX], r[NMAX];
     float *sp = state + b * a.N * a.H + h;
 #pragma unroll
-    for (int n = 0; n < NMAX; ++n) {
-        s[n] = n < a.N ? sp[(int64_t)n * a.H] : 0.0f;
-        r[n] = n < a.N ? a.A[(int64_t)n * a.H + h] : 0.0f;
+    for (int n = 0; n < NMAX; ++n)  // rows past N repeat the last and are not stored
+        s[n] = sp[(int64_t)(n < a.N ? n : a.N - 1) * a.H];
+    float mine = 0.0f;
+    if (one_group) {
+        const int n = threadIdx.x % 32;
+        if (n < a.N)
+            mine = to_f32<DT>(threadIdx.x < 32 ? a.B.p[b * a.B.b + g0 * a.B.g + n * a.B.n]
+                                               : a.C.p[b * a.C.b + g0 * a.C.g + n * a.C.n]);
     }
-    const int64_t g = h / a.K;
-    const uint16_t *bp = a.B.p + b * a.B.b + g * a.B.g, *cp = a.C.p + b * a.C.b + g * a.C.g;
+#pragma unroll
+    for (int n = 0; n < NMAX; ++n) r[n] = a.A[(int64_t)(n < a.N ? n : a.N - 1) * a.H + h];
     const float x = to_f32<DT>(a.x.p[b * a.x.b + h * a.x.h]);
-    const float v = to_f32<DT>(a.dt.p[b * a.dt.b + h * a.dt.h]) + (a.bias ? a.bias[h] : 0.0f);
-    const float d = a.softplus ? softplus_f(v) : v;
+    const float t = to_f32<DT>(a.dt.p[b * a.dt.b + h * a.dt.h]) + (a.bias ? a.bias[h] : 0.0f);
+    const float z = a.z.p ? to_f32<DT>(a.z.p[b * a.z.b + h * a.z.h]) : 0.0f;
+    const float d = a.softplus ? softplus_f(t) : t;
     float y = a.D ? a.D[h] * x : 0.0f;
     const float dx = d * x, d2 = d * kLog2e;
+    if (one_group) {
 #pragma unroll
-    for (int n = 0; n < NMAX; ++n) {
-        if (n >= a.N) break;
-        s[n] = __builtin_fmaf(exp2_f(d2 * r[n]), s[n], dx * to_f32<DT>(bp[n * a.B.n]));
-        y = __builtin_fmaf(to_f32<DT>(cp[n * a.C.n]), s[n], y);
-        sp[(int64_t)n * a.H] = s[n];
+        for (int n = 0; n < NMAX; ++n) {
+            const float Bn = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(mine), n));
+            const float Cn = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(mine), n + 32));
+            s[n] = __builtin_fmaf(exp2_f(d2 * r[n]), s[n], dx * Bn);
+            if (n < a.N) y = __builtin_fmaf(Cn, s[n], y);
+        }
+    } else {
+        const int64_t g = h / a.K;
+#pragma unroll
+        for (int n = 0; n < NMAX; ++n) {
+            const int row = n < a.N ? n : a.N - 1;
+            const float Bn = to_f32<DT>(a.B.p[b * a.B.b + g * a.B.g + row * a.B.n]);
+            const float Cn = to_f32<DT>(a.C.p[b * a.C.b + g * a.C.g + row * a.C.n]);
+            s[n] = __builtin_fmaf(exp2_f(d2 * r[n]), s[n], dx * Bn);
+            if (n < a.N) y = __builtin_fmaf(Cn, s[n], y);
+        }
     }
-    if (a.z.p) y *= silu_f(to_f32<DT>(a.z.p[b * a.z.b + h * a.z.h]));
-    out[b * a.H + h] = from_f32<DT>(y);
+    if (!on) return;
+#pragma unroll
+    for (int n = 0; n < NMAX; ++n)
+        if (n < a.N) sp[(int64_t)n * a.H] = s[n];
+    out[b * a.H + h] = from_f32<DT>(a.z.p ? y * silu_f(z) : y);
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -944,13 +992,14 @@ ScanPlan plan_of(const mccb_scan_t *a) {
     p.per_group = (K + kWave - 1) / kWave;
     p.blocks = p.per_group * a->G;
     // Chunks cost a second pass over the recurrence, so they pay only where they multiply the waves
-    // well beyond that: at most half the card's SIMDs busy without them. Then as many as give two
-    // waves a SIMD, no shorter than four tiles.
+    // well beyond that: at most half the card's SIMDs busy without them. Then as many as give six
+    // waves a SIMD (three at a time; 24 chunks of S=16384 H=4096 take 570 us, 8 take 640), of three
+    // tiles at least (S=777 B=5 H=1000 N=8: 32 us, four tiles 34, two 35).
     const int64_t waves = p.blocks * a->B * p.waves, tiles = (a->S + kTile - 1) / kTile;
     int64_t chunks = 1;
     if (waves <= 512) {
-        chunks = 2048 / waves;
-        if (chunks > tiles / 4) chunks = tiles / 4;
+        chunks = 6144 / waves;
+        if (chunks > tiles / 3) chunks = tiles / 3;
         if (chunks > 64) chunks = 64;
         if (chunks < 4) chunks = 1;
     }
@@ -1202,12 +1251,13 @@ int mccb_scan_step(const mccb_scan_t *a, float *state, void *out, void *stream) 
     return by_dtype(a->dtype, [&](auto dt) {
         constexpr int DT = decltype(dt)::value;
         const hipStream_t st = (hipStream_t)stream;
+        uint16_t *o = (uint16_t *)out;
         if (a->N <= 8)
-            hipLaunchKernelGGL((scan_one<DT, 8>), grid, dim3(kWave), 0, st, da, state, (uint16_t *)out);
+            hipLaunchKernelGGL((scan_one<DT, 8>), grid, dim3(kWave), 0, st, da, state, o);
         else if (a->N <= 16)
-            hipLaunchKernelGGL((scan_one<DT, 16>), grid, dim3(kWave), 0, st, da, state, (uint16_t *)out);
+            hipLaunchKernelGGL((scan_one<DT, 16>), grid, dim3(kWave), 0, st, da, state, o);
         else
-            hipLaunchKernelGGL((scan_one<DT, 32>), grid, dim3(kWave), 0, st, da, state, (uint16_t *)out);
+            hipLaunchKernelGGL((scan_one<DT, 32>), grid, dim3(kWave), 0, st, da, state, o);
         return launched();
     });
 }

@@ -9,6 +9,7 @@ an autograd graph: each backward is a call of its own.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from typing import NamedTuple, Optional
 
@@ -18,6 +19,7 @@ from . import build as _build
 from ._lib import MccbError, load
 
 _OK = 0
+_address = ctypes.addressof
 _DTYPE = {torch.bfloat16: 0, torch.float16: 1}
 ACTIVATIONS = {None: 0, "none": 0, "relu": 1, "silu": 2, "gelu": 3, "softplus": 4}
 
@@ -96,6 +98,12 @@ def ssm_lib() -> ctypes.CDLL:
 
 # -- argument checks ---------------------------------------------------------------------------------
 def _check(name, t, shape, dtype, device, contiguous=False):
+    try:
+        if t.shape == shape and t.dtype is dtype and t.get_device() == device.index and \
+                not (contiguous and not t.is_contiguous()):
+            return
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.device != device:
@@ -104,8 +112,7 @@ def _check(name, t, shape, dtype, device, contiguous=False):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.dtype != dtype:
         raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if contiguous and not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _data(name, t, dims):
@@ -133,24 +140,24 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+# The handle of torch's current stream, without the Stream object around it (2 us of a 6 us call).
+_current = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _handle(stream, device):
-    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    if _current is not None:
+        return _current(device.index)
+    return torch.cuda.current_stream(device).cuda_stream
 
 
-class _On:
+_here = contextlib.nullcontext()
+
+
+def _On(stream):
     """What a call allocates belongs to the stream that its kernels run on."""
-    __slots__ = ("stream", "ctx")
-
-    def __init__(self, stream):
-        self.ctx = None if stream is None else torch.cuda.stream(stream)
-
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
+    return _here if stream is None else torch.cuda.stream(stream)
 
 
 def _size(name, args):
@@ -167,7 +174,7 @@ def _workspace(name, args, device):
 
 
 def _run(name, args, *rest):
-    rc = getattr(_lib or ssm_lib(), name)(ctypes.addressof(args), *rest)
+    rc = getattr(_lib or ssm_lib(), name)(_address(args), *rest)
     if rc != _OK:
         raise MccbError(rc, name)
 
