@@ -56,6 +56,20 @@ struct HVec<1> {
     };
 };
 
+// A wave-uniform address plus a lane's 32-bit offset. The empty asm keeps the base in scalar
+// registers, so that loads and stores take the form with a scalar base and a 32-bit lane offset
+// instead of a 64-bit vector addition each. (Unoptimized builds do not keep it uniform.)
+template <typename P>
+__device__ static inline P *lane_at(P *base, uint32_t offset) {
+#if defined(__OPTIMIZE__)
+    asm("" : "+s"(base));
+    typedef __attribute__((address_space(1))) P gP;
+    return (P *)((gP *)base + offset);
+#else
+    return base + offset;
+#endif
+}
+
 // A barrier for data in LDS: this wave's LDS accesses are done, its global loads and stores may stay
 // in flight (__syncthreads waits for those too, which ends every prefetch at the barrier).
 __device__ static inline void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }

@@ -15,9 +15,9 @@
 // The epilogue works on fp32 sums staged through LDS, so that bias, residual, pre and out are read
 // and written as whole rows.
 //
-// Operands that the direct-to-LDS loads cannot take (rows not 16-byte aligned) are first copied into
-// the workspace with rows padded by zeros. The backward needs w, x and g with the other dimension
-// contiguous; those are transposed into the workspace first.
+// Operands that the direct-to-LDS loads cannot take (rows not 16-byte aligned) go through registers
+// instead, by loads that may start at any element. The backward needs w, x and g with the other
+// dimension contiguous; those are transposed into the workspace first.
 #include "ssm_common.h"
 
 using namespace ssm;
@@ -115,7 +115,7 @@ __device__ static inline void finish8(const Epilogue &e, int64_t m, int64_t n, i
     put(e.out + m * e.N + n);
 }
 
-// Two operands whose rows run along the contraction: P [M,K] and Q [N,K], 16-byte aligned rows.
+// Two operands whose rows run along the contraction: P [M,K] and Q [N,K].
 struct Product {
     const uint16_t *p, *q;
     int64_t p_ld, q_ld;
@@ -138,13 +138,19 @@ __device__ static inline void tile_of(const Product &g, int &tm, int &tn) {
     tn = r / rows;
 }
 
-template <int DT, int BM, int BN, int WM, int WN>
+// DIRECT: both operands' rows are 16-byte aligned whole chunks.
+template <int DT, int BM, int BN, int WM, int WN, bool DIRECT>
 __global__ void __launch_bounds__(WM *WN *kWave)
     product_tiles(Product g, Epilogue e) {
     constexpr int kWaves = WM * WN, kThreads = kWaves * kWave;
     constexpr int TM = BM / WM / 32, TN = BN / WN / 32;      // a wave's 32x32 tiles
     constexpr int kRows = BM + BN, kLoads = kRows / 8 / kWaves;  // a wave's load takes 8 rows
     constexpr int kBuf = kRows * kBK;                        // 16-bit values of a buffer
+    // Tiles with a compute unit to themselves, and registers for it: the next operands are read while
+    // this one's products run, and the next step's loads go out behind the first products, not
+    // before them (M=4096 K=4096 N=8192: 254 us without, 241 with). The others have more waves to
+    // fill such gaps, or (256x320) no registers left.
+    constexpr bool kPipe = kWaves == 8 && TM * TN <= 8;
     constexpr int kStage = BN + 4;                           // fp32 row of the epilogue's staging
     constexpr int kRound = BM / WM;                          // rows it stages at a time
     constexpr size_t kBytes = sizeof(uint16_t) * 2 * kBuf > sizeof(float) * kRound * kStage
@@ -161,33 +167,73 @@ __global__ void __launch_bounds__(WM *WN *kWave)
     const int s0 = blockIdx.y * g.steps_per_split;
     const int s1 = s0 + g.steps_per_split < all_steps ? s0 + g.steps_per_split : all_steps;
 
-    // Row r of a buffer (P's rows, then Q's) holds its eight chunks in the order c ^ (r % 8), so
-    // that reading one chunk of 32 rows spreads over the banks. A load's lane i fills place i % 8 of
-    // row i / 8 of the wave's eight rows. Rows past the matrix repeat its last row.
-    const uint16_t *src[kLoads];
-    int chunk = (lane % 8) ^ (lane / 8);
+    // Row r of a buffer (P's rows, then Q's) holds its eight chunks in the order c ^ (r / 2 % 8), so
+    // that reading one chunk of 16 rows (256 bytes, all banks) meets every bank once. A load's lane i
+    // fills place i % 8 of row i / 8 of a group of eight rows; groups go round the waves, P's before
+    // Q's, so that a wave's groups are all even or all odd. Rows past the matrix repeat its last row.
+    constexpr int kLoadsP = BM / 8 / kWaves;
+    static_assert(BM / 8 % kWaves == 0 && BN / 8 % kWaves == 0 && kWaves % 2 == 0, "whole groups");
+    const int chunk = (lane % 8) ^ (lane / 16) ^ (wave % 2 * 4);
+    uint32_t at[kLoads];  // bytes from the tile's first row of P or Q (DIRECT: below 2^32)
+    const uint8_t *p0 = (const uint8_t *)(g.p + m0 * g.p_ld), *q0 = (const uint8_t *)(g.q + n0 * g.q_ld);
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-        const int r = (wave * kLoads + i) * 8 + lane / 8;
-        if (r < BM) {
-            const int64_t m = m0 + r < g.M ? m0 + r : g.M - 1;
-            src[i] = g.p + m * g.p_ld + chunk * 8;
-        } else {
-            const int64_t n = n0 + r - BM < g.N ? n0 + r - BM : g.N - 1;
-            src[i] = g.q + n * g.q_ld + chunk * 8;
-        }
+        const bool of_p = i < kLoadsP;
+        const int64_t r = ((of_p ? i : i - kLoadsP) * kWaves + wave) * 8 + lane / 8;
+        const int64_t left = of_p ? g.M - m0 : g.N - n0;
+        at[i] = (uint32_t)((r < left ? r : left - 1) * (of_p ? g.p_ld : g.q_ld) * 2 + chunk * 16);
     }
     typedef __attribute__((address_space(1))) const uint32_t gmem;
     typedef __attribute__((address_space(3))) uint32_t lmem;
-    auto fill = [&](int step, int buf) {
+    u16x8 held[DIRECT ? 1 : kLoads];
+    auto place_of = [&](int i, int buf) {
+        const int group = i < kLoadsP ? i * kWaves + wave : BM / 8 + (i - kLoadsP) * kWaves + wave;
+        return lds + buf * kBuf + group * 8 * kBK;
+    };
+    auto fill = [&](int step, int buf) {  // straight to LDS
         const int64_t k = (int64_t)step * kBK;
-        const bool past = k + chunk * 8 >= g.K;  // rows are padded to whole chunks
+        const uint8_t *ps = p0 + k * 2, *qs = q0 + k * 2;
+        if (k + kBK <= g.K) {
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i)
+                __builtin_amdgcn_global_load_lds((gmem *)lane_at(i < kLoadsP ? ps : qs, at[i]),
+                                                 (lmem *)place_of(i, buf), 16, 0, 0);
+        } else {
+            const bool past = k + chunk * 8 >= g.K;
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                const uint8_t *s = past ? (const uint8_t *)zero_chunk : (i < kLoadsP ? ps : qs) + at[i];
+                __builtin_amdgcn_global_load_lds((gmem *)s, (lmem *)place_of(i, buf), 16, 0, 0);
+            }
+        }
+    };
+    // Operands that direct loads cannot take, by way of registers.
+    auto row_of = [&](int i) {
+        const bool of_p = i < kLoadsP;
+        const int64_t r = ((of_p ? i : i - kLoadsP) * kWaves + wave) * 8 + lane / 8;
+        const int64_t left = of_p ? g.M - m0 : g.N - n0;
+        return (of_p ? g.p + (m0 + (r < left ? r : left - 1)) * g.p_ld
+                     : g.q + (n0 + (r < left ? r : left - 1)) * g.q_ld) + chunk * 8;
+    };
+    auto take = [&](int step) {
+        const int64_t k = (int64_t)step * kBK;
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
-            const uint16_t *s = past ? (const uint16_t *)zero_chunk : src[i] + k;
-            __builtin_amdgcn_global_load_lds(
-                (gmem *)s, (lmem *)(lds + buf * kBuf + (wave * kLoads + i) * 8 * kBK), 16, 0, 0);
+            const uint16_t *s = row_of(i) + k;
+            const int64_t left = g.K - k - chunk * 8;
+            if (left >= 8) {
+                held[i] = *(const HVec<8>::t *)s;
+            } else {
+                held[i] = u16x8{0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+                for (int v = 0; v < 7; ++v)
+                    if (v < left) held[i][v] = s[v];
+            }
         }
+    };
+    auto put = [&](int buf) {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) *(u16x8 *)(place_of(i, buf) + lane * 8) = held[i];
     };
     f32x16 acc[TN][TM];
 #pragma unroll
@@ -197,33 +243,59 @@ __global__ void __launch_bounds__(WM *WN *kWave)
 #pragma unroll
             for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
 
-    fill(s0, 0);
+    if (DIRECT) {
+        fill(s0, 0);
+    } else {
+        take(s0);
+        put(0);
+    }
     for (int s = s0; s < s1; ++s) {
         const int buf = (s - s0) & 1;
         // this step's loads have landed, and every wave is done with the other buffer
         __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
         __syncthreads();
-        if (s + 1 < s1) fill(s + 1, buf ^ 1);
         const uint16_t *base = lds + buf * kBuf;
-#pragma unroll
-        for (int ks = 0; ks < kBK / 16; ++ks) {
-            const int c = (ks * 2 + lane / 32) ^ (lane % 8);  // rows below are lane % 8 modulo 8
-            u16x8 a[TN], b[TM];
+        // The operands of 16 of the contraction, and their products.
+        u16x8 a[kPipe ? 2 : 1][TN], b[kPipe ? 2 : 1][TM];
+        auto operands = [&](int ks, int to) {
+            const int c = (ks * 2 + lane / 32) ^ (lane / 2 % 8);  // rows below are lane % 32 modulo 32
 #pragma unroll
             for (int i = 0; i < TN; ++i) {
                 const int r = BM + (wn * TN + i) * 32 + lane % 32;
-                a[i] = *(const u16x8 *)(base + r * kBK + c * 8);
+                a[to][i] = *(const u16x8 *)(base + r * kBK + c * 8);
             }
 #pragma unroll
             for (int j = 0; j < TM; ++j) {
                 const int r = (wm * TM + j) * 32 + lane % 32;
-                b[j] = *(const u16x8 *)(base + r * kBK + c * 8);
+                b[to][j] = *(const u16x8 *)(base + r * kBK + c * 8);
             }
+        };
+        auto multiply = [&](int from) {
 #pragma unroll
             for (int i = 0; i < TN; ++i)
 #pragma unroll
-                for (int j = 0; j < TM; ++j) acc[i][j] = mfma32<DT>(a[i], b[j], acc[i][j]);
+                for (int j = 0; j < TM; ++j) acc[i][j] = mfma32<DT>(a[from][i], b[from][j], acc[i][j]);
+        };
+        if (!DIRECT && s + 1 < s1) take(s + 1);
+        if (kPipe) {
+            operands(0, 0);
+#pragma unroll
+            for (int ks = 0; ks < kBK / 16; ++ks) {
+                if (ks + 1 < kBK / 16) operands(ks + 1, (ks + 1) & 1);
+                __builtin_amdgcn_sched_barrier(0);
+                multiply(ks & 1);
+                __builtin_amdgcn_sched_barrier(0);
+                if (DIRECT && ks == 0 && s + 1 < s1) fill(s + 1, buf ^ 1);
+            }
+        } else {
+            if (DIRECT && s + 1 < s1) fill(s + 1, buf ^ 1);
+#pragma unroll
+            for (int ks = 0; ks < kBK / 16; ++ks) {
+                operands(ks, 0);
+                multiply(0);
+            }
         }
+        if (!DIRECT && s + 1 < s1) put(buf ^ 1);
     }
     // Epilogue, kRound rows at a time. A lane's 16 sums of a 32x32 tile are column lane % 32 (a row
     // of P) and rows 8 (v / 4) + 4 (lane / 32) + v % 4 (rows of Q, columns of the output).
@@ -290,8 +362,10 @@ __global__ void __launch_bounds__(256)
     finish8<DT>(e, m, n, count, v);
 }
 
-// M up to 16 MB: a block has 16 rows of Q; its waves take chunks of 32 of the contraction in turn and
-// add their sums in LDS. Loads are 16 bytes at any 2-byte address, so nothing is packed.
+// M up to 16 MB: a block has 16 rows of Q; its waves take parts of 64 of the contraction in turn and
+// add their sums in LDS. A lane reads 32 adjacent bytes of its row for two matrix instructions (the
+// order of the contraction is free as long as P's is the same), so a wave takes whole lines of its
+// 16 rows. Loads may start at any 2-byte address.
 template <int DT, int MB, int WAVES>
 __global__ void __launch_bounds__(WAVES *kWave)
     product_skinny(Product g, Epilogue e) {
@@ -299,6 +373,7 @@ __global__ void __launch_bounds__(WAVES *kWave)
     const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
     const int64_t n0 = (int64_t)blockIdx.x * 16;
     const int64_t n = n0 + lane % 16 < g.N ? n0 + lane % 16 : g.N - 1;
+    const int64_t own = (lane / 16) * 16;  // the lane's 16 of a part
     const uint16_t *qp = g.q + n * g.q_ld, *pp[MB];
 #pragma unroll
     for (int b = 0; b < MB; ++b) {
@@ -308,7 +383,7 @@ __global__ void __launch_bounds__(WAVES *kWave)
     f32x4 acc[MB];
 #pragma unroll
     for (int b = 0; b < MB; ++b) acc[b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    auto chunk = [&](const uint16_t *p, int64_t k) {
+    auto guarded = [&](const uint16_t *p, int64_t k) {
         u16x8 v;
         if (k + 8 <= g.K) {
             v = *(const HVec<8>::t *)(p + k);
@@ -318,26 +393,36 @@ __global__ void __launch_bounds__(WAVES *kWave)
         }
         return v;
     };
-    // the whole part without a bounds check: eight steps' loads in flight
-    constexpr int kAhead = 8;
-    const int64_t own = (lane / 16) * 8, stride = WAVES * 32;
-    int64_t k = wave * 32;
-    for (; k + (kAhead - 1) * stride + 32 <= g.K; k += kAhead * stride) {
-        u16x8 q[kAhead];
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) q[i] = *(const HVec<8>::t *)(qp + k + i * stride + own);
+    // several parts' loads in flight, without a check of bounds; then part by part
+    constexpr int kAhead = MB == 1 ? 4 : 2;
+    constexpr int64_t kStride = WAVES * 64;
+    int64_t k = wave * 64;
+    for (; k + (kAhead - 1) * kStride + 64 <= g.K; k += kAhead * kStride) {
+        u16x8 q[kAhead][2], p[kAhead][MB][2];
 #pragma unroll
         for (int i = 0; i < kAhead; ++i)
 #pragma unroll
-            for (int b = 0; b < MB; ++b) {
-                const u16x8 p = *(const HVec<8>::t *)(pp[b] + k + i * stride + own);
-                acc[b] = mfma16<DT>(q[i], p, acc[b]);
-            }
-    }
-    for (; k < g.K; k += stride) {
-        const u16x8 q = chunk(qp, k + own);
+            for (int h = 0; h < 2; ++h) {
+                q[i][h] = *(const HVec<8>::t *)(qp + k + i * kStride + own + h * 8);
 #pragma unroll
-        for (int b = 0; b < MB; ++b) acc[b] = mfma16<DT>(q, chunk(pp[b], k + own), acc[b]);
+                for (int b = 0; b < MB; ++b)
+                    p[i][b][h] = *(const HVec<8>::t *)(pp[b] + k + i * kStride + own + h * 8);
+            }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int b = 0; b < MB; ++b) acc[b] = mfma16<DT>(q[i][h], p[i][b][h], acc[b]);
+    }
+    for (; k < g.K; k += kStride) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const u16x8 q = guarded(qp, k + own + h * 8);
+#pragma unroll
+            for (int b = 0; b < MB; ++b)
+                acc[b] = mfma16<DT>(q, guarded(pp[b], k + own + h * 8), acc[b]);
+        }
     }
     // a lane's four sums: row lane % 16 of P, rows 4 (lane / 16) + 0..3 of Q
 #pragma unroll
@@ -359,23 +444,6 @@ __global__ void __launch_bounds__(WAVES *kWave)
 // ---------------------------------------------------------------------------------------------
 // Operands laid out for the products
 // ---------------------------------------------------------------------------------------------
-// dst [R, Cp] = src [R, C], zeros past C.
-__global__ void __launch_bounds__(256)
-    pack_rows(const uint16_t *__restrict__ src, int64_t ld, int64_t R, int64_t C, int64_t Cp,
-              uint16_t *__restrict__ dst) {
-    const int64_t id = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
-    if (id >= R * Cp) return;
-    const int64_t r = id / Cp, c = id % Cp;  // Cp is a multiple of 8
-    u16x8 v;
-    if (c + 8 <= C) {
-        v = *(const HVec<8>::t *)(src + r * ld + c);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = c + i < C ? src[r * ld + c + i] : 0;
-    }
-    *(u16x8 *)(dst + id) = v;
-}
-
 // What the backward makes of gout (or of a plain matrix, without `pre`): g = gout act'(pre), kept by
 // rows and / or by columns, and the column sums of 64 rows. One 64x64 tile a block.
 struct Turn {
@@ -485,42 +553,86 @@ __global__ void __launch_bounds__(256)
 int64_t up8(int64_t v) { return (v + 7) & ~(int64_t)7; }
 uint64_t area(int64_t rows, int64_t ld) { return align16((uint64_t)rows * (uint64_t)ld * 2); }
 
+// Rows that the loads straight to LDS can take: aligned chunks, a tile's rows within 32-bit offsets.
 bool direct_rows(const void *p, int64_t ld, int64_t K) {
-    return !misaligned(p, 16) && ld % 8 == 0 && K % 8 == 0;
+    return !misaligned(p, 16) && ld % 8 == 0 && K % 8 == 0 && ld <= (int64_t)1 << 22;
 }
 
 // How a product is cut; a function of its sizes alone.
+enum { kSkinny, k256x256, k256x320, k256x192, k128x128, k64x64, kForms };
+struct Tile {
+    int m, n;
+    // cycles of a compute unit a step of 64 of the contraction: with one tile on it, and its share
+    // of several (the smaller tiles'), measured with bf16 over M, N, K from 64 to 16384
+    double alone, shared;
+};
+constexpr Tile kTiles[kForms] = {{0, 0, 0, 0},           {256, 256, 4200, 4200}, {256, 320, 4700, 4700},
+                                 {256, 192, 3100, 3100}, {128, 128, 1900, 1350}, {64, 64, 900, 440}};
+
 struct Cut {
-    bool skinny, large;
-    int splits, steps_per_split;
+    int form, splits, steps_per_split;
     int64_t tiles_m, tiles_n;
     uint64_t partial;  // workspace bytes
 };
 
+// The form and split with the least estimated time, in cycles: a compute unit's share of the tiles,
+// each its steps and its epilogue, and for a split contraction another launch and the partial sums'
+// way through memory.
 Cut cut_of(int64_t M, int64_t N, int64_t K) {
-    Cut c{};
-    c.skinny = M <= 64;
-    c.splits = 1;
-    if (c.skinny) return c;
-    // 256x256 tiles read half as much of LDS and L2 a product as 128x128 ones, which in turn fill the
-    // 256 compute units from a quarter of the output.
-    const int64_t big = ((M + 255) / 256) * ((N + 255) / 256);
-    c.large = big >= 200;
-    const int64_t b = c.large ? 256 : 128;
-    c.tiles_m = (M + b - 1) / b, c.tiles_n = (N + b - 1) / b;
-    const int64_t tiles = c.tiles_m * c.tiles_n, steps = (K + kBK - 1) / kBK;
-    int64_t splits = 1;
-    if (tiles < 256) {  // fewer blocks than compute units
-        splits = 512 / tiles;
-        if (splits > steps / 4) splits = steps / 4;
-        if (splits > 32) splits = 32;
-        if (splits < 2) splits = 1;
+    Cut best{};
+    best.splits = 1;
+    if (M <= 64) return best;  // skinny: w is read once however few the rows
+    const int64_t steps = (K + kBK - 1) / kBK;
+    double least = 0.0;
+    for (int f = k256x256; f < kForms; ++f) {
+        const Tile &t = kTiles[f];
+        const int64_t tm = (M + t.m - 1) / t.m, tn = (N + t.n - 1) / t.n;
+        for (int64_t want = 1; want <= 32 && (want == 1 || want * 4 <= steps); want *= 2) {
+            const int64_t per = (steps + want - 1) / want, splits = (steps + per - 1) / per;
+            const double share = (double)((tm * tn * splits + 255) / 256);  // of 256 compute units
+            double cost = share * (per * (share > 1.0 ? t.shared : t.alone) + t.m * t.n * 0.25);
+            if (splits > 1) cost += 12000.0 + (double)M * N * splits * 8.0 / 900.0;
+            if (best.tiles_m == 0 || cost < least) {
+                least = cost;
+                best = {f, (int)splits, (int)per, tm, tn,
+                        splits > 1 ? (uint64_t)splits * (uint64_t)M * (uint64_t)N * 4 : 0};
+            }
+        }
     }
-    const int64_t per = (steps + splits - 1) / splits;
-    c.steps_per_split = (int)per;
-    c.splits = (int)((steps + per - 1) / per);
-    if (c.splits > 1) c.partial = (uint64_t)c.splits * (uint64_t)M * (uint64_t)N * 4;
-    return c;
+    return best;
+}
+
+template <int DT, bool DIRECT>
+void launch_tiles(const Cut &c, const Product &g, const Epilogue &e, hipStream_t st) {
+    const dim3 grid((unsigned)(c.tiles_m * c.tiles_n), (unsigned)c.splits);
+    switch (c.form) {
+        case k256x256:
+            hipLaunchKernelGGL((product_tiles<DT, 256, 256, 2, 4, DIRECT>), grid, dim3(512), 0, st, g, e);
+            break;
+        case k256x320:
+            hipLaunchKernelGGL((product_tiles<DT, 256, 320, 4, 2, DIRECT>), grid, dim3(512), 0, st, g, e);
+            break;
+        case k256x192:
+            hipLaunchKernelGGL((product_tiles<DT, 256, 192, 4, 2, DIRECT>), grid, dim3(512), 0, st, g, e);
+            break;
+        case k128x128:
+            hipLaunchKernelGGL((product_tiles<DT, 128, 128, 2, 2, DIRECT>), grid, dim3(256), 0, st, g, e);
+            break;
+        default:
+            hipLaunchKernelGGL((product_tiles<DT, 64, 64, 2, 2, DIRECT>), grid, dim3(256), 0, st, g, e);
+    }
+}
+
+template <int DT, int MB>
+void launch_skinny(const Product &g, const Epilogue &e, hipStream_t st) {
+    const dim3 grid((unsigned)((g.N + 15) / 16));
+    // enough waves a block that each has a few parts of the contraction
+    if (g.K >= 4096)
+        hipLaunchKernelGGL((product_skinny<DT, MB, 16>), grid, dim3(1024), 0, st, g, e);
+    else if (g.K >= 512)
+        hipLaunchKernelGGL((product_skinny<DT, MB, 8>), grid, dim3(512), 0, st, g, e);
+    else
+        hipLaunchKernelGGL((product_skinny<DT, MB, 2>), grid, dim3(128), 0, st, g, e);
 }
 
 template <int DT>
@@ -529,32 +641,18 @@ int launch_product(const uint16_t *p, int64_t p_ld, const uint16_t *q, int64_t q
     const Cut c = cut_of(M, N, K);
     Product g{p, q, p_ld, q_ld, M, N, K, (int)c.tiles_m, (int)c.tiles_n, c.splits, c.steps_per_split,
               c.splits > 1 ? (float *)partial : nullptr};
-    if (c.skinny) {
-        const dim3 grid((unsigned)((N + 15) / 16));
-        if (M <= 16)
-            hipLaunchKernelGGL((product_skinny<DT, 1, 8>), grid, dim3(512), 0, st, g, e);
-        else if (M <= 32)
-            hipLaunchKernelGGL((product_skinny<DT, 2, 8>), grid, dim3(512), 0, st, g, e);
-        else
-            hipLaunchKernelGGL((product_skinny<DT, 4, 8>), grid, dim3(512), 0, st, g, e);
+    if (c.form == kSkinny) {
+        if (M <= 16) launch_skinny<DT, 1>(g, e, st);
+        else if (M <= 32) launch_skinny<DT, 2>(g, e, st);
+        else launch_skinny<DT, 4>(g, e, st);
         return launched();
     }
-    const dim3 grid((unsigned)(c.tiles_m * c.tiles_n), (unsigned)c.splits);
-    if (c.large)
-        hipLaunchKernelGGL((product_tiles<DT, 256, 256, 2, 4>), grid, dim3(512), 0, st, g, e);
-    else
-        hipLaunchKernelGGL((product_tiles<DT, 128, 128, 2, 2>), grid, dim3(256), 0, st, g, e);
+    if (direct_rows(p, p_ld, K) && direct_rows(q, q_ld, K)) launch_tiles<DT, true>(c, g, e, st);
+    else launch_tiles<DT, false>(c, g, e, st);
     const int rc = launched();
     if (rc != MCCB_OK || c.splits == 1) return rc;
     const int64_t ids = M * ((N + 7) / 8);
     hipLaunchKernelGGL((finish<DT>), dim3((unsigned)((ids + 255) / 256)), dim3(256), 0, st, g, e);
-    return launched();
-}
-
-int pack(const void *src, int64_t ld, int64_t R, int64_t C, void *dst, hipStream_t st) {
-    const int64_t n = R * up8(C) / 8;
-    hipLaunchKernelGGL(pack_rows, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st,
-                       (const uint16_t *)src, ld, R, C, up8(C), (uint16_t *)dst);
     return launched();
 }
 
@@ -589,28 +687,6 @@ int check_linear_inputs(const mccb_linear_t *a, Span *in) {
     in[1] = {a->weight, w};
     in[2] = {a->bias, (uint64_t)a->N * 2};
     return MCCB_OK;
-}
-
-struct FwdLayout {
-    bool pack_x, pack_w;
-    uint64_t x, w, partial, total;  // offsets, and the size
-};
-
-FwdLayout fwd_layout(const mccb_linear_t *a) {
-    FwdLayout l{};
-    const Cut c = cut_of(a->M, a->N, a->K);
-    uint64_t at = 0;
-    if (!c.skinny) {
-        l.pack_x = !direct_rows(a->x, a->x_ld, a->K);
-        l.pack_w = !direct_rows(a->weight, a->weight_ld, a->K);
-        l.x = at;
-        if (l.pack_x) at += area(a->M, up8(a->K));
-        l.w = at;
-        if (l.pack_w) at += area(a->N, up8(a->K));
-    }
-    l.partial = at;
-    l.total = at + c.partial;
-    return l;
 }
 
 // The backward's: g by rows and by columns, x and w by columns, the column sums, and the larger of
@@ -659,7 +735,7 @@ int mccb_linear_forward_get_workspace_size(const mccb_linear_t *a, uint64_t *siz
     if (!size) return MCCB_ERR_PARAM_NULLPTR;
     const int rc = check_linear(a);
     if (rc != MCCB_OK) return rc;
-    *size = fwd_layout(a).total;
+    *size = a->M > 0 ? cut_of(a->M, a->N, a->K).partial : 0;
     return MCCB_OK;
 }
 
@@ -675,34 +751,22 @@ int mccb_linear_forward(const mccb_linear_t *a, const void *residual, int64_t re
     uint64_t r_bytes = 0;
     if (residual && (!extent(2, size, stride, 2, &r_bytes) || misaligned(residual, 2)))
         return MCCB_ERR_PARAM_INVALID;
-    const FwdLayout l = fwd_layout(a);
-    rc = check_workspace(ws, ws_size, l.total);
+    const uint64_t need = a->M > 0 ? cut_of(a->M, a->N, a->K).partial : 0;
+    rc = check_workspace(ws, ws_size, need);
     if (rc != MCCB_OK) return rc;
     in[3] = {residual, r_bytes};
     const uint64_t n_out = (uint64_t)a->M * (uint64_t)a->N * 2;
-    const Span outs[3] = {{out, n_out}, {pre, n_out}, {ws, l.total}};
+    const Span outs[3] = {{out, n_out}, {pre, n_out}, {ws, need}};
     if (misaligned(out, 2) || misaligned(pre, 2) || outputs_clash(in, 4, outs, 3))
         return MCCB_ERR_PARAM_INVALID;
     if (a->M == 0) return MCCB_OK;
     const hipStream_t st = (hipStream_t)stream;
-    uint8_t *at = (uint8_t *)ws;
-    const void *x = a->x, *w = a->weight;
-    int64_t x_ld = a->x_ld, w_ld = a->weight_ld;
-    if (l.pack_x) {
-        rc = pack(x, x_ld, a->M, a->K, at + l.x, st);
-        if (rc != MCCB_OK) return rc;
-        x = at + l.x, x_ld = up8(a->K);
-    }
-    if (l.pack_w) {
-        rc = pack(w, w_ld, a->N, a->K, at + l.w, st);
-        if (rc != MCCB_OK) return rc;
-        w = at + l.w, w_ld = up8(a->K);
-    }
     const Epilogue e{(const uint16_t *)a->bias, (const uint16_t *)residual, (uint16_t *)out,
                      (uint16_t *)pre, residual_ld, a->N, a->activation};
     return by_dtype(a->dtype, [&](auto dt) {
-        return launch_product<decltype(dt)::value>((const uint16_t *)x, x_ld, (const uint16_t *)w, w_ld,
-                                                   a->M, a->N, a->K, e, at + l.partial, st);
+        return launch_product<decltype(dt)::value>((const uint16_t *)a->x, a->x_ld,
+                                                   (const uint16_t *)a->weight, a->weight_ld, a->M,
+                                                   a->N, a->K, e, ws, st);
     });
 }
 
@@ -751,10 +815,13 @@ int mccb_linear_backward(const mccb_linear_t *a, const void *gout, int64_t gout_
     return by_dtype(a->dtype, [&](auto dt) {
         constexpr int DT = decltype(dt)::value;
         const bool slope = a->activation != MCCB_ACT_NONE;
+        // without an activation g is gradOut, which the first product can read where it is
+        const uint16_t *g = slope ? g_rows : (const uint16_t *)gout;
+        const int64_t g_ld = slope ? Np : gout_ld;
         const Turn tg{(const uint16_t *)gout, slope ? (const uint16_t *)pre : nullptr,
-                      gout_ld, a->M, a->N, gx ? g_rows : nullptr, gw ? g_cols : nullptr,
+                      gout_ld, a->M, a->N, gx && slope ? g_rows : nullptr, gw ? g_cols : nullptr,
                       gb ? sums : nullptr, Np, Mp, a->activation};
-        int r = gx || gw || gb ? launch_turn<DT>(tg, st) : MCCB_OK;
+        int r = tg.rows || tg.columns || tg.sums ? launch_turn<DT>(tg, st) : MCCB_OK;
         if (r == MCCB_OK && gb) {
             hipLaunchKernelGGL((sum_columns<DT>), dim3((unsigned)((a->N + 63) / 64)), dim3(256), 0, st,
                                sums, (a->M + 63) / 64, a->N, (uint16_t *)gb);
@@ -766,7 +833,7 @@ int mccb_linear_backward(const mccb_linear_t *a, const void *gout, int64_t gout_
             r = launch_turn<DT>(tw, st);
             const Epilogue e{nullptr, nullptr, (uint16_t *)gx, nullptr, 0, a->K, MCCB_ACT_NONE};
             if (r == MCCB_OK)
-                r = launch_product<DT>(g_rows, Np, w_cols, Np, a->M, a->K, a->N, e, at + l.partial, st);
+                r = launch_product<DT>(g, g_ld, w_cols, Np, a->M, a->K, a->N, e, at + l.partial, st);
         }
         if (r == MCCB_OK && gw) {
             const Turn tx{(const uint16_t *)a->x, nullptr, a->x_ld, a->M, a->K,
