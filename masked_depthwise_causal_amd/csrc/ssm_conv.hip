@@ -50,12 +50,12 @@ __device__ static inline void store(uint16_t *p, const typename HVec<V>::t q) {
     *(typename HVec<V>::t *)p = q;
 }
 
-// The lane's batch and first channel; false past the last lane.
+// Lane id's batch and first channel; false past the last lane.
 template <int V>
-__device__ static inline bool lane_place(int64_t B, int64_t H, uint32_t per_batch, int64_t &b,
-                                         int64_t &h) {
-    const uint32_t id = blockIdx.x * (uint32_t)kThreads + threadIdx.x;
+__device__ static inline bool lane_place(uint32_t id, int64_t B, int64_t H, uint32_t per_batch,
+                                         int64_t &b, int64_t &h) {
     const uint32_t j = id / per_batch;
+    b = h = 0;
     if (j >= B) return false;
     const int64_t first = (int64_t)(id - j * per_batch) * V;
     b = j;
@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(kThreads)
                  int64_t H, uint32_t per_batch, int rows) {
     typedef typename HVec<V>::t vec;
     int64_t b, h;
-    if (!lane_place<V>(B, H, per_batch, b, h)) return;
+    if (!lane_place<V>(blockIdx.x * (uint32_t)kThreads + threadIdx.x, B, H, per_batch, b, h)) return;
     const int64_t len = clamp_len(lengths, b, S);
     const int64_t t0 = (int64_t)blockIdx.y * rows, t1 = t0 + rows < S ? t0 + rows : S;
     if (W > 1 && blockIdx.y == 0 && final_state) {
@@ -167,9 +167,10 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 // Backward. A strip's lane walks its rows and the W-1 after it: g of row i completes gx of row
-// i-W+1. Its own rows add to the weight's and bias's sums (fp32 over the strip's rows), which go to
-// the workspace as [strip][b][W+1][H]; the second kernel adds them over strips and batches in fp64,
-// in a fixed order.
+// i-W+1. Its own rows add to the weight's and bias's sums (fp32 over the strip's rows). A block has 64
+// lanes' columns and four consecutive strips, a wave each, whose sums it adds and writes to the
+// workspace as [block of strips][b][W+1][H]; the second kernel adds them over blocks and batches in
+// fp64, in a fixed order. (With a wave for every strip's sums they were a fifth of the traffic.)
 template <int DT, int W, bool SILU, int V>
 __global__ void __launch_bounds__(kThreads)
     conv_act_bwd(Rows x, Rows gy, const uint16_t *__restrict__ weight,
@@ -179,135 +180,158 @@ __global__ void __launch_bounds__(kThreads)
                  float *__restrict__ partial, int64_t S, int64_t B, int64_t H, uint32_t per_batch,
                  int rows) {
     typedef typename HVec<V>::t vec;
+    constexpr int kWaves = kThreads / kWave;
+    __shared__ float part[kWaves][(W + 1) * V][kWave];
+    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
     int64_t b, h;
-    if (!lane_place<V>(B, H, per_batch, b, h)) return;
-    const int64_t len = clamp_len(lengths, b, S);
-    const int64_t t0 = (int64_t)blockIdx.y * rows, t1 = t0 + rows < S ? t0 + rows : S;
+    const bool on = lane_place<V>(blockIdx.x * (uint32_t)kWave + lane, B, H, per_batch, b, h);
+    const int64_t strip = (int64_t)blockIdx.y * kWaves + wave;
+    const int64_t t0 = strip * rows, t1 = t0 + rows < S ? t0 + rows : S;
     const int64_t BH = B * H, at = b * H + h;
-    float w[W][V], bv[V], win[W][V], g[W][V], gw[W][V], gb[V];
+    float gw[W][V], gb[V];
 #pragma unroll
-    for (int k = 0; k < W; ++k) {
-        widen<DT, V>(load<V>(weight + k * H + h), w[k]);
+    for (int v = 0; v < V; ++v) {
+        gb[v] = 0.0f;
 #pragma unroll
-        for (int v = 0; v < V; ++v) g[k][v] = gw[k][v] = 0.0f;
+        for (int k = 0; k < W; ++k) gw[k][v] = 0.0f;
     }
+    // strip 0 is walked without rows too: it has the carried rows' gradient
+    if (on && (t0 < S || strip == 0)) {
+        const int64_t len = clamp_len(lengths, b, S);
+        float w[W][V], bv[V], win[W][V], g[W][V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) bv[v] = gb[v] = 0.0f;
-    if (bias) widen<DT, V>(load<V>(bias + h), bv);
+        for (int k = 0; k < W; ++k) {
+            widen<DT, V>(load<V>(weight + k * H + h), w[k]);
 #pragma unroll
-    for (int k = 0; k < W - 1; ++k) {
-        // rows past the length are in no live row's window, and may hold anything
-        if (t0 - (W - 1) + k < len) {
-            row_before<DT, W, V>(x, state, t0 - (W - 1) + k, B, H, b, h, win[k]);
-        } else {
-#pragma unroll
-            for (int v = 0; v < V; ++v) win[k][v] = 0.0f;
+            for (int v = 0; v < V; ++v) g[k][v] = 0.0f;
         }
-    }
-    const uint16_t *xp = x.p + b * x.b + h * x.h, *gp = gy.p + b * gy.b + h * gy.h;
+#pragma unroll
+        for (int v = 0; v < V; ++v) bv[v] = 0.0f;
+        if (bias) widen<DT, V>(load<V>(bias + h), bv);
+#pragma unroll
+        for (int k = 0; k < W - 1; ++k) {
+            // rows past the length are in no live row's window, and may hold anything
+            if (t0 - (W - 1) + k < len) {
+                row_before<DT, W, V>(x, state, t0 - (W - 1) + k, B, H, b, h, win[k]);
+            } else {
+#pragma unroll
+                for (int v = 0; v < V; ++v) win[k][v] = 0.0f;
+            }
+        }
+        const uint16_t *xp = x.p + b * x.b + h * x.h, *gp = gy.p + b * gy.b + h * gy.h;
 
-    // gx of row t = i-W+1 from g of rows t..i (g[0] the oldest)
-    auto emit = [&](int64_t i) {
-        const int64_t t = i - (W - 1);
-        float o[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            o[v] = 0.0f;
-#pragma unroll
-            for (int k = 0; k < W; ++k) o[v] = __builtin_fmaf(g[k][v], w[W - 1 - k][v], o[v]);
-        }
-        // the last W-1 rows before the length are the final state
-        if (W > 1 && gfinal && t < len && t >= len - (W - 1)) {
-            float f[V];
-            widen<DT, V>(load<V>(gfinal + (t - len + (W - 1)) * BH + at), f);
-#pragma unroll
-            for (int v = 0; v < V; ++v) o[v] += f[v];
-        }
-        if (t >= t0)
-            store<V>(gx + t * BH + at, narrow<DT, V>(o));
-        else if (W > 1 && t < 0 && gstate)
-            store<V>(gstate + (t + W - 1) * BH + at, narrow<DT, V>(o));
-    };
-    auto shift = [&]() {
-#pragma unroll
-        for (int k = 0; k < W - 1; ++k)
+        // gx of row t = i-W+1 from g of rows t..i (g[0] the oldest)
+        auto emit = [&](int64_t i) {
+            const int64_t t = i - (W - 1);
+            float o[V];
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                win[k][v] = win[k + 1][v];
-                g[k][v] = g[k + 1][v];
+                o[v] = 0.0f;
+#pragma unroll
+                for (int k = 0; k < W; ++k) o[v] = __builtin_fmaf(g[k][v], w[W - 1 - k][v], o[v]);
             }
-    };
-    auto row = [&](const vec qx, const vec qg, bool mine) {
-        widen<DT, V>(qx, win[W - 1]);
-        widen<DT, V>(qg, g[W - 1]);
+            // the last W-1 rows before the length are the final state
+            if (W > 1 && gfinal && t < len && t >= len - (W - 1)) {
+                float f[V];
+                widen<DT, V>(load<V>(gfinal + (t - len + (W - 1)) * BH + at), f);
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            if (SILU) {
-                float pre = bv[v];
-#pragma unroll
-                for (int k = 0; k < W; ++k) pre = __builtin_fmaf(w[k][v], win[k][v], pre);
-                g[W - 1][v] *= silu_slope_f(pre);
+                for (int v = 0; v < V; ++v) o[v] += f[v];
             }
-            if (mine) {
-                gb[v] += g[W - 1][v];
+            if (t >= t0)
+                store<V>(gx + t * BH + at, narrow<DT, V>(o));
+            else if (W > 1 && t < 0 && gstate)
+                store<V>(gstate + (t + W - 1) * BH + at, narrow<DT, V>(o));
+        };
+        auto shift = [&]() {
 #pragma unroll
-                for (int k = 0; k < W; ++k)
-                    gw[k][v] = __builtin_fmaf(g[W - 1][v], win[k][v], gw[k][v]);
-            }
-        }
-    };
-    int64_t i = t0;
-    const int64_t end = len < t1 ? len : t1;
-    vec nx[kBwdBatch], ng[kBwdBatch];
-    if (i < end) {
-        auto fetch = [&](int64_t from) {
+            for (int k = 0; k < W - 1; ++k)
 #pragma unroll
-            for (int r = 0; r < kBwdBatch; ++r) {
-                const int64_t t = from + r < end ? from + r : end - 1;
-                nx[r] = load<V>(xp + t * x.s);
-                ng[r] = load<V>(gp + t * gy.s);
+                for (int v = 0; v < V; ++v) {
+                    win[k][v] = win[k + 1][v];
+                    g[k][v] = g[k + 1][v];
+                }
+        };
+        auto row = [&](const vec qx, const vec qg, bool mine) {
+            widen<DT, V>(qx, win[W - 1]);
+            widen<DT, V>(qg, g[W - 1]);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                if (SILU) {
+                    float pre = bv[v];
+#pragma unroll
+                    for (int k = 0; k < W; ++k) pre = __builtin_fmaf(w[k][v], win[k][v], pre);
+                    g[W - 1][v] *= silu_slope_f(pre);
+                }
+                if (mine) {
+                    gb[v] += g[W - 1][v];
+#pragma unroll
+                    for (int k = 0; k < W; ++k)
+                        gw[k][v] = __builtin_fmaf(g[W - 1][v], win[k][v], gw[k][v]);
+                }
             }
         };
-        fetch(i);
-        while (i + kBwdBatch <= end) {
-            vec cx[kBwdBatch], cg[kBwdBatch];
+        int64_t i = t0;
+        const int64_t end = len < t1 ? len : t1;
+        vec nx[kBwdBatch], ng[kBwdBatch];
+        if (i < end) {
+            auto fetch = [&](int64_t from) {
 #pragma unroll
-            for (int r = 0; r < kBwdBatch; ++r) cx[r] = nx[r], cg[r] = ng[r];
-            fetch(i + kBwdBatch);
+                for (int r = 0; r < kBwdBatch; ++r) {
+                    const int64_t t = from + r < end ? from + r : end - 1;
+                    nx[r] = load<V>(xp + t * x.s);
+                    ng[r] = load<V>(gp + t * gy.s);
+                }
+            };
+            fetch(i);
+            while (i + kBwdBatch <= end) {
+                vec cx[kBwdBatch], cg[kBwdBatch];
 #pragma unroll
-            for (int r = 0; r < kBwdBatch; ++r) {
-                row(cx[r], cg[r], true);
-                emit(i + r);
-                shift();
+                for (int r = 0; r < kBwdBatch; ++r) cx[r] = nx[r], cg[r] = ng[r];
+                fetch(i + kBwdBatch);
+#pragma unroll
+                for (int r = 0; r < kBwdBatch; ++r) {
+                    row(cx[r], cg[r], true);
+                    emit(i + r);
+                    shift();
+                }
+                i += kBwdBatch;
             }
-            i += kBwdBatch;
-        }
 #pragma unroll
-        for (int r = 0; r < kBwdBatch - 1; ++r)
-            if (i < end) {
-                row(nx[r], ng[r], true);
-                emit(i);
-                shift();
-                ++i;
+            for (int r = 0; r < kBwdBatch - 1; ++r)
+                if (i < end) {
+                    row(nx[r], ng[r], true);
+                    emit(i);
+                    shift();
+                    ++i;
+                }
+        }
+        // rows after the strip that are still live, then rows past the length
+        for (; i < t1 + (W - 1); ++i) {
+            if (i >= t1 && i < len) {
+                row(load<V>(xp + i * x.s), load<V>(gp + i * gy.s), false);
+            } else {
+#pragma unroll
+                for (int v = 0; v < V; ++v) g[W - 1][v] = win[W - 1][v] = 0.0f;
             }
-    }
-    // rows after the strip that are still live, then rows past the length
-    for (; i < t1 + (W - 1); ++i) {
-        if (i >= t1 && i < len) {
-            row(load<V>(xp + i * x.s), load<V>(gp + i * gy.s), false);
-        } else {
-#pragma unroll
-            for (int v = 0; v < V; ++v) g[W - 1][v] = win[W - 1][v] = 0.0f;
+            emit(i);
+            shift();
         }
-        emit(i);
-        shift();
     }
-    float *pp = partial + ((int64_t)blockIdx.y * B + b) * (W + 1) * H + h;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
 #pragma unroll
-        for (int k = 0; k < W; ++k) pp[k * H + v] = gw[k][v];
-        pp[W * H + v] = gb[v];
+        for (int k = 0; k < W; ++k) part[wave][k * V + v][lane] = gw[k][v];
+        part[wave][W * V + v][lane] = gb[v];
+    }
+    __syncthreads();
+    if (!on) return;
+    float *pp = partial + ((int64_t)blockIdx.y * B + b) * (W + 1) * H + h;
+#pragma unroll
+    for (int i = wave; i < (W + 1) * V; i += kWaves) {
+        float f = 0.0f;
+#pragma unroll
+        for (int q = 0; q < kWaves; ++q) f += part[q][i][lane];
+        pp[i / V * H + i % V] = f;
     }
 }
 
@@ -388,11 +412,11 @@ struct Strips {
     int64_t rows, n;
 };
 
-// Rows of a strip: whole batches of loads, as long as leaves 2048 blocks (8 per compute unit),
-// within [lo, hi]: a strip reads W-1 rows of its neighbour again.
+// Rows of a strip: whole batches of loads, as long as leaves 8192 waves (8 a SIMD), within [lo, hi]: a
+// strip reads W-1 rows of its neighbours again.
 Strips strips(int64_t S, int64_t lanes, int64_t lo, int64_t hi) {
-    const int64_t across = (lanes + kThreads - 1) / kThreads;
-    int64_t rows = S * across / 2048 / lo * lo;
+    const int64_t across = (lanes + kWave - 1) / kWave;
+    int64_t rows = S * across / 8192 / 4 * 4;
     rows = rows < lo ? lo : rows > hi ? hi : rows;
     while ((S + rows - 1) / rows > 65535) rows *= 2;
     return {rows, (S + rows - 1) / rows};
@@ -433,8 +457,11 @@ int check_conv_inputs(const mccb_conv_t *a, Span *in, int *n) {
 
 Rows rows_of(const void *p, const int64_t *st) { return {(const uint16_t *)p, st[0], st[1], st[2]}; }
 
+// Of the backward, n counts blocks of four strips.
 Strips bwd_strips(const mccb_conv_t *a) {
-    return strips(a->S > 0 ? a->S : 1, a->B * lanes_of(a->H, kBwdVec), 32, 128);
+    Strips s = strips(a->S > 0 ? a->S : 1, a->B * lanes_of(a->H, kBwdVec), 8, 64);
+    s.n = (s.n + kThreads / kWave - 1) / (kThreads / kWave);
+    return s;
 }
 
 template <typename F>
@@ -463,7 +490,7 @@ int by_form(const mccb_conv_t *a, F f) {
 template <int V>
 int launch_fwd(const mccb_conv_t *a, void *y, void *final_state, hipStream_t st) {
     const int64_t per = lanes_of(a->H, V), lanes = a->B * per;
-    const Strips s = strips(a->S > 0 ? a->S : 1, lanes, 16, 64);
+    const Strips s = strips(a->S > 0 ? a->S : 1, lanes, 8, 16);
     const dim3 grid((unsigned)((lanes + kThreads - 1) / kThreads), (unsigned)s.n);
     return by_form(a, [&](auto dt, auto w, auto silu) {
         hipLaunchKernelGGL((conv_act_fwd<decltype(dt)::value, decltype(w)::value,
@@ -480,7 +507,7 @@ template <int V>
 int launch_bwd(const mccb_conv_t *a, const void *gy, const int64_t *gs, const void *gfinal, void *gx,
                void *gstate, float *partial, const Strips &s, hipStream_t st) {
     const int64_t per = lanes_of(a->H, V), lanes = a->B * per;
-    const dim3 grid((unsigned)((lanes + kThreads - 1) / kThreads), (unsigned)s.n);
+    const dim3 grid((unsigned)((lanes + kWave - 1) / kWave), (unsigned)s.n);
     return by_form(a, [&](auto dt, auto w, auto silu) {
         hipLaunchKernelGGL((conv_act_bwd<decltype(dt)::value, decltype(w)::value,
                                          decltype(silu)::value, V>),
