@@ -20,6 +20,8 @@
 // dimension contiguous; those are transposed into the workspace first.
 #include "ssm_common.h"
 
+#include <type_traits>
+
 using namespace ssm;
 
 namespace {
@@ -67,38 +69,37 @@ __device__ static inline void act8(float (&v)[8]) {
     for (int i = 0; i < 8; ++i) v[i] = act_f(v[i], ACT);
 }
 
-// Eight adjacent columns of row m from column n (`count` of them inside the matrix).
+// Eight adjacent values, `count` of them inside the matrix, the others 0.
 template <int DT>
-__device__ static inline void finish8(const Epilogue &e, int64_t m, int64_t n, int count, float (&v)[8]) {
-    typedef HVec<8>::t vec;
-    auto get = [&](const uint16_t *p, float (&f)[8]) {
-        if (count == 8) {
-            const vec q = *(const vec *)p;
+__device__ static inline void get8(const uint16_t *p, int count, float (&f)[8]) {
+    if (count == 8) {
+        const HVec<8>::t q = *(const HVec<8>::t *)p;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] = to_f32<DT>(q[i]);
-        } else {
+        for (int i = 0; i < 8; ++i) f[i] = to_f32<DT>(q[i]);
+    } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] = i < count ? to_f32<DT>(p[i]) : 0.0f;
-        }
-    };
+        for (int i = 0; i < 8; ++i) f[i] = i < count ? to_f32<DT>(p[i]) : 0.0f;
+    }
+}
+
+// The sums v of eight adjacent columns of row m from column n, with the bias and the residual there.
+template <int DT>
+__device__ static inline void finish8(const Epilogue &e, int64_t m, int64_t n, int count, float (&v)[8],
+                                      const float (&bias)[8], const float (&residual)[8]) {
     auto put = [&](uint16_t *p) {
         if (count == 8) {
-            vec q;
+            HVec<8>::t q;
 #pragma unroll
             for (int i = 0; i < 8; ++i) q[i] = from_f32<DT>(v[i]);
-            *(vec *)p = q;
+            *(HVec<8>::t *)p = q;
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 if (i < count) p[i] = from_f32<DT>(v[i]);
         }
     };
-    float f[8];
-    if (e.bias) {
-        get(e.bias + n, f);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] += f[i];
-    }
+    for (int i = 0; i < 8; ++i) v[i] += bias[i];
     if (e.pre) put(e.pre + m * e.N + n);
     switch (e.act) {
         case MCCB_ACT_RELU: act8<MCCB_ACT_RELU>(v); break;
@@ -108,11 +109,17 @@ __device__ static inline void finish8(const Epilogue &e, int64_t m, int64_t n, i
         default: break;
     }
     if (e.residual) {
-        get(e.residual + m * e.residual_ld + n, f);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] += f[i];
+        for (int i = 0; i < 8; ++i) v[i] += residual[i];
     }
     put(e.out + m * e.N + n);
+}
+template <int DT>
+__device__ static inline void finish8(const Epilogue &e, int64_t m, int64_t n, int count, float (&v)[8]) {
+    float bias[8] = {}, residual[8] = {};
+    if (e.bias) get8<DT>(e.bias + n, count, bias);
+    if (e.residual) get8<DT>(e.residual + m * e.residual_ld + n, count, residual);
+    finish8<DT>(e, m, n, count, v, bias, residual);
 }
 
 // Two operands whose rows run along the contraction: P [M,K] and Q [N,K].
@@ -146,11 +153,13 @@ __global__ void __launch_bounds__(WM *WN *kWave)
     constexpr int TM = BM / WM / 32, TN = BN / WN / 32;      // a wave's 32x32 tiles
     constexpr int kRows = BM + BN, kLoads = kRows / 8 / kWaves;  // a wave's load takes 8 rows
     constexpr int kBuf = kRows * kBK;                        // 16-bit values of a buffer
-    // Tiles with a compute unit to themselves, and registers for it: the next operands are read while
-    // this one's products run, and the next step's loads go out behind the first products, not
-    // before them (M=4096 K=4096 N=8192: 254 us without, 241 with). The others have more waves to
-    // fill such gaps, or (256x320) no registers left.
-    constexpr bool kPipe = kWaves == 8 && TM * TN <= 8;
+    // Tiles with a compute unit to themselves read the next operands while this one's products run,
+    // over the step's end too: the one barrier of a step stands before its last products, whose
+    // operands are in registers by then, and the loads of the step after the next go out behind them,
+    // into the buffer that came free (M=4096 K=4096 N=8192: 254 us without; 241 with the barrier
+    // first; 227; 233 with each load behind two products). The others have more waves to fill such
+    // gaps, or (256x320 through registers) no registers left.
+    constexpr bool kPipe = kWaves == 8 && (DIRECT || TM * TN <= 8);
     constexpr int kStage = BN + 4;                           // fp32 row of the epilogue's staging
     constexpr int kRound = BM / WM;                          // rows it stages at a time
     constexpr size_t kBytes = sizeof(uint16_t) * 2 * kBuf > sizeof(float) * kRound * kStage
@@ -190,15 +199,19 @@ __global__ void __launch_bounds__(WM *WN *kWave)
         const int group = i < kLoadsP ? i * kWaves + wave : BM / 8 + (i - kLoadsP) * kWaves + wave;
         return lds + buf * kBuf + group * 8 * kBK;
     };
-    auto fill = [&](int step, int buf) {  // straight to LDS
-        const int64_t k = (int64_t)step * kBK;
-        const uint8_t *ps = p0 + k * 2, *qs = q0 + k * 2;
-        if (k + kBK <= g.K) {
+    auto fill_whole = [&](int step, int buf) {  // straight to LDS, 64 of the contraction
+        const uint8_t *ps = p0 + (int64_t)step * kBK * 2, *qs = q0 + (int64_t)step * kBK * 2;
 #pragma unroll
-            for (int i = 0; i < kLoads; ++i)
-                __builtin_amdgcn_global_load_lds((gmem *)lane_at(i < kLoadsP ? ps : qs, at[i]),
-                                                 (lmem *)place_of(i, buf), 16, 0, 0);
+        for (int i = 0; i < kLoads; ++i)
+            __builtin_amdgcn_global_load_lds((gmem *)lane_at(i < kLoadsP ? ps : qs, at[i]),
+                                             (lmem *)place_of(i, buf), 16, 0, 0);
+    };
+    auto fill = [&](int step, int buf) {  // or what is left of it, and zeros
+        const int64_t k = (int64_t)step * kBK;
+        if (k + kBK <= g.K) {
+            fill_whole(step, buf);
         } else {
+            const uint8_t *ps = p0 + k * 2, *qs = q0 + k * 2;
             const bool past = k + chunk * 8 >= g.K;
 #pragma unroll
             for (int i = 0; i < kLoads; ++i) {
@@ -243,65 +256,109 @@ __global__ void __launch_bounds__(WM *WN *kWave)
 #pragma unroll
             for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
 
+    // The operands of 16 of the contraction, and their products.
+    u16x8 a[kPipe ? 2 : 1][TN], b[kPipe ? 2 : 1][TM];
+    auto operands = [&](int buf, int ks, int to) {
+        const uint16_t *base = lds + buf * kBuf;
+        const int c = (ks * 2 + lane / 32) ^ (lane / 2 % 8);  // rows below are lane % 32 modulo 32
+#pragma unroll
+        for (int i = 0; i < TN; ++i) {
+            const int r = BM + (wn * TN + i) * 32 + lane % 32;
+            a[to][i] = *(const u16x8 *)(base + r * kBK + c * 8);
+        }
+#pragma unroll
+        for (int j = 0; j < TM; ++j) {
+            const int r = (wm * TM + j) * 32 + lane % 32;
+            b[to][j] = *(const u16x8 *)(base + r * kBK + c * 8);
+        }
+    };
+    auto multiply = [&](int from) {
+#pragma unroll
+        for (int i = 0; i < TN; ++i)
+#pragma unroll
+            for (int j = 0; j < TM; ++j) acc[i][j] = mfma32<DT>(a[from][i], b[from][j], acc[i][j]);
+    };
+    auto landed = [&] {  // this wave's loads, and every wave is here
+        __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
+        __syncthreads();
+    };
     if (DIRECT) {
         fill(s0, 0);
     } else {
         take(s0);
         put(0);
     }
-    for (int s = s0; s < s1; ++s) {
-        const int buf = (s - s0) & 1;
-        // this step's loads have landed, and every wave is done with the other buffer
-        __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
-        __syncthreads();
-        const uint16_t *base = lds + buf * kBuf;
-        // The operands of 16 of the contraction, and their products.
-        u16x8 a[kPipe ? 2 : 1][TN], b[kPipe ? 2 : 1][TM];
-        auto operands = [&](int ks, int to) {
-            const int c = (ks * 2 + lane / 32) ^ (lane / 2 % 8);  // rows below are lane % 32 modulo 32
-#pragma unroll
-            for (int i = 0; i < TN; ++i) {
-                const int r = BM + (wn * TN + i) * 32 + lane % 32;
-                a[to][i] = *(const u16x8 *)(base + r * kBK + c * 8);
-            }
-#pragma unroll
-            for (int j = 0; j < TM; ++j) {
-                const int r = (wm * TM + j) * 32 + lane % 32;
-                b[to][j] = *(const u16x8 *)(base + r * kBK + c * 8);
-            }
+    if constexpr (kPipe) {
+        auto next = [&](int step, int buf) { DIRECT ? fill(step, buf) : take(step); };
+        // products from operands `from`, the reads of the next operands behind the first of them
+        auto first = [&](int from) {
+            acc[0][0] = mfma32<DT>(a[from][0], b[from][0], acc[0][0]);
+            __builtin_amdgcn_sched_barrier(0);
         };
-        auto multiply = [&](int from) {
+        auto rest = [&](int from) {
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int i = 0; i < TN; ++i)
 #pragma unroll
-                for (int j = 0; j < TM; ++j) acc[i][j] = mfma32<DT>(a[from][i], b[from][j], acc[i][j]);
+                for (int j = i == 0 ? 1 : 0; j < TM; ++j)
+                    acc[i][j] = mfma32<DT>(a[from][i], b[from][j], acc[i][j]);
+            __builtin_amdgcn_sched_barrier(0);
         };
-        if (!DIRECT && s + 1 < s1) take(s + 1);
-        if (kPipe) {
-            operands(0, 0);
+        constexpr int kLast = kBK / 16 - 1;
+        landed();
+        operands(0, 0, 0);
+        if (s0 + 1 < s1) next(s0 + 1, 1);
+        for (int s = s0; s < s1; ++s) {
+            const int buf = (s - s0) & 1;
 #pragma unroll
-            for (int ks = 0; ks < kBK / 16; ++ks) {
-                if (ks + 1 < kBK / 16) operands(ks + 1, (ks + 1) & 1);
-                __builtin_amdgcn_sched_barrier(0);
-                multiply(ks & 1);
-                __builtin_amdgcn_sched_barrier(0);
-                if (DIRECT && ks == 0 && s + 1 < s1) fill(s + 1, buf ^ 1);
+            for (int ks = 0; ks < kLast; ++ks) {
+                first(ks & 1);
+                operands(buf, ks + 1, (ks + 1) & 1);
+                rest(ks & 1);
             }
-        } else {
-            if (DIRECT && s + 1 < s1) fill(s + 1, buf ^ 1);
+            if (!DIRECT && s + 1 < s1) put(buf ^ 1);
+            landed();
+            first(kLast & 1);
+            operands(buf ^ 1, 0, 0);  // behind the last step nothing that is used
+            rest(kLast & 1);
+            if (s + 2 < s1) next(s + 2, buf);
+        }
+    } else {
+        for (int s = s0; s < s1; ++s) {
+            const int buf = (s - s0) & 1;
+            landed();
+            if (s + 1 < s1) DIRECT ? fill(s + 1, buf ^ 1) : take(s + 1);
 #pragma unroll
             for (int ks = 0; ks < kBK / 16; ++ks) {
-                operands(ks, 0);
+                operands(buf, ks, 0);
                 multiply(0);
             }
+            if (!DIRECT && s + 1 < s1) put(buf ^ 1);
         }
-        if (!DIRECT && s + 1 < s1) put(buf ^ 1);
     }
     // Epilogue, kRound rows at a time. A lane's 16 sums of a 32x32 tile are column lane % 32 (a row
     // of P) and rows 8 (v / 4) + 4 (lane / 32) + v % 4 (rows of Q, columns of the output).
+    // The rows of the residual are on their way while the sums are staged (M=16384 K=2048 N=2048 with
+    // bias, relu and residual: 141 us read where they are added, 130).
     float *stage = (float *)smem;
+    constexpr int kAcross = BN / 8, kDown = kThreads / kAcross, kTimes = (kRound + kDown - 1) / kDown;
+    const int n = threadIdx.x % kAcross * 8;
+    const int64_t left = g.N - n0 - n;
+    const int count = left < 8 ? (int)left : 8;
+    float bias[8] = {};
+    if (e.bias && left > 0) get8<DT>(e.bias + n0 + n, count, bias);
 #pragma unroll
     for (int round = 0; round < WM; ++round) {
+        const int64_t m1 = m0 + round * kRound;
+        u16x8 rows[kTimes];
+        const bool ahead = e.residual && !g.partial && left >= 8;
+        if (ahead) {
+#pragma unroll
+            for (int t = 0; t < kTimes; ++t) {
+                const int64_t m = m1 + threadIdx.x / kAcross + t * kDown;
+                rows[t] = *(const HVec<8>::t *)(e.residual + (m < g.M ? m : g.M - 1) * e.residual_ld + n0 + n);
+            }
+        }
         __syncthreads();
         if (wm == round) {
 #pragma unroll
@@ -310,35 +367,39 @@ __global__ void __launch_bounds__(WM *WN *kWave)
                 for (int j = 0; j < TM; ++j)
 #pragma unroll
                     for (int v = 0; v < 4; ++v) {
-                        const int m = j * 32 + lane % 32;
-                        const int n = (wn * TN + i) * 32 + 8 * v + 4 * (lane / 32);
-                        *(f32x4 *)(stage + m * kStage + n) =
+                        const int row = j * 32 + lane % 32;
+                        const int at_n = (wn * TN + i) * 32 + 8 * v + 4 * (lane / 32);
+                        *(f32x4 *)(stage + row * kStage + at_n) =
                             f32x4{acc[i][j][4 * v], acc[i][j][4 * v + 1], acc[i][j][4 * v + 2],
                                   acc[i][j][4 * v + 3]};
                     }
         }
         __syncthreads();
-        constexpr int kAcross = BN / 8, kDown = kThreads / kAcross;
-        const int n = threadIdx.x % kAcross * 8;
-        const int64_t left = g.N - n0 - n;
         if (left <= 0) continue;
-        for (int r = threadIdx.x / kAcross; r < kRound; r += kDown) {
-            const int64_t m = m0 + round * kRound + r;
-            if (m >= g.M) break;
-            float v[8];
+#pragma unroll
+        for (int t = 0; t < kTimes; ++t) {
+            const int r = threadIdx.x / kAcross + t * kDown;
+            const int64_t m = m1 + r;
+            if (r >= kRound || m >= g.M) break;
+            float v[8], residual[8] = {};
             const f32x4 lo = *(const f32x4 *)(stage + r * kStage + n);
             const f32x4 hi = *(const f32x4 *)(stage + r * kStage + n + 4);
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[i] = lo[i], v[4 + i] = hi[i];
-            const int count = left < 8 ? (int)left : 8;
             if (g.partial) {
                 float *q = g.partial + ((int64_t)blockIdx.y * g.M + m) * g.N + n0 + n;
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                     if (i < count) q[i] = v[i];
-            } else {
-                finish8<DT>(e, m, n0 + n, count, v);
+                continue;
             }
+            if (ahead) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) residual[i] = to_f32<DT>(rows[t][i]);
+            } else if (e.residual) {
+                get8<DT>(e.residual + m * e.residual_ld + n0 + n, count, residual);
+            }
+            finish8<DT>(e, m, n0 + n, count, v, bias, residual);
         }
     }
 }
@@ -566,8 +627,8 @@ struct Tile {
     // of several (the smaller tiles'), measured with bf16 over M, N, K from 64 to 16384
     double alone, shared;
 };
-constexpr Tile kTiles[kForms] = {{0, 0, 0, 0},           {256, 256, 4200, 4200}, {256, 320, 4700, 4700},
-                                 {256, 192, 3100, 3100}, {128, 128, 1900, 1350}, {64, 64, 900, 440}};
+constexpr Tile kTiles[kForms] = {{0, 0, 0, 0},           {256, 256, 4100, 4100}, {256, 320, 4570, 4570},
+                                 {256, 192, 2930, 2930}, {128, 128, 1900, 1350}, {64, 64, 900, 440}};
 
 struct Cut {
     int form, splits, steps_per_split;
