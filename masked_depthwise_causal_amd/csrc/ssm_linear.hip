@@ -4,8 +4,7 @@
 //   out[m,n] = act(sum_k x[m,k] w[n,k] + bias[n]) + residual[m,n]
 //   g = gout act'(pre),  gx[m,k] = sum_n g[m,n] w[n,k],  gw[n,k] = sum_m g[m,n] x[m,k]
 //
-// Three kernels carry the products, all of the form C = P Q^T with both operands' rows contiguous
-// along the contraction:
+// Two kernels carry the products, all of the form C = P Q^T:
 //   tiles   (M above 64): a block computes a BM x BN tile with 32x32x16 matrix instructions from two
 //           LDS buffers that are filled by loads straight to LDS, 64 of the contraction at a time.
 //           Few tiles and a long contraction: the contraction is split over blocks, which leave fp32
@@ -16,8 +15,10 @@
 // and written as whole rows.
 //
 // Operands that the direct-to-LDS loads cannot take (rows not 16-byte aligned) go through registers
-// instead, by loads that may start at any element. The backward needs w, x and g with the other
-// dimension contiguous; those are transposed into the workspace first.
+// instead, by loads that may start at any element. In the backward w, and g and x for gw, lie the other
+// way round, with rows across the contraction; the tiles turn them as they read LDS. Only rows that are
+// not aligned, and the skinny products, have them transposed into the workspace first (M=4096 K=5120
+// N=4096, silu: 364 us with that, 335 without; M=1024 K=512 N=768: 34.6 and 25.0).
 #include "ssm_common.h"
 
 #include <type_traits>
@@ -122,7 +123,7 @@ __device__ static inline void finish8(const Epilogue &e, int64_t m, int64_t n, i
     finish8<DT>(e, m, n, count, v, bias, residual);
 }
 
-// Two operands whose rows run along the contraction: P [M,K] and Q [N,K].
+// Operands as P [M,K] and Q [N,K]; an operand that lies the other way is [K,M] or [K,N].
 struct Product {
     const uint16_t *p, *q;
     int64_t p_ld, q_ld;
@@ -145,8 +146,23 @@ __device__ static inline void tile_of(const Product &g, int &tm, int &tn) {
     tn = r / rows;
 }
 
-// DIRECT: both operands' rows are 16-byte aligned whole chunks.
-template <int DT, int BM, int BN, int WM, int WN, bool DIRECT>
+// Lane l's operand of 32x32x16 products, eight of the contraction from 8 (l / 32) of row l % 32, from LDS
+// where the contraction's rows are `columns` apart. In each read a group of 16 lanes takes 16 columns of
+// four rows, lane i the columns 4 (i % 4) .. + 3 of row i / 4, and gets column i of the four. (Without
+// __restrict__, which holds until the barrier that lets the buffer be filled again, the compiler has every
+// such read wait for all loads to LDS, the next step's too: backward of
+// M=4096 K=4096 N=8192 578 us, 530 with.)
+__device__ static inline u16x8 turned(const uint16_t *__restrict__ p, int columns) {
+    typedef short s16x4 __attribute__((ext_vector_type(4)));
+    typedef __attribute__((address_space(3))) s16x4 lds4;
+    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)p);
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(p + 4 * columns));
+    return __builtin_bit_cast(u16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
+// DIRECT: both operands' rows are 16-byte aligned whole chunks. TP, TQ: that operand lies the other
+// way, its rows along M or N, and is turned on its way from LDS to the registers.
+template <int DT, int BM, int BN, int WM, int WN, bool DIRECT, bool TP, bool TQ>
 __global__ void __launch_bounds__(WM *WN *kWave)
     product_tiles(Product g, Epilogue e) {
     constexpr int kWaves = WM * WN, kThreads = kWaves * kWave;
@@ -158,8 +174,8 @@ __global__ void __launch_bounds__(WM *WN *kWave)
     // operands are in registers by then, and the loads of the step after the next go out behind them,
     // into the buffer that came free (M=4096 K=4096 N=8192: 254 us without; 241 with the barrier
     // first; 227; 233 with each load behind two products). The others have more waves to fill such
-    // gaps, or (256x320 through registers) no registers left.
-    constexpr bool kPipe = kWaves == 8 && (DIRECT || TM * TN <= 8);
+    // gaps, or (256x320 by way of registers or with operands turned) no registers left.
+    constexpr bool kPipe = kWaves == 8 && (TM * TN <= 8 || (DIRECT && !TQ));
     constexpr int kStage = BN + 4;                           // fp32 row of the epilogue's staging
     constexpr int kRound = BM / WM;                          // rows it stages at a time
     constexpr size_t kBytes = sizeof(uint16_t) * 2 * kBuf > sizeof(float) * kRound * kStage
@@ -182,15 +198,33 @@ __global__ void __launch_bounds__(WM *WN *kWave)
     // Q's, so that a wave's groups are all even or all odd. Rows past the matrix repeat its last row.
     constexpr int kLoadsP = BM / 8 / kWaves;
     static_assert(BM / 8 % kWaves == 0 && BN / 8 % kWaves == 0 && kWaves % 2 == 0, "whole groups");
+    static_assert(DIRECT || !(TP || TQ), "operands by way of registers are not turned");
     const int chunk = (lane % 8) ^ (lane / 16) ^ (wave % 2 * 4);
+    // An operand that lies the other way fills its part of the buffer with 64 rows of BM or BN columns,
+    // in the order of the loads. A read takes 64 bytes (32 columns) of four rows; those are moved by
+    // `apart`, so that the four meet different banks whether a row is a multiple of all banks or not.
+    auto apart = [](int row, int columns) { return columns % 128 == 0 ? row % 4 : row / 2 % 2; };
+    auto row_across = [&](int i) {
+        return (((i < kLoadsP ? i : i - kLoadsP) * kWaves + wave) * kWave + lane) /
+               ((i < kLoadsP ? BM : BN) / 8);
+    };
     uint32_t at[kLoads];  // bytes from the tile's first row of P or Q (DIRECT: below 2^32)
-    const uint8_t *p0 = (const uint8_t *)(g.p + m0 * g.p_ld), *q0 = (const uint8_t *)(g.q + n0 * g.q_ld);
+    const uint8_t *p0 = (const uint8_t *)(TP ? g.p + m0 : g.p + m0 * g.p_ld);
+    const uint8_t *q0 = (const uint8_t *)(TQ ? g.q + n0 : g.q + n0 * g.q_ld);
+    const int64_t p_step = (TP ? g.p_ld : 1) * kBK * 2, q_step = (TQ ? g.q_ld : 1) * kBK * 2;  // bytes
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
         const bool of_p = i < kLoadsP;
-        const int64_t r = ((of_p ? i : i - kLoadsP) * kWaves + wave) * 8 + lane / 8;
-        const int64_t left = of_p ? g.M - m0 : g.N - n0;
-        at[i] = (uint32_t)((r < left ? r : left - 1) * (of_p ? g.p_ld : g.q_ld) * 2 + chunk * 16);
+        const int64_t left = of_p ? g.M - m0 : g.N - n0, ld = of_p ? g.p_ld : g.q_ld;
+        if (of_p ? TP : TQ) {
+            const int across = (of_p ? BM : BN) / 8, r = row_across(i);
+            const int id = ((of_p ? i : i - kLoadsP) * kWaves + wave) * kWave + lane;
+            const int64_t c = ((id - r * across) ^ (apart(r, across * 8) * 4)) * 8;  // past: the last chunk
+            at[i] = (uint32_t)((r * ld + (c < left ? c : left - 8)) * 2);
+        } else {
+            const int64_t r = ((of_p ? i : i - kLoadsP) * kWaves + wave) * 8 + lane / 8;
+            at[i] = (uint32_t)((r < left ? r : left - 1) * ld * 2 + chunk * 16);
+        }
     }
     typedef __attribute__((address_space(1))) const uint32_t gmem;
     typedef __attribute__((address_space(3))) uint32_t lmem;
@@ -200,7 +234,7 @@ __global__ void __launch_bounds__(WM *WN *kWave)
         return lds + buf * kBuf + group * 8 * kBK;
     };
     auto fill_whole = [&](int step, int buf) {  // straight to LDS, 64 of the contraction
-        const uint8_t *ps = p0 + (int64_t)step * kBK * 2, *qs = q0 + (int64_t)step * kBK * 2;
+        const uint8_t *ps = p0 + step * p_step, *qs = q0 + step * q_step;
 #pragma unroll
         for (int i = 0; i < kLoads; ++i)
             __builtin_amdgcn_global_load_lds((gmem *)lane_at(i < kLoadsP ? ps : qs, at[i]),
@@ -211,10 +245,10 @@ __global__ void __launch_bounds__(WM *WN *kWave)
         if (k + kBK <= g.K) {
             fill_whole(step, buf);
         } else {
-            const uint8_t *ps = p0 + k * 2, *qs = q0 + k * 2;
-            const bool past = k + chunk * 8 >= g.K;
+            const uint8_t *ps = p0 + step * p_step, *qs = q0 + step * q_step;
 #pragma unroll
             for (int i = 0; i < kLoads; ++i) {
+                const bool past = k + ((i < kLoadsP ? TP : TQ) ? row_across(i) : chunk * 8) >= g.K;
                 const uint8_t *s = past ? (const uint8_t *)zero_chunk : (i < kLoadsP ? ps : qs) + at[i];
                 __builtin_amdgcn_global_load_lds((gmem *)s, (lmem *)place_of(i, buf), 16, 0, 0);
             }
@@ -258,18 +292,27 @@ __global__ void __launch_bounds__(WM *WN *kWave)
 
     // The operands of 16 of the contraction, and their products.
     u16x8 a[kPipe ? 2 : 1][TN], b[kPipe ? 2 : 1][TM];
+    // Where operands lie the other way: what `turned` reads first for this lane, of a tile's columns and 16
+    // of the contraction.
+    auto across = [&](int ks, int tile, int columns) {
+        const int r = lane % 16 / 4;
+        return (ks * 16 + lane / 32 * 8 + r) * columns + (tile ^ apart(r, columns)) * 32 +
+               lane / 16 % 2 * 16 + lane % 4 * 4;
+    };
     auto operands = [&](int buf, int ks, int to) {
         const uint16_t *base = lds + buf * kBuf;
         const int c = (ks * 2 + lane / 32) ^ (lane / 2 % 8);  // rows below are lane % 32 modulo 32
 #pragma unroll
         for (int i = 0; i < TN; ++i) {
             const int r = BM + (wn * TN + i) * 32 + lane % 32;
-            a[to][i] = *(const u16x8 *)(base + r * kBK + c * 8);
+            if constexpr (TQ) a[to][i] = turned(base + BM * kBK + across(ks, wn * TN + i, BN), BN);
+            else a[to][i] = *(const u16x8 *)(base + r * kBK + c * 8);
         }
 #pragma unroll
         for (int j = 0; j < TM; ++j) {
             const int r = (wm * TM + j) * 32 + lane % 32;
-            b[to][j] = *(const u16x8 *)(base + r * kBK + c * 8);
+            if constexpr (TP) b[to][j] = turned(base + across(ks, wm * TM + j, BM), BM);
+            else b[to][j] = *(const u16x8 *)(base + r * kBK + c * 8);
         }
     };
     auto multiply = [&](int from) {
@@ -615,8 +658,8 @@ int64_t up8(int64_t v) { return (v + 7) & ~(int64_t)7; }
 uint64_t area(int64_t rows, int64_t ld) { return align16((uint64_t)rows * (uint64_t)ld * 2); }
 
 // Rows that the loads straight to LDS can take: aligned chunks, a tile's rows within 32-bit offsets.
-bool direct_rows(const void *p, int64_t ld, int64_t K) {
-    return !misaligned(p, 16) && ld % 8 == 0 && K % 8 == 0 && ld <= (int64_t)1 << 22;
+bool direct_rows(const void *p, int64_t ld, int64_t along) {
+    return !misaligned(p, 16) && ld % 8 == 0 && along % 8 == 0 && ld <= (int64_t)1 << 22;
 }
 
 // How a product is cut; a function of its sizes alone.
@@ -663,24 +706,18 @@ Cut cut_of(int64_t M, int64_t N, int64_t K) {
     return best;
 }
 
-template <int DT, bool DIRECT>
+template <int DT, bool DIRECT, bool TP = false, bool TQ = false>
 void launch_tiles(const Cut &c, const Product &g, const Epilogue &e, hipStream_t st) {
     const dim3 grid((unsigned)(c.tiles_m * c.tiles_n), (unsigned)c.splits);
+    auto launch = [&](auto kernel, int threads) {
+        hipLaunchKernelGGL(kernel, grid, dim3(threads), 0, st, g, e);
+    };
     switch (c.form) {
-        case k256x256:
-            hipLaunchKernelGGL((product_tiles<DT, 256, 256, 2, 4, DIRECT>), grid, dim3(512), 0, st, g, e);
-            break;
-        case k256x320:
-            hipLaunchKernelGGL((product_tiles<DT, 256, 320, 4, 2, DIRECT>), grid, dim3(512), 0, st, g, e);
-            break;
-        case k256x192:
-            hipLaunchKernelGGL((product_tiles<DT, 256, 192, 4, 2, DIRECT>), grid, dim3(512), 0, st, g, e);
-            break;
-        case k128x128:
-            hipLaunchKernelGGL((product_tiles<DT, 128, 128, 2, 2, DIRECT>), grid, dim3(256), 0, st, g, e);
-            break;
-        default:
-            hipLaunchKernelGGL((product_tiles<DT, 64, 64, 2, 2, DIRECT>), grid, dim3(256), 0, st, g, e);
+        case k256x256: launch(product_tiles<DT, 256, 256, 2, 4, DIRECT, TP, TQ>, 512); break;
+        case k256x320: launch(product_tiles<DT, 256, 320, 4, 2, DIRECT, TP, TQ>, 512); break;
+        case k256x192: launch(product_tiles<DT, 256, 192, 4, 2, DIRECT, TP, TQ>, 512); break;
+        case k128x128: launch(product_tiles<DT, 128, 128, 2, 2, DIRECT, TP, TQ>, 256); break;
+        default: launch(product_tiles<DT, 64, 64, 2, 2, DIRECT, TP, TQ>, 256);
     }
 }
 
@@ -698,7 +735,8 @@ void launch_skinny(const Product &g, const Epilogue &e, hipStream_t st) {
 
 template <int DT>
 int launch_product(const uint16_t *p, int64_t p_ld, const uint16_t *q, int64_t q_ld, int64_t M,
-                   int64_t N, int64_t K, const Epilogue &e, void *partial, hipStream_t st) {
+                   int64_t N, int64_t K, const Epilogue &e, void *partial, hipStream_t st, bool tp = false,
+                   bool tq = false) {
     const Cut c = cut_of(M, N, K);
     Product g{p, q, p_ld, q_ld, M, N, K, (int)c.tiles_m, (int)c.tiles_n, c.splits, c.steps_per_split,
               c.splits > 1 ? (float *)partial : nullptr};
@@ -708,7 +746,9 @@ int launch_product(const uint16_t *p, int64_t p_ld, const uint16_t *q, int64_t q
         else launch_skinny<DT, 4>(g, e, st);
         return launched();
     }
-    if (direct_rows(p, p_ld, K) && direct_rows(q, q_ld, K)) launch_tiles<DT, true>(c, g, e, st);
+    if (tp) launch_tiles<DT, true, true, true>(c, g, e, st);
+    else if (tq) launch_tiles<DT, true, false, true>(c, g, e, st);
+    else if (direct_rows(p, p_ld, K) && direct_rows(q, q_ld, K)) launch_tiles<DT, true>(c, g, e, st);
     else launch_tiles<DT, false>(c, g, e, st);
     const int rc = launched();
     if (rc != MCCB_OK || c.splits == 1) return rc;
@@ -750,8 +790,9 @@ int check_linear_inputs(const mccb_linear_t *a, Span *in) {
     return MCCB_OK;
 }
 
-// The backward's: g by rows and by columns, x and w by columns, the column sums, and the larger of
-// the two products' partial sums.
+// The backward's: g by rows and by columns, x and w by columns (columns for products that do not read
+// them as they lie; the size is a matter of sizes alone, not of alignment), the column sums, and the
+// larger of the two products' partial sums.
 struct BwdLayout {
     uint64_t g_rows, g_cols, x_cols, w_cols, sums, partial, total;
 };
@@ -876,11 +917,15 @@ int mccb_linear_backward(const mccb_linear_t *a, const void *gout, int64_t gout_
     return by_dtype(a->dtype, [&](auto dt) {
         constexpr int DT = decltype(dt)::value;
         const bool slope = a->activation != MCCB_ACT_NONE;
-        // without an activation g is gradOut, which the first product can read where it is
+        // without an activation g is gradOut, which the products can read where it is
         const uint16_t *g = slope ? g_rows : (const uint16_t *)gout;
         const int64_t g_ld = slope ? Np : gout_ld;
-        const Turn tg{(const uint16_t *)gout, slope ? (const uint16_t *)pre : nullptr,
-                      gout_ld, a->M, a->N, gx && slope ? g_rows : nullptr, gw ? g_cols : nullptr,
+        const uint16_t *x = (const uint16_t *)a->x, *w = (const uint16_t *)a->weight;
+        // tiles read w, g and x as they lie; skinny products and unaligned rows need them turned
+        const bool w_lies = a->M > 64 && direct_rows(g, g_ld, a->N) && direct_rows(w, a->weight_ld, a->K);
+        const bool x_lies = a->N > 64 && direct_rows(g, g_ld, a->N) && direct_rows(x, a->x_ld, a->K);
+        const Turn tg{(const uint16_t *)gout, slope ? (const uint16_t *)pre : nullptr, gout_ld, a->M, a->N,
+                      slope && (gx || (gw && x_lies)) ? g_rows : nullptr, gw && !x_lies ? g_cols : nullptr,
                       gb ? sums : nullptr, Np, Mp, a->activation};
         int r = tg.rows || tg.columns || tg.sums ? launch_turn<DT>(tg, st) : MCCB_OK;
         if (r == MCCB_OK && gb) {
@@ -889,20 +934,21 @@ int mccb_linear_backward(const mccb_linear_t *a, const void *gout, int64_t gout_
             r = launched();
         }
         if (r == MCCB_OK && gx) {
-            const Turn tw{(const uint16_t *)a->weight, nullptr, a->weight_ld, a->N, a->K,
-                          nullptr, w_cols, nullptr, 0, Np, MCCB_ACT_NONE};
-            r = launch_turn<DT>(tw, st);
+            const Turn tw{w, nullptr, a->weight_ld, a->N, a->K, nullptr, w_cols, nullptr, 0, Np, MCCB_ACT_NONE};
+            if (!w_lies) r = launch_turn<DT>(tw, st);
             const Epilogue e{nullptr, nullptr, (uint16_t *)gx, nullptr, 0, a->K, MCCB_ACT_NONE};
             if (r == MCCB_OK)
-                r = launch_product<DT>(g, g_ld, w_cols, Np, a->M, a->K, a->N, e, at + l.partial, st);
+                r = launch_product<DT>(g, g_ld, w_lies ? w : w_cols, w_lies ? a->weight_ld : Np, a->M, a->K,
+                                       a->N, e, at + l.partial, st, false, w_lies);
         }
         if (r == MCCB_OK && gw) {
-            const Turn tx{(const uint16_t *)a->x, nullptr, a->x_ld, a->M, a->K,
-                          nullptr, x_cols, nullptr, 0, Mp, MCCB_ACT_NONE};
-            r = launch_turn<DT>(tx, st);
+            const Turn tx{x, nullptr, a->x_ld, a->M, a->K, nullptr, x_cols, nullptr, 0, Mp, MCCB_ACT_NONE};
+            if (!x_lies) r = launch_turn<DT>(tx, st);
             const Epilogue e{nullptr, nullptr, (uint16_t *)gw, nullptr, 0, a->K, MCCB_ACT_NONE};
             if (r == MCCB_OK)
-                r = launch_product<DT>(g_cols, Mp, x_cols, Mp, a->N, a->K, a->M, e, at + l.partial, st);
+                r = launch_product<DT>(x_lies ? g : g_cols, x_lies ? g_ld : Mp, x_lies ? x : x_cols,
+                                       x_lies ? a->x_ld : Mp, a->N, a->K, a->M, e, at + l.partial, st,
+                                       x_lies, x_lies);
         }
         return r;
     });

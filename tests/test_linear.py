@@ -90,6 +90,37 @@ def test_large_tiles(M, K, N, dtype):
     check(M, K, N, dtype, "silu", True, True, 0)
 
 
+@pytest.mark.parametrize("M,K,N,dtype,act", [
+    (100, 72, 88, "bf16", "gelu"), (100, 72, 88, "fp16", None),
+    (4001, 2040, 600, "bf16", "silu"),   # 128x128 tiles for gx,
+    (700, 2040, 4088, "fp16", "relu"),   # for gw
+    (3500, 3704, 200, "bf16", "silu"),   # 256x256
+    (200, 4088, 4088, "bf16", None),
+    (2040, 6136, 72, "fp16", "silu"),    # 256x192
+    (200, 6136, 2040, "bf16", "silu"),
+    (4090, 5112, 72, "bf16", "relu"),    # 256x320, and gw's contraction split
+    (201, 5112, 4088, "fp16", "silu"),
+])
+def test_backward_reads_operands_as_they_lie(M, K, N, dtype, act):
+    """Aligned rows, inside wider ones; every tile, its last ones and the contraction partial."""
+    g = torch.Generator().manual_seed(M + K + N)
+    dt = DT[dtype]
+    x, w, go = rand(g, M, K, dt=dt), rand(g, N, K, dt=dt, scale=K ** -0.5), rand(g, M, N, dt=dt)
+    pre = rand(g, M, N, dt=dt)
+    announce(f"linear backward M={M} K={K} N={N} {dtype} {act}")
+    dirty()
+    grads = mdc.linear_backward(wide(go, 16, 8), wide(x, 24, 16), wide(w, 16, 8),
+                                None if act is None else pre.cuda(), activation=act)
+    torch.cuda.synchronize()
+    x64, w64, p, go64 = x.to(F), w.to(F), pre.to(F), go.to(F)
+    gg = go64 * ref.act_slope(p, act)
+    gm = go64.abs() * (ref.act_slope(p, act).abs() + 2.0 ** -10 * (1 + p.abs()))
+    half = torch.finfo(dt).eps / 2 if act is not None else 0.0
+    ref.close(grads.x, (gg @ w64, gm @ w64.abs()), half + slack(N), "gx")
+    ref.close(grads.weight, (gg.t() @ x64, gm.t() @ x64.abs()), half + slack(M), "gw")
+    ref.close(grads.bias, (gg.sum(0), gm.sum(0)), slack(M), "gbias")
+
+
 def test_leading_dimensions_and_no_rows():
     g = torch.Generator().manual_seed(2)
     x, w, r = rand(g, 5, 3, 32).cuda(), rand(g, 24, 32).cuda(), rand(g, 5, 3, 24).cuda()
