@@ -484,6 +484,13 @@ __global__ void __launch_bounds__(WAVES *kWave)
         const int64_t m = b * 16 + lane % 16;
         pp[b] = g.p + (m < g.M ? m : g.M - 1) * g.p_ld;
     }
+    // Eight sums go to a thread at the end; its bias and residual are on their way from the start.
+    static_assert(MB * 16 * 2 <= WAVES * kWave, "a thread for every eight sums");
+    const int64_t own_m = threadIdx.x / 2, own_n = n0 + threadIdx.x % 2 * 8, left = g.N - own_n;
+    const bool sums = threadIdx.x < MB * 16 * 2 && own_m < g.M && left > 0, ahead = sums && left >= 8;
+    u16x8 bias8 = {}, residual8 = {};
+    if (ahead && e.bias) bias8 = *(const HVec<8>::t *)(e.bias + own_n);
+    if (ahead && e.residual) residual8 = *(const HVec<8>::t *)(e.residual + own_m * e.residual_ld + own_n);
     f32x4 acc[MB];
 #pragma unroll
     for (int b = 0; b < MB; ++b) acc[b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -533,16 +540,21 @@ __global__ void __launch_bounds__(WAVES *kWave)
     for (int b = 0; b < MB; ++b)
         *(f32x4 *)&part[wave][b * 16 + lane % 16][lane / 16 * 4] = acc[b];
     __syncthreads();
-    for (int id = threadIdx.x; id < MB * 16 * 2; id += WAVES * kWave) {
-        const int64_t m = id / 2, c = id % 2 * 8, left = g.N - n0 - c;
-        if (m >= g.M || left <= 0) continue;
-        float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    if (!sums) return;
+    float v[8] = {}, bias[8] = {}, residual[8] = {};
+    // not unrolled whole: that many sums on their way take registers which spill
+#pragma unroll 4
+    for (int w = 0; w < WAVES; ++w)
 #pragma unroll
-        for (int w = 0; w < WAVES; ++w)
+        for (int i = 0; i < 8; ++i) v[i] += part[w][own_m][threadIdx.x % 2 * 8 + i];
+    if (ahead) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] += part[w][m][c + i];
-        finish8<DT>(e, m, n0 + c, left < 8 ? (int)left : 8, v);
+        for (int i = 0; i < 8; ++i) bias[i] = to_f32<DT>(bias8[i]), residual[i] = to_f32<DT>(residual8[i]);
+    } else {
+        if (e.bias) get8<DT>(e.bias + own_n, (int)left, bias);
+        if (e.residual) get8<DT>(e.residual + own_m * e.residual_ld + own_n, (int)left, residual);
     }
+    finish8<DT>(e, own_m, own_n, left < 8 ? (int)left : 8, v, bias, residual);
 }
 
 // ---------------------------------------------------------------------------------------------
