@@ -7,6 +7,9 @@
 //
 // Rows x[-W+1..-1] come from the carried state. All three kernels are bound by HBM: a row element
 // is read once and written once (backward: two read, one written) for about 20 lane operations.
+// S=4096 B=4 H=4096 bf16, W=4 with silu: forward 53 us (5.0 TB/s), backward 101 us (4.0 TB/s) and 5 for
+// the partial sums of gw and gbias; a large copy reaches 4.8 TB/s. The single token (B=8 H=5120) is 3 us,
+// a launch's own time.
 // A lane owns V adjacent channels of one batch and walks down a strip of rows, with the last W-1
 // rows in registers; the next rows' loads are in flight while it computes. Channels have no
 // alignment to keep (loads of 16-bit vectors may start at any element), and where V does not

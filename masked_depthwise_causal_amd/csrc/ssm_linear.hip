@@ -8,9 +8,11 @@
 //   tiles   (M above 64): a block computes a BM x BN tile with 32x32x16 matrix instructions from two
 //           LDS buffers that are filled by loads straight to LDS, 64 of the contraction at a time.
 //           Few tiles and a long contraction: the contraction is split over blocks, which leave fp32
-//           partial tiles for `finish` to add in a fixed order.
+//           partial tiles for `finish` to add in a fixed order. bf16 M=4096 K=4096 N=8192: 227 us,
+//           1.21 PFLOP/s; M=4096 K=4096 N=5120: 140 us, 1.23.
 //   skinny  (M up to 64): bound by reading w once. A wave takes 16 rows of w and every WAVES-th
 //           part of the contraction, straight from memory into 16x16x32 matrix instructions.
+//           M=4 K=5120 N=4096 with w not in any cache: 11.7 us, 3.6 TB/s.
 // The epilogue works on fp32 sums staged through LDS, so that bias, residual, pre and out are read
 // and written as whole rows.
 //
@@ -561,7 +563,8 @@ __global__ void __launch_bounds__(WAVES *kWave)
 // Operands laid out for the products
 // ---------------------------------------------------------------------------------------------
 // What the backward makes of gout (or of a plain matrix, without `pre`): g = gout act'(pre), kept by
-// rows and / or by columns, and the column sums of 64 rows. One 64x64 tile a block.
+// rows and / or by columns, and the column sums of 64 rows. One 64x64 tile a block; bound by memory
+// (4096 x 4096, g by rows and sums: 24 us, 4.2 TB/s).
 struct Turn {
     const uint16_t *src, *pre;
     int64_t ld, R, C;

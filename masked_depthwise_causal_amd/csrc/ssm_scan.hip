@@ -23,6 +23,12 @@
 // chunk from a zero state and keeps its end state and sum of d; since the decay over a chunk is
 // exp(A sum d), the second kernel's blocks fold the chunks before theirs into their initial state.
 // The backward does the same from the other end for the gradient of the state.
+//
+// Bound by instruction issue, not by memory: each of N states of each element takes an exp (8 cycles of
+// a SIMD for 64 lanes) and, forward, about 4 multiply-adds (2.5 cycles each), backward 12. S=2048 B=8
+// H=4096 N=16 bf16, gated: forward 326 us (1.6 TB/s), backward 774 us, sums of gB, gC and the parameters
+// 33; the counters put 91 to 93 % of the issue slots in use. The single token (B=64 H=5120) is bound by
+// its state: 9.2 us, 4.9 TB/s.
 #include "ssm_common.h"
 
 using namespace ssm;
