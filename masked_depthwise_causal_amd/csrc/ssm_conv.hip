@@ -416,7 +416,8 @@ struct Strips {
 };
 
 // Rows of a strip: whole batches of loads, as long as leaves 8192 waves (8 a SIMD), within [lo, hi]: a
-// strip reads W-1 rows of its neighbours again.
+// strip reads W-1 rows of its neighbours again (forward, S=8192 B=1 H=1024: 9.4 us with at least 8
+// rows, 11.4 with 4, 10.0 with 12).
 Strips strips(int64_t S, int64_t lanes, int64_t lo, int64_t hi) {
     const int64_t across = (lanes + kWave - 1) / kWave;
     int64_t rows = S * across / 8192 / 4 * 4;
