@@ -92,13 +92,14 @@ __device__ static inline float log1p_unit(float e) {
     return __builtin_fmaf(__builtin_amdgcn_logf(u), kLn2, e - (u - 1.0f));
 }
 
-// softplus(v) = max(v,0) + log(1 + exp(-|v|)), max(v,0) as half of v + |v| (exact); `slope` gets its
-// derivative, the logistic function.
+// softplus(v) = max(v,0) + log(1 + exp(-|v|)): 0 at -infinity, v itself from where the logarithm is
+// below half a step of v (up to the largest values and infinity); the logarithm keeps NaN, which the
+// maximum drops. `slope` gets its derivative, the logistic function.
 __device__ static inline float softplus_f(float v, float &slope) {
     const float e = exp_f(-__builtin_fabsf(v));
     const float r = rcp_f(1.0f + e);
     slope = v >= 0.0f ? r : e * r;
-    return __builtin_fmaf(0.5f, v + __builtin_fabsf(v), log1p_unit(e));
+    return __builtin_fmaxf(v, 0.0f) + log1p_unit(e);
 }
 __device__ static inline float softplus_f(float v) {
     float unused;

@@ -1,0 +1,122 @@
+"""Infinities, NaN and the types' largest values in live rows of the state space block's operators.
+
+Each case is compared bit for bit with the same call on finite values of the same limit (a step size's
+pre-activation of -200 has exp(-200), which is below the smallest fp32 number), and that call with the
+64-bit form, to the bounds of the operators' own tests."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+import masked_depthwise_causal_amd as mdc
+
+from . import ssm_ref as ref
+from .gpu_util import announce
+from .test_conv_act import DT, dirty
+from .test_scan import inputs, slack
+
+pytestmark = pytest.mark.gpu
+INF, NAN = float("inf"), float("nan")
+
+
+def same(a, b, name):
+    """Equal bits, NaN equal to NaN."""
+    assert a.shape == b.shape and a.dtype == b.dtype, name
+    ok = (a == b) | (torch.isnan(a) & torch.isnan(b))
+    assert bool(ok.all()), f"{name}: {int((~ok).sum())} of {ok.numel()} differ"
+
+
+def scan_both(v, go, gf, lengths=None):
+    """Everything that the scan's forward and backward give for the inputs `v`, by name."""
+    d = {k: None if t is None else t.cuda() for k, t in v.items()}
+    ins = tuple(d[k] for k in ("x", "dt", "A", "Bm", "Cm"))
+    opt = {k: d[k] for k in ("D", "z", "dt_bias", "state")}
+    opt["lengths"] = None if lengths is None else torch.tensor(lengths, device="cuda")
+    dirty()
+    out, fs, saved = mdc.scan_forward(*ins, **opt, return_state=True, return_saved=True)
+    gr = mdc.scan_backward(go.cuda(), *ins, saved, **opt, gradFinalState=gf.cuda())
+    torch.cuda.synchronize()
+    return {"out": out, "state": fs, "gx": gr.x, "gdt": gr.dt, "gA": gr.A, "gB": gr.B, "gC": gr.C,
+            "gD": gr.D, "gz": gr.z, "gbias": gr.dt_bias, "gs": gr.state}
+
+
+def against_64_bits(got, v, go, gf, S, lengths=None):
+    r = ref.scan(v["x"], v["dt"], v["A"], v["Bm"], v["Cm"], v["D"], v["z"], v["dt_bias"], True, lengths,
+                 v["state"], go, gf)
+    for k, t in got.items():
+        ref.close(t, r[k], slack(S), k)
+
+
+@pytest.mark.parametrize("S,H,N,dtype", [(37, 70, 16, "bf16"), (20, 64, 8, "fp16"), (40, 33, 32, "bf16"),
+                                         (600, 40, 16, "bf16")])  # the last one is cut into chunks
+def test_step_of_minus_infinity_leaves_the_state_alone(S, H, N, dtype):
+    v, go, gf = inputs(S, 2, H, N, 1, dtype, seed=S)
+    rows = torch.rand((S, 2, H), generator=torch.Generator().manual_seed(1)) < 0.3
+    rows[S // 2] = True  # a whole row
+    v["dt"][rows] = -200.0
+    v["dt_bias"][3] = -200.0  # a whole channel
+    announce(f"scan, steps of -200 S={S} H={H} N={N}")
+    want = scan_both(v, go, gf)
+    against_64_bits(want, v, go, gf, S)
+    w = dict(v, dt=v["dt"].clone(), dt_bias=v["dt_bias"].clone())
+    w["dt"][rows] = -INF
+    w["dt_bias"][3] = -INF
+    announce(f"scan, steps of -inf S={S} H={H} N={N}")
+    got = scan_both(w, go, gf)
+    for k in want:
+        same(got[k], want[k], k)
+    assert not got["gdt"][rows.cuda()].any()
+
+
+@pytest.mark.parametrize("N,dtype", [(16, "bf16"), (5, "fp16")])
+def test_token_of_minus_infinity_leaves_the_state_alone(N, dtype):
+    v, _, _ = inputs(1, 3, 70, N, 1, dtype, seed=N)
+    d = {k: t.cuda() for k, t in v.items()}
+    d["dt"][0, 1] = -INF
+    st = d["state"].clone()
+    out = mdc.scan_step(st, d["x"][0], d["dt"][0], d["A"], d["Bm"][0], d["Cm"][0], D=d["D"], z=d["z"][0],
+                        dt_bias=d["dt_bias"])
+    assert torch.equal(st[1], d["state"][1])
+    v["dt"][0, 1] = -200.0
+    r = ref.scan(v["x"], v["dt"], v["A"], v["Bm"], v["Cm"], v["D"], v["z"], v["dt_bias"], True, None,
+                 v["state"])
+    ref.close(out[None], r["out"], slack(1), "out")
+
+
+@pytest.mark.parametrize("value", [INF, NAN])
+def test_other_channels_do_not_see_a_step_that_is_not_finite(value):
+    S, H = 37, 70
+    v, go, gf = inputs(S, 2, H, 16, 1, "bf16", seed=4)
+    want = scan_both(v, go, gf)
+    w = dict(v, dt=v["dt"].clone())
+    w["dt"][S // 2, 0, 5] = value
+    got = scan_both(w, go, gf)
+    others = torch.arange(H, device="cuda") != 5
+    for k in ("out", "state", "gx", "gdt", "gA", "gD", "gz", "gbias", "gs"):
+        same(got[k][..., others], want[k][..., others], k)
+    same(got["out"][:S // 2, 0, 5], want["out"][:S // 2, 0, 5], "rows before")
+    assert not torch.isfinite(got["out"][S // 2:, 0, 5]).any()
+    same(got["out"][:, 1], want["out"][:, 1], "the other sequence")
+
+
+@pytest.mark.parametrize("M,N", [(3, 40), (130, 72)])  # few rows and tiles
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_softplus_epilogue_at_the_ends(M, N, dtype):
+    dt = DT[dtype]
+    big = torch.finfo(dt).max
+    ends = [-INF, -big, -200.0, -20.0, 0.0, 20.0, big / 2, big, INF, NAN]
+    bias = torch.tensor([ends[i % len(ends)] for i in range(N)]).to(dt)
+    g = torch.Generator().manual_seed(M)
+    x, w = torch.randn((M, 64), generator=g).to(dt), torch.randn((N, 64), generator=g).to(dt) * 0.1
+    w[6::len(ends)] = w[7::len(ends)] = 0  # sums beyond the type are another matter
+    pre = x.to(ref.F) @ w.to(ref.F).t() + bias.to(ref.F)
+    mag = x.to(ref.F).abs() @ w.to(ref.F).abs().t() + bias.to(ref.F).abs()
+    want = ref.softplus(pre)
+    # an error of pre counts by the slope there, and softplus has a relative error of its own
+    mag = torch.nan_to_num(mag * ref.sigmoid(pre), nan=0.0) + want
+    announce(f"linear softplus ends M={M} N={N} {dtype}")
+    got = mdc.linear_forward(x.cuda(), w.cuda(), bias.cuda(), activation="softplus").cpu()
+    assert torch.equal(torch.isnan(got), torch.isnan(want))
+    assert torch.equal(got[torch.isinf(want)].to(ref.F), want[torch.isinf(want)])
+    fine = torch.isfinite(want)
+    ref.close(got[fine], (want[fine], mag[fine]), (64 + 64) * 2.0 ** -23, "softplus")
