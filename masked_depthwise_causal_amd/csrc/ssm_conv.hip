@@ -17,6 +17,8 @@
 // neighbour a second time to the same values.
 #include "ssm_common.h"
 
+#include <type_traits>
+
 using namespace ssm;
 
 namespace {
@@ -223,16 +225,17 @@ __global__ void __launch_bounds__(kThreads)
         }
         const uint16_t *xp = x.p + b * x.b + h * x.h, *gp = gy.p + b * gy.b + h * gy.h;
 
-        // gx of row t = i-W+1 from g of rows t..i (g[0] the oldest)
-        auto emit = [&](int64_t i) {
-            const int64_t t = i - (W - 1);
-            float o[V];
+        // gx of row t = i-W+1 from g of rows t..i (g[0] the oldest). Unless `all` of them are rows from 0
+        // to the length, the sum leaves the others out: a zero times an infinite weight is not zero.
+        auto gradient = [&](int64_t t, auto all, float (&o)[V]) {
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                o[v] = 0.0f;
+            for (int v = 0; v < V; ++v) o[v] = 0.0f;
 #pragma unroll
-                for (int k = 0; k < W; ++k) o[v] = __builtin_fmaf(g[k][v], w[W - 1 - k][v], o[v]);
-            }
+            for (int k = 0; k < W; ++k)
+                if (decltype(all)::value || (t + k >= 0 && t + k < len))
+#pragma unroll
+                    for (int v = 0; v < V; ++v)
+                        o[v] = __builtin_fmaf(g[k][v], w[W - 1 - k][v], o[v]);
             // the last W-1 rows before the length are the final state
             if (W > 1 && gfinal && t < len && t >= len - (W - 1)) {
                 float f[V];
@@ -240,10 +243,17 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
                 for (int v = 0; v < V; ++v) o[v] += f[v];
             }
-            if (t >= t0)
+        };
+        auto emit = [&](int64_t i, auto all) {
+            const int64_t t = i - (W - 1);
+            float o[V];
+            if (t >= t0) {
+                gradient(t, all, o);
                 store<V>(gx + t * BH + at, narrow<DT, V>(o));
-            else if (W > 1 && t < 0 && gstate)
+            } else if (W > 1 && t < 0 && gstate) {
+                gradient(t, std::false_type{}, o);
                 store<V>(gstate + (t + W - 1) * BH + at, narrow<DT, V>(o));
+            }
         };
         auto shift = [&]() {
 #pragma unroll
@@ -294,7 +304,7 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
                 for (int r = 0; r < kBwdBatch; ++r) {
                     row(cx[r], cg[r], true);
-                    emit(i + r);
+                    emit(i + r, std::true_type{});
                     shift();
                 }
                 i += kBwdBatch;
@@ -303,7 +313,7 @@ __global__ void __launch_bounds__(kThreads)
             for (int r = 0; r < kBwdBatch - 1; ++r)
                 if (i < end) {
                     row(nx[r], ng[r], true);
-                    emit(i);
+                    emit(i, std::true_type{});
                     shift();
                     ++i;
                 }
@@ -316,7 +326,7 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
                 for (int v = 0; v < V; ++v) g[W - 1][v] = win[W - 1][v] = 0.0f;
             }
-            emit(i);
+            emit(i, std::false_type{});
             shift();
         }
     }

@@ -12,7 +12,7 @@ import masked_depthwise_causal_amd as mdc
 
 from . import ssm_ref as ref
 from .gpu_util import announce
-from .test_conv_act import DT, dirty
+from .test_conv_act import DT, GX, dirty, rand
 from .test_scan import inputs, slack
 
 pytestmark = pytest.mark.gpu
@@ -120,3 +120,30 @@ def test_softplus_epilogue_at_the_ends(M, N, dtype):
     assert torch.equal(got[torch.isinf(want)].to(ref.F), want[torch.isinf(want)])
     fine = torch.isfinite(want)
     ref.close(got[fine], (want[fine], mag[fine]), (64 + 64) * 2.0 ** -23, "softplus")
+
+
+@pytest.mark.parametrize("S,H,W,lengths", [(37, 20, 4, [37, 0, 30]), (11, 7, 3, [11, 1, 8]),
+                                           (70, 133, 2, [64, 70, 63]), (9, 64, 1, [9, 4, 0])])
+@pytest.mark.parametrize("value", [INF, -INF, NAN])
+def test_conv_rows_past_a_length_do_not_meet_the_weights(S, H, W, lengths, value):
+    """Zeros there, and nothing of them in the last rows before the length, for weights that make
+    something else of a product with zero."""
+    g = torch.Generator().manual_seed(S)
+    x, gy, w = rand(g, S, 3, H), rand(g, S, 3, H), rand(g, W, H)
+    state, gf = rand(g, W - 1, 3, H), rand(g, W - 1, 3, H)
+    for k in range(W):
+        w[k, k::7] = value
+    r = ref.conv(x, w, None, None, lengths, state, gy, gf)
+    n = torch.tensor(lengths, device="cuda")
+    announce(f"conv weights of {value} S={S} H={H} W={W}")
+    dirty()
+    gr = mdc.conv_act_backward(gy.cuda(), x.cuda(), w.cuda(), activation=None, lengths=n,
+                               state=state.cuda(), gradFinalState=gf.cuda())
+    for b, m in enumerate(lengths):
+        assert not gr.x[m:, b].any(), "rows past the length"
+    for got, key in ((gr.x, "gx"), (gr.state, "gs")):
+        got, (want, mag) = got.cpu(), r[key]
+        fine = torch.isfinite(want)
+        same(torch.where(fine, torch.zeros((), dtype=ref.F), got.to(ref.F)),
+             torch.where(fine, torch.zeros((), dtype=ref.F), want), key)
+        ref.close(got[fine], (want[fine], mag[fine]), GX, key)
