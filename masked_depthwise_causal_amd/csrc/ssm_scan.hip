@@ -126,12 +126,19 @@ __device__ static inline void step_sizes(const ScanIn &a, const float (&v)[JR], 
     }
 }
 
+// An infinite rate as the largest one: its decay over a step is the same 0, and a row without a step
+// (past the length, or of a step size of 0) has the decay 1, not the NaN of zero times infinity.
+__device__ static inline float finite_rate(float v) {
+    constexpr float kMost = 3.402823466e38f;
+    return v < -kMost ? -kMost : v > kMost ? kMost : v;
+}
+
 // A [N,H] times log2(e), so that the decay is one exp2; zero for states past N, which then stay 0.
 __device__ static inline void load_rates(const ScanIn &a, const Place &p, float (&A2)[kPer]) {
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         const int n = p.wave * kPer + i;
-        A2[i] = n < a.N ? a.A[(int64_t)n * a.H + p.h] * kLog2e : 0.0f;
+        A2[i] = n < a.N ? finite_rate(a.A[(int64_t)n * a.H + p.h] * kLog2e) : 0.0f;
     }
 }
 
@@ -908,7 +915,7 @@ __global__ void __launch_bounds__(kWave)
                                                : a.C.p[b * a.C.b + g0 * a.C.g + n * a.C.n]);
     }
 #pragma unroll
-    for (int n = 0; n < NMAX; ++n) r[n] = a.A[(int64_t)(n < a.N ? n : a.N - 1) * a.H + h];
+    for (int n = 0; n < NMAX; ++n) r[n] = finite_rate(a.A[(int64_t)(n < a.N ? n : a.N - 1) * a.H + h]);
     const float x = to_f32<DT>(a.x.p[b * a.x.b + h * a.x.h]);
     const float t = to_f32<DT>(a.dt.p[b * a.dt.b + h * a.dt.h]) + (a.bias ? a.bias[h] : 0.0f);
     const float z = a.z.p ? to_f32<DT>(a.z.p[b * a.z.b + h * a.z.h]) : 0.0f;

@@ -147,3 +147,36 @@ def test_conv_rows_past_a_length_do_not_meet_the_weights(S, H, W, lengths, value
         same(torch.where(fine, torch.zeros((), dtype=ref.F), got.to(ref.F)),
              torch.where(fine, torch.zeros((), dtype=ref.F), want), key)
         ref.close(got[fine], (want[fine], mag[fine]), GX, key)
+
+
+@pytest.mark.parametrize("S,H,N,dtype,lengths", [(37, 70, 16, "bf16", None), (16, 64, 8, "fp16", [16, 3]),
+                                                 (600, 40, 16, "bf16", [600, 290])])  # in chunks
+def test_rates_of_minus_infinity_forget_the_state(S, H, N, dtype, lengths):
+    """The decay is 0 then, and 1 in rows past the length, which leave the state alone."""
+    v, go, gf = inputs(S, 2, H, N, 1, dtype, seed=S)
+    rates = torch.rand((N, H), generator=torch.Generator().manual_seed(2)) < 0.3
+    v["A"][rates] = -1e30
+    announce(f"scan, rates of -1e30 S={S} H={H} N={N}")
+    want = scan_both(v, go, gf, lengths)
+    against_64_bits(want, v, go, gf, S, lengths)
+    for value in (-3e38, -INF):
+        announce(f"scan, rates of {value} S={S} H={H} N={N}")
+        got = scan_both(dict(v, A=torch.where(rates, value, v["A"])), go, gf, lengths)
+        for k in want:
+            same(got[k], want[k], k)
+
+
+def test_token_with_rates_of_minus_infinity():
+    v, _, _ = inputs(1, 3, 70, 5, 1, "bf16", seed=6)
+    d = {k: t.cuda() for k, t in v.items()}
+    d["dt"][0, 0] = -INF  # no step: the state stays, whatever the rate
+    res = []
+    for value in (-1e30, -INF):
+        A, st = d["A"].clone(), d["state"].clone()
+        A[2] = value
+        out = mdc.scan_step(st, d["x"][0], d["dt"][0], A, d["Bm"][0], d["Cm"][0], D=d["D"], z=d["z"][0],
+                            dt_bias=d["dt_bias"])
+        res.append((out, st))
+    same(res[1][0], res[0][0], "out")
+    same(res[1][1], res[0][1], "state")
+    assert torch.equal(res[1][1][0], d["state"][0])
