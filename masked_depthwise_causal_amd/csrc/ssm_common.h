@@ -107,9 +107,13 @@ __device__ static inline float softplus_f(float v) {
 }
 
 __device__ static inline float silu_f(float v) { return v * sigmoid_f(v); }
+// Slopes are 0 and 1 at the ends. There sigmoid_f is exactly 0 or 1, and the factor v (in gelu's also
+// v^2, which overflows from 2e19 on) is taken as +-128, so that it leaves no zero times infinity.
+// (Of NaN it makes a number; sigmoid_f keeps it.)
+__device__ static inline float bounded(float v) { return __builtin_amdgcn_fmed3f(v, -128.0f, 128.0f); }
 __device__ static inline float silu_slope_f(float v) {
     const float g = sigmoid_f(v);
-    return g * __builtin_fmaf(v, 1.0f - g, 1.0f);
+    return g * __builtin_fmaf(bounded(v), 1.0f - g, 1.0f);
 }
 
 // tanh-form gelu: 0.5 (1 + tanh u) is the logistic function of 2u, u = c (v + 0.044715 v^3).
@@ -130,8 +134,8 @@ __device__ static inline float act_slope_f(float v, int act) {
         case MCCB_ACT_SILU: return silu_slope_f(v);
         case MCCB_ACT_GELU: {
             const float g = sigmoid_f(kGelu2c * v * __builtin_fmaf(0.044715f * v, v, 1.0f));
-            const float du = kGelu2c * __builtin_fmaf(0.134145f * v, v, 1.0f);
-            return __builtin_fmaf(v * g * (1.0f - g), du, g);
+            const float c = bounded(v), du = kGelu2c * __builtin_fmaf(0.134145f * c, c, 1.0f);
+            return __builtin_fmaf(c * g * (1.0f - g), du, g);
         }
         case MCCB_ACT_SOFTPLUS: return sigmoid_f(v);
         default: return 1.0f;

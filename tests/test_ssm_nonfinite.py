@@ -180,3 +180,53 @@ def test_token_with_rates_of_minus_infinity():
     same(res[1][0], res[0][0], "out")
     same(res[1][1], res[0][1], "state")
     assert torch.equal(res[1][1][0], d["state"][0])
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu", "relu", "softplus"])
+@pytest.mark.parametrize("dtype,big", [("fp16", 65504.0), ("bf16", 1e20), ("bf16", 3.3895313892515355e38)])
+@pytest.mark.parametrize("M", [5, 100])
+def test_slopes_of_large_and_infinite_values(act, dtype, big, M):
+    """Slopes are 0 and 1 at the ends; pre is infinite where its sum is beyond a 16-bit type."""
+    dt, N, K = DT[dtype], 48, 40
+    g = torch.Generator().manual_seed(M)
+    x, w, go = (torch.randn(s, generator=g).to(dt) for s in ((M, K), (N, K), (M, N)))
+    pre = torch.randn((M, N), generator=g).to(dt)
+    p64 = pre.to(ref.F)
+    for i, v in enumerate((big, -big, INF, -INF, 300.0, -300.0)):
+        pre[:, i::8] = v
+        p64[:, i::8] = max(min(v, 1e5), -1e5)  # whose slopes are 0 and 1 in 64 bits
+    announce(f"linear slopes {act} {dtype} {big} M={M}")
+    gr = mdc.linear_backward(go.cuda(), x.cuda(), w.cuda(), pre.cuda(), activation=act)
+    slope = ref.act_slope(p64, act)
+    gg = go.to(ref.F) * slope
+    gm = go.to(ref.F).abs() * (slope.abs() + 2.0 ** -10 * (1 + p64.abs().clamp(max=4)))
+    half = torch.finfo(dt).eps / 2
+    e = lambda K: (K + 64) * 2.0 ** -23  # noqa: E731  as in test_linear.py
+    ref.close(gr.x, (gg @ w.to(ref.F), gm @ w.to(ref.F).abs()), half + e(N), "gx")
+    ref.close(gr.weight, (gg.t() @ x.to(ref.F), gm.t() @ x.to(ref.F).abs()), half + e(M), "gw")
+    ref.close(gr.bias, (gg.sum(0), gm.sum(0)), e(M), "gbias")
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_gradients_where_pre_is_beyond_fp16(act):
+    """The forward's sums are fp32, and its output is finite where pre is far below the type's range."""
+    g = torch.Generator().manual_seed(1)
+    x, w, go = (torch.randn(s, generator=g).half() for s in ((70, 64), (40, 64), (70, 40)))
+    x[:, 0], w[::2, 0] = 300.0, -300.0  # pre near -90000 in every other column
+    out, pre = mdc.linear_forward(x.cuda(), w.cuda(), activation=act, return_pre=True)
+    assert not out[:, ::2].any() and torch.isinf(pre[:, ::2]).all()
+    gr = mdc.linear_backward(go.cuda(), x.cuda(), w.cuda(), pre, activation=act)
+    assert all(torch.isfinite(t).all() for t in gr)
+    assert not gr.weight[::2].any() and not gr.bias[::2].any()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_gates_slope_at_large_values(dtype):
+    """gz where the gate is large, up to the type's largest value and infinity."""
+    S, H, big = 20, 64, torch.finfo(DT[dtype]).max
+    v, go, gf = inputs(S, 1, H, 16, 1, dtype, seed=3)
+    v["z"][:, :, 0], v["z"][:, :, 1] = -big, -300.0
+    got = scan_both(v, go, gf)
+    assert not got["gz"][:, :, :2].any() and not got["out"][:, :, :2].any()
+    v["z"][:, :, 0] = INF  # a slope of 1
+    assert bool(torch.isfinite(scan_both(v, go, gf)["gz"]).all())
