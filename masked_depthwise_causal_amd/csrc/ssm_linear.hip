@@ -475,7 +475,7 @@ __global__ void __launch_bounds__(256)
 template <int DT, int MB, int WAVES>
 __global__ void __launch_bounds__(WAVES *kWave)
     product_skinny(Product g, Epilogue e) {
-    __shared__ float part[WAVES][MB * 16][16 + 4];
+    __shared__ __align__(16) float part[WAVES][MB * 16][16 + 4];
     const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
     const int64_t n0 = (int64_t)blockIdx.x * 16;
     const int64_t n = n0 + lane % 16 < g.N ? n0 + lane % 16 : g.N - 1;

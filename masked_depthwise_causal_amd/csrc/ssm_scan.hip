@@ -38,6 +38,11 @@ namespace {
 constexpr int kTile = 16;  // rows; the forward keeps the state before each tile for the backward
 constexpr int kPer = 4;    // states a lane holds
 
+// How a thread takes its channels of a row: one by one, or by one load, since they are adjacent and every
+// block has as many; then, in LDS, at any channel or (as where it takes them one by one) at a multiple of
+// its vectors' four floats (of two, where it takes two).
+enum { kApart, kAdjacent, kWide };
+
 struct Rows {  // a strided [S,B,H] input
     const uint16_t *p;
     int64_t s, b, h;
@@ -82,7 +87,7 @@ __device__ static inline void take_turn(int tile) {
     else __builtin_amdgcn_s_setprio(0);
 }
 
-template <int NW, bool WIDE>
+template <int NW, int ROWS>
 __device__ static inline Place place(const ScanIn &a) {
     constexpr int JR = kTile / NW;
     Place p;
@@ -97,7 +102,7 @@ __device__ static inline Place place(const ScanIn &a) {
     p.row = threadIdx.x / (kWave / JR);
     p.c = threadIdx.x % (kWave / JR) * JR;
     // in a block with fewer channels the last threads take the last JR, twice
-    if (WIDE && p.c > p.channels - JR) p.c = p.channels - JR;
+    if (ROWS != kApart && p.c > p.channels - JR) p.c = p.channels - JR;
     p.b = blockIdx.y;
     int64_t len = a.S;
     if (a.lengths) {
@@ -187,22 +192,21 @@ __device__ static inline void fold_chunks(const float *ends, const float *dsum, 
 }
 
 // A thread's way through a [S,B,H] tensor, tile by tile from one that is whole or the chunk's last:
-// JR channels of its row. WIDE: channels are adjacent and every block has JR, one load. Else one by
-// one, channels past the group's last repeating it.
-template <int NW, bool WIDE>
+// JR channels of its row; one by one channels past the group's last repeat it.
+template <int NW, int ROWS>
 struct Walk {
     static constexpr int JR = kTile / NW;
     typedef typename HVec<JR>::t vec;
     const uint16_t *p;  // the thread's row of the tile
     int64_t step, s, h;
     __device__ inline Walk(const Rows &r, const Place &q, int64_t row, int dir)
-        : p(r.p ? r.p + (row + q.row) * r.s + q.b * r.b + q.h0 * r.h + (WIDE ? q.c : 0) : nullptr),
+        : p(r.p ? r.p + (row + q.row) * r.s + q.b * r.b + q.h0 * r.h + (ROWS != kApart ? q.c : 0) : nullptr),
           step(dir * kTile * r.s), s(r.s), h(r.h) {}
     // The tile's values. `last`: its last live row; rows past it repeat it
     __device__ inline vec fetch(const Place &q, int last) const {
         const uint16_t *at = p;
         if (last < kTile - 1) at -= (q.row > last ? q.row - last : 0) * s;
-        if (WIDE) return *(const vec *)at;
+        if (ROWS != kApart) return *(const vec *)at;
         vec v;
 #pragma unroll
         for (int i = 0; i < JR; ++i) {
@@ -215,9 +219,9 @@ struct Walk {
 };
 
 // The same channels of the thread's row to a contiguous [S,B,H] output.
-template <bool WIDE, int JR>
+template <int ROWS, int JR>
 __device__ static inline void store_rows(uint16_t *p, const Place &q, const typename HVec<JR>::t v) {
-    if (WIDE) {
+    if (ROWS != kApart) {
         *(typename HVec<JR>::t *)p = v;
     } else {
 #pragma unroll
@@ -226,10 +230,14 @@ __device__ static inline void store_rows(uint16_t *p, const Place &q, const type
     }
 }
 
-// JR adjacent floats of LDS.
-template <int JR>
+// JR adjacent floats of LDS, from where their vectors are aligned or (kAdjacent) from any float, of which
+// the compiler then takes two at a time.
+template <int ROWS, int JR>
 __device__ static inline void load_floats(const float *p, float (&f)[JR]) {
-    if constexpr (JR == 2) {
+    if constexpr (ROWS == kAdjacent) {
+#pragma unroll
+        for (int i = 0; i < JR; ++i) f[i] = p[i];
+    } else if constexpr (JR == 2) {
         const float2 q = *(const float2 *)p;
         f[0] = q.x, f[1] = q.y;
     } else {
@@ -240,9 +248,12 @@ __device__ static inline void load_floats(const float *p, float (&f)[JR]) {
         }
     }
 }
-template <int JR>
+template <int ROWS, int JR>
 __device__ static inline void store_floats(float *p, const float (&f)[JR]) {
-    if constexpr (JR == 2) {
+    if constexpr (ROWS == kAdjacent) {
+#pragma unroll
+        for (int i = 0; i < JR; ++i) p[i] = f[i];
+    } else if constexpr (JR == 2) {
         *(float2 *)p = make_float2(f[0], f[1]);
     } else {
 #pragma unroll
@@ -304,7 +315,7 @@ __device__ static inline void load4(const float *p, float (&f)[kPer]) {
 // Forward. ENDS: only the end state of each chunk from a zero state, and its sum of d (the last
 // chunk's is not needed). One barrier a tile: while the waves scan tile k, whose operands one half
 // of the LDS buffers holds, tile k+1 is prepared in the other half.
-template <int DT, int NW, bool ENDS, bool GATE, bool WIDE>
+template <int DT, int NW, bool ENDS, bool GATE, int ROWS>
 __global__ void __launch_bounds__(NW *kWave)
     scan_fwd(ScanIn a, uint16_t *__restrict__ out, float *__restrict__ final_state,
              float *__restrict__ saved, float *__restrict__ ends, float *__restrict__ dsum) {
@@ -313,7 +324,7 @@ __global__ void __launch_bounds__(NW *kWave)
     __shared__ __align__(16) float sd[2][kTile][2][kWave];  // d, d x
     __shared__ __align__(16) float sB[2][kTile][NP], sC[ENDS ? 1 : 2][kTile][NP];
     __shared__ __align__(16) float sy[ENDS ? 1 : 2][ENDS ? 1 : NW][ENDS ? 1 : kTile][kWave];
-    const Place p = place<NW, WIDE>(a);
+    const Place p = place<NW, ROWS>(a);
     float A2[kPer], s[kPer], total = 0.0f;
     load_rates(a, p, A2);
     load_state(ENDS ? nullptr : a.state, a, p, s);
@@ -321,7 +332,7 @@ __global__ void __launch_bounds__(NW *kWave)
     float bias[JR], D[JR];
     load_param(a.bias, p, bias);
     load_param(ENDS ? nullptr : a.D, p, D);
-    Walk<NW, WIDE> xw(a.x, p, p.r0, 1), dw(a.dt, p, p.r0, 1), zw(a.z, p, p.r0, 1);
+    Walk<NW, ROWS> xw(a.x, p, p.r0, 1), dw(a.dt, p, p.r0, 1), zw(a.z, p, p.r0, 1);
     CoefWalk<DT, NW> coef(a, p, p.r0, 1);
     const int64_t BH = a.nb * a.H, states = BH * a.N;
     uint16_t *op = ENDS ? nullptr : out + (p.r0 + p.row) * BH + p.b * a.H + p.h0 + p.c;
@@ -353,8 +364,8 @@ __global__ void __launch_bounds__(NW *kWave)
 #pragma unroll
             for (int j = 0; j < JR; ++j) d[j] = dx[j] = 0.0f;
         }
-        store_floats(&sd[at][p.row][0][p.c], d);
-        store_floats(&sd[at][p.row][1][p.c], dx);
+        store_floats<ROWS>(&sd[at][p.row][0][p.c], d);
+        store_floats<ROWS>(&sd[at][p.row][1][p.c], dx);
         sB[at][coef.t][coef.n] = coef.b(last);
         if (!ENDS) sC[at][coef.t][coef.n] = coef.c(last);
     };
@@ -366,7 +377,7 @@ __global__ void __launch_bounds__(NW *kWave)
 #pragma unroll
         for (int w = 0; w < NW; ++w) {
             float f[JR];
-            load_floats(&sy[k & 1][w][p.row][p.c], f);
+            load_floats<ROWS>(&sy[k & 1][w][p.row][p.c], f);
 #pragma unroll
             for (int j = 0; j < JR; ++j) y[j] += f[j];
         }
@@ -374,10 +385,10 @@ __global__ void __launch_bounds__(NW *kWave)
 #pragma unroll
         for (int j = 0; j < JR; ++j)
             v[j] = from_f32<DT>(GATE ? y[j] * silu_f(to_f32<DT>(zc[j])) : y[j]);
-        if (p.row <= (k + 1 < tiles ? kTile - 1 : tail)) store_rows<WIDE, JR>(op, p, v);
+        if (p.row <= (k + 1 < tiles ? kTile - 1 : tail)) store_rows<ROWS, JR>(op, p, v);
         op += kTile * BH;
     };
-    if (WIDE && p.channels < kWave) {  // columns that no thread writes
+    if (ROWS != kApart && p.channels < kWave) {  // columns that no thread writes
         for (int r = p.wave; r < 2 * kTile * 2; r += NW)
             if (!p.on) (&sd[0][0][0][0])[r * kWave + p.lane] = 0.0f;
     }
@@ -493,20 +504,20 @@ __device__ static inline float join(float a, float b, bool second) {
 }
 
 // Carry of a chunk from a zero gradient behind it: gs a at its first row, and its sum of d.
-template <int DT, int NW, bool GATE, bool WIDE>
+template <int DT, int NW, bool GATE, int ROWS>
 __global__ void __launch_bounds__(NW *kWave)
     scan_bwd_ends(ScanIn a, ScanGrad q) {
     constexpr int NP = NW * kPer, JR = kTile / NW;
     typedef typename HVec<JR>::t vec;
     __shared__ __align__(16) float sd[2][kTile][2][kWave];  // d, gy
     __shared__ __align__(16) float sC[2][kTile][NP];
-    const Place p = place<NW, WIDE>(a);
+    const Place p = place<NW, ROWS>(a);
     float A2[kPer], carry[kPer] = {0.0f, 0.0f, 0.0f, 0.0f}, total = 0.0f, bias[JR];
     load_rates(a, p, A2);
     load_param(a.bias, p, bias);
     const int tiles = p.end > p.r0 ? (int)((p.end - p.r0 + kTile - 1) / kTile) : 0;
     const int64_t t0 = p.r0 + (int64_t)(tiles - 1) * kTile;
-    Walk<NW, WIDE> dw(a.dt, p, t0, -1), zw(a.z, p, t0, -1), gw(q.go, p, t0, -1);
+    Walk<NW, ROWS> dw(a.dt, p, t0, -1), zw(a.z, p, t0, -1), gw(q.go, p, t0, -1);
     CoefWalk<DT, NW> coef(a, p, t0, -1);
     const int tail = (int)(p.end - t0) - 1;  // the last tile may be partial, the others are whole
     vec dr, zr, gr;
@@ -535,11 +546,11 @@ __global__ void __launch_bounds__(NW *kWave)
 #pragma unroll
             for (int j = 0; j < JR; ++j) d[j] = gy[j] = 0.0f;
         }
-        store_floats(&sd[at][p.row][0][p.c], d);
-        store_floats(&sd[at][p.row][1][p.c], gy);
+        store_floats<ROWS>(&sd[at][p.row][0][p.c], d);
+        store_floats<ROWS>(&sd[at][p.row][1][p.c], gy);
         sC[at][coef.t][coef.n] = coef.c(last);
     };
-    if (WIDE && p.channels < kWave) {
+    if (ROWS != kApart && p.channels < kWave) {
         for (int r = p.wave; r < 2 * kTile * 2; r += NW)
             if (!p.on) (&sd[0][0][0][0])[r * kWave + p.lane] = 0.0f;
     }
@@ -590,7 +601,7 @@ __global__ void __launch_bounds__(NW *kWave)
 
 // Two waves a SIMD: a single one issues an fp32 instruction every five cycles, two together one every
 // two and a half. The tile's history takes 128 registers of the 256 that leaves.
-template <int DT, int NW, bool GATE, bool WIDE>
+template <int DT, int NW, bool GATE, int ROWS>
 __global__ void __launch_bounds__(NW *kWave, 2)
     scan_bwd(ScanIn a, ScanGrad q) {
     constexpr int NP = NW * kPer, JR = kTile / NW;
@@ -601,7 +612,7 @@ __global__ void __launch_bounds__(NW *kWave, 2)
     __shared__ __align__(16) float su[NW][kTile][kWave], sw[NW][kTile][kWave];
     __shared__ __align__(16) float sy[GATE ? NW : 1][GATE ? kTile : 1][kWave];
     __shared__ __align__(16) float sparam[2][kWave];  // dt_bias, D
-    const Place p = place<NW, WIDE>(a);
+    const Place p = place<NW, ROWS>(a);
     if (p.wave == 0) {
         sparam[0][p.lane] = a.bias ? a.bias[p.h] : 0.0f;
         sparam[1][p.lane] = a.D ? a.D[p.h] : 0.0f;
@@ -626,7 +637,7 @@ __global__ void __launch_bounds__(NW *kWave, 2)
             q.gdt[o] = 0;
             if (GATE) q.gz[o] = 0;
         }
-    Walk<NW, WIDE> xw(a.x, p, t0, -1), dw(a.dt, p, t0, -1), zw(a.z, p, t0, -1), gw(q.go, p, t0, -1);
+    Walk<NW, ROWS> xw(a.x, p, t0, -1), dw(a.dt, p, t0, -1), zw(a.z, p, t0, -1), gw(q.go, p, t0, -1);
     CoefWalk<DT, NW> coef(a, p, t0, -1);
     // the lane's state n before the tile at kept[n H]
     const float *kept = q.saved + t0 / kTile * states + (p.b * a.N + p.wave * kPer) * a.H + p.h;
@@ -660,7 +671,7 @@ __global__ void __launch_bounds__(NW *kWave, 2)
     auto prepare = [&](int k) {
         const int last = k + 1 < tiles ? kTile - 1 : tail;
         float v[JR], d[JR], dx[JR], gy[JR];
-        load_floats(&sparam[0][p.c], v);
+        load_floats<ROWS>(&sparam[0][p.c], v);
 #pragma unroll
         for (int j = 0; j < JR; ++j) v[j] += to_f32<DT>(dr[j]);
         step_sizes<true>(a, v, d, slope);
@@ -670,14 +681,14 @@ __global__ void __launch_bounds__(NW *kWave, 2)
             gy[j] = to_f32<DT>(gr[j]);
             if (GATE) gy[j] *= silu_f(to_f32<DT>(zr[j]));
         }
-        if (p.row > last || (!WIDE && p.channels < kWave)) {
+        if (p.row > last || (ROWS == kApart && p.channels < kWave)) {
 #pragma unroll
             for (int j = 0; j < JR; ++j)
                 if (p.row > last || p.c + j >= p.channels) d[j] = dx[j] = gy[j] = 0.0f;
         }
-        store_floats(&sd[p.row][0][p.c], d);
-        store_floats(&sd[p.row][1][p.c], dx);
-        store_floats(&sd[p.row][2][p.c], gy);
+        store_floats<ROWS>(&sd[p.row][0][p.c], d);
+        store_floats<ROWS>(&sd[p.row][1][p.c], dx);
+        store_floats<ROWS>(&sd[p.row][2][p.c], gy);
         sB[coef.t][coef.n] = coef.b(last);
         sC[coef.t][coef.n] = coef.c(last);
     };
@@ -685,20 +696,20 @@ __global__ void __launch_bounds__(NW *kWave, 2)
     // the next tile's took their place.
     auto finish = [&](int k, const float (&d)[JR], const float (&gy)[JR], const float (&slope)[JR]) {
         float D[JR], u[JR], w[JR], y[JR], f[JR];
-        load_floats(&sparam[1][p.c], D);
-        load_floats(&su[0][p.row][p.c], u);
-        load_floats(&sw[0][p.row][p.c], w);
-        if (GATE) load_floats(&sy[0][p.row][p.c], y);
+        load_floats<ROWS>(&sparam[1][p.c], D);
+        load_floats<ROWS>(&su[0][p.row][p.c], u);
+        load_floats<ROWS>(&sw[0][p.row][p.c], w);
+        if (GATE) load_floats<ROWS>(&sy[0][p.row][p.c], y);
 #pragma unroll
         for (int i = 1; i < NW; ++i) {
-            load_floats(&su[i][p.row][p.c], f);
+            load_floats<ROWS>(&su[i][p.row][p.c], f);
 #pragma unroll
             for (int j = 0; j < JR; ++j) u[j] += f[j];
-            load_floats(&sw[i][p.row][p.c], f);
+            load_floats<ROWS>(&sw[i][p.row][p.c], f);
 #pragma unroll
             for (int j = 0; j < JR; ++j) w[j] += f[j];
             if (GATE) {
-                load_floats(&sy[i][p.row][p.c], f);
+                load_floats<ROWS>(&sy[i][p.row][p.c], f);
 #pragma unroll
                 for (int j = 0; j < JR; ++j) y[j] += f[j];
             }
@@ -717,9 +728,9 @@ __global__ void __launch_bounds__(NW *kWave, 2)
                     gz[j] = from_f32<DT>(to_f32<DT>(gc[j]) * __builtin_fmaf(D[j], x, y[j]) *
                                          silu_slope_f(to_f32<DT>(zc[j])));
             }
-            store_rows<WIDE, JR>(q.gx + to, p, gx);
-            store_rows<WIDE, JR>(q.gdt + to, p, gdt);
-            if (GATE) store_rows<WIDE, JR>(q.gz + to, p, gz);
+            store_rows<ROWS, JR>(q.gx + to, p, gx);
+            store_rows<ROWS, JR>(q.gdt + to, p, gdt);
+            if (GATE) store_rows<ROWS, JR>(q.gz + to, p, gz);
         }
         to -= kTile * BH;
         if (k % 32 == 0) {
@@ -730,7 +741,7 @@ __global__ void __launch_bounds__(NW *kWave, 2)
             }
         }
     };
-    if (WIDE && p.channels < kWave) {  // columns that no thread writes add nothing to the sums
+    if (ROWS != kApart && p.channels < kWave) {  // columns that no thread writes add nothing to the sums
         for (int r = p.wave; r < kTile * 3; r += NW)
             if (!p.on) (&sd[0][0][0])[r * kWave + p.lane] = 0.0f;
     }
@@ -739,8 +750,8 @@ __global__ void __launch_bounds__(NW *kWave, 2)
     for (int k = tiles - 1; k >= 0; --k) {
         take_turn(k);
         float d[JR], gy[JR], last_slope[JR], s0[kPer];
-        load_floats(&sd[p.row][0][p.c], d);
-        load_floats(&sd[p.row][2][p.c], gy);
+        load_floats<ROWS>(&sd[p.row][0][p.c], d);
+        load_floats<ROWS>(&sd[p.row][2][p.c], gy);
 #pragma unroll
         for (int j = 0; j < JR; ++j) last_slope[j] = slope[j];
 #pragma unroll
@@ -818,15 +829,15 @@ __global__ void __launch_bounds__(NW *kWave, 2)
     }
     if (tiles > 0) {
         float d[JR], gy[JR];
-        load_floats(&sd[p.row][0][p.c], d);
-        load_floats(&sd[p.row][2][p.c], gy);
+        load_floats<ROWS>(&sd[p.row][0][p.c], d);
+        load_floats<ROWS>(&sd[p.row][2][p.c], gy);
         finish(0, d, gy, slope);
         lds_barrier();  // the sums below take the place of what finish read
     }
     if (blockIdx.z == 0 && q.gstate) store_state(q.gstate, a, p, carry);
     double *pa = q.pa + ((int64_t)blockIdx.z * a.nb + p.b) * (a.N + 2) * a.H;
-    store_floats(&su[0][p.row][p.c], gD[1]);
-    store_floats(&sw[0][p.row][p.c], gb[1]);
+    store_floats<ROWS>(&su[0][p.row][p.c], gD[1]);
+    store_floats<ROWS>(&sw[0][p.row][p.c], gb[1]);
     lds_barrier();
     if (!p.on) return;
 #pragma unroll
@@ -1045,12 +1056,14 @@ ScanIn device_args(const mccb_scan_t *a, const ScanPlan &p) {
     return in;
 }
 
-// Whether a block's threads can take their channels of a row by one load: adjacent channels, and in
-// every block as many as a thread takes.
-bool wide(const mccb_scan_t *a, const ScanPlan &p) {
+// How a block's threads take their channels of a row (`out` is the gradient of the output, or NULL).
+int rows_form(const mccb_scan_t *a, const ScanPlan &p, const int64_t *out) {
     const int64_t K = a->H / a->G, JR = kTile / p.waves, tail = K % kWave;
-    return a->x_stride[2] == 1 && a->dt_stride[2] == 1 && (!a->z || a->z_stride[2] == 1) &&
-           (tail == 0 || tail >= JR);
+    if (a->x_stride[2] != 1 || a->dt_stride[2] != 1 || (a->z && a->z_stride[2] != 1) ||
+        (out && out[2] != 1) || (tail && tail < JR))
+        return kApart;
+    // the last threads of the last block start at its channel tail - JR
+    return tail % (JR < 4 ? JR : 4) ? kAdjacent : kWide;
 }
 
 // Workspace for handing states between chunks.
@@ -1073,6 +1086,14 @@ int by_waves(int waves, F f) {
         case 2: return f(std::integral_constant<int, 2>{});
         case 4: return f(std::integral_constant<int, 4>{});
         default: return f(std::integral_constant<int, 8>{});
+    }
+}
+template <typename F>
+int by_rows(int form, F f) {
+    switch (form) {
+        case kApart: return f(std::integral_constant<int, kApart>{});
+        case kAdjacent: return f(std::integral_constant<int, kAdjacent>{});
+        default: return f(std::integral_constant<int, kWide>{});
     }
 }
 template <typename F>
@@ -1136,19 +1157,19 @@ int mccb_scan_forward(const mccb_scan_t *a, void *out, float *final_state, void 
     const hipStream_t st = (hipStream_t)stream;
     return by_dtype(a->dtype, [&](auto dt) {
         return by_waves(p.waves, [&](auto nw) {
-            return by_flag(wide(a, p), [&](auto wd) {
+            return by_rows(rows_form(a, p, nullptr), [&](auto rows) {
                 constexpr int DT = decltype(dt)::value, NW = decltype(nw)::value;
-                constexpr bool W = decltype(wd)::value;
+                constexpr int R = decltype(rows)::value;
                 const dim3 block(NW * kWave);
                 if (p.chunks > 1) {
-                    hipLaunchKernelGGL((scan_fwd<DT, NW, true, false, W>), first, block, 0, st, da,
+                    hipLaunchKernelGGL((scan_fwd<DT, NW, true, false, R>), first, block, 0, st, da,
                                        (uint16_t *)nullptr, (float *)nullptr, (float *)nullptr, ends,
                                        dsum);
                     const int r = launched();
                     if (r != MCCB_OK) return r;
                 }
                 return by_flag(a->z != nullptr, [&](auto gate) {
-                    hipLaunchKernelGGL((scan_fwd<DT, NW, false, decltype(gate)::value, W>), grid, block,
+                    hipLaunchKernelGGL((scan_fwd<DT, NW, false, decltype(gate)::value, R>), grid, block,
                                        0, st, da, (uint16_t *)out, final_state, (float *)saved, ends,
                                        dsum);
                     return launched();
@@ -1223,16 +1244,16 @@ int mccb_scan_backward(const mccb_scan_t *a, const mccb_scan_grads_t *g, const v
         return by_waves(p.waves, [&](auto nw) {
             constexpr int DT = decltype(dt)::value, NW = decltype(nw)::value;
             const dim3 block(NW * kWave);
-            const bool w = wide(a, p) && g->gout_stride[2] == 1;
-            int e = by_flag(w, [&](auto wd) {
+            int e = by_rows(rows_form(a, p, g->gout_stride), [&](auto form) {
                 return by_flag(a->z != nullptr, [&](auto gate) {
-                    constexpr bool W = decltype(wd)::value, GATE = decltype(gate)::value;
+                    constexpr int R = decltype(form)::value;
+                    constexpr bool GATE = decltype(gate)::value;
                     if (p.chunks > 1) {
-                        hipLaunchKernelGGL((scan_bwd_ends<DT, NW, GATE, W>), grid, block, 0, st, da, q);
+                        hipLaunchKernelGGL((scan_bwd_ends<DT, NW, GATE, R>), grid, block, 0, st, da, q);
                         const int r = launched();
                         if (r != MCCB_OK) return r;
                     }
-                    hipLaunchKernelGGL((scan_bwd<DT, NW, GATE, W>), grid, block, 0, st, da, q);
+                    hipLaunchKernelGGL((scan_bwd<DT, NW, GATE, R>), grid, block, 0, st, da, q);
                     return launched();
                 });
             });
