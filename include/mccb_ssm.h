@@ -9,9 +9,10 @@
  * status codes, work enqueued on `stream` (a hipStream_t; NULL = the default stream) without
  * waiting. All checks run on the host before any HIP call, and on an error nothing is enqueued:
  * NULL pointers (MCCB_ERR_PARAM_NULLPTR), dtype, activation, strides, alignment, overlap and
- * workspace (MCCB_ERR_PARAM_INVALID), sizes (MCCB_ERR_SHAPE); MCCB_ERR_RUNTIME reports a failed
- * launch. Nothing is allocated and nothing is kept between calls, so every call can be recorded
- * into a HIP graph. Results are the same bits on every call with the same inputs.
+ * workspace (MCCB_ERR_PARAM_INVALID), sizes (MCCB_ERR_SHAPE); MCCB_ERR_RUNTIME reports a launch
+ * that the HIP runtime refused, before which a call's earlier kernels may have been enqueued.
+ * Nothing is allocated and nothing is kept between calls, so every call can be recorded into a HIP
+ * graph. Results are the same bits on every call with the same inputs.
  *
  * Data tensors are time-major, [S,B,...], as in mccb.h, and are read through element strides
  * (>= 0; 0 repeats). Element strides are in the tensor's own elements. Outputs are contiguous, are
@@ -52,7 +53,7 @@ typedef enum {
  * of two 16-bit values are exact in fp32; the sum, the activation and the gradients are fp32 (the
  * sums over rows and batches fp64 from one strip of rows to the next), rounded once.
  *
- * B in [1, 65535], S in [0, 2^31), H in [1, 2^24], W in 1..4; activation none or silu.
+ * B in [1, 65535], S in [0, 2^31), H in [1, 2^24], B H < 2^31, W in 1..4; activation none or silu.
  * -----------------------------------------------------------------------------------------------*/
 typedef struct {
     int64_t S, B, H, W;
@@ -95,7 +96,8 @@ int mccb_conv_act_step(const mccb_conv_t *args, void *state, void *y, void *stre
  * computed in fp32 and rounded once (sums over rows, batches and channels go on in fp64 or in a
  * fixed order of fp32 partial sums).
  *
- * B in [1, 65535], S in [0, 2^31), H in [1, 2^24] and a multiple of G, N in 1..32.
+ * B in [1, 65535], S in [0, 2^31), H in [1, 2^24], B H < 2^31, G in [1, 2^22] and a divisor of H, N in
+ * 1..32.
  * -----------------------------------------------------------------------------------------------*/
 typedef struct {
     int64_t S, B, H, N, G;

@@ -189,7 +189,8 @@ __global__ void __launch_bounds__(kThreads)
     __shared__ float part[kWaves][(W + 1) * V][kWave];
     const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
     int64_t b, h;
-    const bool on = lane_place<V>(blockIdx.x * (uint32_t)kWave + lane, B, H, per_batch, b, h);
+    const uint32_t column = blockIdx.z * gridDim.x + blockIdx.x;  // of 64 lanes
+    const bool on = lane_place<V>(column * (uint32_t)kWave + lane, B, H, per_batch, b, h);
     const int64_t strip = (int64_t)blockIdx.y * kWaves + wave;
     const int64_t t0 = strip * rows, t1 = t0 + rows < S ? t0 + rows : S;
     const int64_t BH = B * H, at = b * H + h;
@@ -521,7 +522,10 @@ template <int V>
 int launch_bwd(const mccb_conv_t *a, const void *gy, const int64_t *gs, const void *gfinal, void *gx,
                void *gstate, float *partial, const Strips &s, hipStream_t st) {
     const int64_t per = lanes_of(a->H, V), lanes = a->B * per;
-    const dim3 grid((unsigned)((lanes + kWave - 1) / kWave), (unsigned)s.n);
+    // a grid has less than 2^32 threads along an axis; the rest goes along z
+    const int64_t columns = (lanes + kWave - 1) / kWave, most = (int64_t)1 << 23;
+    const int64_t deep = (columns + most - 1) / most, across = (columns + deep - 1) / deep;
+    const dim3 grid((unsigned)across, (unsigned)s.n, (unsigned)deep);
     return by_form(a, [&](auto dt, auto w, auto silu) {
         hipLaunchKernelGGL((conv_act_bwd<decltype(dt)::value, decltype(w)::value,
                                          decltype(silu)::value, V>),

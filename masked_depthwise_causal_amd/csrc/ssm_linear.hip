@@ -835,12 +835,13 @@ int by_dtype(int dtype, F f) {
 
 // Zeros for a gradient that sums no rows.
 __global__ void __launch_bounds__(256) fill_zero(uint16_t *p, int64_t n) {
-    const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (id < n) p[id] = 0;
+    for (int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x; id < n; id += (int64_t)gridDim.x * 256) p[id] = 0;
 }
 int zero(void *p, int64_t n, hipStream_t st) {
     if (!p) return MCCB_OK;
-    hipLaunchKernelGGL(fill_zero, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, (uint16_t *)p, n);
+    const int64_t blocks = (n + 255) / 256, most = (int64_t)1 << 16;
+    hipLaunchKernelGGL(fill_zero, dim3((unsigned)(blocks < most ? blocks : most)), dim3(256), 0, st,
+                       (uint16_t *)p, n);
     return launched();
 }
 

@@ -857,28 +857,29 @@ __global__ void __launch_bounds__(NW *kWave, 2)
     }
 }
 
-// gB and gC: the sums of each group's blocks, in their order; a thread for each (row, batch, group,
-// which, n), n fastest.
+// gB and gC: the sums of each group's blocks, in their order; (row, batch, group, which, n), n fastest, go
+// round the threads.
 template <int DT>
 __global__ void __launch_bounds__(256)
     scan_sum_bc(const float *__restrict__ pbc, const int64_t *__restrict__ lengths, int64_t S,
                 int64_t pbc_rows, int64_t nb, int N, int NP, int G, int per_group, uint16_t *__restrict__ gB,
                 uint16_t *__restrict__ gC) {
-    const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int64_t rows = S * nb;
-    const int n = (int)(id % NP), which = (int)(id / NP % 2);
-    const int64_t rg = id / (2 * NP);  // group slowest, so that neighbours read one block's sums
-    const int64_t row = rg % rows, g = rg / rows;
-    if (g >= G || n >= N) return;
-    const int64_t t = row / nb, b = row - t * nb;
-    float s = 0.0f;
-    if (!lengths || t < lengths[b]) {
-        const int64_t block = pbc_rows * nb;
-        const float *p = pbc + ((g * per_group * block + row) * 2 + which) * NP + n;
+    const int64_t rows = S * nb, all = rows * G * 2 * NP;
+    for (int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x; id < all; id += (int64_t)gridDim.x * 256) {
+        const int n = (int)(id % NP), which = (int)(id / NP % 2);
+        const int64_t rg = id / (2 * NP);  // group slowest, so that neighbours read one block's sums
+        const int64_t row = rg % rows, g = rg / rows;
+        if (n >= N) continue;
+        const int64_t t = row / nb, b = row - t * nb;
+        float s = 0.0f;
+        if (!lengths || t < lengths[b]) {
+            const int64_t block = pbc_rows * nb;
+            const float *p = pbc + ((g * per_group * block + row) * 2 + which) * NP + n;
 #pragma unroll 8
-        for (int i = 0; i < per_group; ++i) s += p[(int64_t)i * block * 2 * NP];
+            for (int i = 0; i < per_group; ++i) s += p[(int64_t)i * block * 2 * NP];
+        }
+        (which ? gC : gB)[(row * G + g) * N + n] = from_f32<DT>(s);
     }
-    (which ? gC : gB)[(row * G + g) * N + n] = from_f32<DT>(s);
 }
 
 // gA, gD and gdt_bias: [P][(N+2) H] doubles over P.
@@ -969,8 +970,9 @@ __global__ void __launch_bounds__(kWave)
 int check_scan(const mccb_scan_t *a, bool token) {
     if (!a) return MCCB_ERR_PARAM_NULLPTR;
     if (a->dtype != MCCB_BF16 && a->dtype != MCCB_FP16) return MCCB_ERR_PARAM_INVALID;
+    // a group has a block of 128 to 512 threads at least, and a grid less than 2^32 along an axis
     if (a->B < 1 || a->B > kMaxBatch || a->S < 0 || a->S >= kMaxRows || a->H < 1 ||
-        a->H > kMaxWidth || a->N < 1 || a->N > 32 || a->G < 1 || a->H % a->G ||
+        a->H > kMaxWidth || a->N < 1 || a->N > 32 || a->G < 1 || a->G > (int64_t)1 << 22 || a->H % a->G ||
         a->B * a->H >= kMaxRows || (token && a->S != 1))
         return MCCB_ERR_SHAPE;
     return MCCB_OK;
@@ -1258,8 +1260,10 @@ int mccb_scan_backward(const mccb_scan_t *a, const mccb_scan_grads_t *g, const v
                 });
             });
             if (e != MCCB_OK || a->S == 0) return e;
-            const int64_t ids = a->S * a->B * a->G * 2 * NW * kPer;
-            hipLaunchKernelGGL((scan_sum_bc<DT>), dim3((unsigned)((ids + 255) / 256)), dim3(256), 0,
+            // a grid has less than 2^32 threads along an axis
+            const int64_t ids = a->S * a->B * a->G * 2 * NW * kPer, wanted = (ids + 255) / 256;
+            const int64_t most = (int64_t)1 << 22;
+            hipLaunchKernelGGL((scan_sum_bc<DT>), dim3((unsigned)(wanted < most ? wanted : most)), dim3(256), 0,
                                st, q.pbc, a->lengths, a->S, q.pbc_rows, a->B, (int)a->N, NW * kPer, (int)a->G,
                                (int)p.per_group, (uint16_t *)g->gradB, (uint16_t *)g->gradC);
             return launched();
