@@ -93,8 +93,9 @@ int mccb_conv_act_step(const mccb_conv_t *args, void *state, void *y, void *stre
  *   out[t] = y[t] silu(z[t])                         (without z: y[t])
  *
  * x, dt, z, out, Bm and Cm have the dtype, A, D, dt_bias and the states are fp32; everything is
- * computed in fp32 and rounded once (sums over rows, batches and channels go on in fp64 or in a
- * fixed order of fp32 partial sums).
+ * computed in fp32 and rounded once. Gradients' sums: gradB and gradC add 64 channels in fp32 and such
+ * blocks in fp64; gradA adds 16 rows in fp32, gradD and gradDtBias every 16th row of up to 512 and
+ * then those sums, and all go on in fp64 over rows (gradA), chunks and batches. Every order is fixed.
  *
  * B in [1, 65535], S in [0, 2^31), H in [1, 2^24], B H < 2^31, G in [1, 2^22] and a divisor of H, N in
  * 1..32.

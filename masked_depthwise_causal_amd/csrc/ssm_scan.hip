@@ -857,8 +857,8 @@ __global__ void __launch_bounds__(NW *kWave, 2)
     }
 }
 
-// gB and gC: the sums of each group's blocks, in their order; (row, batch, group, which, n), n fastest, go
-// round the threads.
+// gB and gC: the sums of each group's blocks (fp32, of 64 channels each) in their order, in fp64: there may
+// be 2^18 of them. (row, batch, group, which, n), n fastest, go round the threads.
 template <int DT>
 __global__ void __launch_bounds__(256)
     scan_sum_bc(const float *__restrict__ pbc, const int64_t *__restrict__ lengths, int64_t S,
@@ -871,14 +871,14 @@ __global__ void __launch_bounds__(256)
         const int64_t row = rg % rows, g = rg / rows;
         if (n >= N) continue;
         const int64_t t = row / nb, b = row - t * nb;
-        float s = 0.0f;
+        double s = 0.0;
         if (!lengths || t < lengths[b]) {
             const int64_t block = pbc_rows * nb;
             const float *p = pbc + ((g * per_group * block + row) * 2 + which) * NP + n;
 #pragma unroll 8
-            for (int i = 0; i < per_group; ++i) s += p[(int64_t)i * block * 2 * NP];
+            for (int i = 0; i < per_group; ++i) s += (double)p[(int64_t)i * block * 2 * NP];
         }
-        (which ? gC : gB)[(row * G + g) * N + n] = from_f32<DT>(s);
+        (which ? gC : gB)[(row * G + g) * N + n] = from_f32<DT>((float)s);
     }
 }
 
