@@ -122,6 +122,10 @@ def _call(function, stream, *args):
     """function(*args) of the front end, on `stream` if one is given."""
     if stream is None:
         return getattr(_module or ssm_module(), function)(*args)
+    # the front end launches on the current stream of the tensors' device, which would not be this one
+    device = next((a.device for a in args if isinstance(a, torch.Tensor)), stream.device)
+    if stream.device != device:
+        raise ValueError(f"stream lives on {stream.device}, the tensors on {device}")
     with torch.cuda.stream(stream):
         return getattr(_module or ssm_module(), function)(*args)
 
