@@ -117,6 +117,12 @@ Tensor bytes(uint64_t n, const Tensor &like) {
     return n ? make({(int64_t)n}, like, at::kByte) : Tensor();
 }
 
+// Tensors of the caller's that a call wrote: their version moves on, as an in-place operation's does.
+void wrote(std::initializer_list<Tensor> ts) {
+    for (const Tensor &t : ts)
+        if (t.defined() && !t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 PyObject *out(const Tensor &t) {
     if (!t.defined()) Py_RETURN_NONE;
     return THPVariable_Wrap(t);
@@ -176,6 +182,7 @@ PyObject *conv_forward(PyObject *const *v) {
     check_if("final_state", final_state, carried, type, c.x.device());
     if (with_state && !final_state.defined()) final_state = make(carried, c.x);
     ok(lib.conv_forward(&c.a, ptr(y), ptr(final_state), stream_of(c.x)), "mccb_conv_act_forward");
+    wrote({y, final_state});
     return with_state ? tuple({y, final_state}) : out(y);
 }
 
@@ -214,6 +221,7 @@ PyObject *conv_step(PyObject *const *v) {
     if (y.defined()) check("y", y, c.x.sizes(), type, c.x.device(), true);
     else y = make(c.x.sizes(), c.x);
     ok(lib.conv_step(&c.a, ptr(state), ptr(y), stream_of(c.x)), "mccb_conv_act_step");
+    wrote({state, y});
     return out(y);
 }
 
@@ -293,6 +301,7 @@ PyObject *scan_forward(PyObject *const *v) {
     const Tensor ws = bytes(n, c.x);
     ok(lib.scan_forward(&c.a, ptr(y), (float *)ptr(final_state), ptr(saved), ptr(ws), n, stream_of(c.x)),
        "mccb_scan_forward");
+    wrote({y, final_state});
     if (with_state) return with_saved ? tuple({y, final_state, saved}) : tuple({y, final_state});
     return with_saved ? tuple({y, saved}) : out(y);
 }
@@ -339,6 +348,7 @@ PyObject *scan_step(PyObject *const *v) {
     if (y.defined()) check("out", y, c.x.sizes(), c.x.scalar_type(), c.x.device(), true);
     else y = make(c.x.sizes(), c.x);
     ok(lib.scan_step(&c.a, (float *)ptr(state), ptr(y), stream_of(c.x)), "mccb_scan_step");
+    wrote({state, y});
     return out(y);
 }
 
@@ -408,6 +418,7 @@ PyObject *linear_forward(PyObject *const *v) {
     const Tensor ws = bytes(n, c.x);
     ok(lib.linear_forward(&c.a, ptr(residual), residual_ld, ptr(y), ptr(pre), ptr(ws), n, stream_of(c.x)),
        "mccb_linear_forward");
+    wrote({y});
     return pre.defined() ? tuple({y, pre}) : out(y);
 }
 
