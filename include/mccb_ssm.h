@@ -163,6 +163,7 @@ typedef struct {
     const void *weight; /* [N,K] */
     const void *bias;   /* [N] or NULL */
     int64_t x_ld, weight_ld;
+    int32_t pre_fp32;   /* nonzero: pre is fp32, else of the dtype */
 } mccb_linear_t;
 
 /* out [M,N] contiguous; pre [M,N] contiguous or NULL: the pre-activation, for the backward;
@@ -172,11 +173,12 @@ int mccb_linear_forward(const mccb_linear_t *args, const void *residual, int64_t
                         void *out, void *pre, void *workspace, uint64_t workspace_size,
                         void *stream);
 
-/* With g = gradOut act'(pre) (rounded to the dtype once, since the matrix instructions take 16-bit
- * operands; gradBias sums it before that rounding): gradX = g weight [M,K], gradWeight = g^T x
- * [N,K], gradBias = column sums [N]. Each may be NULL and is then not computed; gradient of the
- * residual is gradOut itself. pre is needed unless the activation is none. gradOut's rows are
- * gout_ld elements apart. */
+/* With g = gradOut act'(pre): gradX = g weight [M,K], gradWeight = g^T x [N,K], gradBias = column
+ * sums [N]. Each may be NULL and is then not computed; gradient of the residual is gradOut itself.
+ * pre is needed unless the activation is none. gradOut's rows are gout_ld elements apart.
+ * Two roundings to the dtype lie between these gradients and the exact ones, besides their own:
+ *   - g's, since the matrix instructions take 16-bit operands (gradBias sums it before);
+ *   - pre's, unless it is kept in fp32: act' is then taken up to half a step of pre away. */
 int mccb_linear_backward_get_workspace_size(const mccb_linear_t *args, uint64_t *workspace_size);
 int mccb_linear_backward(const mccb_linear_t *args, const void *gradOut, int64_t gout_ld,
                          const void *pre, void *gradX, void *gradWeight, void *gradBias,

@@ -398,7 +398,7 @@ void linear_args(Linear &c, PyObject *x, PyObject *weight, PyObject *bias, long 
     c.shape.back() = c.a.N;
 }
 
-// (x, weight, bias, act, residual, return_pre, out)
+// (x, weight, bias, act, residual, return_pre, out, whether pre is fp32)
 PyObject *linear_forward(PyObject *const *v) {
     Linear c;
     linear_args(c, v[0], v[1], v[2], PyLong_AsLong(v[3]));
@@ -412,7 +412,8 @@ PyObject *linear_forward(PyObject *const *v) {
     Tensor y = maybe(v[6], "out"), pre;
     if (y.defined()) check("out", y, c.shape, type, c.x.device(), true);
     else y = make(c.shape, c.x);
-    if (v[5] == Py_True) pre = make(c.shape, c.x);
+    c.a.pre_fp32 = v[7] == Py_True;
+    if (v[5] == Py_True) pre = make(c.shape, c.x, c.a.pre_fp32 ? at::kFloat : type);
     uint64_t n = 0;
     ok(lib.linear_forward_size(&c.a, &n), "mccb_linear_forward_get_workspace_size");
     const Tensor ws = bytes(n, c.x);
@@ -431,7 +432,8 @@ PyObject *linear_backward(PyObject *const *v) {
     check("gradOut", go, c.shape, type, c.x.device(), false);
     int64_t rows, go_ld;
     rows_of("gradOut", go, rows, go_ld);
-    check_if("pre", pre, c.shape, type, c.x.device());
+    c.a.pre_fp32 = pre.defined() && pre.scalar_type() == at::kFloat;
+    check_if("pre", pre, c.shape, c.a.pre_fp32 ? at::kFloat : type, c.x.device());
     uint64_t n = 0;
     ok(lib.linear_backward_size(&c.a, &n), "mccb_linear_backward_get_workspace_size");
     const Tensor gx = v[5] == Py_True ? make(c.x.sizes(), c.x) : Tensor();
@@ -503,7 +505,7 @@ PyMethodDef methods[] = {
     ENTRY(scan_forward, 15),
     ENTRY(scan_backward, 14),
     ENTRY(scan_step, 11),
-    ENTRY(linear_forward, 7),
+    ENTRY(linear_forward, 8),
     ENTRY(linear_backward, 8),
     {nullptr, nullptr, 0, nullptr},
 };

@@ -61,9 +61,10 @@ __device__ __align__(16) const uint32_t zero_chunk[4] = {0, 0, 0, 0};
 // What happens to a finished sum of out[m, n].
 struct Epilogue {
     const uint16_t *bias, *residual;
-    uint16_t *out, *pre;
+    uint16_t *out;
+    void *pre;  // of the dtype, or fp32
     int64_t residual_ld, N;
-    int act;
+    int act, pre_fp32;
 };
 
 template <int ACT>
@@ -85,6 +86,29 @@ __device__ static inline void get8(const uint16_t *p, int count, float (&f)[8]) 
     }
 }
 
+// Eight adjacent floats, from any one on.
+typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
+__device__ static inline void put_floats(float *p, int count, const float (&v)[8]) {
+    if (count == 8) {
+        *(f32x4_any *)p = f32x4_any{v[0], v[1], v[2], v[3]};
+        *(f32x4_any *)(p + 4) = f32x4_any{v[4], v[5], v[6], v[7]};
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < count) p[i] = v[i];
+    }
+}
+__device__ static inline void get_floats(const float *p, int count, float (&f)[8]) {
+    if (count == 8) {
+        const f32x4_any lo = *(const f32x4_any *)p, hi = *(const f32x4_any *)(p + 4);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = lo[i], f[4 + i] = hi[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = i < count ? p[i] : 0.0f;
+    }
+}
+
 // The sums v of eight adjacent columns of row m from column n, with the bias and the residual there.
 template <int DT>
 __device__ static inline void finish8(const Epilogue &e, int64_t m, int64_t n, int count, float (&v)[8],
@@ -103,7 +127,10 @@ __device__ static inline void finish8(const Epilogue &e, int64_t m, int64_t n, i
     };
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] += bias[i];
-    if (e.pre) put(e.pre + m * e.N + n);
+    if (e.pre) {
+        if (e.pre_fp32) put_floats((float *)e.pre + m * e.N + n, count, v);
+        else put((uint16_t *)e.pre + m * e.N + n);
+    }
     switch (e.act) {
         case MCCB_ACT_RELU: act8<MCCB_ACT_RELU>(v); break;
         case MCCB_ACT_SILU: act8<MCCB_ACT_SILU>(v); break;
@@ -566,16 +593,19 @@ __global__ void __launch_bounds__(WAVES *kWave)
 // rows and / or by columns, and the column sums of 64 rows. One 64x64 tile a block; bound by memory
 // (4096 x 4096, g by rows and sums: 24 us, 4.2 TB/s).
 struct Turn {
-    const uint16_t *src, *pre;
+    const uint16_t *src;
+    const void *pre;
     int64_t ld, R, C;
     uint16_t *rows;     // [R, rows_ld] or NULL
     uint16_t *columns;  // [C, columns_ld] or NULL, zeros past R
     float *sums;        // [row tiles][C] or NULL
     int64_t rows_ld, columns_ld;
-    int act;
+    int act, pre_fp32;
 };
 
-template <int DT>
+// PRE: without pre, with one of the dtype, of fp32.
+enum { kNoPre, kPre16, kPre32 };
+template <int DT, int PRE>
 __global__ void __launch_bounds__(256)
     turn(Turn t) {
     __shared__ uint16_t tile[64][64 + 2];
@@ -590,24 +620,23 @@ __global__ void __launch_bounds__(256)
         u16x8 v = {0, 0, 0, 0, 0, 0, 0, 0};
         if (r0 + r < t.R && left > 0) {
             const uint16_t *p = t.src + (r0 + r) * t.ld + c0 + c;
-            const uint16_t *z = t.pre ? t.pre + (r0 + r) * t.C + c0 + c : nullptr;
-            u16x8 q = {0, 0, 0, 0, 0, 0, 0, 0};
-            if (left >= 8) {
+            const int64_t at = (r0 + r) * t.C + c0 + c;
+            const int count = left < 8 ? (int)left : 8;
+            if (count == 8) {
                 v = *(const HVec<8>::t *)p;
-                if (z) q = *(const HVec<8>::t *)z;
             } else {
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    if (i < left) {
-                        v[i] = p[i];
-                        if (z) q[i] = z[i];
-                    }
+                    if (i < count) v[i] = p[i];
             }
+            float z[8];
+            if (PRE == kPre16) get8<DT>((const uint16_t *)t.pre + at, count, z);
+            if (PRE == kPre32) get_floats((const float *)t.pre + at, count, z);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 float f = to_f32<DT>(v[i]);
-                if (z) {
-                    f *= act_slope_f(to_f32<DT>(q[i]), t.act);
+                if (PRE != kNoPre) {
+                    f *= act_slope_f(z[i], t.act);
                     v[i] = from_f32<DT>(f);
                 }
                 s[i] += f;
@@ -775,7 +804,9 @@ int launch_product(const uint16_t *p, int64_t p_ld, const uint16_t *q, int64_t q
 template <int DT>
 int launch_turn(const Turn &t, hipStream_t st) {
     const dim3 grid((unsigned)((t.C + 63) / 64), (unsigned)((t.R + 63) / 64));
-    hipLaunchKernelGGL((turn<DT>), grid, dim3(256), 0, st, t);
+    if (!t.pre) hipLaunchKernelGGL((turn<DT, kNoPre>), grid, dim3(256), 0, st, t);
+    else if (!t.pre_fp32) hipLaunchKernelGGL((turn<DT, kPre16>), grid, dim3(256), 0, st, t);
+    else hipLaunchKernelGGL((turn<DT, kPre32>), grid, dim3(256), 0, st, t);
     return launched();
 }
 
@@ -873,14 +904,14 @@ int mccb_linear_forward(const mccb_linear_t *a, const void *residual, int64_t re
     rc = check_workspace(ws, ws_size, need);
     if (rc != MCCB_OK) return rc;
     in[3] = {residual, r_bytes};
-    const uint64_t n_out = (uint64_t)a->M * (uint64_t)a->N * 2;
-    const Span outs[3] = {{out, n_out}, {pre, n_out}, {ws, need}};
-    if (misaligned(out, 2) || misaligned(pre, 2) || outputs_clash(in, 4, outs, 3))
+    const uint64_t n_out = (uint64_t)a->M * (uint64_t)a->N, pre_size = a->pre_fp32 ? 4 : 2;
+    const Span outs[3] = {{out, n_out * 2}, {pre, n_out * pre_size}, {ws, need}};
+    if (misaligned(out, 2) || misaligned(pre, pre_size) || outputs_clash(in, 4, outs, 3))
         return MCCB_ERR_PARAM_INVALID;
     if (a->M == 0) return MCCB_OK;
     const hipStream_t st = (hipStream_t)stream;
     const Epilogue e{(const uint16_t *)a->bias, (const uint16_t *)residual, (uint16_t *)out,
-                     (uint16_t *)pre, residual_ld, a->N, a->activation};
+                     pre, residual_ld, a->N, a->activation, a->pre_fp32};
     return by_dtype(a->dtype, [&](auto dt) {
         return launch_product<decltype(dt)::value>((const uint16_t *)a->x, a->x_ld,
                                                    (const uint16_t *)a->weight, a->weight_ld, a->M,
@@ -906,13 +937,14 @@ int mccb_linear_backward(const mccb_linear_t *a, const void *gout, int64_t gout_
     if (rc != MCCB_OK) return rc;
     const int64_t size[2] = {a->M, a->N}, stride[2] = {gout_ld, 1};
     uint64_t g_bytes = 0, need = 0;
-    if (!extent(2, size, stride, 2, &g_bytes) || misaligned(gout, 2) || misaligned(pre, 2))
+    const uint64_t pre_size = a->pre_fp32 ? 4 : 2;
+    if (!extent(2, size, stride, 2, &g_bytes) || misaligned(gout, 2) || misaligned(pre, pre_size))
         return MCCB_ERR_PARAM_INVALID;
     mccb_linear_backward_get_workspace_size(a, &need);
     rc = check_workspace(ws, ws_size, need);
     if (rc != MCCB_OK) return rc;
     in[3] = {gout, g_bytes};
-    in[4] = {pre, (uint64_t)a->M * (uint64_t)a->N * 2};
+    in[4] = {pre, (uint64_t)a->M * (uint64_t)a->N * pre_size};
     const Span outs[4] = {{gx, (uint64_t)a->M * (uint64_t)a->K * 2},
                           {gw, (uint64_t)a->N * (uint64_t)a->K * 2},
                           {gb, (uint64_t)a->N * 2},
@@ -940,9 +972,9 @@ int mccb_linear_backward(const mccb_linear_t *a, const void *gout, int64_t gout_
         // tiles read w, g and x as they lie; skinny products and unaligned rows need them turned
         const bool w_lies = a->M > 64 && direct_rows(g, g_ld, a->N) && direct_rows(w, a->weight_ld, a->K);
         const bool x_lies = a->N > 64 && direct_rows(g, g_ld, a->N) && direct_rows(x, a->x_ld, a->K);
-        const Turn tg{(const uint16_t *)gout, slope ? (const uint16_t *)pre : nullptr, gout_ld, a->M, a->N,
+        const Turn tg{(const uint16_t *)gout, slope ? pre : nullptr, gout_ld, a->M, a->N,
                       slope && (gx || (gw && x_lies)) ? g_rows : nullptr, gw && !x_lies ? g_cols : nullptr,
-                      gb ? sums : nullptr, Np, Mp, a->activation};
+                      gb ? sums : nullptr, Np, Mp, a->activation, a->pre_fp32};
         int r = tg.rows || tg.columns || tg.sums ? launch_turn<DT>(tg, st) : MCCB_OK;
         if (r == MCCB_OK && gb) {
             hipLaunchKernelGGL((sum_columns<DT>), dim3((unsigned)((a->N + 63) / 64)), dim3(256), 0, st,
@@ -950,17 +982,17 @@ int mccb_linear_backward(const mccb_linear_t *a, const void *gout, int64_t gout_
             r = launched();
         }
         if (r == MCCB_OK && gx) {
-            const Turn tw{w, nullptr, a->weight_ld, a->N, a->K, nullptr, w_cols, nullptr, 0, Np, MCCB_ACT_NONE};
+            const Turn tw{w, nullptr, a->weight_ld, a->N, a->K, nullptr, w_cols, nullptr, 0, Np, MCCB_ACT_NONE, 0};
             if (!w_lies) r = launch_turn<DT>(tw, st);
-            const Epilogue e{nullptr, nullptr, (uint16_t *)gx, nullptr, 0, a->K, MCCB_ACT_NONE};
+            const Epilogue e{nullptr, nullptr, (uint16_t *)gx, nullptr, 0, a->K, MCCB_ACT_NONE, 0};
             if (r == MCCB_OK)
                 r = launch_product<DT>(g, g_ld, w_lies ? w : w_cols, w_lies ? a->weight_ld : Np, a->M, a->K,
                                        a->N, e, at + l.partial, st, false, w_lies);
         }
         if (r == MCCB_OK && gw) {
-            const Turn tx{x, nullptr, a->x_ld, a->M, a->K, nullptr, x_cols, nullptr, 0, Mp, MCCB_ACT_NONE};
+            const Turn tx{x, nullptr, a->x_ld, a->M, a->K, nullptr, x_cols, nullptr, 0, Mp, MCCB_ACT_NONE, 0};
             if (!x_lies) r = launch_turn<DT>(tx, st);
-            const Epilogue e{nullptr, nullptr, (uint16_t *)gw, nullptr, 0, a->K, MCCB_ACT_NONE};
+            const Epilogue e{nullptr, nullptr, (uint16_t *)gw, nullptr, 0, a->K, MCCB_ACT_NONE, 0};
             if (r == MCCB_OK)
                 r = launch_product<DT>(x_lies ? g : g_cols, x_lies ? g_ld : Mp, x_lies ? x : x_cols,
                                        x_lies ? a->x_ld : Mp, a->N, a->K, a->M, e, at + l.partial, st,

@@ -59,7 +59,8 @@ class ScanGradArgs(ctypes.Structure):
 
 class LinearArgs(ctypes.Structure):
     """mccb_linear_t."""
-    _fields_ = _fields("i: M K N; w: dtype activation; p: x weight bias; i: x_ld weight_ld")
+    _fields_ = _fields("i: M K N; w: dtype activation; p: x weight bias; i: x_ld weight_ld; "
+                       "w: pre_fp32")
 
 
 _SIGNATURES = {
@@ -216,19 +217,24 @@ class LinearGrads(NamedTuple):
 
 
 def linear_forward(x, weight, bias=None, activation=None, residual=None, return_pre=False, out=None,
-                   stream=None):
+                   stream=None, pre_dtype=None):
     """out [...,N] = activation(x weight^T + bias) + residual; x [...,K], weight [N,K], bias [N],
     residual [...,N], activation None, "relu", "silu", "gelu" (tanh form) or "softplus". The rows of
     x and residual are contiguous and evenly spaced. With `return_pre` the result is (out, pre),
-    pre = x weight^T + bias as linear_backward needs it."""
+    pre = x weight^T + bias as linear_backward needs it, in `pre_dtype`: x's (the default) or
+    torch.float32, which twice as many bytes keep from rounding."""
+    if pre_dtype is not None and pre_dtype not in (torch.float32, x.dtype):
+        raise ValueError(f"pre_dtype {pre_dtype} not supported (x's dtype, float32)")
     return _call("linear_forward", stream, x, weight, bias, _activation(activation, (0, 1, 2, 3, 4)),
-                 residual, bool(return_pre), out)
+                 residual, bool(return_pre), out, pre_dtype == torch.float32)
 
 
 def linear_backward(gradOut, x, weight, pre=None, activation=None, grad_x=True, grad_weight=True,
                     grad_bias=True, stream=None) -> LinearGrads:
     """Gradients of linear_forward for gradOut [...,N]: of x, weight and bias, as asked for. `pre` is
-    linear_forward's (not needed without an activation). The residual's gradient is gradOut."""
+    linear_forward's, in either type (not needed without an activation): the activation's slope is
+    taken at it as it was rounded. gradOut times that slope is rounded to gradOut's type for the
+    products. The residual's gradient is gradOut."""
     return LinearGrads(*_call("linear_backward", stream, gradOut, x, weight, pre,
                               _activation(activation, (0, 1, 2, 3, 4)), bool(grad_x),
                               bool(grad_weight), bool(grad_bias)))
