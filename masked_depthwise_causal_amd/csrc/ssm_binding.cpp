@@ -262,7 +262,7 @@ void scan_args(Scan &c, PyObject *const *v, bool token) {
     check("C", c.C, coef, type, device, false);
     check_if("D", c.D, {a.H}, at::kFloat, device);
     check_if("dt_bias", c.bias, {a.H}, at::kFloat, device);
-    a.softplus = PyObject_IsTrue(v[8]) == 1;
+    a.softplus = v[8] == Py_True;
     a.x = ptr(c.x), a.dt = ptr(c.dt), a.z = ptr(c.z), a.Bm = ptr(c.B), a.Cm = ptr(c.C);
     strides3(c.x, a.x_stride, token);
     strides3(c.dt, a.dt_stride, token);

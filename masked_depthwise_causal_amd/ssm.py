@@ -189,7 +189,7 @@ def scan_forward(x, dt, A, B, C, D=None, z=None, dt_bias=None, softplus=True, le
     a tuple of it with the state after each sequence's last row (`return_state`) and what
     scan_backward needs (`return_saved`). Rows at or past `lengths` (int64 [B] on the device) give
     zeros and leave the state alone."""
-    return _call("scan_forward", stream, x, dt, A, B, C, D, z, dt_bias, softplus, lengths, state,
+    return _call("scan_forward", stream, x, dt, A, B, C, D, z, dt_bias, bool(softplus), lengths, state,
                  bool(return_state), bool(return_saved), out, final_state)
 
 
@@ -198,15 +198,15 @@ def scan_backward(gradOut, x, dt, A, B, C, saved, D=None, z=None, dt_bias=None, 
     """Gradients of scan_forward with the same arguments and what it saved: of every input that was
     given. gradOut [S,B,H] may be strided; gradFinalState [B,N,H] fp32 is the gradient of the
     returned state, if one flows back."""
-    return ScanGrads(*_call("scan_backward", stream, x, dt, A, B, C, D, z, dt_bias, softplus, lengths,
-                            state, gradOut, saved, gradFinalState))
+    return ScanGrads(*_call("scan_backward", stream, x, dt, A, B, C, D, z, dt_bias, bool(softplus),
+                            lengths, state, gradOut, saved, gradFinalState))
 
 
 def scan_step(state, x, dt, A, B, C, D=None, z=None, dt_bias=None, softplus=True, out=None,
               stream=None):
     """One token: out [B,H] from x, dt, z [B,H], B and C [B,G,N] or [B,N]; `state` [B,N,H] fp32 is
     updated in place."""
-    return _call("scan_step", stream, x, dt, A, B, C, D, z, dt_bias, softplus, state, out)
+    return _call("scan_step", stream, x, dt, A, B, C, D, z, dt_bias, bool(softplus), state, out)
 
 
 # -- matrix product with its epilogue ----------------------------------------------------------------

@@ -1,4 +1,4 @@
-"""The `stream` argument of the state space block's operators."""
+"""How the state space block's operators are called: the stream they run on, and flags."""
 from __future__ import annotations
 
 import pytest
@@ -69,3 +69,16 @@ def test_calls_run_on_the_stream_that_is_given():
     side.synchronize()
     for k in want:
         assert torch.equal(got[k], want[k]), k
+
+
+def test_flags_are_read_before_anything_runs():
+    """A flag without a truth value is refused first, not once the kernels are enqueued."""
+    x, c = torch.zeros((4, 2, 8), dtype=BF), torch.zeros((4, 2, 1), dtype=BF)
+    A = torch.zeros((1, 8))
+    flag = torch.zeros(2)
+    with pytest.raises(RuntimeError, match="Boolean value"):
+        mdc.scan_forward(x, x, A, c, c, softplus=flag)
+    with pytest.raises(RuntimeError, match="Boolean value"):
+        mdc.scan_backward(x, x, x, A, c, c, c, softplus=flag)
+    with pytest.raises(RuntimeError, match="Boolean value"):
+        mdc.scan_step(torch.zeros((2, 1, 8)), x[0], x[0], A, c[0], c[0], softplus=flag)
