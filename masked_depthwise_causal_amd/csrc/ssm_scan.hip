@@ -934,16 +934,18 @@ __global__ void __launch_bounds__(kWave)
     const float d = a.softplus ? softplus_f(t) : t;
     float y = a.D ? a.D[h] * x : 0.0f;
     const float dx = d * x, d2 = d * kLog2e;
-    // no step leaves the state alone, also with an infinite rate (9.95 us; with
-    // finite_rate on every rate 10.3)
-    const bool still = d == 0.0f;
-    auto decay = [&](float rate) { return still ? 1.0f : exp2_f(d2 * rate); };
+    // No step leaves the state alone, also with an infinite rate. Rates are bounded where a lane has none:
+    // always, the token is 5 to 10 % slower.
+    if (__builtin_amdgcn_ballot_w64(d == 0.0f)) {
+#pragma unroll
+        for (int n = 0; n < NMAX; ++n) r[n] = finite_rate(r[n]);
+    }
     if (one_group) {
 #pragma unroll
         for (int n = 0; n < NMAX; ++n) {
             const float Bn = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(mine), n));
             const float Cn = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(mine), n + 32));
-            s[n] = __builtin_fmaf(decay(r[n]), s[n], dx * Bn);
+            s[n] = __builtin_fmaf(exp2_f(d2 * r[n]), s[n], dx * Bn);
             if (n < a.N) y = __builtin_fmaf(Cn, s[n], y);
         }
     } else {
@@ -953,7 +955,7 @@ __global__ void __launch_bounds__(kWave)
             const int row = n < a.N ? n : a.N - 1;
             const float Bn = to_f32<DT>(a.B.p[b * a.B.b + g * a.B.g + row * a.B.n]);
             const float Cn = to_f32<DT>(a.C.p[b * a.C.b + g * a.C.g + row * a.C.n]);
-            s[n] = __builtin_fmaf(decay(r[n]), s[n], dx * Bn);
+            s[n] = __builtin_fmaf(exp2_f(d2 * r[n]), s[n], dx * Bn);
             if (n < a.N) y = __builtin_fmaf(Cn, s[n], y);
         }
     }
