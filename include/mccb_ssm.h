@@ -50,8 +50,9 @@ typedef enum {
  *   y[t,b,h] = act(bias[h] + sum_{k<W} weight[k,h] x[t-W+1+k,b,h]),
  *
  * rows before the first taken from `state` (state[r] is row r-W+1), or zero without one. Products
- * of two 16-bit values are exact in fp32; the sum, the activation and the gradients are fp32 (the
- * sums over rows and batches fp64 from one strip of rows to the next), rounded once.
+ * of two 16-bit values are exact in fp32; the sum, the activation and the gradients are fp32, rounded
+ * once. gradWeight and gradBias add strips of up to 64 rows, and four of those, in fp32 and go on in
+ * fp64 over rows and batches (strips grow from S = 65535 * 64 on).
  *
  * B in [1, 65535], S in [0, 2^31), H in [1, 2^24], B H < 2^31, W in 1..4; activation none or silu.
  * -----------------------------------------------------------------------------------------------*/

@@ -172,10 +172,10 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 // Backward. A strip's lane walks its rows and the W-1 after it: g of row i completes gx of row
-// i-W+1. Its own rows add to the weight's and bias's sums (fp32 over the strip's rows). A block has 64
-// lanes' columns and four consecutive strips, a wave each, whose sums it adds and writes to the
-// workspace as [block of strips][b][W+1][H]; the second kernel adds them over blocks and batches in
-// fp64, in a fixed order. (With a wave for every strip's sums they were a fifth of the traffic.)
+// i-W+1. Its own rows add to the weight's and bias's sums, in fp32 over the strip's rows (64 at most, up
+// to S of 4 million). A block has 64 lanes' columns and four consecutive strips, a wave each, whose sums
+// it adds in fp32 and writes to the workspace as [block of strips][b][W+1][H]; the second kernel adds
+// them over blocks and batches in fp64, in a fixed order. (With a wave for every strip's sums they were a fifth of the traffic.)
 template <int DT, int W, bool SILU, int V>
 __global__ void __launch_bounds__(kThreads)
     conv_act_bwd(Rows x, Rows gy, const uint16_t *__restrict__ weight,

@@ -13,6 +13,10 @@
 //   skinny  (M up to 64): bound by reading w once. A wave takes 16 rows of w and every WAVES-th
 //           part of the contraction, straight from memory into 16x16x32 matrix instructions.
 //           M=4 K=5120 N=4096 with w not in any cache: 11.7 us, 3.6 TB/s.
+// Rounded to 16 bits on the way to the gradients: g, a matrix instruction's operand (kept in two 16-bit
+// terms it would double the backward's products), and pre, unless the caller asks for it in fp32. At
+// M=4096 K=5120 N=4096 with silu, bf16, gx and gw are 0.0024 off in relation to their norm, of which
+// their own rounding is 0.0017; pre in fp32 makes that 0.00235 and takes 12 us more of 535.
 // The epilogue works on fp32 sums staged through LDS, so that bias, residual, pre and out are read
 // and written as whole rows.
 //

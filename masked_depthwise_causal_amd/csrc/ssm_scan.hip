@@ -24,11 +24,13 @@
 // exp(A sum d), the second kernel's blocks fold the chunks before theirs into their initial state.
 // The backward does the same from the other end for the gradient of the state.
 //
-// Bound by instruction issue, not by memory: each of N states of each element takes an exp (8 cycles of
-// a SIMD for 64 lanes) and, forward, about 4 multiply-adds (2.5 cycles each), backward 12. S=2048 B=8
-// H=4096 N=16 bf16, gated: forward 326 us (1.6 TB/s), backward 774 us, sums of gB, gC and the parameters
-// 33; the counters put 91 to 93 % of the issue slots in use. The single token (B=64 H=5120) is bound by
-// its state: 9.2 us, 4.9 TB/s.
+// Bound by vector instructions, not by memory: each of N states of each element takes an exp (8.5 cycles
+// of a SIMD for 64 lanes, measured) and, forward, about 4 multiply-adds, backward 12 (2.8 cycles with
+// three vector registers, 4.4 with a scalar one). S=2048 B=8 H=4096 N=16 bf16, gated: forward 326 us
+// (1.6 TB/s), backward 775 us, sums of gB, gC and the parameters 34. By the counters a wave takes 480
+// vector instructions a tile forward and 1420 backward, at 4.7 and 4.5 cycles on average; they are
+// active in 72 and 89 % of the cycles. The single token (B=64 H=5120) is bound by its state: 9.2 us,
+// 4.9 TB/s, of which the last-level cache has most from call to call.
 #include "ssm_common.h"
 
 using namespace ssm;
@@ -599,8 +601,10 @@ __global__ void __launch_bounds__(NW *kWave)
     if (p.wave == 0 && p.on) q.dsum[((int64_t)blockIdx.z * a.nb + p.b) * a.H + p.h] = total;
 }
 
-// Two waves a SIMD: a single one issues an fp32 instruction every five cycles, two together one every
-// two and a half. The tile's history takes 128 registers of the 256 that leaves.
+// Two waves a SIMD: a single one issues a multiply-add every 5.1 cycles, two together one every 3.3, four
+// every 2.8. The tile's history takes 128 registers of the 256 that leaves. Up to 8 states (two waves
+// with eight channels a thread) the rest does not: 66 registers are spilled, 36 without a gate, and 143
+// and 89 where channels are taken one by one (16 states: none; one by one 24 and 5).
 template <int DT, int NW, bool GATE, int ROWS>
 __global__ void __launch_bounds__(NW *kWave, 2)
     scan_bwd(ScanIn a, ScanGrad q) {

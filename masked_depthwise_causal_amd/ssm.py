@@ -7,6 +7,9 @@ tensors are time-major ([S,B,...]) and may be strided views; weights and states 
 enqueue on `stream` (default: torch's current stream) and return without synchronizing. What a call
 allocates (outputs that are not given, workspaces) belongs to that stream. Nothing here builds an
 autograd graph: each backward is a call of its own.
+
+``ssm_lib()`` is the library itself, for calls of the C-ABI with device addresses; its argument structs are
+``ConvArgs``, ``ScanArgs``, ``ScanGradArgs`` and ``LinearArgs``.
 """
 from __future__ import annotations
 
