@@ -15,7 +15,8 @@ SRC = os.path.join(PKG, "csrc", "mccb.hip")
 LIB = os.environ.get("MCCB_LIBRARY") or os.path.join(PKG, "libmccb.so")
 INCLUDE = os.path.join(ROOT, "include")
 # the state space block's operators; MCCB_SSM_LIBRARY as above
-SSM_SRCS = [os.path.join(PKG, "csrc", f) for f in ("ssm_conv.hip", "ssm_scan.hip", "ssm_linear.hip")]
+SSM_SRCS = [os.path.join(PKG, "csrc", f) for f in ("ssm_conv.hip", "ssm_scan.hip", "ssm_linear.hip",
+                                                  "ssm_norm.hip")]
 SSM_LIB = os.environ.get("MCCB_SSM_LIBRARY") or os.path.join(PKG, "libmccb_ssm.so")
 BINDING_SRC = os.path.join(PKG, "csrc", "ssm_binding.cpp")
 BINDING = os.path.join(PKG, "_ssm.so")
