@@ -16,10 +16,11 @@ import ctypes
 import torch
 
 from ._lib import MccbError, Plan, Strides, lib, status_string  # noqa: F401
-from .ssm import (ACTIVATIONS, ConvGrads, LinearGrads, PostnormGrads, PrenormGrads,  # noqa: F401
-                  ScanGrads, conv_act_backward, conv_act_forward, conv_act_step, linear_backward,
-                  linear_forward, postnorm_backward, postnorm_forward, prenorm_backward,
-                  prenorm_forward, scan_backward, scan_forward, scan_step, ssm_lib)
+from .delta import (PostnormGrads, PrenormGrads, delta_lib, postnorm_backward,  # noqa: F401
+                    postnorm_forward, prenorm_backward, prenorm_forward)
+from .ssm import (ACTIVATIONS, ConvGrads, LinearGrads, ScanGrads,  # noqa: F401
+                  conv_act_backward, conv_act_forward, conv_act_step, linear_backward,
+                  linear_forward, scan_backward, scan_forward, scan_step, ssm_lib)
 
 MCCB_BF16, MCCB_FP16 = 0, 1
 MCCB_OK = 0

@@ -2,7 +2,10 @@
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
+
+import torch
 
 from . import build as _build
 
@@ -39,6 +42,28 @@ def load(path: str, env: str, build) -> ctypes.CDLL:
             raise OSError(f"{env}={path} does not exist")
         build()
     return ctypes.CDLL(path)
+
+
+def bound_module(name: str, path: str, build, library: ctypes.CDLL, functions):
+    """The compiled front end at `path`, built first if there is none, with the addresses of the library's
+    `functions`."""
+    if not os.path.exists(path):
+        build()
+    spec = importlib.util.spec_from_file_location(name, path)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    m.bind(MccbError, tuple(ctypes.cast(getattr(library, n), ctypes.c_void_p).value for n in functions))
+    return m
+
+
+def on_stream(function, stream, args):
+    """function(*args) of a front end, on `stream`."""
+    # it launches on the current stream of the tensors' device, which would not be this one
+    device = next((a.device for a in args if isinstance(a, torch.Tensor)), stream.device)
+    if stream.device != device:
+        raise ValueError(f"stream lives on {stream.device}, the tensors on {device}")
+    with torch.cuda.stream(stream):
+        return function(*args)
 
 
 def lib() -> ctypes.CDLL:

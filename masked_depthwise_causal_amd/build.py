@@ -1,5 +1,5 @@
-"""Compile the HIP libraries (libmccb.so, libmccb_ssm.so) for gfx950, and the binding of the second
-(_ssm.so), in-tree."""
+"""Compile the HIP libraries (libmccb.so, libmccb_ssm.so, libmccb_delta.so) for gfx950, and the bindings
+of the last two (_ssm.so, _delta.so), in-tree."""
 from __future__ import annotations
 
 import os
@@ -15,11 +15,15 @@ SRC = os.path.join(PKG, "csrc", "mccb.hip")
 LIB = os.environ.get("MCCB_LIBRARY") or os.path.join(PKG, "libmccb.so")
 INCLUDE = os.path.join(ROOT, "include")
 # the state space block's operators; MCCB_SSM_LIBRARY as above
-SSM_SRCS = [os.path.join(PKG, "csrc", f) for f in ("ssm_conv.hip", "ssm_scan.hip", "ssm_linear.hip",
-                                                  "ssm_norm.hip")]
+SSM_SRCS = [os.path.join(PKG, "csrc", f) for f in ("ssm_conv.hip", "ssm_scan.hip", "ssm_linear.hip")]
 SSM_LIB = os.environ.get("MCCB_SSM_LIBRARY") or os.path.join(PKG, "libmccb_ssm.so")
 BINDING_SRC = os.path.join(PKG, "csrc", "ssm_binding.cpp")
 BINDING = os.path.join(PKG, "_ssm.so")
+# the gated delta rule and the norms; MCCB_DELTA_LIBRARY as above
+DELTA_SRCS = [os.path.join(PKG, "csrc", f) for f in ("delta_norm.hip",)]
+DELTA_LIB = os.environ.get("MCCB_DELTA_LIBRARY") or os.path.join(PKG, "libmccb_delta.so")
+DELTA_BINDING_SRC = os.path.join(PKG, "csrc", "delta_binding.cpp")
+DELTA_BINDING = os.path.join(PKG, "_delta.so")
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-shared", "-fPIC",
@@ -40,8 +44,7 @@ def build_library(out: str = LIB, extra: list[str] | None = None, verbose: bool 
     return out
 
 
-def build_ssm_library(out: str = SSM_LIB, extra: list[str] | None = None,
-                      verbose: bool = False) -> str:
+def _build_objects(srcs: list[str], out: str, extra: list[str] | None, verbose: bool) -> str:
     """One object a source, compiled side by side, then linked."""
     hipcc = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
@@ -53,11 +56,11 @@ def build_ssm_library(out: str = SSM_LIB, extra: list[str] | None = None,
             print(res.stderr)
 
     flags = [f for f in HIPCC_FLAGS if f != "-shared"] + (extra or [])
-    objects = [f"{out}.{os.path.basename(src)}.o" for src in SSM_SRCS]
+    objects = [f"{out}.{os.path.basename(src)}.o" for src in srcs]
     try:
-        with ThreadPoolExecutor(len(SSM_SRCS)) as pool:
+        with ThreadPoolExecutor(len(srcs)) as pool:
             list(pool.map(lambda so: run([hipcc, *flags, "-I", INCLUDE, "-c", so[0], "-o", so[1]]),
-                          zip(SSM_SRCS, objects)))
+                          zip(srcs, objects)))
         run([hipcc, *HIPCC_FLAGS, *(extra or []), *objects, "-o", out + ".tmp"])
     finally:
         for o in objects:
@@ -67,8 +70,18 @@ def build_ssm_library(out: str = SSM_LIB, extra: list[str] | None = None,
     return out
 
 
-def build_binding(out: str = BINDING) -> str:
-    """The tensor front end of libmccb_ssm.so, host code against torch's C++ interface."""
+def build_ssm_library(out: str = SSM_LIB, extra: list[str] | None = None,
+                      verbose: bool = False) -> str:
+    return _build_objects(SSM_SRCS, out, extra, verbose)
+
+
+def build_delta_library(out: str = DELTA_LIB, extra: list[str] | None = None,
+                        verbose: bool = False) -> str:
+    return _build_objects(DELTA_SRCS, out, extra, verbose)
+
+
+def build_binding(out: str = BINDING, src: str = BINDING_SRC) -> str:
+    """The tensor front end of a library, host code against torch's C++ interface."""
     import torch
     from torch.utils import cpp_extension
 
@@ -78,7 +91,7 @@ def build_binding(out: str = BINDING) -> str:
            "-I", INCLUDE, "-I", sysconfig.get_paths()["include"]]
     for path in cpp_extension.include_paths("cuda"):
         cmd += ["-isystem", path]
-    cmd += [BINDING_SRC, "-o", out + ".tmp"]
+    cmd += [src, "-o", out + ".tmp"]
     for path in cpp_extension.library_paths("cuda"):
         cmd += ["-L", path]
     cmd += ["-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch", "-ltorch_python"]
@@ -89,11 +102,16 @@ def build_binding(out: str = BINDING) -> str:
     return out
 
 
+def build_delta_binding(out: str = DELTA_BINDING) -> str:
+    return build_binding(out, DELTA_BINDING_SRC)
+
+
 def build_all() -> list[str]:
-    """Both libraries and the binding, side by side."""
-    with ThreadPoolExecutor(3) as pool:
+    """The libraries and the bindings, side by side."""
+    with ThreadPoolExecutor(5) as pool:
         return [f.result() for f in [pool.submit(b) for b in
-                                     (build_library, build_ssm_library, build_binding)]]
+                                     (build_library, build_ssm_library, build_binding,
+                                      build_delta_library, build_delta_binding)]]
 
 
 if __name__ == "__main__":

@@ -1,0 +1,138 @@
+// delta_binding.cpp -- the gated delta rule and the norms around a block on torch tensors, as a CPython module
+// (_delta): checks and marshals arguments, allocates outputs and workspaces with torch, and calls the C-ABI
+// of mccb_delta.h on torch's current stream; nothing is computed here. The functions of the library are
+// handed over by address (bind), so that the module works with whichever build is loaded.
+#include "binding.h"
+#include "mccb_delta.h"
+
+namespace {
+
+// The library's functions, in the order in which bind takes their addresses.
+struct Library {
+    decltype(&mccb_prenorm_forward) prenorm_forward;
+    decltype(&mccb_prenorm_backward_get_workspace_size) prenorm_backward_size;
+    decltype(&mccb_prenorm_backward) prenorm_backward;
+    decltype(&mccb_postnorm_forward) postnorm_forward;
+    decltype(&mccb_postnorm_backward_get_workspace_size) postnorm_backward_size;
+    decltype(&mccb_postnorm_backward) postnorm_backward;
+};
+Library lib{};
+
+// -- norms ----------------------------------------------------------------------------------------
+struct Norm {
+    mccb_norm_t a{};
+    Tensor x, weight, residual, scale, z;
+    c10::hip::OptionalHIPGuard here;
+};
+
+void norm_args(Norm &c, PyObject *x, PyObject *weight, PyObject *residual, PyObject *scale, PyObject *z,
+               int64_t groups, double eps) {
+    c.x = tensor(x, "x");
+    TORCH_CHECK_VALUE(c.x.dim() >= 2, "x must be a [...,H] tensor of at least two dimensions");
+    c.a.dtype = kind_of("x", c.x, c.x.dim(), "[...,H]");
+    c.here.set_index(c.x.device().index());
+    rows_of("x", c.x, c.a.R, c.a.x_ld);
+    const auto type = c.x.scalar_type();
+    const auto device = c.x.device();
+    c.a.H = c.x.size(-1), c.a.groups = groups, c.a.eps = (float)eps;
+    TORCH_CHECK_VALUE(groups >= 1 && c.a.H % groups == 0, "groups must divide H");
+    c.weight = tensor(weight, "weight");
+    c.a.weight_shared = groups > 1 && c.weight.dim() == 1 && c.weight.size(0) == c.a.H / groups;
+    check("weight", c.weight, {c.a.weight_shared ? c.a.H / groups : c.a.H}, type, device, true);
+    c.residual = maybe(residual, "residual"), c.scale = maybe(scale, "scale"), c.z = maybe(z, "z");
+    check_if("scale", c.scale, {c.a.H}, type, device);
+    int64_t rows;
+    check_if("residual", c.residual, c.x.sizes(), type, device, false);
+    if (c.residual.defined()) rows_of("residual", c.residual, rows, c.a.residual_ld);
+    check_if("z", c.z, c.x.sizes(), type, device, false);
+    if (c.z.defined()) rows_of("z", c.z, rows, c.a.z_ld);
+    c.a.x = ptr(c.x), c.a.weight = ptr(c.weight), c.a.residual = ptr(c.residual);
+    c.a.scale = ptr(c.scale), c.a.z = ptr(c.z);
+}
+// A result [...,H], the caller's or a new one.
+Tensor norm_out(const char *name, PyObject *o, const Norm &c) {
+    Tensor t = maybe(o, name);
+    if (t.defined()) check(name, t, c.x.sizes(), c.x.scalar_type(), c.x.device(), true);
+    else t = make(c.x.sizes(), c.x);
+    return t;
+}
+int64_t gradient_rows(const char *name, const Tensor &t, const Norm &c) {
+    int64_t rows, ld;
+    check(name, t, c.x.sizes(), c.x.scalar_type(), c.x.device(), false);
+    rows_of(name, t, rows, ld);
+    return ld;
+}
+
+// (x, weight, residual, scale, eps, return_sum, out, sum_out)
+PyObject *prenorm_forward(PyObject *const *v) {
+    Norm c;
+    norm_args(c, v[0], v[1], v[2], v[3], Py_None, 1, PyFloat_AsDouble(v[4]));
+    const bool with_sum = v[5] == Py_True;
+    const Tensor y = norm_out("out", v[6], c);
+    Tensor sum;
+    if (v[7] != Py_None || (with_sum && (c.residual.defined() || c.scale.defined()))) sum = norm_out("sum_out", v[7], c);
+    ok(lib.prenorm_forward(&c.a, ptr(y), ptr(sum), stream_of(c.x)), "mccb_prenorm_forward");
+    wrote({y, sum});
+    return with_sum ? tuple({y, sum.defined() ? sum : c.x}) : out(y);
+}
+
+// (gradOut, x, weight, residual, scale, eps, gradSum)
+PyObject *prenorm_backward(PyObject *const *v) {
+    Norm c;
+    norm_args(c, v[1], v[2], v[3], v[4], Py_None, 1, PyFloat_AsDouble(v[5]));
+    const Tensor go = tensor(v[0], "gradOut"), gsum = maybe(v[6], "gradSum");
+    const int64_t go_ld = gradient_rows("gradOut", go, c);
+    const int64_t gsum_ld = gsum.defined() ? gradient_rows("gradSum", gsum, c) : 0;
+    uint64_t n = 0;
+    ok(lib.prenorm_backward_size(&c.a, &n), "mccb_prenorm_backward_get_workspace_size");
+    const Tensor gx = make(c.x.sizes(), c.x), gw = make(c.weight.sizes(), c.x), ws = bytes(n, c.x);
+    const Tensor gs = c.scale.defined() ? make(c.scale.sizes(), c.x) : Tensor();
+    const Tensor gr = c.residual.defined() && c.scale.defined() ? make(c.x.sizes(), c.x) : Tensor();
+    ok(lib.prenorm_backward(&c.a, ptr(go), go_ld, ptr(gsum), gsum_ld, ptr(gx), ptr(gr), ptr(gw), ptr(gs), ptr(ws), n,
+                            stream_of(c.x)),
+       "mccb_prenorm_backward");
+    return tuple({gx, gw, c.residual.defined() && !gr.defined() ? gx : gr, gs});
+}
+
+// (x, weight, z, residual, scale, groups, eps, out)
+PyObject *postnorm_forward(PyObject *const *v) {
+    Norm c;
+    norm_args(c, v[0], v[1], v[3], v[4], v[2], PyLong_AsLongLong(v[5]), PyFloat_AsDouble(v[6]));
+    const Tensor y = norm_out("out", v[7], c);
+    ok(lib.postnorm_forward(&c.a, ptr(y), stream_of(c.x)), "mccb_postnorm_forward");
+    wrote({y});
+    return out(y);
+}
+
+// (gradOut, x, weight, z, scale, groups, eps)
+PyObject *postnorm_backward(PyObject *const *v) {
+    Norm c;
+    norm_args(c, v[1], v[2], Py_None, v[4], v[3], PyLong_AsLongLong(v[5]), PyFloat_AsDouble(v[6]));
+    const Tensor go = tensor(v[0], "gradOut");
+    const int64_t go_ld = gradient_rows("gradOut", go, c);
+    uint64_t n = 0;
+    ok(lib.postnorm_backward_size(&c.a, &n), "mccb_postnorm_backward_get_workspace_size");
+    const Tensor gx = make(c.x.sizes(), c.x), gw = make(c.weight.sizes(), c.x), ws = bytes(n, c.x);
+    const Tensor gz = c.z.defined() ? make(c.x.sizes(), c.x) : Tensor();
+    const Tensor gs = c.scale.defined() ? make(c.scale.sizes(), c.x) : Tensor();
+    ok(lib.postnorm_backward(&c.a, ptr(go), go_ld, ptr(gx), ptr(gz), ptr(gw), ptr(gs), ptr(ws), n, stream_of(c.x)),
+       "mccb_postnorm_backward");
+    return tuple({gx, gw, gz, gs});
+}
+
+// -- the module -----------------------------------------------------------------------------------
+PyObject *bind(PyObject *, PyObject *args) { return bind_to(lib, args); }
+
+PyMethodDef methods[] = {
+    {"bind", &bind, METH_VARARGS, nullptr},
+    ENTRY(prenorm_forward, 8),
+    ENTRY(prenorm_backward, 7),
+    ENTRY(postnorm_forward, 8),
+    ENTRY(postnorm_backward, 7),
+    {nullptr, nullptr, 0, nullptr},
+};
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_delta", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__delta() { return PyModule_Create(&module); }

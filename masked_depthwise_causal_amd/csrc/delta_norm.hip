@@ -1,4 +1,4 @@
-// ssm_norm.hip -- the norms before and after a block, with what stands next to them: the scaled residual
+// delta_norm.hip -- the norms before and after a block, with what stands next to them: the scaled residual
 // addition before (prenorm), and weight, gate, residual scale and addition after (postnorm).
 //
 //   prenorm   r = residual + scale x,  out = r rstd w                  rstd = 1/sqrt(mean(r^2) + eps)
@@ -12,6 +12,7 @@
 // the reduction and its use, and each result written once. A team of T lanes takes a group, so many that
 // a lane has one or two vectors of 8 values; teams keep their group and walk over rows, with the
 // weights of their columns in registers, and in the backward also the columns' sums.
+#include "mccb_delta.h"
 #include "ssm_common.h"
 
 using namespace ssm;

@@ -5,24 +5,10 @@
 // are handed over by address (bind), so that the module works with whichever build is loaded.
 // Written against torch's C++ interface because a call's cost is this marshalling: a single-token call
 // takes 9-12 us with the same steps in Python, against 3 us for the launch.
-#include <Python.h>
-
-#include <ATen/ATen.h>
-#include <c10/hip/HIPGuard.h>
-#include <c10/hip/HIPStream.h>
-#include <torch/csrc/Exceptions.h>
-#include <torch/csrc/autograd/python_variable.h>
-
-#include <array>
-#include <cstring>
-#include <string>
-
+#include "binding.h"
 #include "mccb_ssm.h"
 
 namespace {
-
-using at::Tensor;
-using Shape = at::IntArrayRef;
 
 // The library's functions, in the order in which bind takes their addresses.
 struct Library {
@@ -40,106 +26,8 @@ struct Library {
     decltype(&mccb_linear_forward) linear_forward;
     decltype(&mccb_linear_backward_get_workspace_size) linear_backward_size;
     decltype(&mccb_linear_backward) linear_backward;
-    decltype(&mccb_prenorm_forward) prenorm_forward;
-    decltype(&mccb_prenorm_backward_get_workspace_size) prenorm_backward_size;
-    decltype(&mccb_prenorm_backward) prenorm_backward;
-    decltype(&mccb_postnorm_forward) postnorm_forward;
-    decltype(&mccb_postnorm_backward_get_workspace_size) postnorm_backward_size;
-    decltype(&mccb_postnorm_backward) postnorm_backward;
 };
 Library lib{};
-constexpr Py_ssize_t kFunctions = sizeof(Library) / sizeof(void *);
-PyObject *error_class = nullptr;  // MccbError(status, where)
-
-// A status that is not MCCB_OK, on its way to Python.
-struct Status {
-    int code;
-    const char *where;
-};
-void ok(int code, const char *where) {
-    if (code != MCCB_OK) throw Status{code, where};
-}
-
-// -- arguments ------------------------------------------------------------------------------------
-Tensor tensor(PyObject *o, const char *name) {
-    if (!THPVariable_Check(o)) TORCH_CHECK_TYPE(false, name, " must be a torch.Tensor");
-    return THPVariable_Unpack(o);
-}
-Tensor maybe(PyObject *o, const char *name) { return o == Py_None ? Tensor() : tensor(o, name); }
-
-std::string text(Shape s) {
-    std::string t = "(";
-    for (size_t i = 0; i < s.size(); ++i) t += (i ? ", " : "") + std::to_string(s[i]);
-    return t + (s.size() == 1 ? ",)" : ")");
-}
-
-void check(const char *name, const Tensor &t, Shape shape, at::ScalarType type, at::Device device,
-           bool contiguous) {
-    TORCH_CHECK_VALUE(t.device() == device, name, " must live on ", device.str(), " (a HIP device)");
-    TORCH_CHECK_VALUE(t.sizes() == shape, name, " has shape ", text(t.sizes()), ", expected ", text(shape));
-    TORCH_CHECK_VALUE(t.scalar_type() == type, name, " has dtype ", toString(t.scalar_type()),
-                      ", expected ", toString(type));
-    if (contiguous) TORCH_CHECK_VALUE(t.is_contiguous(), name, " must be contiguous");
-}
-void check_if(const char *name, const Tensor &t, Shape shape, at::ScalarType type, at::Device device,
-              bool contiguous = true) {
-    if (t.defined()) check(name, t, shape, type, device, contiguous);
-}
-
-// The tensor that sets a call's type and device.
-int32_t kind_of(const char *name, const Tensor &t, int64_t dims, const char *layout) {
-    TORCH_CHECK_VALUE(t.is_cuda(), name, " must live on a HIP device");
-    TORCH_CHECK_VALUE(t.dim() == dims, name, " must be ", layout);
-    if (t.scalar_type() == at::kBFloat16) return MCCB_BF16;
-    TORCH_CHECK_VALUE(t.scalar_type() == at::kHalf, "dtype ", toString(t.scalar_type()),
-                      " not supported (bfloat16, float16)");
-    return MCCB_FP16;
-}
-
-void *ptr(const Tensor &t) { return t.defined() ? t.data_ptr() : nullptr; }
-void strides3(const Tensor &t, int64_t (&s)[3], bool token) {
-    if (!t.defined()) return;
-    const auto v = t.strides();
-    if (token) s[0] = 0, s[1] = v[0], s[2] = v[1];
-    else s[0] = v[0], s[1] = v[1], s[2] = v[2];
-}
-// Strides along S, B, G, N of B or C, whose group axis may be left out.
-void strides4(const Tensor &t, int64_t (&s)[4], bool token, bool grouped) {
-    const auto v = t.strides();
-    size_t i = 0;
-    s[0] = token ? 0 : v[i++];
-    s[1] = v[i++];
-    s[2] = grouped ? v[i++] : 0;
-    s[3] = v[i];
-}
-
-void *stream_of(const Tensor &t) { return (void *)c10::hip::getCurrentHIPStream(t.device().index()).stream(); }
-
-Tensor make(Shape shape, const Tensor &like) { return at::empty(shape, like.options()); }
-Tensor make(Shape shape, const Tensor &like, at::ScalarType type) {
-    return at::empty(shape, like.options().dtype(type));
-}
-Tensor bytes(uint64_t n, const Tensor &like) {
-    return n ? make({(int64_t)n}, like, at::kByte) : Tensor();
-}
-
-// Tensors of the caller's that a call wrote: their version moves on, as an in-place operation's does.
-void wrote(std::initializer_list<Tensor> ts) {
-    for (const Tensor &t : ts)
-        if (t.defined() && !t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
-}
-
-PyObject *out(const Tensor &t) {
-    if (!t.defined()) Py_RETURN_NONE;
-    return THPVariable_Wrap(t);
-}
-PyObject *tuple(std::initializer_list<Tensor> ts) {
-    PyObject *r = PyTuple_New((Py_ssize_t)ts.size());
-    if (!r) return nullptr;
-    Py_ssize_t i = 0;
-    for (const Tensor &t : ts) PyTuple_SET_ITEM(r, i++, out(t));
-    return r;
-}
 
 // -- convolution ----------------------------------------------------------------------------------
 struct Conv {
@@ -359,23 +247,6 @@ PyObject *scan_step(PyObject *const *v) {
 }
 
 // -- matrix product -------------------------------------------------------------------------------
-// A [...,C] tensor as R evenly spaced, contiguous rows.
-void rows_of(const char *name, const Tensor &t, int64_t &R, int64_t &ld) {
-    const auto size = t.sizes(), stride = t.strides();
-    const int64_t last = t.dim() - 1, C = size[last];
-    TORCH_CHECK_VALUE(C <= 1 || stride[last] == 1, name, "'s last dimension must be contiguous");
-    R = 1, ld = -1;
-    for (int64_t i = last - 1; i >= 0; --i) {
-        if (size[i] != 1) {
-            if (ld < 0) ld = stride[i];
-            else TORCH_CHECK_VALUE(size[i] == 0 || R == 0 || stride[i] == ld * R, name,
-                                   "'s rows are not evenly spaced: make it contiguous");
-        }
-        R *= size[i];
-    }
-    if (ld < 0) ld = C;
-}
-
 struct Linear {
     mccb_linear_t a{};
     Tensor x, weight, bias;
@@ -452,159 +323,9 @@ PyObject *linear_backward(PyObject *const *v) {
     return tuple({gx, gw, gb});
 }
 
-// -- norms ----------------------------------------------------------------------------------------
-struct Norm {
-    mccb_norm_t a{};
-    Tensor x, weight, residual, scale, z;
-    c10::hip::OptionalHIPGuard here;
-};
-
-void norm_args(Norm &c, PyObject *x, PyObject *weight, PyObject *residual, PyObject *scale, PyObject *z,
-               int64_t groups, double eps) {
-    c.x = tensor(x, "x");
-    TORCH_CHECK_VALUE(c.x.dim() >= 2, "x must be a [...,H] tensor of at least two dimensions");
-    c.a.dtype = kind_of("x", c.x, c.x.dim(), "[...,H]");
-    c.here.set_index(c.x.device().index());
-    rows_of("x", c.x, c.a.R, c.a.x_ld);
-    const auto type = c.x.scalar_type();
-    const auto device = c.x.device();
-    c.a.H = c.x.size(-1), c.a.groups = groups, c.a.eps = (float)eps;
-    TORCH_CHECK_VALUE(groups >= 1 && c.a.H % groups == 0, "groups must divide H");
-    c.weight = tensor(weight, "weight");
-    c.a.weight_shared = groups > 1 && c.weight.dim() == 1 && c.weight.size(0) == c.a.H / groups;
-    check("weight", c.weight, {c.a.weight_shared ? c.a.H / groups : c.a.H}, type, device, true);
-    c.residual = maybe(residual, "residual"), c.scale = maybe(scale, "scale"), c.z = maybe(z, "z");
-    check_if("scale", c.scale, {c.a.H}, type, device);
-    int64_t rows;
-    check_if("residual", c.residual, c.x.sizes(), type, device, false);
-    if (c.residual.defined()) rows_of("residual", c.residual, rows, c.a.residual_ld);
-    check_if("z", c.z, c.x.sizes(), type, device, false);
-    if (c.z.defined()) rows_of("z", c.z, rows, c.a.z_ld);
-    c.a.x = ptr(c.x), c.a.weight = ptr(c.weight), c.a.residual = ptr(c.residual);
-    c.a.scale = ptr(c.scale), c.a.z = ptr(c.z);
-}
-// A result [...,H], the caller's or a new one.
-Tensor norm_out(const char *name, PyObject *o, const Norm &c) {
-    Tensor t = maybe(o, name);
-    if (t.defined()) check(name, t, c.x.sizes(), c.x.scalar_type(), c.x.device(), true);
-    else t = make(c.x.sizes(), c.x);
-    return t;
-}
-int64_t gradient_rows(const char *name, const Tensor &t, const Norm &c) {
-    int64_t rows, ld;
-    check(name, t, c.x.sizes(), c.x.scalar_type(), c.x.device(), false);
-    rows_of(name, t, rows, ld);
-    return ld;
-}
-
-// (x, weight, residual, scale, eps, return_sum, out, sum_out)
-PyObject *prenorm_forward(PyObject *const *v) {
-    Norm c;
-    norm_args(c, v[0], v[1], v[2], v[3], Py_None, 1, PyFloat_AsDouble(v[4]));
-    const bool with_sum = v[5] == Py_True;
-    const Tensor y = norm_out("out", v[6], c);
-    Tensor sum;
-    if (v[7] != Py_None || (with_sum && (c.residual.defined() || c.scale.defined()))) sum = norm_out("sum_out", v[7], c);
-    ok(lib.prenorm_forward(&c.a, ptr(y), ptr(sum), stream_of(c.x)), "mccb_prenorm_forward");
-    wrote({y, sum});
-    return with_sum ? tuple({y, sum.defined() ? sum : c.x}) : out(y);
-}
-
-// (gradOut, x, weight, residual, scale, eps, gradSum)
-PyObject *prenorm_backward(PyObject *const *v) {
-    Norm c;
-    norm_args(c, v[1], v[2], v[3], v[4], Py_None, 1, PyFloat_AsDouble(v[5]));
-    const Tensor go = tensor(v[0], "gradOut"), gsum = maybe(v[6], "gradSum");
-    const int64_t go_ld = gradient_rows("gradOut", go, c);
-    const int64_t gsum_ld = gsum.defined() ? gradient_rows("gradSum", gsum, c) : 0;
-    uint64_t n = 0;
-    ok(lib.prenorm_backward_size(&c.a, &n), "mccb_prenorm_backward_get_workspace_size");
-    const Tensor gx = make(c.x.sizes(), c.x), gw = make(c.weight.sizes(), c.x), ws = bytes(n, c.x);
-    const Tensor gs = c.scale.defined() ? make(c.scale.sizes(), c.x) : Tensor();
-    const Tensor gr = c.residual.defined() && c.scale.defined() ? make(c.x.sizes(), c.x) : Tensor();
-    ok(lib.prenorm_backward(&c.a, ptr(go), go_ld, ptr(gsum), gsum_ld, ptr(gx), ptr(gr), ptr(gw), ptr(gs), ptr(ws), n,
-                            stream_of(c.x)),
-       "mccb_prenorm_backward");
-    return tuple({gx, gw, c.residual.defined() && !gr.defined() ? gx : gr, gs});
-}
-
-// (x, weight, z, residual, scale, groups, eps, out)
-PyObject *postnorm_forward(PyObject *const *v) {
-    Norm c;
-    norm_args(c, v[0], v[1], v[3], v[4], v[2], PyLong_AsLongLong(v[5]), PyFloat_AsDouble(v[6]));
-    const Tensor y = norm_out("out", v[7], c);
-    ok(lib.postnorm_forward(&c.a, ptr(y), stream_of(c.x)), "mccb_postnorm_forward");
-    wrote({y});
-    return out(y);
-}
-
-// (gradOut, x, weight, z, scale, groups, eps)
-PyObject *postnorm_backward(PyObject *const *v) {
-    Norm c;
-    norm_args(c, v[1], v[2], Py_None, v[4], v[3], PyLong_AsLongLong(v[5]), PyFloat_AsDouble(v[6]));
-    const Tensor go = tensor(v[0], "gradOut");
-    const int64_t go_ld = gradient_rows("gradOut", go, c);
-    uint64_t n = 0;
-    ok(lib.postnorm_backward_size(&c.a, &n), "mccb_postnorm_backward_get_workspace_size");
-    const Tensor gx = make(c.x.sizes(), c.x), gw = make(c.weight.sizes(), c.x), ws = bytes(n, c.x);
-    const Tensor gz = c.z.defined() ? make(c.x.sizes(), c.x) : Tensor();
-    const Tensor gs = c.scale.defined() ? make(c.scale.sizes(), c.x) : Tensor();
-    ok(lib.postnorm_backward(&c.a, ptr(go), go_ld, ptr(gx), ptr(gz), ptr(gw), ptr(gs), ptr(ws), n, stream_of(c.x)),
-       "mccb_postnorm_backward");
-    return tuple({gx, gw, gz, gs});
-}
-
 // -- the module -----------------------------------------------------------------------------------
-// Every entry checks the argument count and turns what is thrown into a Python exception.
-template <PyObject *(*F)(PyObject *const *), Py_ssize_t N>
-PyObject *entry(PyObject *, PyObject *const *v, Py_ssize_t n) {
-    HANDLE_TH_ERRORS
-    if (n != N || !error_class) {
-        PyErr_Format(PyExc_TypeError, "%zd arguments, %zd expected", n, N);
-        return nullptr;
-    }
-    try {
-        PyObject *r = F(v);
-        if (PyErr_Occurred()) {
-            Py_XDECREF(r);
-            return nullptr;
-        }
-        return r;
-    } catch (const Status &s) {
-        PyObject *e = PyObject_CallFunction(error_class, "is", s.code, s.where);
-        if (e) {
-            PyErr_SetObject(error_class, e);
-            Py_DECREF(e);
-        }
-        return nullptr;
-    }
-    END_HANDLE_TH_ERRORS
-}
+PyObject *bind(PyObject *, PyObject *args) { return bind_to(lib, args); }
 
-// bind(error class, addresses)
-PyObject *bind(PyObject *, PyObject *args) {
-    PyObject *cls, *addresses;
-    if (!PyArg_ParseTuple(args, "OO!", &cls, &PyTuple_Type, &addresses)) return nullptr;
-    if (PyTuple_GET_SIZE(addresses) != kFunctions) {
-        PyErr_SetString(PyExc_ValueError, "wrong number of functions");
-        return nullptr;
-    }
-    void *table[kFunctions];
-    for (Py_ssize_t i = 0; i < kFunctions; ++i) {
-        table[i] = PyLong_AsVoidPtr(PyTuple_GET_ITEM(addresses, i));
-        if (!table[i]) {
-            if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "a function has no address");
-            return nullptr;
-        }
-    }
-    static_assert(sizeof(table) == sizeof(lib), "a table of function pointers");
-    std::memcpy(&lib, table, sizeof(lib));
-    Py_INCREF(cls);
-    Py_XSETREF(error_class, cls);
-    Py_RETURN_NONE;
-}
-
-#define ENTRY(name, n) {#name, (PyCFunction)(void *)&entry<name, n>, METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {
     {"bind", &bind, METH_VARARGS, nullptr},
     ENTRY(conv_forward, 9),
@@ -615,10 +336,6 @@ PyMethodDef methods[] = {
     ENTRY(scan_step, 11),
     ENTRY(linear_forward, 8),
     ENTRY(linear_backward, 8),
-    ENTRY(prenorm_forward, 8),
-    ENTRY(prenorm_backward, 7),
-    ENTRY(postnorm_forward, 8),
-    ENTRY(postnorm_backward, 7),
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_ssm", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -1,6 +1,5 @@
 """The selective state space block's operators on device tensors: causal convolution with activation
-and carried rows, selective scan, matrix product with its epilogue, and the norms before and after a block
-(``include/mccb_ssm.h``).
+and carried rows, selective scan, and matrix product with its epilogue (``include/mccb_ssm.h``).
 
 Like the rest of the package this layer only checks and marshals arguments (here in ``_ssm``, compiled
 from ``csrc/ssm_binding.cpp``); every step of the computation runs in the library's HIP kernels. Data
@@ -10,19 +9,17 @@ allocates (outputs that are not given, workspaces) belongs to that stream. Nothi
 autograd graph: each backward is a call of its own.
 
 ``ssm_lib()`` is the library itself, for calls of the C-ABI with device addresses; its argument structs are
-``ConvArgs``, ``ScanArgs``, ``ScanGradArgs``, ``LinearArgs`` and ``NormArgs``.
+``ConvArgs``, ``ScanArgs``, ``ScanGradArgs`` and ``LinearArgs``.
 """
 from __future__ import annotations
 
 import ctypes
-import importlib.util
-import os
 from typing import NamedTuple, Optional
 
 import torch
 
 from . import build as _build
-from ._lib import MccbError, load
+from ._lib import bound_module, load, on_stream
 
 ACTIVATIONS = {None: 0, "none": 0, "relu": 1, "silu": 2, "gelu": 3, "softplus": 4}
 
@@ -67,12 +64,6 @@ class LinearArgs(ctypes.Structure):
                        "w: pre_fp32")
 
 
-class NormArgs(ctypes.Structure):
-    """mccb_norm_t."""
-    _fields_ = _fields("i: R H groups; w: dtype weight_shared; f: eps; p: x weight residual scale z; "
-                       "i: x_ld residual_ld z_ld")
-
-
 _SIGNATURES = {
     "mccb_conv_act_forward": (ConvArgs, _vp, _vp, _vp),
     "mccb_conv_act_backward_get_workspace_size": (ConvArgs, _vp),
@@ -88,12 +79,6 @@ _SIGNATURES = {
     "mccb_linear_forward": (LinearArgs, _vp, _i64, _vp, _vp, _vp, _u64, _vp),
     "mccb_linear_backward_get_workspace_size": (LinearArgs, _vp),
     "mccb_linear_backward": (LinearArgs, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _u64, _vp),
-    "mccb_prenorm_forward": (NormArgs, _vp, _vp, _vp),
-    "mccb_prenorm_backward_get_workspace_size": (NormArgs, _vp),
-    "mccb_prenorm_backward": (NormArgs, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _u64, _vp),
-    "mccb_postnorm_forward": (NormArgs, _vp, _vp),
-    "mccb_postnorm_backward_get_workspace_size": (NormArgs, _vp),
-    "mccb_postnorm_backward": (NormArgs, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _u64, _vp),
 }
 
 _lib = None
@@ -117,14 +102,7 @@ def ssm_module():
     """The compiled front end, bound to the library; built first if no build exists."""
     global _module
     if _module is None:
-        if not os.path.exists(_build.BINDING):
-            _build.build_binding()
-        spec = importlib.util.spec_from_file_location("_ssm", _build.BINDING)
-        m = importlib.util.module_from_spec(spec)
-        spec.loader.exec_module(m)
-        L = ssm_lib()
-        m.bind(MccbError, tuple(ctypes.cast(getattr(L, n), _vp).value for n in _SIGNATURES))
-        _module = m
+        _module = bound_module("_ssm", _build.BINDING, _build.build_binding, ssm_lib(), _SIGNATURES)
     return _module
 
 
@@ -139,12 +117,7 @@ def _call(function, stream, *args):
     """function(*args) of the front end, on `stream` if one is given."""
     if stream is None:
         return getattr(_module or ssm_module(), function)(*args)
-    # the front end launches on the current stream of the tensors' device, which would not be this one
-    device = next((a.device for a in args if isinstance(a, torch.Tensor)), stream.device)
-    if stream.device != device:
-        raise ValueError(f"stream lives on {stream.device}, the tensors on {device}")
-    with torch.cuda.stream(stream):
-        return getattr(_module or ssm_module(), function)(*args)
+    return on_stream(getattr(_module or ssm_module(), function), stream, args)
 
 
 # -- causal convolution with activation and carried rows ---------------------------------------------
@@ -254,54 +227,3 @@ def linear_backward(gradOut, x, weight, pre=None, activation=None, grad_x=True, 
     return LinearGrads(*_call("linear_backward", stream, gradOut, x, weight, pre,
                               _activation(activation, (0, 1, 2, 3, 4)), bool(grad_x),
                               bool(grad_weight), bool(grad_bias)))
-
-
-# -- norms before and after a block ------------------------------------------------------------------
-class PrenormGrads(NamedTuple):
-    x: torch.Tensor
-    weight: torch.Tensor
-    residual: Optional[torch.Tensor]
-    scale: Optional[torch.Tensor]
-
-
-class PostnormGrads(NamedTuple):
-    x: torch.Tensor
-    weight: torch.Tensor
-    z: Optional[torch.Tensor]
-    scale: Optional[torch.Tensor]
-
-
-def prenorm_forward(x, weight, residual=None, scale=None, eps=1e-6, return_sum=False, out=None,
-                    sum_out=None, stream=None):
-    """out [...,H] = sum / sqrt(mean(sum^2) + eps) * weight, with sum = residual + scale * x; x and residual
-    [...,H] of evenly spaced, contiguous rows, weight and scale [H], H up to 16384. With `return_sum` the
-    result is (out, sum), to add the next block's output to; where neither residual nor scale is given
-    that sum is x itself (unless `sum_out` asks for a copy). The norm is of the sum before its rounding."""
-    return _call("prenorm_forward", stream, x, weight, residual, scale, float(eps), bool(return_sum), out,
-                 sum_out)
-
-
-def prenorm_backward(gradOut, x, weight, residual=None, scale=None, eps=1e-6, gradSum=None,
-                     stream=None) -> PrenormGrads:
-    """Gradients of prenorm_forward with the same arguments: of x, weight, and residual and scale where
-    those were given. gradSum [...,H] is the gradient that reaches the sum from elsewhere, as from the
-    next addition. Without a scale the residual's gradient is x's, the same tensor."""
-    return PrenormGrads(*_call("prenorm_backward", stream, gradOut, x, weight, residual, scale, float(eps),
-                               gradSum))
-
-
-def postnorm_forward(x, weight, z=None, residual=None, scale=None, groups=1, eps=1e-6, out=None,
-                     stream=None):
-    """out [...,H] = residual + scale * (x / sqrt(mean(x^2) + eps) * weight * silu(z)), the mean over each
-    of `groups` equal parts of a row (up to 16384 values); x, z and residual [...,H] of evenly spaced,
-    contiguous rows, scale [H], weight [H], or [H/groups] for a weight that all groups share. z, residual
-    and scale may be left out."""
-    return _call("postnorm_forward", stream, x, weight, z, residual, scale, int(groups), float(eps), out)
-
-
-def postnorm_backward(gradOut, x, weight, z=None, scale=None, groups=1, eps=1e-6,
-                      stream=None) -> PostnormGrads:
-    """Gradients of postnorm_forward with the same arguments: of x, weight, and z and scale where those
-    were given. The residual's gradient is gradOut."""
-    return PostnormGrads(*_call("postnorm_backward", stream, gradOut, x, weight, z, scale, int(groups),
-                                float(eps)))
