@@ -23,6 +23,52 @@ extern "C" {
 #endif
 
 /* ------------------------------------------------------------------------------------------------
+ * Gated delta rule. For every value head h, of key head g = h / (H/G), a state S [K,V]:
+ *
+ *   d    = softplus(dt[t,b,h] + dt_bias[h])       (without softplus: the sum itself)
+ *   a    = exp(A[h] d),  beta = sigmoid(b[t,b,h])
+ *   kn   = k / sqrt(sum(k^2) + 1e-6),  qn = q / sqrt(sum(q^2) + 1e-6)     (without normalize: k and q)
+ *   u    = beta (v[t,b,h] - a S^T kn)
+ *   S    = a S + kn u^T
+ *   out  = scale S^T qn
+ *
+ * q, k [S,B,G,K], v and out [S,B,H,V], dt and b [S,B,H] have the dtype; A, dt_bias [H] and the states are
+ * fp32. Rows of q, k and v are contiguous; the other axes have element strides (>= 0; 0 repeats). The
+ * states are computed with products of two 16-bit terms each, about 22 bits, and fp32 sums; gates and
+ * decays in fp32, sums of their logarithms in fp64; results are rounded once. Rates A are negative in
+ * ordinary use (decay); A d below -1e5 counts as -1e5, whose decay is 0.
+ *
+ * lengths: optional int64 [B] on the device, clamped to [0, S]; NULL = all S. Rows at or past a sequence's
+ * length are not computed with, whatever they hold: outputs and gradients there are zero, and states are
+ * those after the last row before it. A length of zero hands the initial state on.
+ *
+ * S in [0, 2^28), B H in [1, 65535], G a divisor of H, K in 1..128, V in 1..256, scale finite.
+ * -----------------------------------------------------------------------------------------------*/
+typedef struct {
+    int64_t S, B, H, G, K, V;
+    int32_t dtype, softplus, normalize;  /* softplus, normalize: nonzero = applied */
+    float scale;
+    const void *q, *k, *v, *dt, *b;
+    int64_t q_stride[3], k_stride[3];    /* along S, B, G */
+    int64_t v_stride[3], dt_stride[3], b_stride[3]; /* along S, B, H */
+    const float *A;           /* [H] */
+    const float *dt_bias;     /* [H] or NULL (zero) */
+    const int64_t *lengths;   /* [B] or NULL */
+    const float *state;       /* [B,H,K,V] contiguous, the state before the first row; NULL = zeros */
+} mccb_delta_t;
+
+/* out [S,B,H,V]; final_state [B,H,K,V] or NULL; saved: NULL, or mccb_delta_saved_size bytes that the
+ * backward reads (the state before every 64th row among them). With saved no workspace is needed. */
+int mccb_delta_saved_size(const mccb_delta_t *args, uint64_t *bytes);
+int mccb_delta_forward_get_workspace_size(const mccb_delta_t *args, uint64_t *workspace_size);
+int mccb_delta_forward(const mccb_delta_t *args, void *out, float *final_state, void *saved,
+                       void *workspace, uint64_t workspace_size, void *stream);
+
+/* One token: q, k [B,G,K], v and out [B,H,V], dt and b [B,H] (args->S = 1, the strides along S unused);
+ * `state` [B,H,K,V] is updated in place. args->state and args->lengths are NULL. */
+int mccb_delta_step(const mccb_delta_t *args, float *state, void *out, void *stream);
+
+/* ------------------------------------------------------------------------------------------------
  * Norms before and after a block, over rows of H values:
  *
  *   prenorm   sum = residual + scale x,  out = sum / sqrt(mean(sum^2) + eps) weight

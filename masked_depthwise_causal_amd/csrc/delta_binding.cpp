@@ -2,6 +2,8 @@
 // (_delta): checks and marshals arguments, allocates outputs and workspaces with torch, and calls the C-ABI
 // of mccb_delta.h on torch's current stream; nothing is computed here. The functions of the library are
 // handed over by address (bind), so that the module works with whichever build is loaded.
+#include <cmath>
+
 #include "binding.h"
 #include "mccb_delta.h"
 
@@ -9,6 +11,10 @@ namespace {
 
 // The library's functions, in the order in which bind takes their addresses.
 struct Library {
+    decltype(&mccb_delta_saved_size) delta_saved_size;
+    decltype(&mccb_delta_forward_get_workspace_size) delta_forward_size;
+    decltype(&mccb_delta_forward) delta_forward;
+    decltype(&mccb_delta_step) delta_step;
     decltype(&mccb_prenorm_forward) prenorm_forward;
     decltype(&mccb_prenorm_backward_get_workspace_size) prenorm_backward_size;
     decltype(&mccb_prenorm_backward) prenorm_backward;
@@ -17,6 +23,102 @@ struct Library {
     decltype(&mccb_postnorm_backward) postnorm_backward;
 };
 Library lib{};
+
+// -- gated delta rule -----------------------------------------------------------------------------
+struct Delta {
+    mccb_delta_t a{};
+    Tensor q, k, v, dt, b, A, bias, lengths, state;
+    c10::hip::OptionalHIPGuard here;  // launches go to the current device: make it q's
+};
+
+// A tensor [S,B,heads,width] ([B,heads,width] for one token) whose rows are contiguous, and its strides.
+void head_rows(const char *name, const Tensor &t, Shape shape, const Tensor &like, int64_t (&s)[3], bool token) {
+    check(name, t, shape, like.scalar_type(), like.device(), false);
+    TORCH_CHECK_VALUE(t.size(-1) <= 1 || t.stride(-1) == 1, name, "'s last dimension must be contiguous");
+    strides3(t, s, token);
+}
+
+// v: q, k, v, dt, b, A, dt_bias, softplus, normalize, scale
+void delta_args(Delta &c, PyObject *const *v, bool token) {
+    c.q = tensor(v[0], "q");
+    c.a.dtype = kind_of("q", c.q, token ? 3 : 4, token ? "[B,G,K]" : "[S,B,G,K]");
+    c.here.set_index(c.q.device().index());
+    c.k = tensor(v[1], "k"), c.v = tensor(v[2], "v"), c.dt = tensor(v[3], "dt"), c.b = tensor(v[4], "b");
+    c.A = tensor(v[5], "A"), c.bias = maybe(v[6], "dt_bias");
+    const auto size = c.q.sizes();
+    const size_t lead = token ? 0 : 1;
+    mccb_delta_t &a = c.a;
+    a.S = token ? 1 : size[0];
+    a.B = size[lead], a.G = size[lead + 1], a.K = size[lead + 2];
+    TORCH_CHECK_VALUE(c.v.dim() == c.q.dim(), "v must be ", token ? "[B,H,V]" : "[S,B,H,V]");
+    a.H = c.v.size(-2), a.V = c.v.size(-1);
+    at::DimVector rows(size.begin(), size.begin() + lead + 1), values = rows;
+    rows.push_back(a.H);
+    values.push_back(a.H), values.push_back(a.V);
+    head_rows("q", c.q, size, c.q, a.q_stride, token);
+    head_rows("k", c.k, size, c.q, a.k_stride, token);
+    head_rows("v", c.v, values, c.q, a.v_stride, token);
+    const auto type = c.q.scalar_type();
+    const auto device = c.q.device();
+    check("dt", c.dt, rows, type, device, false);
+    check("b", c.b, rows, type, device, false);
+    strides3(c.dt, a.dt_stride, token);
+    strides3(c.b, a.b_stride, token);
+    check("A", c.A, {a.H}, at::kFloat, device, true);
+    check_if("dt_bias", c.bias, {a.H}, at::kFloat, device);
+    a.softplus = v[7] == Py_True, a.normalize = v[8] == Py_True;
+    a.scale = v[9] == Py_None ? (float)(1.0 / std::sqrt((double)(a.K > 0 ? a.K : 1))) : (float)PyFloat_AsDouble(v[9]);
+    a.q = ptr(c.q), a.k = ptr(c.k), a.v = ptr(c.v), a.dt = ptr(c.dt), a.b = ptr(c.b);
+    a.A = (const float *)ptr(c.A), a.dt_bias = (const float *)ptr(c.bias);
+}
+void delta_rows(Delta &c, PyObject *lengths, PyObject *state) {
+    c.lengths = maybe(lengths, "lengths"), c.state = maybe(state, "state");
+    check_if("lengths", c.lengths, {c.a.B}, at::kLong, c.q.device());
+    check_if("state", c.state, {c.a.B, c.a.H, c.a.K, c.a.V}, at::kFloat, c.q.device());
+    c.a.lengths = (const int64_t *)ptr(c.lengths), c.a.state = (const float *)ptr(c.state);
+}
+int64_t saved_bytes(const Delta &c) {
+    uint64_t n = 0;
+    ok(lib.delta_saved_size(&c.a, &n), "mccb_delta_saved_size");
+    return (int64_t)n;
+}
+
+// (q, k, v, dt, b, A, dt_bias, softplus, normalize, scale, lengths, state, return_state, return_saved, out, final_state)
+PyObject *delta_forward(PyObject *const *v) {
+    Delta c;
+    delta_args(c, v, false);
+    delta_rows(c, v[10], v[11]);
+    const bool with_state = v[12] == Py_True, with_saved = v[13] == Py_True;
+    Tensor y = maybe(v[14], "out"), final_state = maybe(v[15], "final_state"), saved;
+    if (y.defined()) check("out", y, c.v.sizes(), c.v.scalar_type(), c.v.device(), true);
+    else y = make(c.v.sizes(), c.v);
+    const std::array<int64_t, 4> states{c.a.B, c.a.H, c.a.K, c.a.V};
+    check_if("final_state", final_state, states, at::kFloat, c.v.device());
+    if (with_state && !final_state.defined()) final_state = make(states, c.v, at::kFloat);
+    uint64_t n = 0;
+    if (with_saved) saved = make({saved_bytes(c)}, c.v, at::kByte);
+    else ok(lib.delta_forward_size(&c.a, &n), "mccb_delta_forward_get_workspace_size");
+    const Tensor ws = bytes(n, c.v);
+    ok(lib.delta_forward(&c.a, ptr(y), (float *)ptr(final_state), ptr(saved), ptr(ws), n, stream_of(c.v)),
+       "mccb_delta_forward");
+    wrote({y, final_state});
+    if (with_state) return with_saved ? tuple({y, final_state, saved}) : tuple({y, final_state});
+    return with_saved ? tuple({y, saved}) : out(y);
+}
+
+// (q, k, v, dt, b, A, dt_bias, softplus, normalize, scale, state, out)
+PyObject *delta_step(PyObject *const *v) {
+    Delta c;
+    delta_args(c, v, true);
+    const Tensor state = tensor(v[10], "state");
+    check("state", state, {c.a.B, c.a.H, c.a.K, c.a.V}, at::kFloat, c.q.device(), true);
+    Tensor y = maybe(v[11], "out");
+    if (y.defined()) check("out", y, c.v.sizes(), c.v.scalar_type(), c.v.device(), true);
+    else y = make(c.v.sizes(), c.v);
+    ok(lib.delta_step(&c.a, (float *)ptr(state), ptr(y), stream_of(c.v)), "mccb_delta_step");
+    wrote({state, y});
+    return out(y);
+}
 
 // -- norms ----------------------------------------------------------------------------------------
 struct Norm {
@@ -125,6 +227,8 @@ PyObject *bind(PyObject *, PyObject *args) { return bind_to(lib, args); }
 
 PyMethodDef methods[] = {
     {"bind", &bind, METH_VARARGS, nullptr},
+    ENTRY(delta_forward, 16),
+    ENTRY(delta_step, 12),
     ENTRY(prenorm_forward, 8),
     ENTRY(prenorm_backward, 7),
     ENTRY(postnorm_forward, 8),

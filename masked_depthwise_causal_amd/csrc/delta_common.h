@@ -1,0 +1,207 @@
+// delta_common.h -- what the kernels of the gated delta rule share: the chunk, the operands' images, and
+// numbers in two 16-bit terms.
+//
+// In chunks of C = 64 rows, with G the running sum of the log decays within the chunk, M[i,j] =
+// exp(G[i] - G[j]) for j <= i, and S0 the state before the chunk, the recurrence is
+//
+//   L = diag(beta) tril(M o Kn Kn^T, -1),   X = (I + L)^-1,   A = scale tril(M o Qn Kn^T)
+//   U = X diag(beta) (V - exp(G) Kn S0),    out = scale exp(G) Qn S0 + A U
+//   S = exp(G[C-1]) S0 + Kn^T diag(exp(G[C-1] - G)) U
+//
+// (Kn, Qn: the normalized rows.) X and A need no state, so every chunk's are made at once by one kernel;
+// another then walks over the chunks with the state in registers.
+//
+// Numbers. Products run on the matrix units in fp16, in as many terms as they need to come out as in fp32:
+// rows of q and k are exact in one (with a power of two a row taken out, bf16's 8 bits fit wherever fp16 is
+// normal; smaller values lose less than 2^-25 of the row's largest); everything that is computed is split
+// in two, hi + lo, 22 bits (a power of two a column, or a matrix, taken out, so that no value's size
+// matters; what is lost is below 2^-22 of a value or 2^-25 of the largest). An exact operand with a split
+// one takes two products, two split ones three (lo lo is below 2^-22). On this card that is 8 and 5 times
+// the rate of the fp32 matrix instructions; in bf16 terms it would take three and six products.
+#pragma once
+
+#include "mccb_delta.h"
+#include "ssm_common.h"
+
+namespace delta {
+
+using namespace ssm;
+
+constexpr int kC = 64;              // rows of a chunk
+constexpr float kNormEps = 1e-6f;   // in the rows' norms
+constexpr int kSquare = kC * kC;    // values of X, of A
+
+typedef _Float16 h4 __attribute__((ext_vector_type(4)));
+typedef _Float16 h8 __attribute__((ext_vector_type(8)));
+typedef float f4 __attribute__((ext_vector_type(4)));
+
+// ---------------------------------------------------------------------------------------------
+// What one kernel hands to the next for a chunk. A key head's: the images of its rows of k and q, and the
+// factors that make them normalized rows, kn = kr k~, qn = qr q~ (without the scale). A value head's: the
+// images of X and A in two terms each, and what belongs to single rows.
+// ---------------------------------------------------------------------------------------------
+struct RowCoef {
+    float p[kC];        // exp(G) kr: V - p (K~ S0)
+    float beta[kC];
+    float q[kC];        // scale exp(G) qr
+    float u[kC];        // exp(G[C-1] - G) kr
+    float whole;        // exp(G[C-1])
+    float x, a;         // X = x (hi + lo), A = a (hi + lo)
+    float pad[13];
+    double cum[kC];     // G in units of log 2
+};
+constexpr int kStaged = 4 * kC * (int)sizeof(float);  // the bytes of RowCoef that the walk stages: four rows
+
+constexpr size_t key_bytes(int kp) { return 2 * kC * kp * sizeof(uint16_t) + 2 * kC * sizeof(float); }
+constexpr size_t kXaBytes = 4 * kSquare * sizeof(uint16_t);  // X hi, X lo, A hi, A lo
+
+// An image row R holds its chunks of 8 values in the order c ^ swizzle(R). The matrix instructions' rows m
+// stand for rows 32 j + 8 (m / 4) + 4 p + m % 4 (below); sixteen of those read one chunk each from
+// different banks, and a transposing read's four rows too.
+template <int COLS>
+__device__ static inline int swizzle(int row) {
+    static_assert(COLS == 64 || COLS == 128, "images have 8 or 16 chunks a row");
+    return COLS == 128 ? ((row >> 3) & 3) | ((row & 3) << 2) : ((row >> 3) & 3) | ((row & 2) << 1);
+}
+template <int COLS>
+__device__ static inline int image_at(int row, int chunk) {  // in 16-bit values
+    return row * COLS + ((chunk ^ swizzle<COLS>(row)) << 3);
+}
+
+// Rows of 16x16 results. Two neighbouring tiles, p = 0 and 1, cover 32 rows so that lane group g = lane / 16
+// holds rows 8 g + 4 p + i in its four registers i: both tiles' registers, one after the other, are then
+// eight consecutive rows, just what the next product wants of its right operand.
+__device__ static inline int row_of(int tile, int m) { return 32 * (tile >> 1) + 8 * (m >> 2) + 4 * (tile & 1) + (m & 3); }
+
+// Left operand, rows of `tile`, step s of 32 along the image's columns.
+template <int COLS>
+__device__ static inline h8 left(const uint16_t *image, int tile, int s, int lane) {
+    return *(const h8 *)(image + image_at<COLS>(row_of(tile, lane & 15), 4 * s + (lane >> 4)));
+}
+// Left operand of the transposed image: its columns as rows (`tile` of them), step s of 32 along its rows.
+// A transposing read gives lane i of 16 column i of the four rows that those lanes read 8 bytes of.
+template <int COLS>
+__device__ static inline h8 left_turned(const uint16_t *__restrict__ image, int tile, int s, int lane) {
+    typedef short s16x4 __attribute__((ext_vector_type(4)));
+    typedef __attribute__((address_space(3))) s16x4 lds4;
+    const int i = lane & 15, row = 32 * s + 8 * (lane >> 4) + (i >> 2);
+    const int chunk = 4 * (tile >> 1) + (i & 3), half = 4 * (tile & 1);
+    const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(image + image_at<COLS>(row, chunk) + half));
+    const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(image + image_at<COLS>(row + 4, chunk) + half));
+    return __builtin_bit_cast(h8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
+__device__ static inline f4 mma(h8 a, h8 b, f4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
+
+// ---------------------------------------------------------------------------------------------
+// Two terms.
+// ---------------------------------------------------------------------------------------------
+struct Split {
+    h8 hi, lo;
+};
+__device__ static inline Split split(const f4 &a, const f4 &b, float inv) {
+    Split s;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float v = (i < 4 ? a[i & 3] : b[i & 3]) * inv;
+        s.hi[i] = (_Float16)v;
+        s.lo[i] = (_Float16)(v - (float)s.hi[i]);
+    }
+    return s;
+}
+
+// The power of two at or below m (0 for 0 and subnormal values), and its inverse. Infinities and the largest
+// binade keep 2^126, and stay what they are; NaN is not counted by the maximum that comes in.
+struct Power {
+    float back, inv;
+};
+__device__ static inline Power power_of(float m) {
+    uint32_t e = __float_as_uint(m) & 0x7f800000u;
+    e = e > (253u << 23) ? 253u << 23 : e;
+    Power p;
+    p.back = __uint_as_float(e);
+    p.inv = __uint_as_float((254u << 23) - e);
+    return p;
+}
+
+// The largest magnitude over the four lanes that hold a column.
+__device__ static inline float column_max(float m) {
+    m = __builtin_fmaxf(m, __shfl_xor(m, 16));
+    return __builtin_fmaxf(m, __shfl_xor(m, 32));
+}
+template <int N>
+__device__ static inline Power column_power(const f4 (&v)[N]) {
+    float m = 0.0f;
+#pragma unroll
+    for (int t = 0; t < N; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m = __builtin_fmaxf(m, __builtin_fabsf(v[t][i]));
+    return power_of(column_max(m));
+}
+
+// Lane sums and maxima over 16 lanes, by rotations.
+template <int CTRL>
+__device__ static inline float turn16(float v) {
+    return __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v), CTRL, 0xf, 0xf, true));
+}
+__device__ static inline float sum16(float v) {
+    v += turn16<0x128>(v);
+    v += turn16<0x124>(v);
+    v += turn16<0x122>(v);
+    return v + turn16<0x121>(v);
+}
+__device__ static inline float max16(float v) {
+    v = __builtin_fmaxf(v, turn16<0x128>(v));
+    v = __builtin_fmaxf(v, turn16<0x124>(v));
+    v = __builtin_fmaxf(v, turn16<0x122>(v));
+    return __builtin_fmaxf(v, turn16<0x121>(v));
+}
+
+// ---------------------------------------------------------------------------------------------
+// Arguments.
+// ---------------------------------------------------------------------------------------------
+struct Delta {
+    int S, B, H, G, K, V;
+    int softplus, normalize;
+    float scale;
+    const uint16_t *q, *k, *v, *dt, *b;
+    int64_t qs[3], ks[3], vs[3], ds[3], bs[3];
+    const float *A, *bias;
+    const int64_t *lengths;
+};
+__device__ static inline int length_of(const Delta &a, int b) {
+    if (!a.lengths) return a.S;
+    const int64_t n = a.lengths[b];
+    return n < 0 ? 0 : n > a.S ? a.S : (int)n;
+}
+
+// A head's step size and log2 decay for one row. A rate of -infinity is a decay of 0, and of 1 where there is
+// no step; beyond e^-100000 a decay is 0 in any case, and a bound keeps sums and differences finite.
+__device__ static inline float step_size(float raw, int softplus) { return softplus ? softplus_f(raw) : raw; }
+__device__ static inline double log2_decay(float step, float rate) {
+    const double g = step == 0.0f ? 0.0 : (double)step * (double)rate * 1.4426950408889634;
+    return g < -1.5e5 ? -1.5e5 : g;
+}
+
+// The records of chunk n: [batch, head][chunk].
+struct Records {
+    uint8_t *key;       // key_bytes each
+    uint8_t *xa;        // kXaBytes each
+    RowCoef *coef;
+    int64_t chunks;     // of a head
+};
+__host__ __device__ static inline uint64_t records_bytes(uint64_t key_heads, uint64_t heads, uint64_t chunks, int kp) {
+    return chunks * (key_heads * key_bytes(kp) + heads * (kXaBytes + sizeof(RowCoef)));
+}
+__host__ static inline Records records_at(void *p, uint64_t key_heads, uint64_t heads, uint64_t chunks, int kp) {
+    Records r;
+    r.key = (uint8_t *)p;
+    r.xa = r.key + chunks * key_heads * key_bytes(kp);
+    r.coef = (RowCoef *)(r.xa + chunks * heads * kXaBytes);
+    r.chunks = (int64_t)chunks;
+    return r;
+}
+
+__host__ static inline int padded(int64_t K) { return K <= 64 ? 64 : 128; }
+
+}  // namespace delta

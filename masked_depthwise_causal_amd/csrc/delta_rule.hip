@@ -1,0 +1,787 @@
+// delta_rule.hip -- the gated delta rule forward: chunks of 64 rows for prompts and training, and the
+// single-token form. The formulas and the numbers' two 16-bit terms are in delta_common.h.
+//
+// delta_prepare makes what a chunk has without a state: the images of its rows of k and q, X and A. One
+// block a chunk and key head; all chunks at once.
+// delta_walk goes over a head's chunks with the state in registers. A wave owns 16 (or 32) columns of V
+// and nothing passes between waves: results of one product are the right operand of the next as they stand
+// in the registers (row_of in delta_common.h), and the left operands, the same for all of a head's columns,
+// come from LDS, where the next chunk's are written straight from memory while this one's run.
+// delta_step reads and writes the state once.
+#include "delta_common.h"
+
+using namespace delta;
+
+namespace {
+
+// ---------------------------------------------------------------------------------------------
+// Preparation.
+// ---------------------------------------------------------------------------------------------
+constexpr int kPrepThreads = 256;
+constexpr int kLd = kC + 4;         // fp32 row of the triangular matrices in LDS
+
+// One 16-bit row chunk of 8 values, zeros past K.
+__device__ static inline HVec<8>::t row_chunk(const uint16_t *p, int left) {
+    HVec<8>::t v = {};
+    if (left >= 8) v = *(const HVec<8>::t *)p;
+    else
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < left) v[i] = p[i];
+    return v;
+}
+
+// The 64 rows of q or k as an image in LDS and in memory, and the rows' factors.
+template <int DT, int KP>
+__device__ static inline void image_rows(const Delta &a, const uint16_t *base, const int64_t (&st)[3], int b, int g,
+                                         int row0, int live, uint16_t *lds, uint16_t *image, float *factor,
+                                         float *factor_out) {
+    constexpr int kLanes = KP / 8, kRows = kPrepThreads / kLanes;
+    const int lane = threadIdx.x % kLanes;
+    for (int r = threadIdx.x / kLanes; r < kC; r += kRows) {
+        HVec<8>::t raw = {};
+        if (r < live) raw = row_chunk(base + (int64_t)(row0 + r) * st[0] + b * st[1] + g * st[2] + 8 * lane, a.K - 8 * lane);
+        float v[8], m = 0.0f, ss = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = to_f32<DT>(raw[i]), m = __builtin_fmaxf(m, __builtin_fabsf(v[i]));
+        // the row's largest value is brought to 1..2
+#pragma unroll
+        for (int i = 1; i < kLanes; i *= 2) m = __builtin_fmaxf(m, __shfl_xor(m, i));
+        int e = m > 0.0f ? ((__float_as_uint(m) >> 23) & 255) - 127 : 0;
+        e = e < -100 ? -100 : e > 126 ? 126 : e;
+        h8 h;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            v[i] = __builtin_ldexpf(v[i], -e);
+            ss = __builtin_fmaf(v[i], v[i], ss);
+            h[i] = (_Float16)v[i];
+        }
+#pragma unroll
+        for (int i = 1; i < kLanes; i *= 2) ss += __shfl_xor(ss, i);
+        const int at = image_at<KP>(r, lane);
+        *(h8 *)(lds + at) = h;
+        *(h8 *)(image + at) = h;
+        if (lane == 0) {
+            const float f = a.normalize ? 1.0f / __builtin_sqrtf(ss + __builtin_ldexpf(kNormEps, -2 * e))
+                                        : __builtin_ldexpf(1.0f, e);
+            factor[r] = f;
+            factor_out[r] = f;
+        }
+    }
+}
+
+// A 64x64 matrix in LDS as two terms in memory, each an image; returns the power of two taken out.
+__device__ static inline float image_square(const float *m, uint16_t *hi, uint16_t *lo, float *part) {
+    const int row = threadIdx.x / 4, c0 = threadIdx.x % 4 * 16;
+    f4 v[4];
+    float big = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[i] = *(const f4 *)(m + row * kLd + c0 + 4 * i);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) big = __builtin_fmaxf(big, __builtin_fabsf(v[i][j]));
+    }
+    big = column_max(max16(big));
+    if (threadIdx.x % kWave == 0) part[threadIdx.x / kWave] = big;
+    lds_barrier();
+    big = __builtin_fmaxf(__builtin_fmaxf(part[0], part[1]), __builtin_fmaxf(part[2], part[3]));
+    const Power p = power_of(big);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const Split s = split(v[2 * i], v[2 * i + 1], p.inv);
+        const int at = image_at<64>(row, c0 / 8 + i);
+        *(h8 *)(hi + at) = s.hi;
+        *(h8 *)(lo + at) = s.lo;
+    }
+    return p.back;
+}
+
+// One 16x16 block of a product of fp32 matrices in LDS, added to c: rows r0.. of `l` from column k0 times `y`
+// (registers of a lane: rows 4 (lane / 16) + i of column lane % 16, as the instruction leaves them).
+__device__ static inline f4 block_product(const float *l, int r0, int k0, f4 y, f4 c, int lane) {
+    const f4 a = *(const f4 *)(l + (r0 + (lane & 15)) * kLd + k0 + 4 * (lane >> 4));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[i], y[i], c, 0, 0, 0);
+    return c;
+}
+__device__ static inline f4 block_at(const float *m, int r0, int c0, int lane) {
+    f4 v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = m[(r0 + 4 * (lane >> 4) + i) * kLd + c0 + (lane & 15)];
+    return v;
+}
+__device__ static inline void block_to(float *m, int r0, int c0, f4 v, int lane) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m[(r0 + 4 * (lane >> 4) + i) * kLd + c0 + (lane & 15)] = -v[i];
+}
+
+// X = (I + L)^-1 of a strictly lower triangular L: the diagonal blocks of 16 by substitution (a lane each
+// column), then twice the lower left quarter, -X2 L21 X1, on the fp32 matrix units. All of X is written.
+__device__ static inline void invert(const float *L, float *X, int wave, int lane) {
+    for (int i = threadIdx.x; i < kC * kC / 4; i += kPrepThreads) *(f4 *)(X + i / 16 * kLd + i % 16 * 4) = f4{};
+    lds_barrier();
+    if (wave == 0) {
+        const int d0 = 16 * (lane >> 4), c = lane & 15;
+        float x[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            x[i] = i == c ? 1.0f : 0.0f;
+#pragma unroll
+            for (int j4 = 0; j4 < i; j4 += 4) {
+                const f4 l = *(const f4 *)(L + (d0 + i) * kLd + d0 + j4);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (j4 + j < i) x[i] = __builtin_fmaf(-l[j], x[j4 + j], x[i]);
+            }
+            X[(d0 + i) * kLd + d0 + c] = x[i];
+        }
+    }
+    lds_barrier();
+    if (wave < 2) {
+        const int a = 32 * wave, b = a + 16;
+        const f4 y = block_product(L, b, a, block_at(X, a, a, lane), f4{}, lane);
+        block_to(X, b, a, block_product(X, b, b, y, f4{}, lane), lane);
+    }
+    lds_barrier();
+    if (wave < 2) {
+        const int c = 16 * wave;
+        const f4 x0 = block_at(X, 0, c, lane), x1 = block_at(X, 16, c, lane);
+        f4 y2 = block_product(L, 32, 0, x0, f4{}, lane), y3 = block_product(L, 48, 0, x0, f4{}, lane);
+        y2 = block_product(L, 32, 16, x1, y2, lane), y3 = block_product(L, 48, 16, x1, y3, lane);
+        const f4 x2 = block_product(X, 32, 32, y2, f4{}, lane);
+        f4 x3 = block_product(X, 48, 32, y2, f4{}, lane);
+        x3 = block_product(X, 48, 48, y3, x3, lane);
+        block_to(X, 32, c, x2, lane);
+        block_to(X, 48, c, x3, lane);
+    }
+    lds_barrier();
+}
+
+template <int DT, int KP>
+__global__ void __launch_bounds__(kPrepThreads) delta_prepare(Delta a, Records rec, int n0) {
+    constexpr int kImages = 2 * kC * KP * (int)sizeof(uint16_t), kSquares = 2 * kC * kLd * (int)sizeof(float);
+    __shared__ __align__(16) uint8_t smem[kImages > kSquares ? kImages : kSquares];  // rows first, then L, X
+    __shared__ float kr[kC], qr[kC], beta[kC], part[4];
+    __shared__ double cum[kC];
+    const int n = blockIdx.x, b = blockIdx.y / a.G, g = blockIdx.y % a.G;
+    const int row0 = (n0 + n) * kC, live = length_of(a, b) - row0;
+    if (live <= 0) return;
+    const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    uint16_t *kt = (uint16_t *)smem, *qt = kt + kC * KP;
+    {
+        uint8_t *key = rec.key + ((int64_t)(b * a.G + g) * rec.chunks + n) * key_bytes(KP);
+        uint16_t *images = (uint16_t *)key;
+        float *factors = (float *)(images + 2 * kC * KP);
+        image_rows<DT, KP>(a, a.k, a.ks, b, g, row0, live, kt, images, kr, factors);
+        image_rows<DT, KP>(a, a.q, a.qs, b, g, row0, live, qt, images + kC * KP, qr, factors + kC);
+    }
+    lds_barrier();
+    // K~ K~^T and Q~ K~^T: wave w has rows 16 w.. of both, up to the diagonal block
+    f4 kk[4] = {}, qk[4] = {};
+    const int m = lane & 15, grp = lane >> 4;
+#pragma unroll
+    for (int s = 0; s < KP / 32; ++s) {
+        const int c = 4 * s + grp;
+        const h8 ak = *(const h8 *)(kt + image_at<KP>(16 * wave + m, c));
+        const h8 aq = *(const h8 *)(qt + image_at<KP>(16 * wave + m, c));
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (j <= wave) {
+                const h8 bk = *(const h8 *)(kt + image_at<KP>(16 * j + m, c));
+                kk[j] = mma(ak, bk, kk[j]);
+                qk[j] = mma(aq, bk, qk[j]);
+            }
+    }
+    float *P = (float *)smem, *X = P + kC * kLd;
+    const int heads = a.H / a.G;
+    for (int hh = 0; hh < heads; ++hh) {
+        const int h = g * heads + hh;
+        const int64_t at = (int64_t)(b * a.H + h) * rec.chunks + n;
+        RowCoef *coef = rec.coef + at;
+        uint16_t *xa = (uint16_t *)(rec.xa + at * kXaBytes);
+        double total = 0.0, mine = 0.0;
+        if (wave == 0) {
+            float bt = 0.0f;
+            if (lane < live) {
+                const int64_t row = row0 + lane;
+                const float raw = to_f32<DT>(a.dt[row * a.ds[0] + b * a.ds[1] + h * a.ds[2]]) + (a.bias ? a.bias[h] : 0.0f);
+                mine = log2_decay(step_size(raw, a.softplus), a.A[h]);
+                bt = sigmoid_f(to_f32<DT>(a.b[row * a.bs[0] + b * a.bs[1] + h * a.bs[2]]));
+            }
+#pragma unroll
+            for (int s = 1; s < kC; s *= 2) {
+                const double o = __shfl_up(mine, s);
+                if (lane >= s) mine += o;
+            }
+            total = __shfl(mine, kC - 1);
+            cum[lane] = mine, beta[lane] = bt;
+        }
+        lds_barrier();  // also: the last head's reads of P and X, or the rows' reads above, are done
+        double gi[4];
+        float bi[4], ki[4], qi[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = 16 * wave + 4 * grp + i;
+            gi[i] = cum[r], bi[i] = beta[r], ki[i] = kr[r], qi[i] = qr[r] * a.scale;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int c = 16 * j + m;
+            const double gj = cum[c];
+            const float kj = kr[c];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = 16 * wave + 4 * grp + i;
+                const float decay = c <= r ? exp2_f((float)(gi[i] - gj)) * kj : 0.0f;
+                P[r * kLd + c] = c <= r ? decay * qi[i] * qk[j][i] : 0.0f;
+                X[r * kLd + c] = c < r ? decay * ki[i] * bi[i] * kk[j][i] : 0.0f;
+            }
+        }
+        lds_barrier();
+        const float sa = image_square(P, xa + 2 * kSquare, xa + 3 * kSquare, part);
+        lds_barrier();
+        invert(X, P, wave, lane);
+        const float sx = image_square(P, xa, xa + kSquare, part);
+        if (wave == 0) {
+            const float ek = exp2_f((float)mine), k1 = kr[lane];
+            coef->p[lane] = ek * k1;
+            coef->beta[lane] = beta[lane];
+            coef->q[lane] = a.scale * ek * qr[lane];
+            coef->u[lane] = exp2_f((float)(total - mine)) * k1;
+            coef->cum[lane] = mine;
+            if (lane == 0) coef->whole = exp2_f((float)total), coef->x = sx, coef->a = sa;
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------------------------
+// The walk.
+// ---------------------------------------------------------------------------------------------
+struct Walk {
+    const float *state_in;          // [B,H,K,V] or NULL
+    float *state_out;               // or NULL
+    uint16_t *out;                  // [S,B,H,V]
+    float *states, *u;              // kept for the backward: [B,H][chunk][K,V] and [B,H][chunk][64,V]; or NULL
+    int n0, n1;                     // chunks
+    int blocks;                     // of columns, a head
+};
+
+// A wave's load of 1 KiB straight to LDS, 16 bytes a lane.
+__device__ static inline void to_lds(const uint8_t *from, uint8_t *to, int lane) {
+    typedef __attribute__((address_space(1))) const uint8_t gmem;
+    typedef __attribute__((address_space(3))) uint8_t lmem;
+    __builtin_amdgcn_global_load_lds((gmem *)(from + 16 * lane), (lmem *)to, 16, 0, 0);
+}
+
+// Blocks of one head, and heads of one key head, next to each other on one of the 8 dies, which have an L2 each.
+__device__ static inline int same_die(int id, int all) { return all % 8 ? id : id % 8 * (all / 8) + id / 8; }
+
+template <int DT, int KP, int NT, int W>
+__global__ void __launch_bounds__(W *kWave) delta_walk(Delta a, Records rec, Walk w) {
+    constexpr int KT = KP / 16, KS = KP / 32;
+    constexpr int kKeys = 2 * kC * KP * 2;                     // bytes of the images of k and q
+    constexpr int kBuf = kKeys + (int)kXaBytes + kStaged;
+    __shared__ __align__(16) uint8_t smem[2 * kBuf];
+    const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int m = lane & 15, grp = lane >> 4;
+    const int id = same_die(blockIdx.x, gridDim.x);
+    const int bh = id / w.blocks, b = bh / a.H, h = bh % a.H, g = h / (a.H / a.G);
+    const int col0 = (id % w.blocks * W + wave) * 16 * NT;
+    const int length = length_of(a, b);
+    const int chunks = (length + kC - 1) / kC, end = chunks < w.n1 ? chunks : w.n1;
+
+    f4 S[NT][KT];
+#pragma unroll
+    for (int c = 0; c < NT; ++c) {
+        const int col = col0 + 16 * c + m;
+#pragma unroll
+        for (int t = 0; t < KT; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int k = row_of(t, 4 * grp + i);
+                S[c][t][i] = w.state_in && k < a.K && col < a.V ? w.state_in[((int64_t)bh * a.K + k) * a.V + col] : 0.0f;
+            }
+    }
+    const uint8_t *keys = rec.key + (int64_t)(b * a.G + g) * rec.chunks * key_bytes(KP);
+    const uint8_t *xas = rec.xa + (int64_t)bh * rec.chunks * kXaBytes;
+    const RowCoef *coefs = rec.coef + (int64_t)bh * rec.chunks;
+    auto fill = [&](int n) {
+        uint8_t *to = smem + (n & 1) * kBuf;
+        const int i = n - w.n0;
+        const uint8_t *key = keys + i * (int64_t)key_bytes(KP), *xa = xas + i * (int64_t)kXaBytes;
+        const uint8_t *coef = (const uint8_t *)(coefs + i);
+        for (int p = wave; p < kBuf / 1024; p += W) {
+            const int o = p * 1024;
+            to_lds(o < kKeys ? key + o : o < kKeys + (int)kXaBytes ? xa + (o - kKeys) : coef, to + o, lane);
+        }
+    };
+    const uint16_t *vbase = a.v + b * a.vs[1] + h * a.vs[2];
+    uint16_t vnext[NT][4][4];
+    auto fetch = [&](int n) {
+#pragma unroll
+        for (int c = 0; c < NT; ++c) {
+            const int col = col0 + 16 * c + m;
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int row = n * kC + row_of(t, 4 * grp + i);
+                    vnext[c][t][i] = row < length && col < a.V ? vbase[(int64_t)row * a.vs[0] + col] : 0;
+                }
+        }
+    };
+    if (w.n0 < end) fill(w.n0), fetch(w.n0);
+    for (int n = w.n0; n < end; ++n) {
+        __syncthreads();  // this chunk's operands are there, and all waves are done with the last one's
+        const uint8_t *buf = smem + (n & 1) * kBuf;
+        const uint16_t *kt = (const uint16_t *)buf, *qt = kt + kC * KP;
+        const uint16_t *xh = (const uint16_t *)(buf + kKeys), *xl = xh + kSquare, *ah = xl + kSquare, *al = ah + kSquare;
+        const float *coef = (const float *)(buf + kKeys + kXaBytes);
+        const float whole = coefs[n - w.n0].whole, sx = coefs[n - w.n0].x, sa = coefs[n - w.n0].a;
+        f4 R[NT][4];
+#pragma unroll
+        for (int c = 0; c < NT; ++c)
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) R[c][t][i] = to_f32<DT>(vnext[c][t][i]);
+        if (n + 1 < end) fill(n + 1), fetch(n + 1);
+        if (w.states) {
+            float *keep = w.states + ((int64_t)bh * rec.chunks + n) * a.K * a.V;
+#pragma unroll
+            for (int c = 0; c < NT; ++c) {
+                const int col = col0 + 16 * c + m;
+#pragma unroll
+                for (int t = 0; t < KT; ++t)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int k = row_of(t, 4 * grp + i);
+                        if (k < a.K && col < a.V) keep[(int64_t)k * a.V + col] = S[c][t][i];
+                    }
+            }
+        }
+        // K~ S0 and Q~ S0
+        f4 P[NT][4] = {}, O[NT][4] = {};
+        float back[NT];
+        {
+            Split sp[NT][KS];
+#pragma unroll
+            for (int c = 0; c < NT; ++c) {
+                const Power p = column_power(S[c]);
+                back[c] = p.back;
+#pragma unroll
+                for (int s = 0; s < KS; ++s) sp[c][s] = split(S[c][2 * s], S[c][2 * s + 1], p.inv);
+            }
+#pragma unroll
+            for (int s = 0; s < KS; ++s)
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    const h8 lk = left<KP>(kt, t, s, lane), lq = left<KP>(qt, t, s, lane);
+#pragma unroll
+                    for (int c = 0; c < NT; ++c) {
+                        P[c][t] = mma(lk, sp[c][s].hi, P[c][t]);
+                        O[c][t] = mma(lq, sp[c][s].hi, O[c][t]);
+                        P[c][t] = mma(lk, sp[c][s].lo, P[c][t]);
+                        O[c][t] = mma(lq, sp[c][s].lo, O[c][t]);
+                    }
+                }
+        }
+        // beta (V - p K~ S0), and out's first part
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const int r = row_of(t, 4 * grp);
+            const f4 cp = *(const f4 *)(coef + r), cb = *(const f4 *)(coef + kC + r), cq = *(const f4 *)(coef + 2 * kC + r);
+#pragma unroll
+            for (int c = 0; c < NT; ++c)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    R[c][t][i] = cb[i] * __builtin_fmaf(-cp[i] * back[c], P[c][t][i], R[c][t][i]);
+                    O[c][t][i] *= cq[i] * back[c];
+                }
+        }
+        // U = X R, in P's registers
+#pragma unroll
+        for (int c = 0; c < NT; ++c) {
+            const Power p = column_power(R[c]);
+            Split sp[2];
+#pragma unroll
+            for (int s = 0; s < 2; ++s) sp[s] = split(R[c][2 * s], R[c][2 * s + 1], p.inv);
+            const float up = p.back * sx;
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                f4 u = {};
+#pragma unroll
+                for (int s = 0; s <= t / 2; ++s) {
+                    const h8 lh = left<64>(xh, t, s, lane), ll = left<64>(xl, t, s, lane);
+                    u = mma(lh, sp[s].hi, u);
+                    u = mma(ll, sp[s].hi, u);
+                    u = mma(lh, sp[s].lo, u);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) P[c][t][i] = u[i] * up;
+            }
+        }
+        if (w.u) {
+            float *keep = w.u + ((int64_t)bh * rec.chunks + n) * kC * a.V;
+#pragma unroll
+            for (int c = 0; c < NT; ++c) {
+                const int col = col0 + 16 * c + m;
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (col < a.V) keep[(int64_t)row_of(t, 4 * grp + i) * a.V + col] = P[c][t][i];
+            }
+        }
+        // out's second part, A U
+#pragma unroll
+        for (int c = 0; c < NT; ++c) {
+            const Power p = column_power(P[c]);
+            Split sp[2];
+#pragma unroll
+            for (int s = 0; s < 2; ++s) sp[s] = split(P[c][2 * s], P[c][2 * s + 1], p.inv);
+            const float up = p.back * sa;
+            const int col = col0 + 16 * c + m;
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                f4 o = {};
+#pragma unroll
+                for (int s = 0; s <= t / 2; ++s) {
+                    const h8 lh = left<64>(ah, t, s, lane), ll = left<64>(al, t, s, lane);
+                    o = mma(lh, sp[s].hi, o);
+                    o = mma(ll, sp[s].hi, o);
+                    o = mma(lh, sp[s].lo, o);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int row = n * kC + row_of(t, 4 * grp + i);
+                    if (row < a.S && col < a.V)
+                        w.out[(((int64_t)row * a.B + b) * a.H + h) * a.V + col] =
+                            from_f32<DT>(__builtin_fmaf(o[i], up, O[c][t][i]));
+                }
+            }
+        }
+        // S = whole S0 + K~^T u U
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const f4 cu = *(const f4 *)(coef + 3 * kC + row_of(t, 4 * grp));
+#pragma unroll
+            for (int c = 0; c < NT; ++c)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) P[c][t][i] *= cu[i];
+        }
+        {
+            Split sp[NT][2];
+#pragma unroll
+            for (int c = 0; c < NT; ++c) {
+                const Power p = column_power(P[c]);
+                back[c] = p.back;
+#pragma unroll
+                for (int s = 0; s < 2; ++s) sp[c][s] = split(P[c][2 * s], P[c][2 * s + 1], p.inv);
+            }
+#pragma unroll
+            for (int t = 0; t < KT; ++t) {
+                f4 d[NT] = {};
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    const h8 lk = left_turned<KP>(kt, t, s, lane);
+#pragma unroll
+                    for (int c = 0; c < NT; ++c) {
+                        d[c] = mma(lk, sp[c][s].hi, d[c]);
+                        d[c] = mma(lk, sp[c][s].lo, d[c]);
+                    }
+                }
+#pragma unroll
+                for (int c = 0; c < NT; ++c)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) S[c][t][i] = __builtin_fmaf(whole, S[c][t][i], back[c] * d[c][i]);
+            }
+        }
+    }
+    if (w.state_out) {
+#pragma unroll
+        for (int c = 0; c < NT; ++c) {
+            const int col = col0 + 16 * c + m;
+#pragma unroll
+            for (int t = 0; t < KT; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int k = row_of(t, 4 * grp + i);
+                    if (k < a.K && col < a.V) w.state_out[((int64_t)bh * a.K + k) * a.V + col] = S[c][t][i];
+                }
+        }
+    }
+    // rows that no chunk covers are zeros
+    const int from = (end > w.n0 ? end : w.n0) * kC, to = w.n1 * kC < a.S ? w.n1 * kC : a.S;
+    for (int row = from + grp; row < to; row += 4)
+#pragma unroll
+        for (int c = 0; c < NT; ++c) {
+            const int col = col0 + 16 * c + m;
+            if (col < a.V) w.out[(((int64_t)row * a.B + b) * a.H + h) * a.V + col] = 0;
+        }
+}
+
+// ---------------------------------------------------------------------------------------------
+// One token. A block has 32 columns of a head's state, a thread four of them in every 32nd row. With
+// a = decay, p = a Kn^T S and o = a Qn^T S from one pass over the state: u = beta (v - p),
+// out = o + (qn . kn) u, S = a S + kn u^T.
+// ---------------------------------------------------------------------------------------------
+constexpr int kStepCols = 32, kStepThreads = 256;
+constexpr int kMaxK = 128, kStepRows = kMaxK / 32;
+
+template <int DT>
+__global__ void __launch_bounds__(kStepThreads) delta_one(Delta a, float *state, uint16_t *out) {
+    __shared__ float kn[kMaxK], qn[kMaxK], norms[3][2];
+    __shared__ __align__(16) float part[4][8][8];
+    const int t = threadIdx.x, lane = t % kWave, wave = t / kWave;
+    const int b = blockIdx.y / a.H, h = blockIdx.y % a.H, g = h / (a.H / a.G);
+    const int c0 = blockIdx.x * kStepCols + (t & 7) * 4, r0 = t >> 3;
+    float *S = state + (int64_t)blockIdx.y * a.K * a.V;
+    typedef float row4 __attribute__((ext_vector_type(4), aligned(4)));
+    row4 s[kStepRows];
+#pragma unroll
+    for (int i = 0; i < kStepRows; ++i) {
+        const int k = r0 + 32 * i;
+        s[i] = row4{};
+        if (k < a.K) {
+            const float *p = S + (int64_t)k * a.V + c0;
+            if (c0 + 4 <= a.V) s[i] = *(const row4 *)p;
+            else
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (c0 + j < a.V) s[i][j] = p[j];
+        }
+    }
+    // the rows of k and q, a value a thread in the first two waves
+    float kv = 0.0f, qv = 0.0f;
+    if (t < a.K) {
+        kv = to_f32<DT>(a.k[b * a.ks[1] + g * a.ks[2] + t]);
+        qv = to_f32<DT>(a.q[b * a.qs[1] + g * a.qs[2] + t]);
+    }
+    const float raw = to_f32<DT>(a.dt[b * a.ds[1] + h * a.ds[2]]) + (a.bias ? a.bias[h] : 0.0f);
+    const float decay = exp2_f((float)log2_decay(step_size(raw, a.softplus), a.A[h]));
+    const float beta = sigmoid_f(to_f32<DT>(a.b[b * a.bs[1] + h * a.bs[2]]));
+    if (t < kMaxK) {
+        const float kk = sum16(kv * kv), qq = sum16(qv * qv), kq = sum16(kv * qv);
+        const float x = kk + __shfl_xor(kk, 16), y = qq + __shfl_xor(qq, 16), z = kq + __shfl_xor(kq, 16);
+        const float x2 = x + __shfl_xor(x, 32), y2 = y + __shfl_xor(y, 32), z2 = z + __shfl_xor(z, 32);
+        if (lane == 0) norms[0][wave] = x2, norms[1][wave] = y2, norms[2][wave] = z2;
+    }
+    __syncthreads();
+    const float rk = a.normalize ? 1.0f / __builtin_sqrtf(norms[0][0] + norms[0][1] + kNormEps) : 1.0f;
+    const float rq = a.scale * (a.normalize ? 1.0f / __builtin_sqrtf(norms[1][0] + norms[1][1] + kNormEps) : 1.0f);
+    const float along = (norms[2][0] + norms[2][1]) * rk * rq;
+    if (t < kMaxK) kn[t] = kv * rk, qn[t] = qv * rq;
+    __syncthreads();
+    float acc[8] = {};
+    float kr[kStepRows];
+#pragma unroll
+    for (int i = 0; i < kStepRows; ++i) {
+        const int k = r0 + 32 * i;
+        kr[i] = kn[k];
+        const float q = qn[k];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            acc[j] = __builtin_fmaf(kr[i], s[i][j], acc[j]);
+            acc[4 + j] = __builtin_fmaf(q, s[i][j], acc[4 + j]);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        acc[j] += turn16<0x128>(acc[j]);
+        acc[j] += __shfl_xor(acc[j], 16);
+        acc[j] += __shfl_xor(acc[j], 32);
+    }
+    if (lane < 8) {
+        *(f4 *)part[wave][lane] = f4{acc[0], acc[1], acc[2], acc[3]};
+        *(f4 *)(part[wave][lane] + 4) = f4{acc[4], acc[5], acc[6], acc[7]};
+    }
+    __syncthreads();
+    f4 p = {}, o = {};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p += *(const f4 *)part[i][t & 7], o += *(const f4 *)(part[i][t & 7] + 4);
+    f4 u;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float v = c0 + j < a.V ? to_f32<DT>(a.v[b * a.vs[1] + h * a.vs[2] + c0 + j]) : 0.0f;
+        u[j] = beta * __builtin_fmaf(-decay, p[j], v);
+        if (r0 == 0 && c0 + j < a.V)
+            out[(int64_t)blockIdx.y * a.V + c0 + j] = from_f32<DT>(__builtin_fmaf(decay, o[j], along * u[j]));
+    }
+#pragma unroll
+    for (int i = 0; i < kStepRows; ++i) {
+        const int k = r0 + 32 * i;
+        if (k >= a.K) continue;
+        row4 x;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] = __builtin_fmaf(decay, s[i][j], kr[i] * u[j]);
+        float *to = S + (int64_t)k * a.V + c0;
+        if (c0 + 4 <= a.V) *(row4 *)to = x;
+        else
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (c0 + j < a.V) to[j] = x[j];
+    }
+}
+
+// ---------------------------------------------------------------------------------------------
+// Host side.
+// ---------------------------------------------------------------------------------------------
+uint64_t chunks_of(const mccb_delta_t *a) { return (uint64_t)((a->S + kC - 1) / kC); }
+uint64_t state_bytes(const mccb_delta_t *a) { return (uint64_t)(a->B * a->H) * (uint64_t)(a->K * a->V) * 4; }
+
+Delta delta_of(const mccb_delta_t *a) {
+    Delta d{};
+    d.S = (int)a->S, d.B = (int)a->B, d.H = (int)a->H, d.G = (int)a->G, d.K = (int)a->K, d.V = (int)a->V;
+    d.softplus = a->softplus, d.normalize = a->normalize, d.scale = a->scale;
+    d.q = (const uint16_t *)a->q, d.k = (const uint16_t *)a->k, d.v = (const uint16_t *)a->v;
+    d.dt = (const uint16_t *)a->dt, d.b = (const uint16_t *)a->b;
+    for (int i = 0; i < 3; ++i)
+        d.qs[i] = a->q_stride[i], d.ks[i] = a->k_stride[i], d.vs[i] = a->v_stride[i], d.ds[i] = a->dt_stride[i],
+        d.bs[i] = a->b_stride[i];
+    d.A = a->A, d.bias = a->dt_bias, d.lengths = a->lengths;
+    return d;
+}
+
+int check_delta(const mccb_delta_t *a, bool token) {
+    if (!a) return MCCB_ERR_PARAM_NULLPTR;
+    if (a->dtype != MCCB_BF16 && a->dtype != MCCB_FP16) return MCCB_ERR_PARAM_INVALID;
+    if (a->S < 0 || a->S >= (1 << 28) || (token && a->S != 1) || a->B < 1 || a->H < 1 || a->B > 65535 ||
+        a->H > 65535 || a->B * a->H > 65535 || a->G < 1 || a->G > a->H || a->H % a->G != 0 || a->K < 1 ||
+        a->K > kMaxK || a->V < 1 || a->V > 256)
+        return MCCB_ERR_SHAPE;
+    if (!(a->scale >= -3.0e38f && a->scale <= 3.0e38f)) return MCCB_ERR_PARAM_INVALID;
+    return MCCB_OK;
+}
+
+// Spans of the inputs; token: without a row axis.
+int delta_inputs(const mccb_delta_t *a, bool token, Span *in, int *count) {
+    if (!a->A || (a->S > 0 && (!a->q || !a->k || !a->v || !a->dt || !a->b))) return MCCB_ERR_PARAM_NULLPTR;
+    const void *const p[5] = {a->q, a->k, a->v, a->dt, a->b};
+    const int64_t *const st[5] = {a->q_stride, a->k_stride, a->v_stride, a->dt_stride, a->b_stride};
+    const int64_t heads[5] = {a->G, a->G, a->H, a->H, a->H}, width[5] = {a->K, a->K, a->V, 1, 1};
+    int n = 0;
+    for (int i = 0; i < 5; ++i) {
+        const int64_t size[4] = {token ? 1 : a->S, a->B, heads[i], width[i]};
+        const int64_t stride[4] = {token ? 0 : st[i][0], st[i][1], st[i][2], 1};
+        uint64_t bytes;
+        if (!extent(4, size, stride, 2, &bytes) || misaligned(p[i], 2)) return MCCB_ERR_PARAM_INVALID;
+        in[n++] = {p[i], bytes};
+    }
+    if (misaligned(a->A, 4) || misaligned(a->dt_bias, 4) || misaligned(a->lengths, 8) || misaligned(a->state, 4))
+        return MCCB_ERR_PARAM_INVALID;
+    in[n++] = {a->A, (uint64_t)a->H * 4};
+    in[n++] = {a->dt_bias, (uint64_t)a->H * 4};
+    in[n++] = {a->lengths, (uint64_t)a->B * 8};
+    in[n++] = {a->state, state_bytes(a)};
+    *count = n;
+    return MCCB_OK;
+}
+
+uint64_t records_size(const mccb_delta_t *a, uint64_t chunks) {
+    return align16(records_bytes((uint64_t)(a->B * a->G), (uint64_t)(a->B * a->H), chunks, padded(a->K)));
+}
+
+template <int DT, int KP>
+int prepare(const Delta &d, const Records &rec, int n0, int n1, hipStream_t st) {
+    hipLaunchKernelGGL((delta_prepare<DT, KP>), dim3((unsigned)(n1 - n0), (unsigned)(d.B * d.G)), dim3(kPrepThreads),
+                       0, st, d, rec, n0);
+    return launched();
+}
+template <int DT, int KP, int NT, int W>
+int walk_as(const Delta &d, const Records &rec, Walk w, hipStream_t st) {
+    w.blocks = (d.V + 16 * NT * W - 1) / (16 * NT * W);
+    hipLaunchKernelGGL((delta_walk<DT, KP, NT, W>), dim3((unsigned)(d.B * d.H * w.blocks)), dim3(W * kWave), 0, st,
+                       d, rec, w);
+    return launched();
+}
+template <int DT, int KP>
+int walk(const Delta &d, const Records &rec, const Walk &w, hipStream_t st) {
+    return walk_as<DT, KP, 1, 4>(d, rec, w, st);
+}
+
+template <int DT>
+int forward(const mccb_delta_t *a, void *out, float *final_state, void *saved, void *ws, hipStream_t st) {
+    const Delta d = delta_of(a);
+    const uint64_t chunks = chunks_of(a);
+    Records rec = records_at(saved ? saved : ws, (uint64_t)(a->B * a->G), (uint64_t)(a->B * a->H), chunks, padded(a->K));
+    Walk w{};
+    w.state_in = a->state, w.state_out = final_state, w.out = (uint16_t *)out;
+    w.n0 = 0, w.n1 = (int)chunks;
+    if (saved) {
+        w.states = (float *)((uint8_t *)saved + records_size(a, chunks));
+        w.u = w.states + chunks * (uint64_t)(a->B * a->H) * (uint64_t)(a->K * a->V);
+    }
+    if (chunks > 0) {
+        const int rc = padded(a->K) == 64 ? prepare<DT, 64>(d, rec, w.n0, w.n1, st) : prepare<DT, 128>(d, rec, w.n0, w.n1, st);
+        if (rc != MCCB_OK) return rc;
+    }
+    return padded(a->K) == 64 ? walk<DT, 64>(d, rec, w, st) : walk<DT, 128>(d, rec, w, st);
+}
+
+}  // namespace
+
+extern "C" {
+
+int mccb_delta_saved_size(const mccb_delta_t *a, uint64_t *bytes) {
+    if (!bytes) return MCCB_ERR_PARAM_NULLPTR;
+    const int rc = check_delta(a, false);
+    if (rc != MCCB_OK) return rc;
+    const uint64_t chunks = chunks_of(a);
+    *bytes = records_size(a, chunks) + chunks * state_bytes(a) + chunks * (uint64_t)(a->B * a->H) * (uint64_t)(kC * a->V) * 4;
+    return MCCB_OK;
+}
+
+int mccb_delta_forward_get_workspace_size(const mccb_delta_t *a, uint64_t *size) {
+    if (!size) return MCCB_ERR_PARAM_NULLPTR;
+    const int rc = check_delta(a, false);
+    if (rc != MCCB_OK) return rc;
+    *size = records_size(a, chunks_of(a));
+    return MCCB_OK;
+}
+
+int mccb_delta_forward(const mccb_delta_t *a, void *out, float *final_state, void *saved, void *ws, uint64_t ws_size,
+                       void *stream) {
+    int rc = check_delta(a, false);
+    if (rc != MCCB_OK) return rc;
+    Span in[9];
+    int n;
+    rc = delta_inputs(a, false, in, &n);
+    if (rc != MCCB_OK) return rc;
+    if (!out && a->S > 0) return MCCB_ERR_PARAM_NULLPTR;
+    uint64_t need = 0, kept = 0;
+    if (saved) mccb_delta_saved_size(a, &kept);
+    else mccb_delta_forward_get_workspace_size(a, &need);
+    rc = check_workspace(ws, ws_size, need);
+    if (rc != MCCB_OK) return rc;
+    const Span o[4] = {{out, (uint64_t)a->S * (uint64_t)(a->B * a->H) * (uint64_t)a->V * 2}, {final_state, state_bytes(a)},
+                       {saved, kept}, {ws, need}};
+    if (misaligned(out, 2) || misaligned(final_state, 4) || misaligned(saved, 16) || outputs_clash(in, n, o, 4))
+        return MCCB_ERR_PARAM_INVALID;
+    if (a->S == 0 && !final_state) return MCCB_OK;
+    return a->dtype == MCCB_BF16 ? forward<MCCB_BF16>(a, out, final_state, saved, ws, (hipStream_t)stream)
+                                 : forward<MCCB_FP16>(a, out, final_state, saved, ws, (hipStream_t)stream);
+}
+
+int mccb_delta_step(const mccb_delta_t *a, float *state, void *out, void *stream) {
+    int rc = check_delta(a, true);
+    if (rc != MCCB_OK) return rc;
+    if (!state || !out) return MCCB_ERR_PARAM_NULLPTR;
+    if (a->state || a->lengths) return MCCB_ERR_PARAM_INVALID;
+    Span in[9];
+    int n;
+    rc = delta_inputs(a, true, in, &n);
+    if (rc != MCCB_OK) return rc;
+    const Span o[2] = {{out, (uint64_t)(a->B * a->H * a->V) * 2}, {state, state_bytes(a)}};
+    if (misaligned(out, 2) || misaligned(state, 4) || outputs_clash(in, n, o, 2)) return MCCB_ERR_PARAM_INVALID;
+    const dim3 grid((unsigned)((a->V + kStepCols - 1) / kStepCols), (unsigned)(a->B * a->H));
+    if (a->dtype == MCCB_BF16)
+        hipLaunchKernelGGL((delta_one<MCCB_BF16>), grid, dim3(kStepThreads), 0, (hipStream_t)stream, delta_of(a), state,
+                           (uint16_t *)out);
+    else
+        hipLaunchKernelGGL((delta_one<MCCB_FP16>), grid, dim3(kStepThreads), 0, (hipStream_t)stream, delta_of(a), state,
+                           (uint16_t *)out);
+    return launched();
+}
+
+}  // extern "C"

@@ -8,7 +8,7 @@ As in ``ssm`` this layer only checks and marshals arguments (in ``_delta``, comp
 backward is a call of its own.
 
 ``delta_lib()`` is the library itself, for calls of the C-ABI with device addresses; its argument structs are
-``NormArgs``.
+``DeltaArgs`` and ``NormArgs``.
 """
 from __future__ import annotations
 
@@ -24,6 +24,13 @@ from .ssm import _fields
 _i64, _u64, _vp = ctypes.c_int64, ctypes.c_uint64, ctypes.c_void_p
 
 
+class DeltaArgs(ctypes.Structure):
+    """mccb_delta_t, its stride arrays as separate fields."""
+    _fields_ = _fields("i: S B H G K V; w: dtype softplus normalize; f: scale; p: q k v dt b; "
+                       "i: q_stride*3 k_stride*3 v_stride*3 dt_stride*3 b_stride*3; "
+                       "p: A dt_bias lengths state")
+
+
 class NormArgs(ctypes.Structure):
     """mccb_norm_t."""
     _fields_ = _fields("i: R H groups; w: dtype weight_shared; f: eps; p: x weight residual scale z; "
@@ -31,6 +38,10 @@ class NormArgs(ctypes.Structure):
 
 
 _SIGNATURES = {
+    "mccb_delta_saved_size": (DeltaArgs, _vp),
+    "mccb_delta_forward_get_workspace_size": (DeltaArgs, _vp),
+    "mccb_delta_forward": (DeltaArgs, _vp, _vp, _vp, _vp, _u64, _vp),
+    "mccb_delta_step": (DeltaArgs, _vp, _vp, _vp),
     "mccb_prenorm_forward": (NormArgs, _vp, _vp, _vp),
     "mccb_prenorm_backward_get_workspace_size": (NormArgs, _vp),
     "mccb_prenorm_backward": (NormArgs, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _u64, _vp),
@@ -69,6 +80,34 @@ def _call(function, stream, *args):
     """function(*args) of the front end, on `stream` if one is given."""
     f = getattr(_module or delta_module(), function)
     return f(*args) if stream is None else on_stream(f, stream, args)
+
+
+# -- gated delta rule --------------------------------------------------------------------------------
+def delta_forward(q, k, v, dt, b, A, dt_bias=None, softplus=True, normalize=True, scale=None, lengths=None,
+                  state=None, return_state=False, return_saved=False, out=None, final_state=None,
+                  stream=None):
+    """Gated delta rule over q, k [S,B,G,K] (K up to 128), v [S,B,H,V] (V up to 256), dt and b [S,B,H], with
+    A and dt_bias [H] fp32; out [S,B,H,V]. H is a multiple of G: value head h has key head h // (H // G).
+
+    Row by row, for a head's state S [K,V]: a = exp(A softplus(dt + dt_bias)), beta = sigmoid(b),
+    u = beta (v - a S^T k), S = a S + k u^T, out = scale S^T q, with q and k divided by their norms unless
+    `normalize` is False; scale is K ** -0.5 unless given. q, k and v have contiguous rows.
+
+    `state` [B,H,K,V] fp32 is the state before the first row (zeros if None). The result is out, or a tuple
+    of it with the state after each sequence's last row (`return_state`) and what delta_backward needs
+    (`return_saved`). Rows at or past `lengths` (int64 [B] on the device) give zeros and leave the state
+    alone."""
+    return _call("delta_forward", stream, q, k, v, dt, b, A, dt_bias, bool(softplus), bool(normalize),
+                 None if scale is None else float(scale), lengths, state, bool(return_state),
+                 bool(return_saved), out, final_state)
+
+
+def delta_step(state, q, k, v, dt, b, A, dt_bias=None, softplus=True, normalize=True, scale=None, out=None,
+               stream=None):
+    """One token: out [B,H,V] from q, k [B,G,K], v [B,H,V], dt and b [B,H]; `state` [B,H,K,V] fp32 is
+    updated in place."""
+    return _call("delta_step", stream, q, k, v, dt, b, A, dt_bias, bool(softplus), bool(normalize),
+                 None if scale is None else float(scale), state, out)
 
 
 # -- norms before and after a block ------------------------------------------------------------------
