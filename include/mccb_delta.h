@@ -64,6 +64,24 @@ int mccb_delta_forward_get_workspace_size(const mccb_delta_t *args, uint64_t *wo
 int mccb_delta_forward(const mccb_delta_t *args, void *out, float *final_state, void *saved,
                        void *workspace, uint64_t workspace_size, void *stream);
 
+/* Gradients. gradOut has strides gout_stride and contiguous rows; gradFinalState may be NULL (zero). Outputs
+ * are contiguous and required, except gradDtBias and gradState. Gradients of q and k add the value heads
+ * of a key head in fp32; gradA and gradDtBias add rows and chunks in fp64. Every order is fixed. */
+typedef struct {
+    const void *gradOut;           /* [S,B,H,V] */
+    int64_t gout_stride[3];        /* along S, B, H */
+    const float *gradFinalState;   /* [B,H,K,V] or NULL */
+    void *gradQ, *gradK;           /* [S,B,G,K] */
+    void *gradV;                   /* [S,B,H,V] */
+    void *gradDt, *gradB;          /* [S,B,H] */
+    float *gradA, *gradDtBias;     /* [H]; gradDtBias may be NULL */
+    float *gradState;              /* [B,H,K,V] or NULL */
+} mccb_delta_grads_t;
+
+int mccb_delta_backward_get_workspace_size(const mccb_delta_t *args, uint64_t *workspace_size);
+int mccb_delta_backward(const mccb_delta_t *args, const mccb_delta_grads_t *grads, const void *saved,
+                        void *workspace, uint64_t workspace_size, void *stream);
+
 /* One token: q, k [B,G,K], v and out [B,H,V], dt and b [B,H] (args->S = 1, the strides along S unused);
  * `state` [B,H,K,V] is updated in place. args->state and args->lengths are NULL. */
 int mccb_delta_step(const mccb_delta_t *args, float *state, void *out, void *stream);

@@ -16,8 +16,9 @@ import ctypes
 import torch
 
 from ._lib import MccbError, Plan, Strides, lib, status_string  # noqa: F401
-from .delta import (PostnormGrads, PrenormGrads, delta_forward, delta_lib, delta_step,  # noqa: F401
-                    postnorm_backward, postnorm_forward, prenorm_backward, prenorm_forward)
+from .delta import (DeltaGrads, PostnormGrads, PrenormGrads, delta_backward, delta_forward,  # noqa: F401
+                    delta_lib, delta_step, postnorm_backward, postnorm_forward, prenorm_backward,
+                    prenorm_forward)
 from .ssm import (ACTIVATIONS, ConvGrads, LinearGrads, ScanGrads,  # noqa: F401
                   conv_act_backward, conv_act_forward, conv_act_step, linear_backward,
                   linear_forward, scan_backward, scan_forward, scan_step, ssm_lib)

@@ -20,7 +20,8 @@ SSM_LIB = os.environ.get("MCCB_SSM_LIBRARY") or os.path.join(PKG, "libmccb_ssm.s
 BINDING_SRC = os.path.join(PKG, "csrc", "ssm_binding.cpp")
 BINDING = os.path.join(PKG, "_ssm.so")
 # the gated delta rule and the norms; MCCB_DELTA_LIBRARY as above
-DELTA_SRCS = [os.path.join(PKG, "csrc", f) for f in ("delta_norm.hip", "delta_rule.hip")]
+DELTA_SRCS = [os.path.join(PKG, "csrc", f) for f in ("delta_norm.hip", "delta_rule.hip",
+                                                    "delta_back.hip")]
 DELTA_LIB = os.environ.get("MCCB_DELTA_LIBRARY") or os.path.join(PKG, "libmccb_delta.so")
 DELTA_BINDING_SRC = os.path.join(PKG, "csrc", "delta_binding.cpp")
 DELTA_BINDING = os.path.join(PKG, "_delta.so")

@@ -14,6 +14,8 @@ struct Library {
     decltype(&mccb_delta_saved_size) delta_saved_size;
     decltype(&mccb_delta_forward_get_workspace_size) delta_forward_size;
     decltype(&mccb_delta_forward) delta_forward;
+    decltype(&mccb_delta_backward_get_workspace_size) delta_backward_size;
+    decltype(&mccb_delta_backward) delta_backward;
     decltype(&mccb_delta_step) delta_step;
     decltype(&mccb_prenorm_forward) prenorm_forward;
     decltype(&mccb_prenorm_backward_get_workspace_size) prenorm_backward_size;
@@ -104,6 +106,32 @@ PyObject *delta_forward(PyObject *const *v) {
     wrote({y, final_state});
     if (with_state) return with_saved ? tuple({y, final_state, saved}) : tuple({y, final_state});
     return with_saved ? tuple({y, saved}) : out(y);
+}
+
+// (q, k, v, dt, b, A, dt_bias, softplus, normalize, scale, lengths, state, gradOut, saved, gradFinalState)
+PyObject *delta_backward(PyObject *const *v) {
+    Delta c;
+    delta_args(c, v, false);
+    delta_rows(c, v[10], v[11]);
+    const Tensor go = tensor(v[12], "gradOut"), saved = tensor(v[13], "saved");
+    const Tensor gfinal = maybe(v[14], "gradFinalState");
+    const std::array<int64_t, 4> states{c.a.B, c.a.H, c.a.K, c.a.V};
+    mccb_delta_grads_t g{};
+    head_rows("gradOut", go, c.v.sizes(), c.q, g.gout_stride, false);
+    check("saved", saved, {saved_bytes(c)}, at::kByte, c.q.device(), true);
+    check_if("gradFinalState", gfinal, states, at::kFloat, c.q.device());
+    uint64_t n = 0;
+    ok(lib.delta_backward_size(&c.a, &n), "mccb_delta_backward_get_workspace_size");
+    const Tensor gq = make(c.q.sizes(), c.q), gk = make(c.k.sizes(), c.q), gv = make(c.v.sizes(), c.q);
+    const Tensor gdt = make(c.dt.sizes(), c.q), gb = make(c.b.sizes(), c.q), gA = make(c.A.sizes(), c.A);
+    const Tensor gbias = c.bias.defined() ? make(c.bias.sizes(), c.bias) : Tensor();
+    const Tensor gstate = c.state.defined() ? make(states, c.state) : Tensor();
+    const Tensor ws = bytes(n, c.q);
+    g.gradOut = ptr(go), g.gradFinalState = (const float *)ptr(gfinal);
+    g.gradQ = ptr(gq), g.gradK = ptr(gk), g.gradV = ptr(gv), g.gradDt = ptr(gdt), g.gradB = ptr(gb);
+    g.gradA = (float *)ptr(gA), g.gradDtBias = (float *)ptr(gbias), g.gradState = (float *)ptr(gstate);
+    ok(lib.delta_backward(&c.a, &g, ptr(saved), ptr(ws), n, stream_of(c.q)), "mccb_delta_backward");
+    return tuple({gq, gk, gv, gdt, gb, gA, gbias, gstate});
 }
 
 // (q, k, v, dt, b, A, dt_bias, softplus, normalize, scale, state, out)
@@ -228,6 +256,7 @@ PyObject *bind(PyObject *, PyObject *args) { return bind_to(lib, args); }
 PyMethodDef methods[] = {
     {"bind", &bind, METH_VARARGS, nullptr},
     ENTRY(delta_forward, 16),
+    ENTRY(delta_backward, 15),
     ENTRY(delta_step, 12),
     ENTRY(prenorm_forward, 8),
     ENTRY(prenorm_backward, 7),

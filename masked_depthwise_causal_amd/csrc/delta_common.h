@@ -36,8 +36,9 @@ typedef _Float16 h8 __attribute__((ext_vector_type(8)));
 typedef float f4 __attribute__((ext_vector_type(4)));
 
 // ---------------------------------------------------------------------------------------------
-// What one kernel hands to the next for a chunk. A key head's: the images of its rows of k and q, and the
-// factors that make them normalized rows, kn = kr k~, qn = qr q~ (without the scale). A value head's: the
+// What one kernel hands to the next for a chunk. A key head's: the images of its rows of k and q, the factors
+// that make them normalized rows, kn = kr k~, qn = qr q~ (without the scale), and those of k~ = k 2^-e and
+// q~ = q 2^-e. A value head's: the
 // images of X and A in two terms each, and what belongs to single rows.
 // ---------------------------------------------------------------------------------------------
 struct RowCoef {
@@ -52,7 +53,7 @@ struct RowCoef {
 };
 constexpr int kStaged = 4 * kC * (int)sizeof(float);  // the bytes of RowCoef that the walk stages: four rows
 
-constexpr size_t key_bytes(int kp) { return 2 * kC * kp * sizeof(uint16_t) + 2 * kC * sizeof(float); }
+constexpr size_t key_bytes(int kp) { return 2 * kC * kp * sizeof(uint16_t) + 4 * kC * sizeof(float); }
 constexpr size_t kXaBytes = 4 * kSquare * sizeof(uint16_t);  // X hi, X lo, A hi, A lo
 
 // An image row R holds its chunks of 8 values in the order c ^ swizzle(R). The matrix instructions' rows m
@@ -201,6 +202,32 @@ __host__ static inline Records records_at(void *p, uint64_t key_heads, uint64_t 
     r.chunks = (int64_t)chunks;
     return r;
 }
+
+// A wave's load of 1 KiB straight to LDS, 16 bytes a lane.
+__device__ static inline void to_lds(const uint8_t *from, uint8_t *to, int lane) {
+    typedef __attribute__((address_space(1))) const uint8_t gmem;
+    typedef __attribute__((address_space(3))) uint8_t lmem;
+    __builtin_amdgcn_global_load_lds((gmem *)(from + 16 * lane), (lmem *)to, 16, 0, 0);
+}
+
+// Blocks of one head, and heads of one key head, next to each other on one of the 8 dies, which have an L2 each.
+__device__ static inline int same_die(int id, int all) { return all % 8 ? id : id % 8 * (all / 8) + id / 8; }
+
+// ---------------------------------------------------------------------------------------------
+// Host side, of both directions.
+// ---------------------------------------------------------------------------------------------
+constexpr int kMaxK = 128;
+
+inline uint64_t chunks_of(const mccb_delta_t *a) { return (uint64_t)((a->S + kC - 1) / kC); }
+inline uint64_t state_bytes(const mccb_delta_t *a) { return (uint64_t)(a->B * a->H) * (uint64_t)(a->K * a->V) * 4; }
+// fp32 values for every chunk's rows and column of V
+inline uint64_t chunk_rows_bytes(const mccb_delta_t *a) {
+    return chunks_of(a) * (uint64_t)(a->B * a->H) * (uint64_t)(kC * a->V) * 4;
+}
+Delta delta_of(const mccb_delta_t *a);
+int check_delta(const mccb_delta_t *a, bool token);
+int delta_inputs(const mccb_delta_t *a, bool token, Span *in, int *count);
+uint64_t records_size(const mccb_delta_t *a, uint64_t chunks);
 
 __host__ static inline int padded(int64_t K) { return K <= 64 ? 64 : 128; }
 

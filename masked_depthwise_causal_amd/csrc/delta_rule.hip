@@ -12,6 +12,62 @@
 
 using namespace delta;
 
+namespace delta {
+
+Delta delta_of(const mccb_delta_t *a) {
+    Delta d{};
+    d.S = (int)a->S, d.B = (int)a->B, d.H = (int)a->H, d.G = (int)a->G, d.K = (int)a->K, d.V = (int)a->V;
+    d.softplus = a->softplus, d.normalize = a->normalize, d.scale = a->scale;
+    d.q = (const uint16_t *)a->q, d.k = (const uint16_t *)a->k, d.v = (const uint16_t *)a->v;
+    d.dt = (const uint16_t *)a->dt, d.b = (const uint16_t *)a->b;
+    for (int i = 0; i < 3; ++i)
+        d.qs[i] = a->q_stride[i], d.ks[i] = a->k_stride[i], d.vs[i] = a->v_stride[i], d.ds[i] = a->dt_stride[i],
+        d.bs[i] = a->b_stride[i];
+    d.A = a->A, d.bias = a->dt_bias, d.lengths = a->lengths;
+    return d;
+}
+
+int check_delta(const mccb_delta_t *a, bool token) {
+    if (!a) return MCCB_ERR_PARAM_NULLPTR;
+    if (a->dtype != MCCB_BF16 && a->dtype != MCCB_FP16) return MCCB_ERR_PARAM_INVALID;
+    if (a->S < 0 || a->S >= (1 << 28) || (token && a->S != 1) || a->B < 1 || a->H < 1 || a->B > 65535 ||
+        a->H > 65535 || a->B * a->H > 65535 || a->G < 1 || a->G > a->H || a->H % a->G != 0 || a->K < 1 ||
+        a->K > kMaxK || a->V < 1 || a->V > 256)
+        return MCCB_ERR_SHAPE;
+    if (!(a->scale >= -3.0e38f && a->scale <= 3.0e38f)) return MCCB_ERR_PARAM_INVALID;
+    return MCCB_OK;
+}
+
+// Spans of the inputs; token: without a row axis.
+int delta_inputs(const mccb_delta_t *a, bool token, Span *in, int *count) {
+    if (!a->A || (a->S > 0 && (!a->q || !a->k || !a->v || !a->dt || !a->b))) return MCCB_ERR_PARAM_NULLPTR;
+    const void *const p[5] = {a->q, a->k, a->v, a->dt, a->b};
+    const int64_t *const st[5] = {a->q_stride, a->k_stride, a->v_stride, a->dt_stride, a->b_stride};
+    const int64_t heads[5] = {a->G, a->G, a->H, a->H, a->H}, width[5] = {a->K, a->K, a->V, 1, 1};
+    int n = 0;
+    for (int i = 0; i < 5; ++i) {
+        const int64_t size[4] = {token ? 1 : a->S, a->B, heads[i], width[i]};
+        const int64_t stride[4] = {token ? 0 : st[i][0], st[i][1], st[i][2], 1};
+        uint64_t bytes;
+        if (!extent(4, size, stride, 2, &bytes) || misaligned(p[i], 2)) return MCCB_ERR_PARAM_INVALID;
+        in[n++] = {p[i], bytes};
+    }
+    if (misaligned(a->A, 4) || misaligned(a->dt_bias, 4) || misaligned(a->lengths, 8) || misaligned(a->state, 4))
+        return MCCB_ERR_PARAM_INVALID;
+    in[n++] = {a->A, (uint64_t)a->H * 4};
+    in[n++] = {a->dt_bias, (uint64_t)a->H * 4};
+    in[n++] = {a->lengths, (uint64_t)a->B * 8};
+    in[n++] = {a->state, state_bytes(a)};
+    *count = n;
+    return MCCB_OK;
+}
+
+uint64_t records_size(const mccb_delta_t *a, uint64_t chunks) {
+    return align16(records_bytes((uint64_t)(a->B * a->G), (uint64_t)(a->B * a->H), chunks, padded(a->K)));
+}
+
+}  // namespace delta
+
 namespace {
 
 // ---------------------------------------------------------------------------------------------
@@ -35,7 +91,7 @@ __device__ static inline HVec<8>::t row_chunk(const uint16_t *p, int left) {
 template <int DT, int KP>
 __device__ static inline void image_rows(const Delta &a, const uint16_t *base, const int64_t (&st)[3], int b, int g,
                                          int row0, int live, uint16_t *lds, uint16_t *image, float *factor,
-                                         float *factor_out) {
+                                         float *factor_out, float *power_out) {
     constexpr int kLanes = KP / 8, kRows = kPrepThreads / kLanes;
     const int lane = threadIdx.x % kLanes;
     for (int r = threadIdx.x / kLanes; r < kC; r += kRows) {
@@ -66,6 +122,7 @@ __device__ static inline void image_rows(const Delta &a, const uint16_t *base, c
                                         : __builtin_ldexpf(1.0f, e);
             factor[r] = f;
             factor_out[r] = f;
+            power_out[r] = __builtin_ldexpf(1.0f, -e);
         }
     }
 }
@@ -172,8 +229,10 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prepare(Delta a, Records r
         uint8_t *key = rec.key + ((int64_t)(b * a.G + g) * rec.chunks + n) * key_bytes(KP);
         uint16_t *images = (uint16_t *)key;
         float *factors = (float *)(images + 2 * kC * KP);
-        image_rows<DT, KP>(a, a.k, a.ks, b, g, row0, live, kt, images, kr, factors);
-        image_rows<DT, KP>(a, a.q, a.qs, b, g, row0, live, qt, images + kC * KP, qr, factors + kC);
+        image_rows<DT, KP>(a, a.k, a.ks, b, g, row0, live, kt, images, kr, factors,
+                           factors + 2 * kC);
+        image_rows<DT, KP>(a, a.q, a.qs, b, g, row0, live, qt, images + kC * KP, qr,
+                           factors + kC, factors + 3 * kC);
     }
     lds_barrier();
     // K~ K~^T and Q~ K~^T: wave w has rows 16 w.. of both, up to the diagonal block
@@ -265,16 +324,6 @@ struct Walk {
     int n0, n1;                     // chunks
     int blocks;                     // of columns, a head
 };
-
-// A wave's load of 1 KiB straight to LDS, 16 bytes a lane.
-__device__ static inline void to_lds(const uint8_t *from, uint8_t *to, int lane) {
-    typedef __attribute__((address_space(1))) const uint8_t gmem;
-    typedef __attribute__((address_space(3))) uint8_t lmem;
-    __builtin_amdgcn_global_load_lds((gmem *)(from + 16 * lane), (lmem *)to, 16, 0, 0);
-}
-
-// Blocks of one head, and heads of one key head, next to each other on one of the 8 dies, which have an L2 each.
-__device__ static inline int same_die(int id, int all) { return all % 8 ? id : id % 8 * (all / 8) + id / 8; }
 
 template <int DT, int KP, int NT, int W>
 __global__ void __launch_bounds__(W *kWave) delta_walk(Delta a, Records rec, Walk w) {
@@ -527,7 +576,7 @@ __global__ void __launch_bounds__(W *kWave) delta_walk(Delta a, Records rec, Wal
 // out = o + (qn . kn) u, S = a S + kn u^T.
 // ---------------------------------------------------------------------------------------------
 constexpr int kStepCols = 32, kStepThreads = 256;
-constexpr int kMaxK = 128, kStepRows = kMaxK / 32;
+constexpr int kStepRows = kMaxK / 32;
 
 template <int DT>
 __global__ void __launch_bounds__(kStepThreads) delta_one(Delta a, float *state, uint16_t *out) {
@@ -627,61 +676,6 @@ __global__ void __launch_bounds__(kStepThreads) delta_one(Delta a, float *state,
 // ---------------------------------------------------------------------------------------------
 // Host side.
 // ---------------------------------------------------------------------------------------------
-uint64_t chunks_of(const mccb_delta_t *a) { return (uint64_t)((a->S + kC - 1) / kC); }
-uint64_t state_bytes(const mccb_delta_t *a) { return (uint64_t)(a->B * a->H) * (uint64_t)(a->K * a->V) * 4; }
-
-Delta delta_of(const mccb_delta_t *a) {
-    Delta d{};
-    d.S = (int)a->S, d.B = (int)a->B, d.H = (int)a->H, d.G = (int)a->G, d.K = (int)a->K, d.V = (int)a->V;
-    d.softplus = a->softplus, d.normalize = a->normalize, d.scale = a->scale;
-    d.q = (const uint16_t *)a->q, d.k = (const uint16_t *)a->k, d.v = (const uint16_t *)a->v;
-    d.dt = (const uint16_t *)a->dt, d.b = (const uint16_t *)a->b;
-    for (int i = 0; i < 3; ++i)
-        d.qs[i] = a->q_stride[i], d.ks[i] = a->k_stride[i], d.vs[i] = a->v_stride[i], d.ds[i] = a->dt_stride[i],
-        d.bs[i] = a->b_stride[i];
-    d.A = a->A, d.bias = a->dt_bias, d.lengths = a->lengths;
-    return d;
-}
-
-int check_delta(const mccb_delta_t *a, bool token) {
-    if (!a) return MCCB_ERR_PARAM_NULLPTR;
-    if (a->dtype != MCCB_BF16 && a->dtype != MCCB_FP16) return MCCB_ERR_PARAM_INVALID;
-    if (a->S < 0 || a->S >= (1 << 28) || (token && a->S != 1) || a->B < 1 || a->H < 1 || a->B > 65535 ||
-        a->H > 65535 || a->B * a->H > 65535 || a->G < 1 || a->G > a->H || a->H % a->G != 0 || a->K < 1 ||
-        a->K > kMaxK || a->V < 1 || a->V > 256)
-        return MCCB_ERR_SHAPE;
-    if (!(a->scale >= -3.0e38f && a->scale <= 3.0e38f)) return MCCB_ERR_PARAM_INVALID;
-    return MCCB_OK;
-}
-
-// Spans of the inputs; token: without a row axis.
-int delta_inputs(const mccb_delta_t *a, bool token, Span *in, int *count) {
-    if (!a->A || (a->S > 0 && (!a->q || !a->k || !a->v || !a->dt || !a->b))) return MCCB_ERR_PARAM_NULLPTR;
-    const void *const p[5] = {a->q, a->k, a->v, a->dt, a->b};
-    const int64_t *const st[5] = {a->q_stride, a->k_stride, a->v_stride, a->dt_stride, a->b_stride};
-    const int64_t heads[5] = {a->G, a->G, a->H, a->H, a->H}, width[5] = {a->K, a->K, a->V, 1, 1};
-    int n = 0;
-    for (int i = 0; i < 5; ++i) {
-        const int64_t size[4] = {token ? 1 : a->S, a->B, heads[i], width[i]};
-        const int64_t stride[4] = {token ? 0 : st[i][0], st[i][1], st[i][2], 1};
-        uint64_t bytes;
-        if (!extent(4, size, stride, 2, &bytes) || misaligned(p[i], 2)) return MCCB_ERR_PARAM_INVALID;
-        in[n++] = {p[i], bytes};
-    }
-    if (misaligned(a->A, 4) || misaligned(a->dt_bias, 4) || misaligned(a->lengths, 8) || misaligned(a->state, 4))
-        return MCCB_ERR_PARAM_INVALID;
-    in[n++] = {a->A, (uint64_t)a->H * 4};
-    in[n++] = {a->dt_bias, (uint64_t)a->H * 4};
-    in[n++] = {a->lengths, (uint64_t)a->B * 8};
-    in[n++] = {a->state, state_bytes(a)};
-    *count = n;
-    return MCCB_OK;
-}
-
-uint64_t records_size(const mccb_delta_t *a, uint64_t chunks) {
-    return align16(records_bytes((uint64_t)(a->B * a->G), (uint64_t)(a->B * a->H), chunks, padded(a->K)));
-}
-
 template <int DT, int KP>
 int prepare(const Delta &d, const Records &rec, int n0, int n1, hipStream_t st) {
     hipLaunchKernelGGL((delta_prepare<DT, KP>), dim3((unsigned)(n1 - n0), (unsigned)(d.B * d.G)), dim3(kPrepThreads),
@@ -728,7 +722,7 @@ int mccb_delta_saved_size(const mccb_delta_t *a, uint64_t *bytes) {
     const int rc = check_delta(a, false);
     if (rc != MCCB_OK) return rc;
     const uint64_t chunks = chunks_of(a);
-    *bytes = records_size(a, chunks) + chunks * state_bytes(a) + chunks * (uint64_t)(a->B * a->H) * (uint64_t)(kC * a->V) * 4;
+    *bytes = records_size(a, chunks) + chunks * state_bytes(a) + chunk_rows_bytes(a);
     return MCCB_OK;
 }
 

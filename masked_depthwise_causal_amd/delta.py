@@ -8,7 +8,7 @@ As in ``ssm`` this layer only checks and marshals arguments (in ``_delta``, comp
 backward is a call of its own.
 
 ``delta_lib()`` is the library itself, for calls of the C-ABI with device addresses; its argument structs are
-``DeltaArgs`` and ``NormArgs``.
+``DeltaArgs``, ``DeltaGradArgs`` and ``NormArgs``.
 """
 from __future__ import annotations
 
@@ -31,6 +31,12 @@ class DeltaArgs(ctypes.Structure):
                        "p: A dt_bias lengths state")
 
 
+class DeltaGradArgs(ctypes.Structure):
+    """mccb_delta_grads_t, its stride array as separate fields."""
+    _fields_ = _fields("p: gradOut; i: gout_stride*3; p: gradFinalState gradQ gradK gradV gradDt gradB "
+                       "gradA gradDtBias gradState")
+
+
 class NormArgs(ctypes.Structure):
     """mccb_norm_t."""
     _fields_ = _fields("i: R H groups; w: dtype weight_shared; f: eps; p: x weight residual scale z; "
@@ -41,6 +47,8 @@ _SIGNATURES = {
     "mccb_delta_saved_size": (DeltaArgs, _vp),
     "mccb_delta_forward_get_workspace_size": (DeltaArgs, _vp),
     "mccb_delta_forward": (DeltaArgs, _vp, _vp, _vp, _vp, _u64, _vp),
+    "mccb_delta_backward_get_workspace_size": (DeltaArgs, _vp),
+    "mccb_delta_backward": (DeltaArgs, _vp, _vp, _vp, _u64, _vp),
     "mccb_delta_step": (DeltaArgs, _vp, _vp, _vp),
     "mccb_prenorm_forward": (NormArgs, _vp, _vp, _vp),
     "mccb_prenorm_backward_get_workspace_size": (NormArgs, _vp),
@@ -83,6 +91,17 @@ def _call(function, stream, *args):
 
 
 # -- gated delta rule --------------------------------------------------------------------------------
+class DeltaGrads(NamedTuple):
+    q: torch.Tensor
+    k: torch.Tensor
+    v: torch.Tensor
+    dt: torch.Tensor
+    b: torch.Tensor
+    A: torch.Tensor
+    dt_bias: Optional[torch.Tensor]
+    state: Optional[torch.Tensor]
+
+
 def delta_forward(q, k, v, dt, b, A, dt_bias=None, softplus=True, normalize=True, scale=None, lengths=None,
                   state=None, return_state=False, return_saved=False, out=None, final_state=None,
                   stream=None):
@@ -100,6 +119,16 @@ def delta_forward(q, k, v, dt, b, A, dt_bias=None, softplus=True, normalize=True
     return _call("delta_forward", stream, q, k, v, dt, b, A, dt_bias, bool(softplus), bool(normalize),
                  None if scale is None else float(scale), lengths, state, bool(return_state),
                  bool(return_saved), out, final_state)
+
+
+def delta_backward(gradOut, q, k, v, dt, b, A, saved, dt_bias=None, softplus=True, normalize=True, scale=None,
+                   lengths=None, state=None, gradFinalState=None, stream=None) -> DeltaGrads:
+    """Gradients of delta_forward with the same arguments and what it saved: of every input that was
+    given. gradOut [S,B,H,V] may be strided, with contiguous rows; gradFinalState [B,H,K,V] fp32 is the
+    gradient of the returned state, if one flows back."""
+    return DeltaGrads(*_call("delta_backward", stream, q, k, v, dt, b, A, dt_bias, bool(softplus),
+                             bool(normalize), None if scale is None else float(scale), lengths, state,
+                             gradOut, saved, gradFinalState))
 
 
 def delta_step(state, q, k, v, dt, b, A, dt_bias=None, softplus=True, normalize=True, scale=None, out=None,
