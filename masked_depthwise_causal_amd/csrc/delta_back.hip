@@ -33,7 +33,7 @@ struct Back {
     const float *gfinal;            // [B,H,K,V] or NULL
     uint16_t *gv;                   // [S,B,H,V]
     float *gstate;                  // [B,H,K,V] or NULL
-    float *gstates, *y;             // [B,H][chunk][K,V], the gradient of S1; [B,H][chunk][64,V]
+    float *gstates, *y;             // [B,H][chunk][K,V], the gradient of S1; [B,H][chunk][64,V]; padded
     const float *states, *u;        // the forward's
     uint16_t *gq, *gk, *gdt, *gb;   // [S,B,G,K], [S,B,H]
     double *part;                   // [2][chunk * B + b][H]: the chunks' parts of gA and gDtBias
@@ -41,17 +41,18 @@ struct Back {
     int blocks;                     // of columns, a head
 };
 
-template <int DT, int KP, int W>
+template <int DT, int KP, int W, bool WIDE>
 __global__ void __launch_bounds__(W *kWave) delta_walk_back(Delta a, Records rec, Back w) {
     constexpr int KT = KP / 16, KS = KP / 32;
-    constexpr int kKeys = 2 * kC * KP * 2;
-    constexpr int kBuf = kKeys + (int)kXaBytes + kStaged;
+    typedef Staged<KP, W> Stage;
+    constexpr int kBuf = Stage::kBytes, kKeys = Stage::kKeys;
     __shared__ __align__(16) uint8_t smem[2 * kBuf];
     const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int m = lane & 15, grp = lane >> 4;
+    const int lk_at = left_place<KP>(lane), tk_at = turned_place<KP>(lane), ts_at = turned_place<64>(lane);
     const int id = same_die(blockIdx.x, gridDim.x);
     const int bh = id / w.blocks, b = bh / a.H, h = bh % a.H, g = h / (a.H / a.G);
-    const int col = (id % w.blocks * W + wave) * 16 + m;
+    const int col = (id % w.blocks * W + wave) * 16 + m, VP = padded_v(a.V);
     const bool mine = col < a.V;
     const int length = length_of(a, b), chunks = (length + kC - 1) / kC;
 
@@ -63,88 +64,76 @@ __global__ void __launch_bounds__(W *kWave) delta_walk_back(Delta a, Records rec
             const int k = row_of(t, 4 * grp + i);
             S[t][i] = w.gfinal && k < a.K && mine ? w.gfinal[((int64_t)bh * a.K + k) * a.V + col] : 0.0f;
         }
-    const uint8_t *keys = rec.key + (int64_t)(b * a.G + g) * rec.chunks * key_bytes(KP);
-    const uint8_t *xas = rec.xa + (int64_t)bh * rec.chunks * kXaBytes;
+    const uint8_t *key = rec.key + (int64_t)(b * a.G + g) * rec.chunks * key_bytes(KP);
+    const uint8_t *xa = rec.xa + (int64_t)bh * rec.chunks * kXaBytes;
     const RowCoef *coefs = rec.coef + (int64_t)bh * rec.chunks;
-    auto fill = [&](int n) {
-        uint8_t *to = smem + (n & 1) * kBuf;
-        const uint8_t *key = keys + n * (int64_t)key_bytes(KP), *xa = xas + n * (int64_t)kXaBytes;
-        const uint8_t *coef = (const uint8_t *)(coefs + n);
-        for (int p = wave; p < kBuf / 1024; p += W) {
-            const int o = p * 1024;
-            to_lds(o < kKeys ? key + o : o < kKeys + (int)kXaBytes ? xa + (o - kKeys) : coef, to + o, lane);
-        }
-    };
-    const uint16_t *gbase = w.gout + b * w.gs[1] + h * w.gs[2];
-    uint16_t next[4][4];
-    auto fetch = [&](int n) {
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int row = n * kC + row_of(t, 4 * grp + i);
-                next[t][i] = row < length && mine ? gbase[(int64_t)row * w.gs[0] + col] : 0;
-            }
-    };
-    if (chunks > 0) fill(chunks - 1), fetch(chunks - 1);
+    Stage stage;
+    auto fetch = [&](int n) { stage.load(key + n * (int64_t)key_bytes(KP), xa + n * (int64_t)kXaBytes, coefs + n); };
+    const Column16 gcol = {w.gout + b * w.gs[1] + h * w.gs[2], w.gs[0], col, a.V};
+    const uint32_t gv_row = 2u * (uint32_t)(a.B * a.H) * a.V;  // bytes
+    const uint32_t gv_at = mine ? 8 * grp * gv_row + 2 * (h * a.V + col) : kNowhere;
+    float *keep_s = w.gstates + ((int64_t)bh * rec.chunks * KP + 8 * grp) * VP + col;
+    float *keep_y = w.y + ((int64_t)bh * rec.chunks * kC + 8 * grp) * VP + col;
+    uint16_t v[4][4];
+    if (chunks > 0) {
+        const int n = chunks - 1;
+        fetch(n);
+        load_rows<WIDE>(gcol, n * kC, length - n * kC, lane, v);
+        stage.store(smem + (n & 1) * kBuf);
+        lds_barrier();
+    }
     for (int n = chunks - 1; n >= 0; --n) {
-        __syncthreads();  // this chunk's operands are there, and all waves are done with the last one's
         const uint8_t *buf = smem + (n & 1) * kBuf;
         const uint16_t *kt = (const uint16_t *)buf, *qt = kt + kC * KP;
         const uint16_t *xh = (const uint16_t *)(buf + kKeys), *xl = xh + kSquare, *ah = xl + kSquare, *al = ah + kSquare;
-        const float *coef = (const float *)(buf + kKeys + kXaBytes);
-        const float whole = coefs[n].whole, sx = coefs[n].x, sa = coefs[n].a;
-        f4 G[4];
+        const RowCoef *coef = (const RowCoef *)(buf + kKeys + kXaBytes);
+        const int next = n > 0 ? n - 1 : 0;
+        fetch(next);
+        {
+            float *to = keep_s + (int64_t)n * KP * VP;
+#pragma unroll
+            for (int t = 0; t < KT; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) to[(row_of(t, 0) + i) * VP] = S[t][i];
+        }
+        f4 G[4], D[4] = {};
 #pragma unroll
         for (int t = 0; t < 4; ++t)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) G[t][i] = to_f32<DT>(next[t][i]);
-        if (n > 0) fill(n - 1), fetch(n - 1);
-        float *keep = w.gstates + ((int64_t)bh * rec.chunks + n) * a.K * a.V;
-#pragma unroll
-        for (int t = 0; t < KT; ++t)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int k = row_of(t, 4 * grp + i);
-                if (k < a.K && mine) keep[(int64_t)k * a.V + col] = S[t][i];
-            }
+            for (int i = 0; i < 4; ++i) G[t][i] = to_f32<DT>(v[t][i]);
+        load_rows<WIDE>(gcol, next * kC, length - next * kC, lane, v);
         // u K~ gS1
-        f4 D[4] = {};
         {
-            const Power p = column_power(S);
+            const Power p = column_power(S, lane);
 #pragma unroll
             for (int s = 0; s < KS; ++s) {
                 const Split sp = split(S[2 * s], S[2 * s + 1], p.inv);
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
-                    const h8 lk = left<KP>(kt, t, s, lane);
+                    const h8 lk = left<KP>(kt, lk_at, t, s);
                     D[t] = mma(lk, sp.hi, D[t]);
                     D[t] = mma(lk, sp.lo, D[t]);
                 }
             }
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                const f4 cu = *(const f4 *)(coef + 3 * kC + row_of(t, 4 * grp));
-#pragma unroll
-                for (int i = 0; i < 4; ++i) D[t][i] *= cu[i] * p.back;
-            }
+            for (int t = 0; t < 4; ++t) D[t] *= *(const f4 *)(coef->u + row_of(t, 4 * grp)) * p.back;
         }
         // + A^T gO, whose 16-bit values are exact in one term
         {
-            const Power p = column_power(G);
+            const Power p = column_power(G, lane);
             h8 one[2];
 #pragma unroll
             for (int s = 0; s < 2; ++s)
 #pragma unroll
                 for (int i = 0; i < 8; ++i) one[s][i] = (_Float16)(G[2 * s + i / 4][i % 4] * p.inv);
-            const float up = p.back * sa;
+            const float up = p.back * coef->a;
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
                 f4 d = {};
 #pragma unroll
                 for (int s = t / 2; s < 2; ++s) {
-                    d = mma(left_turned<64>(ah, t, s, lane), one[s], d);
-                    d = mma(left_turned<64>(al, t, s, lane), one[s], d);
+                    d = mma(left_turned<64>(al, ts_at, t, s), one[s], d);
+                    d = mma(left_turned<64>(ah, ts_at, t, s), one[s], d);
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) D[t][i] = __builtin_fmaf(d[i], up, D[t][i]);
@@ -153,37 +142,40 @@ __global__ void __launch_bounds__(W *kWave) delta_walk_back(Delta a, Records rec
         // Y = X^T gU
         f4 Y[4];
         {
-            const Power p = column_power(D);
-            Split sp[2];
-#pragma unroll
-            for (int s = 0; s < 2; ++s) sp[s] = split(D[2 * s], D[2 * s + 1], p.inv);
-            const float up = p.back * sx;
+            const Power p = column_power(D, lane);
+            const Split s0 = split(D[0], D[1], p.inv), s1 = split(D[2], D[3], p.inv);
+            const float up = p.back * coef->x;
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
                 f4 d = {};
 #pragma unroll
                 for (int s = t / 2; s < 2; ++s) {
-                    const h8 lh = left_turned<64>(xh, t, s, lane), ll = left_turned<64>(xl, t, s, lane);
-                    d = mma(lh, sp[s].hi, d);
-                    d = mma(ll, sp[s].hi, d);
-                    d = mma(lh, sp[s].lo, d);
+                    const h8 lh = left_turned<64>(xh, ts_at, t, s), ll = left_turned<64>(xl, ts_at, t, s);
+                    const Split &sp = s ? s1 : s0;
+                    d = mma(ll, sp.hi, d);
+                    d = mma(lh, sp.lo, d);
+                    d = mma(lh, sp.hi, d);
                 }
                 Y[t] = d * up;
             }
         }
-        float *keep_y = w.y + ((int64_t)bh * rec.chunks + n) * kC * a.V;
+        {
+            float *to = keep_y + (int64_t)n * kC * VP;
+            const int left_rows = a.S - n * kC;
+            const Buffer gv = buffer_of(w.gv + (int64_t)n * kC * (gv_row / 2) + (int64_t)b * a.H * a.V,
+                                        (left_rows < kC ? left_rows - 1 : kC - 1) * gv_row + 2u * a.H * a.V);
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            const int r = row_of(t, 4 * grp);
-            const f4 cp = *(const f4 *)(coef + r), cb = *(const f4 *)(coef + kC + r), cq = *(const f4 *)(coef + 2 * kC + r);
+            for (int t = 0; t < 4; ++t) {
+                const int r = row_of(t, 4 * grp);
+                const f4 cp = *(const f4 *)(coef->p + r), cb = *(const f4 *)(coef->beta + r), cq = *(const f4 *)(coef->q + r);
+                const f4 x = cb * Y[t];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int row = n * kC + r + i;
-                const float v = cb[i] * Y[t][i];
-                if (mine) keep_y[(int64_t)(r + i) * a.V + col] = Y[t][i];
-                if (mine && row < a.S) w.gv[(((int64_t)row * a.B + b) * a.H + h) * a.V + col] = from_f32<DT>(v);
-                Y[t][i] = -cp[i] * v;
-                G[t][i] *= cq[i];
+                for (int i = 0; i < 4; ++i) {
+                    to[(row_of(t, 0) + i) * VP] = Y[t][i];
+                    __builtin_amdgcn_raw_buffer_store_b16(from_f32<DT>(x[i]), gv, gv_at + (row_of(t, 0) + i) * gv_row, 0, 0);
+                }
+                Y[t] = -cp * x;
+                G[t] *= cq;
             }
         }
         // gS0, both products in one sum: their columns have one power of two
@@ -194,28 +186,28 @@ __global__ void __launch_bounds__(W *kWave) delta_walk_back(Delta a, Records rec
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     big = __builtin_fmaxf(big, __builtin_fmaxf(__builtin_fabsf(Y[t][i]), __builtin_fabsf(G[t][i])));
-            const Power p = power_of(column_max(big));
-            Split sy[2], sg[2];
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                sy[s] = split(Y[2 * s], Y[2 * s + 1], p.inv);
-                sg[s] = split(G[2 * s], G[2 * s + 1], p.inv);
-            }
+            const Power p = turned_sign(power_of(column_max(big)), lane);
+            const Split y0 = split(Y[0], Y[1], p.inv), y1 = split(Y[2], Y[3], p.inv);
+            const Split g0 = split(G[0], G[1], p.inv), g1 = split(G[2], G[3], p.inv);
+            const float whole = coef->whole;
 #pragma unroll
             for (int t = 0; t < KT; ++t) {
-                f4 d = {};
-#pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    const h8 lk = left_turned<KP>(kt, t, s, lane), lq = left_turned<KP>(qt, t, s, lane);
-                    d = mma(lk, sy[s].hi, d);
-                    d = mma(lk, sy[s].lo, d);
-                    d = mma(lq, sg[s].hi, d);
-                    d = mma(lq, sg[s].lo, d);
-                }
+                const h8 k0 = left_turned<KP>(kt, tk_at, t, 0), k1 = left_turned<KP>(kt, tk_at, t, 1);
+                const h8 q0 = left_turned<KP>(qt, tk_at, t, 0), q1 = left_turned<KP>(qt, tk_at, t, 1);
+                f4 d = mma(k0, y0.lo, f4{});
+                d = mma(k1, y1.lo, d);
+                d = mma(q0, g0.lo, d);
+                d = mma(q1, g1.lo, d);
+                d = mma(k0, y0.hi, d);
+                d = mma(k1, y1.hi, d);
+                d = mma(q0, g0.hi, d);
+                d = mma(q1, g1.hi, d);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) S[t][i] = __builtin_fmaf(whole, S[t][i], p.back * d[i]);
             }
         }
+        stage.store(smem + (~n & 1) * kBuf);
+        lds_barrier();  // the next chunk's operands are there, and all waves are done with this one's
     }
     if (w.gstate) {
 #pragma unroll
@@ -230,42 +222,45 @@ __global__ void __launch_bounds__(W *kWave) delta_walk_back(Delta a, Records rec
         if (mine) w.gv[(((int64_t)row * a.B + b) * a.H + h) * a.V + col] = 0;
 }
 
-// Right operand from an image's columns 16 tile.., step s of 32 along its rows.
-template <int COLS>
-__device__ static inline h8 right_turned(const uint16_t *__restrict__ image, int tile, int s, int lane) {
-    typedef short s16x4 __attribute__((ext_vector_type(4)));
-    typedef __attribute__((address_space(3))) s16x4 lds4;
-    const int i = lane & 15, row = 32 * s + 8 * (lane >> 4) + (i >> 2);
-    const int chunk = 2 * tile + (i >> 1 & 1), half = 4 * (i & 1);
-    const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(image + image_at<COLS>(row, chunk) + half));
-    const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(image + image_at<COLS>(row + 4, chunk) + half));
-    return __builtin_bit_cast(h8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+// Instructions stay on their side of this: operands are read a few products ahead, and not all of a loop's at once,
+// which would take more registers than there are.
+__device__ static inline void keep_order() { __builtin_amdgcn_sched_barrier(0); }
+
+// The same number, as a new one: what is computed from it is computed where it stands, not ahead of all loops, to
+// be kept in registers that are needed.
+__device__ static inline int anew(int v) {
+    asm volatile("" : "+v"(v));
+    return v;
+}
+__device__ static inline f4 anew(h4 v) {
+    auto u = __builtin_bit_cast(uint2, v);
+    asm volatile("" : "+v"(u.x), "+v"(u.y));
+    v = __builtin_bit_cast(h4, u);
+    return f4{(float)v[0], (float)v[1], (float)v[2], (float)v[3]};
 }
 
-// 8 fp32 values of a row from column c, zeros past V.
-__device__ static inline void eight(const float *row, int c, int V, bool on, f4 &x, f4 &y) {
-    typedef float row4 __attribute__((ext_vector_type(4), aligned(4)));
-    x = f4{}, y = f4{};
-    if (!on) return;
-    if (c + 8 <= V) {
-        x = *(const row4 *)(row + c), y = *(const row4 *)(row + c + 4);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (c + i < V) x[i] = row[c + i];
-            if (c + 4 + i < V) y[i] = row[c + 4 + i];
-        }
-    }
-}
+// 8 values of a row from column c, zeros past V and where the row is not there. ROWS8: V is a multiple of 8.
+template <bool ROWS8>
 __device__ static inline HVec<8>::t eight16(const uint16_t *row, int c, int V, bool on) {
     HVec<8>::t v = {};
-    if (!on) return v;
-    if (c + 8 <= V) v = *(const HVec<8>::t *)(row + c);
-    else
+    if (ROWS8) {
+        if (on && c < V) v = *(const HVec<8>::t *)(row + c);
+    } else if (on) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             if (c + i < V) v[i] = row[c + i];
+    }
     return v;
+}
+// One of 16 values that every lane holds, by its number.
+__device__ static inline float pick(const f4 (&v)[4], int n) {
+    f4 r = v[0];
+#pragma unroll
+    for (int t = 1; t < 4; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r[i] = n >> 2 == t ? v[t][i] : r[i];
+    const float x = n & 1 ? r[1] : r[0], y = n & 1 ? r[3] : r[2];
+    return n & 2 ? y : x;
 }
 __device__ static inline float largest(const f4 &x, const f4 &y, float m) {
 #pragma unroll
@@ -276,7 +271,7 @@ __device__ static inline float largest(const f4 &x, const f4 &y, float m) {
 // A chunk's own gradients. V goes by in blocks of 64 columns: the block's rows of gO, U and Y are staged in LDS
 // (a power of two a row taken out), the states' rows are the waves' right operands straight from memory, each
 // wave with 16 rows of K. Of the 64x64 matrices a wave has a part of a row of tiles.
-template <int DT, int KP>
+template <int DT, int KP, bool ROWS8>
 __global__ void __launch_bounds__(KP / 16 * kWave) delta_grads(Delta a, Records rec, Back w) {
     constexpr int W = KP / 16, kThreads = W * kWave;
     constexpr int kSide = W / 4, NJ = 4 / kSide;         // waves that share a row of tiles, tiles of each
@@ -286,11 +281,12 @@ __global__ void __launch_bounds__(KP / 16 * kWave) delta_grads(Delta a, Records 
     __shared__ __align__(16) float po[kC], pu[kC], py[kC], coef[4 * kC], kr[kC], qr[kC];
     __shared__ float rowf[W][kC], rowe[W][kC], yu[kC], big[2][W];
     __shared__ double cum[kC], dots[W], erow[kSide][kC], ecol[4][kC];
-    const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const int m = lane & 15, grp = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    int lane = threadIdx.x % kWave, m = lane & 15, grp = lane >> 4;
+    int lk_at, rk_at, ls_at, ts_at;                      // where the lane reads operands
     const int rt = wave / kSide, j0 = wave % kSide * NJ; // the wave's row of tiles and its first tile
-    const int kcol = 16 * wave + m;                      // the lane's row of K, a column of gQ~ and gK~
-    const int n = blockIdx.x, b = blockIdx.y / a.G, g = blockIdx.y % a.G, heads = a.H / a.G;
+    int kcol = 16 * wave + m;                            // the lane's row of K, a column of gQ~ and gK~
+    const int n = blockIdx.x, b = blockIdx.y / a.G, g = blockIdx.y % a.G, heads = a.H / a.G, VP = padded_v(a.V);
     const int row0 = n * kC, live = length_of(a, b) - row0;
     const int rows = a.S - row0 < kC ? a.S - row0 : kC;
     if (live <= 0) {
@@ -316,15 +312,16 @@ __global__ void __launch_bounds__(KP / 16 * kWave) delta_grads(Delta a, Records 
     }
     if (threadIdx.x < kC) kr[threadIdx.x] = factors[threadIdx.x], qr[threadIdx.x] = factors[kC + threadIdx.x];
     lds_barrier();
-    auto value = [&](const uint16_t *image, int row) {
-        return (float)__builtin_bit_cast(_Float16, image[image_at<KP>(row, kcol >> 3) + (kcol & 7)]);
-    };
     // this lane's values of K~ and Q~ in the results' layout
-    f4 kd[4], qd[4], aq[4] = {}, ak[4] = {};
+    h4 kd[4], qd[4];
+    f4 aq[4] = {}, ak[4] = {};
 #pragma unroll
     for (int t = 0; t < 4; ++t)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) kd[t][i] = value(kt, row_of(t, 4 * grp + i)), qd[t][i] = value(qt, row_of(t, 4 * grp + i));
+        for (int i = 0; i < 4; ++i) {
+            const int to = image_at<KP>(row_of(t, 4 * grp + i), kcol >> 3) + (kcol & 7);
+            kd[t][i] = __builtin_bit_cast(_Float16, kt[to]), qd[t][i] = __builtin_bit_cast(_Float16, qt[to]);
+        }
 
     for (int hh = 0; hh < heads; ++hh) {
         const int h = g * heads + hh, bh = b * a.H + h;
@@ -337,26 +334,27 @@ __global__ void __launch_bounds__(KP / 16 * kWave) delta_grads(Delta a, Records 
         f4 da[NJ] = {}, dl[NJ] = {}, er[4] = {}, fr[4] = {};
         float s0s1 = 0.0f, dot_u = 0.0f;
         for (int v0 = 0; v0 < a.V; v0 += 64) {
+            lane = anew(threadIdx.x % kWave), m = lane & 15, grp = lane >> 4, kcol = 16 * wave + m;
+            ls_at = left_place<64>(lane);
             // the wave's rows of both states, on their way while the rows are staged
             f4 st[2][2], gt[2][2];
-            const float *s0 = w.states + (at * a.K + kcol) * a.V, *g1 = w.gstates + (at * a.K + kcol) * a.V;
+            const float *s0 = w.states + (at * KP + kcol) * VP + v0 + 8 * grp, *g1 = w.gstates + (at * KP + kcol) * VP + v0 + 8 * grp;
 #pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                eight(s0, v0 + 32 * s + 8 * grp, a.V, kcol < a.K, st[s][0], st[s][1]);
-                eight(g1, v0 + 32 * s + 8 * grp, a.V, kcol < a.K, gt[s][0], gt[s][1]);
-            }
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    st[s][i] = *(const f4 *)(s0 + 32 * s + 4 * i), gt[s][i] = *(const f4 *)(g1 + 32 * s + 4 * i);
             {
                 const int r = threadIdx.x / kPer, c0 = threadIdx.x % kPer * kCols;
                 const uint16_t *go = w.gout + (int64_t)(row0 + r) * w.gs[0] + b * w.gs[1] + h * w.gs[2];
-                const float *ur = w.u + (at * kC + r) * a.V, *yr = w.y + (at * kC + r) * a.V;
+                const float *ur = w.u + (at * kC + r) * VP + v0 + c0, *yr = w.y + (at * kC + r) * VP + v0 + c0;
                 f4 o[kCols / 4], u[kCols / 4], y[kCols / 4];
                 float mo = 0.0f, mu = 0.0f, my = 0.0f;
 #pragma unroll
                 for (int j = 0; j < kCols / 8; ++j) {
-                    const int c = v0 + c0 + 8 * j;
-                    const auto og = eight16(go, c, a.V, r < live);
-                    eight(ur, c, a.V, true, u[2 * j], u[2 * j + 1]);
-                    eight(yr, c, a.V, true, y[2 * j], y[2 * j + 1]);
+                    const auto og = eight16<ROWS8>(go, v0 + c0 + 8 * j, a.V, r < live);
+#pragma unroll
+                    for (int i = 2 * j; i < 2 * j + 2; ++i) u[i] = *(const f4 *)(ur + 4 * i), y[i] = *(const f4 *)(yr + 4 * i);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         o[2 * j + i / 4][i % 4] = to_f32<DT>(og[i]);
@@ -401,7 +399,7 @@ __global__ void __launch_bounds__(KP / 16 * kWave) delta_grads(Delta a, Records 
                         s0s1 = __builtin_fmaf(st[s][1][i], gt[s][1][i], s0s1);
                     }
                 }
-                const Power ps = power_of(column_max(ms)), pg = power_of(column_max(mg));
+                const Power ps = turned_sign(power_of(column_max(ms)), lane), pg = turned_sign(power_of(column_max(mg)), lane);
                 Split ss[2], sg[2];
 #pragma unroll
                 for (int s = 0; s < 2; ++s) {
@@ -410,12 +408,13 @@ __global__ void __launch_bounds__(KP / 16 * kWave) delta_grads(Delta a, Records 
                 }
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
+                    keep_order();
                     f4 x = {}, y = {}, z = {};
 #pragma unroll
                     for (int s = 0; s < 2; ++s) {
-                        const h8 lo = left<64>(oh, t, s, lane);
-                        const h8 lyh = left<64>(yh, t, s, lane), lyl = left<64>(yl, t, s, lane);
-                        const h8 luh = left<64>(uh, t, s, lane), lul = left<64>(ul, t, s, lane);
+                        const h8 lo = left<64>(oh, ls_at, t, s);
+                        const h8 lyh = left<64>(yh, ls_at, t, s), lyl = left<64>(yl, ls_at, t, s);
+                        const h8 luh = left<64>(uh, ls_at, t, s), lul = left<64>(ul, ls_at, t, s);
                         x = mma(lo, ss[s].hi, x);
                         y = mma(lyh, ss[s].hi, y);
                         z = mma(luh, sg[s].hi, z);
@@ -429,11 +428,12 @@ __global__ void __launch_bounds__(KP / 16 * kWave) delta_grads(Delta a, Records 
                     const f4 fo = *(const f4 *)(po + r) * *(const f4 *)(coef + 2 * kC + r) * ps.back;
                     const f4 fy = *(const f4 *)(py + r) * *(const f4 *)(coef + r) * *(const f4 *)(coef + kC + r) * ps.back;
                     const f4 fu = *(const f4 *)(pu + r) * *(const f4 *)(coef + 3 * kC + r) * pg.back;
+                    const f4 kf = anew(kd[t]), qf = anew(qd[t]);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const float e = fu[i] * z[i], o = fo[i] * x[i], l = fy[i] * y[i];
-                        er[t][i] = __builtin_fmaf(e, kd[t][i], er[t][i]);
-                        fr[t][i] = __builtin_fmaf(o, qd[t][i], __builtin_fmaf(-l, kd[t][i], fr[t][i]));
+                        er[t][i] = __builtin_fmaf(e, kf[i], er[t][i]);
+                        fr[t][i] = __builtin_fmaf(o, qf[i], __builtin_fmaf(-l, kf[i], fr[t][i]));
                         aq[t][i] += o;
                         ak[t][i] += e - l;
                     }
@@ -443,12 +443,13 @@ __global__ void __launch_bounds__(KP / 16 * kWave) delta_grads(Delta a, Records 
 #pragma unroll
             for (int j = 0; j < NJ; ++j) {
                 if ((j0 + j) / 2 > rt / 2) continue;
+                keep_order();
                 f4 x = {}, y = {};
 #pragma unroll
                 for (int s = 0; s < 2; ++s) {
-                    const h8 lo = left<64>(oh, rt, s, lane);
-                    const h8 lyh = left<64>(yh, rt, s, lane), lyl = left<64>(yl, rt, s, lane);
-                    const h8 ruh = left<64>(uh, j0 + j, s, lane), rul = left<64>(ul, j0 + j, s, lane);
+                    const h8 lo = left<64>(oh, ls_at, rt, s);
+                    const h8 lyh = left<64>(yh, ls_at, rt, s), lyl = left<64>(yl, ls_at, rt, s);
+                    const h8 ruh = left<64>(uh, ls_at, j0 + j, s), rul = left<64>(ul, ls_at, j0 + j, s);
                     x = mma(lo, ruh, x);
                     y = mma(lyh, ruh, y);
                     x = mma(lo, rul, x);
@@ -466,6 +467,8 @@ __global__ void __launch_bounds__(KP / 16 * kWave) delta_grads(Delta a, Records 
             }
         }
         // sums over a row's columns, and of gS1.S0
+        lane = anew(threadIdx.x % kWave), m = lane & 15, grp = lane >> 4, kcol = 16 * wave + m;
+        lk_at = left_place<KP>(lane);
 #pragma unroll
         for (int i = 1; i < kPer; i *= 2) dot_u += __shfl_xor(dot_u, i);
         if (threadIdx.x % kPer == 0) yu[threadIdx.x / kPer] = dot_u;
@@ -479,13 +482,14 @@ __global__ void __launch_bounds__(KP / 16 * kWave) delta_grads(Delta a, Records 
             double er_[4] = {};
 #pragma unroll
             for (int j = 0; j < NJ; ++j) {
+                keep_order();
                 f4 qk = {}, kk = {};
                 if ((j0 + j) / 2 <= rt / 2)
 #pragma unroll
                     for (int s = 0; s < KP / 32; ++s) {
-                        const h8 rk = left<KP>(kt, j0 + j, s, lane);
-                        qk = mma(left<KP>(qt, rt, s, lane), rk, qk);
-                        kk = mma(left<KP>(kt, rt, s, lane), rk, kk);
+                        const h8 rk = left<KP>(kt, lk_at, j0 + j, s);
+                        qk = mma(left<KP>(qt, lk_at, rt, s), rk, qk);
+                        kk = mma(left<KP>(kt, lk_at, rt, s), rk, kk);
                     }
                 const int c = row_of(j0 + j, m);
                 const double gc = cum[c];
@@ -519,11 +523,9 @@ __global__ void __launch_bounds__(KP / 16 * kWave) delta_grads(Delta a, Records 
 #pragma unroll
         for (int t = 0; t < 4; ++t)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int r = row_of(t, 4 * grp + i);
-                const float f = sum16(fr[t][i]), e = sum16(er[t][i]);
-                if (m == 0) rowf[wave][r] = f, rowe[wave][r] = e;
-            }
+            for (int i = 0; i < 4; ++i) fr[t][i] = sum16(fr[t][i]), er[t][i] = sum16(er[t][i]);
+        rowf[wave][row_of(m >> 2, 4 * grp + (m & 3))] = pick(fr, m);
+        rowe[wave][row_of(m >> 2, 4 * grp + (m & 3))] = pick(er, m);
         lds_barrier();  // also: all reads of the staged rows are done
         mz = big[0][0], mw = big[1][0];
 #pragma unroll
@@ -535,36 +537,38 @@ __global__ void __launch_bounds__(KP / 16 * kWave) delta_grads(Delta a, Records 
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int r = row_of(rt, 4 * grp + i), c = row_of(j0 + j, m);
-                const int to = image_at<64>(r, c >> 3) + (c & 7), across = image_at<64>(c, r >> 3) + (r & 7);
+                const int to = image_at<64>(r, c >> 3) + (c & 7);
                 const float z = da[j][i] * pz.inv, x = dl[j][i] * pw.inv;
                 const _Float16 z0 = (_Float16)z, x0 = (_Float16)x;
                 const _Float16 z1 = (_Float16)(z - (float)z0), x1 = (_Float16)(x - (float)x0);
                 zh[to] = __builtin_bit_cast(uint16_t, z0), zl[to] = __builtin_bit_cast(uint16_t, z1);
-                if (c <= r) {  // both halves; the diagonal's is zero
-                    wh[to] = wh[across] = __builtin_bit_cast(uint16_t, x0);
-                    wl[to] = wl[across] = __builtin_bit_cast(uint16_t, x1);
-                }
+                wh[to] = __builtin_bit_cast(uint16_t, x0), wl[to] = __builtin_bit_cast(uint16_t, x1);
             }
         lds_barrier();
         {
+            lane = anew(threadIdx.x % kWave), m = lane & 15, grp = lane >> 4, kcol = 16 * wave + m;
+            ls_at = left_place<64>(lane), ts_at = turned_place<64>(lane), rk_at = right_place<KP>(lane);
             h8 rk[2], rq[2];
 #pragma unroll
-            for (int s = 0; s < 2; ++s) rk[s] = right_turned<KP>(kt, wave, s, lane), rq[s] = right_turned<KP>(qt, wave, s, lane);
+            for (int s = 0; s < 2; ++s) rk[s] = right_turned<KP>(kt, rk_at, wave, s), rq[s] = right_turned<KP>(qt, rk_at, wave, s);
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
+                keep_order();
                 f4 x = {}, y = {}, z = {};
 #pragma unroll
                 for (int s = 0; s < 2; ++s) {
                     if (s <= t / 2) {
-                        x = mma(left<64>(zh, t, s, lane), rk[s], x);
-                        x = mma(left<64>(zl, t, s, lane), rk[s], x);
+                        x = mma(left<64>(zl, ls_at, t, s), rk[s], x);
+                        z = mma(left<64>(wl, ls_at, t, s), rk[s], z);
+                        x = mma(left<64>(zh, ls_at, t, s), rk[s], x);
+                        z = mma(left<64>(wh, ls_at, t, s), rk[s], z);
                     }
                     if (s >= t / 2) {
-                        y = mma(left_turned<64>(zh, t, s, lane), rq[s], y);
-                        y = mma(left_turned<64>(zl, t, s, lane), rq[s], y);
+                        y = mma(left_turned<64>(zl, ts_at, t, s), rq[s], y);
+                        z = mma(left_turned<64>(wl, ts_at, t, s), rk[s], z);
+                        y = mma(left_turned<64>(zh, ts_at, t, s), rq[s], y);
+                        z = mma(left_turned<64>(wh, ts_at, t, s), rk[s], z);
                     }
-                    z = mma(left<64>(wh, t, s, lane), rk[s], z);
-                    z = mma(left<64>(wl, t, s, lane), rk[s], z);
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -615,35 +619,58 @@ __global__ void __launch_bounds__(KP / 16 * kWave) delta_grads(Delta a, Records 
             }
         }
     }
+    lane = anew(threadIdx.x % kWave), m = lane & 15, grp = lane >> 4, kcol = 16 * wave + m;
     // through the norms: gk = 2^-e (gK~ - K~ kr^2 (K~.gK~))
-    lds_barrier();
+    f4 qs[4], ks[4];
 #pragma unroll
     for (int t = 0; t < 4; ++t)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = row_of(t, 4 * grp + i);
-            const float q = sum16(aq[t][i] * qd[t][i]), k = sum16(ak[t][i] * kd[t][i]);
-            if (m == 0) rowf[wave][r] = q, rowe[wave][r] = k;
-        }
+        for (int i = 0; i < 4; ++i) qs[t][i] = sum16(aq[t][i] * (float)qd[t][i]), ks[t][i] = sum16(ak[t][i] * (float)kd[t][i]);
+    lds_barrier();  // the last head's sums, operands and matrices have been read
+    rowf[wave][row_of(m >> 2, 4 * grp + (m & 3))] = pick(qs, m);
+    rowe[wave][row_of(m >> 2, 4 * grp + (m & 3))] = pick(ks, m);
     lds_barrier();
+    if (threadIdx.x < kC) {  // what a row's values lose along themselves, and the factor of what is left
+        const int r = threadIdx.x;
+        float q = 0.0f, k = 0.0f;
 #pragma unroll
-    for (int t = 0; t < 4; ++t)
+        for (int j = 0; j < W; ++j) q += rowf[j][r], k += rowe[j][r];
+        coef[r] = a.normalize ? q * qr[r] * qr[r] : 0.0f;
+        coef[kC + r] = a.normalize ? k * kr[r] * kr[r] : 0.0f;
+        coef[2 * kC + r] = factors[3 * kC + r];
+        coef[3 * kC + r] = factors[2 * kC + r];
+    }
+    lds_barrier();
+    // by way of LDS, in rows
+    constexpr int kLd = KP + 8;
+    static_assert(kC * kLd <= 5 * kSquare, "one result at a time");
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = row_of(t, 4 * grp + i);
-            if (r >= rows || kcol >= a.K) continue;
-            const bool on = r < live;
-            float q = 0.0f, k = 0.0f;
-            if (a.normalize) {
+    for (int both = 0; both < 2; ++both) {
 #pragma unroll
-                for (int j = 0; j < W; ++j) q += rowf[j][r], k += rowe[j][r];
-                q *= qr[r] * qr[r], k *= kr[r] * kr[r];
-            }
-            const float k2 = factors[2 * kC + r], q2 = factors[3 * kC + r];
-            const int64_t to = (((int64_t)(row0 + r) * a.B + b) * a.G + g) * a.K + kcol;
-            w.gq[to] = on ? from_f32<DT>(q2 * __builtin_fmaf(-q, qd[t][i], aq[t][i])) : 0;
-            w.gk[to] = on ? from_f32<DT>(k2 * __builtin_fmaf(-k, kd[t][i], ak[t][i])) : 0;
+        for (int t = 0; t < 4; ++t) {
+            const int r = row_of(t, 4 * grp);
+            const f4 along = *(const f4 *)(coef + both * kC + r), f = *(const f4 *)(coef + (2 + both) * kC + r);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                stage[(r + i) * kLd + kcol] =
+                    both ? from_f32<DT>(f[i] * __builtin_fmaf(-along[i], (float)kd[t][i], ak[t][i]))
+                         : from_f32<DT>(f[i] * __builtin_fmaf(-along[i], (float)qd[t][i], aq[t][i]));
         }
+        lds_barrier();
+        uint16_t *to = both ? w.gk : w.gq;
+        for (int i = threadIdx.x; i < rows * (KP / 8); i += kThreads) {
+            const int r = i / (KP / 8), c = i % (KP / 8) * 8;
+            HVec<8>::t x = *(const HVec<8>::t *)(stage + r * kLd + c);
+            if (r >= live) x = HVec<8>::t{};
+            uint16_t *p = to + (((int64_t)(row0 + r) * a.B + b) * a.G + g) * a.K + c;
+            if (c + 8 <= a.K) *(HVec<8>::t *)p = x;
+            else
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (c + j < a.K) p[j] = x[j];
+        }
+        lds_barrier();
+    }
 }
 
 // gA and gDtBias: the chunks' parts, in a fixed order.
@@ -673,13 +700,15 @@ uint64_t part_bytes(const mccb_delta_t *a) { return 2 * chunks_of(a) * (uint64_t
 template <int DT, int KP>
 int launch(const Delta &d, const Records &rec, Back w, hipStream_t st) {
     constexpr int W = 4;
-    w.blocks = (d.V + 16 * W - 1) / (16 * W);
-    hipLaunchKernelGGL((delta_walk_back<DT, KP, W>), dim3((unsigned)(d.B * d.H * w.blocks)), dim3(W * kWave), 0, st, d,
-                       rec, w);
+    w.blocks = padded_v(d.V) / (16 * W);
+    const dim3 grid((unsigned)(d.B * d.H * w.blocks)), block(W * kWave);
+    if (row_buffer(w.gs[0], d.V)) hipLaunchKernelGGL((delta_walk_back<DT, KP, W, false>), grid, block, 0, st, d, rec, w);
+    else hipLaunchKernelGGL((delta_walk_back<DT, KP, W, true>), grid, block, 0, st, d, rec, w);
     int rc = launched();
     if (rc != MCCB_OK || w.chunks == 0) return rc;
-    hipLaunchKernelGGL((delta_grads<DT, KP>), dim3((unsigned)w.chunks, (unsigned)(d.B * d.G)), dim3(KP / 16 * kWave), 0, st, d,
-                       rec, w);
+    const dim3 all((unsigned)w.chunks, (unsigned)(d.B * d.G)), threads(KP / 16 * kWave);
+    if (d.V % 8 == 0) hipLaunchKernelGGL((delta_grads<DT, KP, true>), all, threads, 0, st, d, rec, w);
+    else hipLaunchKernelGGL((delta_grads<DT, KP, false>), all, threads, 0, st, d, rec, w);
     return launched();
 }
 
@@ -691,7 +720,7 @@ int mccb_delta_backward_get_workspace_size(const mccb_delta_t *a, uint64_t *size
     if (!size) return MCCB_ERR_PARAM_NULLPTR;
     const int rc = check_delta(a, false);
     if (rc != MCCB_OK) return rc;
-    *size = align16(part_bytes(a)) + chunks_of(a) * state_bytes(a) + chunk_rows_bytes(a);
+    *size = align16(part_bytes(a)) + chunk_states_bytes(a) + chunk_rows_bytes(a);
     return MCCB_OK;
 }
 
@@ -736,9 +765,9 @@ int mccb_delta_backward(const mccb_delta_t *a, const mccb_delta_grads_t *q, cons
     w.gfinal = q->gradFinalState, w.gv = (uint16_t *)q->gradV, w.gstate = q->gradState;
     w.part = (double *)ws;
     w.gstates = (float *)((uint8_t *)ws + align16(part_bytes(a)));
-    w.y = w.gstates + chunks * heads * (uint64_t)(a->K * a->V);
+    w.y = (float *)((uint8_t *)w.gstates + chunk_states_bytes(a));
     w.states = (const float *)((const uint8_t *)saved + records_size(a, chunks));
-    w.u = w.states + chunks * heads * (uint64_t)(a->K * a->V);
+    w.u = (const float *)((const uint8_t *)w.states + chunk_states_bytes(a));
     w.gq = (uint16_t *)q->gradQ, w.gk = (uint16_t *)q->gradK, w.gdt = (uint16_t *)q->gradDt, w.gb = (uint16_t *)q->gradB;
     w.chunks = (int)chunks;
     const hipStream_t st = (hipStream_t)stream;

@@ -50,8 +50,9 @@ struct RowCoef {
     float x, a;         // X = x (hi + lo), A = a (hi + lo)
     float pad[13];
     double cum[kC];     // G in units of log 2
+    float pad2[112];
 };
-constexpr int kStaged = 4 * kC * (int)sizeof(float);  // the bytes of RowCoef that the walk stages: four rows
+static_assert(sizeof(RowCoef) == 2048, "two of the walks' loads");
 
 constexpr size_t key_bytes(int kp) { return 2 * kC * kp * sizeof(uint16_t) + 4 * kC * sizeof(float); }
 constexpr size_t kXaBytes = 4 * kSquare * sizeof(uint16_t);  // X hi, X lo, A hi, A lo
@@ -74,22 +75,44 @@ __device__ static inline int image_at(int row, int chunk) {  // in 16-bit values
 // eight consecutive rows, just what the next product wants of its right operand.
 __device__ static inline int row_of(int tile, int m) { return 32 * (tile >> 1) + 8 * (m >> 2) + 4 * (tile & 1) + (m & 3); }
 
+// Operands from images. Where a lane reads is a place of its own (left_place and so on, once a kernel) with
+// a step or tile exclusive-or'ed in and constants added: the swizzle does not depend on those.
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4 lds4;
+
 // Left operand, rows of `tile`, step s of 32 along the image's columns.
 template <int COLS>
-__device__ static inline h8 left(const uint16_t *image, int tile, int s, int lane) {
-    return *(const h8 *)(image + image_at<COLS>(row_of(tile, lane & 15), 4 * s + (lane >> 4)));
+__device__ static inline int left_place(int lane) {
+    return image_at<COLS>(row_of(0, lane & 15), lane >> 4);
 }
-// Left operand of the transposed image: its columns as rows (`tile` of them), step s of 32 along its rows.
+template <int COLS>
+__device__ static inline h8 left(const uint16_t *image, int place, int tile, int s) {
+    return *(const h8 *)(image + (place ^ s << 5) + row_of(tile, 0) * COLS);
+}
+// The transposed image's: its columns as rows (`tile` of them), step s of 32 along its rows.
 // A transposing read gives lane i of 16 column i of the four rows that those lanes read 8 bytes of.
 template <int COLS>
-__device__ static inline h8 left_turned(const uint16_t *__restrict__ image, int tile, int s, int lane) {
-    typedef short s16x4 __attribute__((ext_vector_type(4)));
-    typedef __attribute__((address_space(3))) s16x4 lds4;
-    const int i = lane & 15, row = 32 * s + 8 * (lane >> 4) + (i >> 2);
-    const int chunk = 4 * (tile >> 1) + (i & 3), half = 4 * (tile & 1);
-    const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(image + image_at<COLS>(row, chunk) + half));
-    const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(image + image_at<COLS>(row + 4, chunk) + half));
+__device__ static inline int turned_place(int lane) {
+    return image_at<COLS>(8 * (lane >> 4) + (lane >> 2 & 3), lane & 3);
+}
+template <int COLS>
+__device__ static inline h8 turned_at(const uint16_t *__restrict__ p) {
+    const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)p);
+    const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(p + 4 * COLS));
     return __builtin_bit_cast(h8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+template <int COLS>
+__device__ static inline h8 left_turned(const uint16_t *image, int place, int tile, int s) {
+    return turned_at<COLS>(image + (place ^ (tile >> 1) << 5) + 32 * s * COLS + 4 * (tile & 1));
+}
+// Right operand: columns 16 tile.. of an image, step s of 32 along its rows.
+template <int COLS>
+__device__ static inline int right_place(int lane) {
+    return image_at<COLS>(8 * (lane >> 4) + (lane >> 2 & 3), lane >> 1 & 1) + 4 * (lane & 1);
+}
+template <int COLS>
+__device__ static inline h8 right_turned(const uint16_t *image, int place, int tile, int s) {
+    return turned_at<COLS>(image + (place ^ tile << 4) + 32 * s * COLS);
 }
 
 __device__ static inline f4 mma(h8 a, h8 b, f4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
@@ -100,14 +123,28 @@ __device__ static inline f4 mma(h8 a, h8 b, f4 c) { return __builtin_amdgcn_mfma
 struct Split {
     h8 hi, lo;
 };
+// hi = fp16(v inv), lo = fp16(v inv - hi), which a mixed-precision multiply-add rounds once. (The empty asm, which
+// has no instruction, keeps the pair hi together: the compiler would round its halves a second time.)
+typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+typedef float f2 __attribute__((ext_vector_type(2)));
+__device__ static inline void split2(float a, float b, float inv, uint32_t &hi, uint32_t &lo) {
+    uint32_t h = __builtin_bit_cast(uint32_t, __builtin_convertvector(f2{a * inv, b * inv}, h2));
+    asm("" : "+v"(h));
+    const h2 t = __builtin_bit_cast(h2, h);
+    const h2 l = {(_Float16)__builtin_fmaf(a, inv, -(float)t[0]), (_Float16)__builtin_fmaf(b, inv, -(float)t[1])};
+    hi = h;
+    lo = __builtin_bit_cast(uint32_t, l);
+}
 __device__ static inline Split split(const f4 &a, const f4 &b, float inv) {
+    typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+    uint32_t h[4], l[4];
+    split2(a[0], a[1], inv, h[0], l[0]);
+    split2(a[2], a[3], inv, h[1], l[1]);
+    split2(b[0], b[1], inv, h[2], l[2]);
+    split2(b[2], b[3], inv, h[3], l[3]);
     Split s;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float v = (i < 4 ? a[i & 3] : b[i & 3]) * inv;
-        s.hi[i] = (_Float16)v;
-        s.lo[i] = (_Float16)(v - (float)s.hi[i]);
-    }
+    s.hi = __builtin_bit_cast(h8, u4{h[0], h[1], h[2], h[3]});
+    s.lo = __builtin_bit_cast(h8, u4{l[0], l[1], l[2], l[3]});
     return s;
 }
 
@@ -125,19 +162,31 @@ __device__ static inline Power power_of(float m) {
     return p;
 }
 
+// The matrix instruction cuts the sum of its 32 products off towards minus infinity (its addition to the accumulator
+// is rounded). Such errors have one sign, and states, keys and queries have means that are not zero: <gS, S> and what
+// else sums over many of them would collect it (2.5e-6 of gradA, at S=448 B=4 H=12 K=128 V=64; 2e-7 without). So
+// half of the columns go through the products with their sign turned, for nothing, since a power of two is taken out
+// of each in any case.
+__device__ static inline Power turned_sign(Power p, int lane) {
+    const uint32_t sign = (uint32_t)__builtin_popcount(lane & 15) << 31;
+    p.back = __uint_as_float(__float_as_uint(p.back) ^ sign);
+    p.inv = __uint_as_float(__float_as_uint(p.inv) ^ sign);
+    return p;
+}
+
 // The largest magnitude over the four lanes that hold a column.
 __device__ static inline float column_max(float m) {
     m = __builtin_fmaxf(m, __shfl_xor(m, 16));
     return __builtin_fmaxf(m, __shfl_xor(m, 32));
 }
 template <int N>
-__device__ static inline Power column_power(const f4 (&v)[N]) {
+__device__ static inline Power column_power(const f4 (&v)[N], int lane) {
     float m = 0.0f;
 #pragma unroll
     for (int t = 0; t < N; ++t)
 #pragma unroll
         for (int i = 0; i < 4; ++i) m = __builtin_fmaxf(m, __builtin_fabsf(v[t][i]));
-    return power_of(column_max(m));
+    return turned_sign(power_of(column_max(m)), lane);
 }
 
 // Lane sums and maxima over 16 lanes, by rotations.
@@ -203,15 +252,79 @@ __host__ static inline Records records_at(void *p, uint64_t key_heads, uint64_t 
     return r;
 }
 
-// A wave's load of 1 KiB straight to LDS, 16 bytes a lane.
-__device__ static inline void to_lds(const uint8_t *from, uint8_t *to, int lane) {
-    typedef __attribute__((address_space(1))) const uint8_t gmem;
-    typedef __attribute__((address_space(3))) uint8_t lmem;
-    __builtin_amdgcn_global_load_lds((gmem *)(from + 16 * lane), (lmem *)to, 16, 0, 0);
+// Buffers of 16-bit values whose bounds the hardware keeps: loads past them give 0, stores past them are dropped.
+// A lane whose column is not there starts at kNowhere, past any bound (bounds are below 2^31, and so is what is
+// added to it).
+constexpr uint32_t kNowhere = 0x80000000u;
+typedef __amdgpu_buffer_rsrc_t Buffer;
+__device__ static inline Buffer buffer_of(const void *p, uint32_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc((void *)p, 0, bytes, 0x00027000);
 }
+
+// Rows of S and V's width in memory: V's tensors are read through strides, the walks' own are padded to whole blocks
+// of 64 columns and KP rows, so that nothing needs a check.
+constexpr int kBlockV = 64;
+__host__ __device__ static inline int padded_v(int V) { return (V + kBlockV - 1) / kBlockV * kBlockV; }
+
+// A wave's 16 columns of a chunk's 64 rows, 16 values a lane, in the products' layout. WIDE: rows so far apart, or so
+// close, that one chunk's are no buffer of their own.
+struct Column16 {
+    const uint16_t *base;       // of the head's first row
+    int64_t stride;             // of a row
+    int col, V;
+};
+__host__ __device__ static inline bool row_buffer(int64_t stride, int V) { return stride >= V && stride < (1 << 24); }
+template <bool WIDE>
+__device__ static inline void load_rows(const Column16 &c, int row0, int rows, int lane, uint16_t (&v)[4][4]) {
+    const int grp = lane >> 4;
+    const uint16_t *p = c.base + row0 * c.stride;
+    const uint32_t st = 2 * (uint32_t)c.stride;
+    const Buffer b = buffer_of(p, WIDE || rows <= 0 ? 0 : (rows < kC ? rows - 1 : kC - 1) * st + 2 * c.V);
+    const uint32_t at = c.col < c.V ? 8 * grp * st + 2 * c.col : kNowhere;
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = row_of(t, 4 * grp + i);
+            if (WIDE) v[t][i] = r < rows && c.col < c.V ? p[r * c.stride + c.col] : 0;
+            else v[t][i] = __builtin_amdgcn_raw_buffer_load_b16(b, at + (row_of(t, 0) + i) * st, 0, 0);
+        }
+}
+
+// A chunk's operands on their way to LDS: read into registers when the last chunk begins, written when it ends. (Loads
+// straight to LDS need no registers, but while one is under way the compiler has any use of any other load wait
+// for all of them.)
+template <int KP, int W>
+struct Staged {
+    static constexpr int kThreads = W * kWave, kKeys = 2 * kC * KP * 2, kBytes = kKeys + (int)kXaBytes + (int)sizeof(RowCoef);
+    static constexpr int kOfKeys = kKeys / 16 / kThreads, kOfXa = (int)kXaBytes / 16 / kThreads;
+    static constexpr int kOfCoef = (int)sizeof(RowCoef) / 4 / kThreads;
+    static_assert(kThreads <= 512 && kOfCoef >= 1, "whole loads");
+    f4 keys[kOfKeys], xa[kOfXa];
+    float coef[kOfCoef];
+
+    __device__ void load(const uint8_t *k, const uint8_t *x, const RowCoef *c) {
+#pragma unroll
+        for (int i = 0; i < kOfKeys; ++i) keys[i] = *lane_at((const f4 *)k + i * kThreads, threadIdx.x);
+#pragma unroll
+        for (int i = 0; i < kOfXa; ++i) xa[i] = *lane_at((const f4 *)x + i * kThreads, threadIdx.x);
+#pragma unroll
+        for (int i = 0; i < kOfCoef; ++i) coef[i] = *lane_at((const float *)c + i * kThreads, threadIdx.x);
+    }
+    __device__ void store(uint8_t *to) const {
+#pragma unroll
+        for (int i = 0; i < kOfKeys; ++i) ((f4 *)to)[i * kThreads + threadIdx.x] = keys[i];
+#pragma unroll
+        for (int i = 0; i < kOfXa; ++i) ((f4 *)(to + kKeys))[i * kThreads + threadIdx.x] = xa[i];
+#pragma unroll
+        for (int i = 0; i < kOfCoef; ++i) ((float *)(to + kKeys + kXaBytes))[i * kThreads + threadIdx.x] = coef[i];
+    }
+};
 
 // Blocks of one head, and heads of one key head, next to each other on one of the 8 dies, which have an L2 each.
 __device__ static inline int same_die(int id, int all) { return all % 8 ? id : id % 8 * (all / 8) + id / 8; }
+
+__host__ static inline int padded(int64_t K) { return K <= 64 ? 64 : 128; }
 
 // ---------------------------------------------------------------------------------------------
 // Host side, of both directions.
@@ -220,15 +333,17 @@ constexpr int kMaxK = 128;
 
 inline uint64_t chunks_of(const mccb_delta_t *a) { return (uint64_t)((a->S + kC - 1) / kC); }
 inline uint64_t state_bytes(const mccb_delta_t *a) { return (uint64_t)(a->B * a->H) * (uint64_t)(a->K * a->V) * 4; }
-// fp32 values for every chunk's rows and column of V
+// fp32 values of every chunk: states, and rows
+inline uint64_t chunk_states_bytes(const mccb_delta_t *a) {
+    return chunks_of(a) * (uint64_t)(a->B * a->H) * (uint64_t)(padded(a->K) * padded_v((int)a->V)) * 4;
+}
 inline uint64_t chunk_rows_bytes(const mccb_delta_t *a) {
-    return chunks_of(a) * (uint64_t)(a->B * a->H) * (uint64_t)(kC * a->V) * 4;
+    return chunks_of(a) * (uint64_t)(a->B * a->H) * (uint64_t)(kC * padded_v((int)a->V)) * 4;
 }
 Delta delta_of(const mccb_delta_t *a);
 int check_delta(const mccb_delta_t *a, bool token);
 int delta_inputs(const mccb_delta_t *a, bool token, Span *in, int *count);
 uint64_t records_size(const mccb_delta_t *a, uint64_t chunks);
 
-__host__ static inline int padded(int64_t K) { return K <= 64 ? 64 : 128; }
 
 }  // namespace delta

@@ -3,10 +3,11 @@
 //
 // delta_prepare makes what a chunk has without a state: the images of its rows of k and q, X and A. One
 // block a chunk and key head; all chunks at once.
-// delta_walk goes over a head's chunks with the state in registers. A wave owns 16 (or 32) columns of V
+// delta_walk goes over a head's chunks with the state in registers. A wave owns 16 columns of V
 // and nothing passes between waves: results of one product are the right operand of the next as they stand
 // in the registers (row_of in delta_common.h), and the left operands, the same for all of a head's columns,
-// come from LDS, where the next chunk's are written straight from memory while this one's run.
+// come from LDS, where the next chunk's are written when this one's are done with, from loads that
+// ran meanwhile.
 // delta_step reads and writes the state once.
 #include "delta_common.h"
 
@@ -320,254 +321,181 @@ struct Walk {
     const float *state_in;          // [B,H,K,V] or NULL
     float *state_out;               // or NULL
     uint16_t *out;                  // [S,B,H,V]
-    float *states, *u;              // kept for the backward: [B,H][chunk][K,V] and [B,H][chunk][64,V]; or NULL
+    float *states, *u;              // kept for the backward, padded: [B,H][chunk][K,V] and [B,H][chunk][64,V]; or NULL
     int n0, n1;                     // chunks
     int blocks;                     // of columns, a head
 };
 
-template <int DT, int KP, int NT, int W>
-__global__ void __launch_bounds__(W *kWave) delta_walk(Delta a, Records rec, Walk w) {
+// KEEP: the states and U are kept. (Two waves a SIMD would fit: with all of a SIMD's registers the compiler has the
+// products' results in accumulation registers and moves each of them.)
+template <int DT, int KP, int W, bool KEEP, bool WIDE>
+__global__ void __launch_bounds__(W *kWave, 2) delta_walk(Delta a, Records rec, Walk w) {
     constexpr int KT = KP / 16, KS = KP / 32;
-    constexpr int kKeys = 2 * kC * KP * 2;                     // bytes of the images of k and q
-    constexpr int kBuf = kKeys + (int)kXaBytes + kStaged;
+    typedef Staged<KP, W> Stage;
+    constexpr int kBuf = Stage::kBytes, kKeys = Stage::kKeys;
     __shared__ __align__(16) uint8_t smem[2 * kBuf];
     const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int m = lane & 15, grp = lane >> 4;
+    const int lk_at = left_place<KP>(lane), tk_at = turned_place<KP>(lane), ls_at = left_place<64>(lane);
     const int id = same_die(blockIdx.x, gridDim.x);
     const int bh = id / w.blocks, b = bh / a.H, h = bh % a.H, g = h / (a.H / a.G);
-    const int col0 = (id % w.blocks * W + wave) * 16 * NT;
+    const int col = (id % w.blocks * W + wave) * 16 + m, VP = padded_v(a.V);
     const int length = length_of(a, b);
     const int chunks = (length + kC - 1) / kC, end = chunks < w.n1 ? chunks : w.n1;
 
-    f4 S[NT][KT];
+    f4 S[KT];
 #pragma unroll
-    for (int c = 0; c < NT; ++c) {
-        const int col = col0 + 16 * c + m;
+    for (int t = 0; t < KT; ++t)
 #pragma unroll
-        for (int t = 0; t < KT; ++t)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int k = row_of(t, 4 * grp + i);
-                S[c][t][i] = w.state_in && k < a.K && col < a.V ? w.state_in[((int64_t)bh * a.K + k) * a.V + col] : 0.0f;
-            }
-    }
-    const uint8_t *keys = rec.key + (int64_t)(b * a.G + g) * rec.chunks * key_bytes(KP);
-    const uint8_t *xas = rec.xa + (int64_t)bh * rec.chunks * kXaBytes;
+        for (int i = 0; i < 4; ++i) {
+            const int k = row_of(t, 4 * grp + i);
+            S[t][i] = w.state_in && k < a.K && col < a.V ? w.state_in[((int64_t)bh * a.K + k) * a.V + col] : 0.0f;
+        }
+    const uint8_t *key = rec.key + (int64_t)(b * a.G + g) * rec.chunks * key_bytes(KP);
+    const uint8_t *xa = rec.xa + (int64_t)bh * rec.chunks * kXaBytes;
     const RowCoef *coefs = rec.coef + (int64_t)bh * rec.chunks;
-    auto fill = [&](int n) {
-        uint8_t *to = smem + (n & 1) * kBuf;
-        const int i = n - w.n0;
-        const uint8_t *key = keys + i * (int64_t)key_bytes(KP), *xa = xas + i * (int64_t)kXaBytes;
-        const uint8_t *coef = (const uint8_t *)(coefs + i);
-        for (int p = wave; p < kBuf / 1024; p += W) {
-            const int o = p * 1024;
-            to_lds(o < kKeys ? key + o : o < kKeys + (int)kXaBytes ? xa + (o - kKeys) : coef, to + o, lane);
-        }
-    };
-    const uint16_t *vbase = a.v + b * a.vs[1] + h * a.vs[2];
-    uint16_t vnext[NT][4][4];
+    Stage stage;
     auto fetch = [&](int n) {
-#pragma unroll
-        for (int c = 0; c < NT; ++c) {
-            const int col = col0 + 16 * c + m;
-#pragma unroll
-            for (int t = 0; t < 4; ++t)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int row = n * kC + row_of(t, 4 * grp + i);
-                    vnext[c][t][i] = row < length && col < a.V ? vbase[(int64_t)row * a.vs[0] + col] : 0;
-                }
-        }
+        const int64_t i = n - w.n0;
+        stage.load(key + i * (int64_t)key_bytes(KP), xa + i * (int64_t)kXaBytes, coefs + i);
     };
-    if (w.n0 < end) fill(w.n0), fetch(w.n0);
+    const Column16 vcol = {a.v + b * a.vs[1] + h * a.vs[2], a.vs[0], col, a.V};
+    const uint32_t out_row = 2u * (uint32_t)(a.B * a.H) * a.V;       // bytes
+    const uint32_t out_at = col < a.V ? 8 * grp * out_row + 2 * (h * a.V + col) : kNowhere;
+    float *keep_s = KEEP ? w.states + ((int64_t)bh * rec.chunks * KP + 8 * grp) * VP + col : nullptr;
+    float *keep_u = KEEP ? w.u + ((int64_t)bh * rec.chunks * kC + 8 * grp) * VP + col : nullptr;
+    uint16_t v[4][4];
+    if (w.n0 < end) {
+        fetch(w.n0);
+        load_rows<WIDE>(vcol, w.n0 * kC, length - w.n0 * kC, lane, v);
+        stage.store(smem + (w.n0 & 1) * kBuf);
+        lds_barrier();
+    }
     for (int n = w.n0; n < end; ++n) {
-        __syncthreads();  // this chunk's operands are there, and all waves are done with the last one's
         const uint8_t *buf = smem + (n & 1) * kBuf;
         const uint16_t *kt = (const uint16_t *)buf, *qt = kt + kC * KP;
         const uint16_t *xh = (const uint16_t *)(buf + kKeys), *xl = xh + kSquare, *ah = xl + kSquare, *al = ah + kSquare;
-        const float *coef = (const float *)(buf + kKeys + kXaBytes);
-        const float whole = coefs[n - w.n0].whole, sx = coefs[n - w.n0].x, sa = coefs[n - w.n0].a;
-        f4 R[NT][4];
+        const RowCoef *coef = (const RowCoef *)(buf + kKeys + kXaBytes);
+        fetch(n + 1 < end ? n + 1 : n);
+        if (KEEP) {
+            float *to = keep_s + (int64_t)n * KP * VP;
 #pragma unroll
-        for (int c = 0; c < NT; ++c)
+            for (int t = 0; t < KT; ++t)
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) R[c][t][i] = to_f32<DT>(vnext[c][t][i]);
-        if (n + 1 < end) fill(n + 1), fetch(n + 1);
-        if (w.states) {
-            float *keep = w.states + ((int64_t)bh * rec.chunks + n) * a.K * a.V;
-#pragma unroll
-            for (int c = 0; c < NT; ++c) {
-                const int col = col0 + 16 * c + m;
-#pragma unroll
-                for (int t = 0; t < KT; ++t)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int k = row_of(t, 4 * grp + i);
-                        if (k < a.K && col < a.V) keep[(int64_t)k * a.V + col] = S[c][t][i];
-                    }
-            }
+                for (int i = 0; i < 4; ++i) to[(row_of(t, 0) + i) * VP] = S[t][i];
         }
         // K~ S0 and Q~ S0
-        f4 P[NT][4] = {}, O[NT][4] = {};
-        float back[NT];
-        {
-            Split sp[NT][KS];
+        f4 P[4] = {}, O[4] = {};
+        const Power ps = column_power(S, lane);
 #pragma unroll
-            for (int c = 0; c < NT; ++c) {
-                const Power p = column_power(S[c]);
-                back[c] = p.back;
+        for (int s = 0; s < KS; ++s) {
+            const Split sp = split(S[2 * s], S[2 * s + 1], ps.inv);
 #pragma unroll
-                for (int s = 0; s < KS; ++s) sp[c][s] = split(S[c][2 * s], S[c][2 * s + 1], p.inv);
+            for (int t = 0; t < 4; ++t) {
+                const h8 lk = left<KP>(kt, lk_at, t, s), lq = left<KP>(qt, lk_at, t, s);
+                P[t] = mma(lk, sp.hi, P[t]);
+                O[t] = mma(lq, sp.hi, O[t]);
+                P[t] = mma(lk, sp.lo, P[t]);
+                O[t] = mma(lq, sp.lo, O[t]);
             }
-#pragma unroll
-            for (int s = 0; s < KS; ++s)
-#pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    const h8 lk = left<KP>(kt, t, s, lane), lq = left<KP>(qt, t, s, lane);
-#pragma unroll
-                    for (int c = 0; c < NT; ++c) {
-                        P[c][t] = mma(lk, sp[c][s].hi, P[c][t]);
-                        O[c][t] = mma(lq, sp[c][s].hi, O[c][t]);
-                        P[c][t] = mma(lk, sp[c][s].lo, P[c][t]);
-                        O[c][t] = mma(lq, sp[c][s].lo, O[c][t]);
-                    }
-                }
         }
-        // beta (V - p K~ S0), and out's first part
+        // beta (V - p K~ S0)
+        f4 R[4];
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
             const int r = row_of(t, 4 * grp);
-            const f4 cp = *(const f4 *)(coef + r), cb = *(const f4 *)(coef + kC + r), cq = *(const f4 *)(coef + 2 * kC + r);
+            const f4 cp = *(const f4 *)(coef->p + r) * ps.back, cb = *(const f4 *)(coef->beta + r);
 #pragma unroll
-            for (int c = 0; c < NT; ++c)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    R[c][t][i] = cb[i] * __builtin_fmaf(-cp[i] * back[c], P[c][t][i], R[c][t][i]);
-                    O[c][t][i] *= cq[i] * back[c];
-                }
+            for (int i = 0; i < 4; ++i) R[t][i] = cb[i] * __builtin_fmaf(-cp[i], P[t][i], to_f32<DT>(v[t][i]));
         }
-        // U = X R, in P's registers
-#pragma unroll
-        for (int c = 0; c < NT; ++c) {
-            const Power p = column_power(R[c]);
-            Split sp[2];
-#pragma unroll
-            for (int s = 0; s < 2; ++s) sp[s] = split(R[c][2 * s], R[c][2 * s + 1], p.inv);
-            const float up = p.back * sx;
+        load_rows<WIDE>(vcol, (n + 1) * kC, length - (n + 1) * kC, lane, v);
+        // U = X R
+        f4 U[4];
+        {
+            const Power p = column_power(R, lane);
+            const Split s0 = split(R[0], R[1], p.inv), s1 = split(R[2], R[3], p.inv);
+            const float up = p.back * coef->x;
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
                 f4 u = {};
 #pragma unroll
                 for (int s = 0; s <= t / 2; ++s) {
-                    const h8 lh = left<64>(xh, t, s, lane), ll = left<64>(xl, t, s, lane);
-                    u = mma(lh, sp[s].hi, u);
-                    u = mma(ll, sp[s].hi, u);
-                    u = mma(lh, sp[s].lo, u);
+                    const h8 lh = left<64>(xh, ls_at, t, s), ll = left<64>(xl, ls_at, t, s);
+                    const Split &sp = s ? s1 : s0;
+                    u = mma(ll, sp.hi, u);
+                    u = mma(lh, sp.lo, u);
+                    u = mma(lh, sp.hi, u);
                 }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) P[c][t][i] = u[i] * up;
+                U[t] = u * up;
             }
         }
-        if (w.u) {
-            float *keep = w.u + ((int64_t)bh * rec.chunks + n) * kC * a.V;
+        if (KEEP) {
+            float *to = keep_u + (int64_t)n * kC * VP;
 #pragma unroll
-            for (int c = 0; c < NT; ++c) {
-                const int col = col0 + 16 * c + m;
+            for (int t = 0; t < 4; ++t)
 #pragma unroll
-                for (int t = 0; t < 4; ++t)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (col < a.V) keep[(int64_t)row_of(t, 4 * grp + i) * a.V + col] = P[c][t][i];
-            }
+                for (int i = 0; i < 4; ++i) to[(row_of(t, 0) + i) * VP] = U[t][i];
         }
-        // out's second part, A U
-#pragma unroll
-        for (int c = 0; c < NT; ++c) {
-            const Power p = column_power(P[c]);
-            Split sp[2];
-#pragma unroll
-            for (int s = 0; s < 2; ++s) sp[s] = split(P[c][2 * s], P[c][2 * s + 1], p.inv);
-            const float up = p.back * sa;
-            const int col = col0 + 16 * c + m;
+        // out = q Q~ S0 + A U
+        {
+            const Power p = column_power(U, lane);
+            const Split s0 = split(U[0], U[1], p.inv), s1 = split(U[2], U[3], p.inv);
+            const float up = p.back * coef->a;
+            const int left_rows = a.S - n * kC;
+            const Buffer to = buffer_of(w.out + (int64_t)n * kC * (out_row / 2) + (int64_t)b * a.H * a.V,
+                                        (left_rows < kC ? left_rows - 1 : kC - 1) * out_row + 2u * a.H * a.V);
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
                 f4 o = {};
 #pragma unroll
                 for (int s = 0; s <= t / 2; ++s) {
-                    const h8 lh = left<64>(ah, t, s, lane), ll = left<64>(al, t, s, lane);
-                    o = mma(lh, sp[s].hi, o);
-                    o = mma(ll, sp[s].hi, o);
-                    o = mma(lh, sp[s].lo, o);
+                    const h8 lh = left<64>(ah, ls_at, t, s), ll = left<64>(al, ls_at, t, s);
+                    const Split &sp = s ? s1 : s0;
+                    o = mma(ll, sp.hi, o);
+                    o = mma(lh, sp.lo, o);
+                    o = mma(lh, sp.hi, o);
                 }
+                const f4 cq = *(const f4 *)(coef->q + row_of(t, 4 * grp)) * ps.back;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int row = n * kC + row_of(t, 4 * grp + i);
-                    if (row < a.S && col < a.V)
-                        w.out[(((int64_t)row * a.B + b) * a.H + h) * a.V + col] =
-                            from_f32<DT>(__builtin_fmaf(o[i], up, O[c][t][i]));
-                }
+                for (int i = 0; i < 4; ++i)
+                    __builtin_amdgcn_raw_buffer_store_b16(from_f32<DT>(__builtin_fmaf(o[i], up, cq[i] * O[t][i])), to,
+                                                          out_at + (row_of(t, 0) + i) * out_row, 0, 0);
             }
         }
         // S = whole S0 + K~^T u U
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            const f4 cu = *(const f4 *)(coef + 3 * kC + row_of(t, 4 * grp));
-#pragma unroll
-            for (int c = 0; c < NT; ++c)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) P[c][t][i] *= cu[i];
-        }
         {
-            Split sp[NT][2];
 #pragma unroll
-            for (int c = 0; c < NT; ++c) {
-                const Power p = column_power(P[c]);
-                back[c] = p.back;
-#pragma unroll
-                for (int s = 0; s < 2; ++s) sp[c][s] = split(P[c][2 * s], P[c][2 * s + 1], p.inv);
-            }
+            for (int t = 0; t < 4; ++t) U[t] *= *(const f4 *)(coef->u + row_of(t, 4 * grp));
+            const Power p = column_power(U, lane);
+            const Split s0 = split(U[0], U[1], p.inv), s1 = split(U[2], U[3], p.inv);
+            const float whole = coef->whole;
 #pragma unroll
             for (int t = 0; t < KT; ++t) {
-                f4 d[NT] = {};
+                const h8 l0 = left_turned<KP>(kt, tk_at, t, 0), l1 = left_turned<KP>(kt, tk_at, t, 1);
+                f4 d = mma(l0, s0.lo, f4{});
+                d = mma(l1, s1.lo, d);
+                d = mma(l0, s0.hi, d);
+                d = mma(l1, s1.hi, d);
 #pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    const h8 lk = left_turned<KP>(kt, t, s, lane);
-#pragma unroll
-                    for (int c = 0; c < NT; ++c) {
-                        d[c] = mma(lk, sp[c][s].hi, d[c]);
-                        d[c] = mma(lk, sp[c][s].lo, d[c]);
-                    }
-                }
-#pragma unroll
-                for (int c = 0; c < NT; ++c)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) S[c][t][i] = __builtin_fmaf(whole, S[c][t][i], back[c] * d[c][i]);
+                for (int i = 0; i < 4; ++i) S[t][i] = __builtin_fmaf(whole, S[t][i], p.back * d[i]);
             }
         }
+        stage.store(smem + (~n & 1) * kBuf);
+        lds_barrier();  // the next chunk's operands are there, and all waves are done with this one's
     }
     if (w.state_out) {
 #pragma unroll
-        for (int c = 0; c < NT; ++c) {
-            const int col = col0 + 16 * c + m;
+        for (int t = 0; t < KT; ++t)
 #pragma unroll
-            for (int t = 0; t < KT; ++t)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int k = row_of(t, 4 * grp + i);
-                    if (k < a.K && col < a.V) w.state_out[((int64_t)bh * a.K + k) * a.V + col] = S[c][t][i];
-                }
-        }
+            for (int i = 0; i < 4; ++i) {
+                const int k = row_of(t, 4 * grp + i);
+                if (k < a.K && col < a.V) w.state_out[((int64_t)bh * a.K + k) * a.V + col] = S[t][i];
+            }
     }
     // rows that no chunk covers are zeros
     const int from = (end > w.n0 ? end : w.n0) * kC, to = w.n1 * kC < a.S ? w.n1 * kC : a.S;
     for (int row = from + grp; row < to; row += 4)
-#pragma unroll
-        for (int c = 0; c < NT; ++c) {
-            const int col = col0 + 16 * c + m;
-            if (col < a.V) w.out[(((int64_t)row * a.B + b) * a.H + h) * a.V + col] = 0;
-        }
+        if (col < a.V) w.out[(((int64_t)row * a.B + b) * a.H + h) * a.V + col] = 0;
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -682,16 +610,22 @@ int prepare(const Delta &d, const Records &rec, int n0, int n1, hipStream_t st) 
                        0, st, d, rec, n0);
     return launched();
 }
-template <int DT, int KP, int NT, int W>
-int walk_as(const Delta &d, const Records &rec, Walk w, hipStream_t st) {
-    w.blocks = (d.V + 16 * NT * W - 1) / (16 * NT * W);
-    hipLaunchKernelGGL((delta_walk<DT, KP, NT, W>), dim3((unsigned)(d.B * d.H * w.blocks)), dim3(W * kWave), 0, st,
-                       d, rec, w);
+template <int DT, int KP, bool KEEP>
+int walk(const Delta &d, const Records &rec, Walk w, hipStream_t st) {
+    constexpr int W = 4;
+    w.blocks = padded_v(d.V) / (16 * W);
+    const dim3 grid((unsigned)(d.B * d.H * w.blocks)), block(W * kWave);
+    if (row_buffer(d.vs[0], d.V)) hipLaunchKernelGGL((delta_walk<DT, KP, W, KEEP, false>), grid, block, 0, st, d, rec, w);
+    else hipLaunchKernelGGL((delta_walk<DT, KP, W, KEEP, true>), grid, block, 0, st, d, rec, w);
     return launched();
 }
 template <int DT, int KP>
-int walk(const Delta &d, const Records &rec, const Walk &w, hipStream_t st) {
-    return walk_as<DT, KP, 1, 4>(d, rec, w, st);
+int all_chunks(const Delta &d, const Records &rec, const Walk &w, hipStream_t st) {
+    if (w.n1 > w.n0) {
+        const int rc = prepare<DT, KP>(d, rec, w.n0, w.n1, st);
+        if (rc != MCCB_OK) return rc;
+    }
+    return w.states ? walk<DT, KP, true>(d, rec, w, st) : walk<DT, KP, false>(d, rec, w, st);
 }
 
 template <int DT>
@@ -704,13 +638,9 @@ int forward(const mccb_delta_t *a, void *out, float *final_state, void *saved, v
     w.n0 = 0, w.n1 = (int)chunks;
     if (saved) {
         w.states = (float *)((uint8_t *)saved + records_size(a, chunks));
-        w.u = w.states + chunks * (uint64_t)(a->B * a->H) * (uint64_t)(a->K * a->V);
+        w.u = (float *)((uint8_t *)w.states + chunk_states_bytes(a));
     }
-    if (chunks > 0) {
-        const int rc = padded(a->K) == 64 ? prepare<DT, 64>(d, rec, w.n0, w.n1, st) : prepare<DT, 128>(d, rec, w.n0, w.n1, st);
-        if (rc != MCCB_OK) return rc;
-    }
-    return padded(a->K) == 64 ? walk<DT, 64>(d, rec, w, st) : walk<DT, 128>(d, rec, w, st);
+    return padded(a->K) == 64 ? all_chunks<DT, 64>(d, rec, w, st) : all_chunks<DT, 128>(d, rec, w, st);
 }
 
 }  // namespace
@@ -722,7 +652,7 @@ int mccb_delta_saved_size(const mccb_delta_t *a, uint64_t *bytes) {
     const int rc = check_delta(a, false);
     if (rc != MCCB_OK) return rc;
     const uint64_t chunks = chunks_of(a);
-    *bytes = records_size(a, chunks) + chunks * state_bytes(a) + chunk_rows_bytes(a);
+    *bytes = records_size(a, chunks) + chunk_states_bytes(a) + chunk_rows_bytes(a);
     return MCCB_OK;
 }
 
