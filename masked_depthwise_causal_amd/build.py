@@ -33,6 +33,11 @@ HIPCC_FLAGS = [
 ]
 
 
+# the delta rule's walks have a SIMD's registers to themselves, where the compiler would have the matrix
+# instructions' results in accumulation registers and move each of them (662 vector instructions a chunk, 581 without)
+DELTA_FLAGS = ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]
+
+
 def build_library(out: str = LIB, extra: list[str] | None = None, verbose: bool = False) -> str:
     hipcc = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
     cmd = [hipcc, *HIPCC_FLAGS, *(extra or []), "-I", INCLUDE, SRC, "-o", out + ".tmp"]
@@ -78,7 +83,7 @@ def build_ssm_library(out: str = SSM_LIB, extra: list[str] | None = None,
 
 def build_delta_library(out: str = DELTA_LIB, extra: list[str] | None = None,
                         verbose: bool = False) -> str:
-    return _build_objects(DELTA_SRCS, out, extra, verbose)
+    return _build_objects(DELTA_SRCS, out, DELTA_FLAGS + (extra or []), verbose)
 
 
 def build_binding(out: str = BINDING, src: str = BINDING_SRC) -> str:

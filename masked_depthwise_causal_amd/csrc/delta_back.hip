@@ -44,12 +44,12 @@ struct Back {
 template <int DT, int KP, int W, bool WIDE>
 __global__ void __launch_bounds__(W *kWave) delta_walk_back(Delta a, Records rec, Back w) {
     constexpr int KT = KP / 16, KS = KP / 32;
-    typedef Staged<KP, W> Stage;
+    typedef Staged<KP, W, 2> Stage;
     constexpr int kBuf = Stage::kBytes, kKeys = Stage::kKeys;
     __shared__ __align__(16) uint8_t smem[2 * kBuf];
     const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int m = lane & 15, grp = lane >> 4;
-    const int lk_at = left_place<KP>(lane), tk_at = turned_place<KP>(lane), ts_at = turned_place<64>(lane);
+    const int lk_at = left_place<KP>(lane), tk_at = turned_place<KP>(lane), ts_at = triangle_turned_place(lane);
     const int id = same_die(blockIdx.x, gridDim.x);
     const int bh = id / w.blocks, b = bh / a.H, h = bh % a.H, g = h / (a.H / a.G);
     const int col = (id % w.blocks * W + wave) * 16 + m, VP = padded_v(a.V);
@@ -85,8 +85,8 @@ __global__ void __launch_bounds__(W *kWave) delta_walk_back(Delta a, Records rec
     for (int n = chunks - 1; n >= 0; --n) {
         const uint8_t *buf = smem + (n & 1) * kBuf;
         const uint16_t *kt = (const uint16_t *)buf, *qt = kt + kC * KP;
-        const uint16_t *xh = (const uint16_t *)(buf + kKeys), *xl = xh + kSquare, *ah = xl + kSquare, *al = ah + kSquare;
-        const RowCoef *coef = (const RowCoef *)(buf + kKeys + kXaBytes);
+        const uint16_t *xh = (const uint16_t *)(buf + kKeys), *xl = xh + kTriangle, *ah = xl + kTriangle, *al = ah + kTriangle;
+        const RowCoef *coef = (const RowCoef *)(buf + kKeys + Stage::kXa);
         const int next = n > 0 ? n - 1 : 0;
         fetch(next);
         {
@@ -108,12 +108,13 @@ __global__ void __launch_bounds__(W *kWave) delta_walk_back(Delta a, Records rec
 #pragma unroll
             for (int s = 0; s < KS; ++s) {
                 const Split sp = split(S[2 * s], S[2 * s + 1], p.inv);
+                h8 lk[4];
 #pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    const h8 lk = left<KP>(kt, lk_at, t, s);
-                    D[t] = mma(lk, sp.hi, D[t]);
-                    D[t] = mma(lk, sp.lo, D[t]);
-                }
+                for (int t = 0; t < 4; ++t) lk[t] = left<KP>(kt, lk_at, t, s);
+#pragma unroll
+                for (int t = 0; t < 4; ++t) D[t] = mma(lk[t], sp.lo, D[t]);
+#pragma unroll
+                for (int t = 0; t < 4; ++t) D[t] = mma(lk[t], sp.hi, D[t]);
             }
 #pragma unroll
             for (int t = 0; t < 4; ++t) D[t] *= *(const f4 *)(coef->u + row_of(t, 4 * grp)) * p.back;
@@ -132,8 +133,8 @@ __global__ void __launch_bounds__(W *kWave) delta_walk_back(Delta a, Records rec
                 f4 d = {};
 #pragma unroll
                 for (int s = t / 2; s < 2; ++s) {
-                    d = mma(left_turned<64>(al, ts_at, t, s), one[s], d);
-                    d = mma(left_turned<64>(ah, ts_at, t, s), one[s], d);
+                    d = mma(triangle_turned(al, ts_at, t, s), one[s], d);
+                    d = mma(triangle_turned(ah, ts_at, t, s), one[s], d);
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) D[t][i] = __builtin_fmaf(d[i], up, D[t][i]);
@@ -143,21 +144,10 @@ __global__ void __launch_bounds__(W *kWave) delta_walk_back(Delta a, Records rec
         f4 Y[4];
         {
             const Power p = column_power(D, lane);
-            const Split s0 = split(D[0], D[1], p.inv), s1 = split(D[2], D[3], p.inv);
             const float up = p.back * coef->x;
+            triangle_times<true, 2>(xh, xl, ts_at, split(D[0], D[1], p.inv), split(D[2], D[3], p.inv), Y);
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                f4 d = {};
-#pragma unroll
-                for (int s = t / 2; s < 2; ++s) {
-                    const h8 lh = left_turned<64>(xh, ts_at, t, s), ll = left_turned<64>(xl, ts_at, t, s);
-                    const Split &sp = s ? s1 : s0;
-                    d = mma(ll, sp.hi, d);
-                    d = mma(lh, sp.lo, d);
-                    d = mma(lh, sp.hi, d);
-                }
-                Y[t] = d * up;
-            }
+            for (int t = 0; t < 4; ++t) Y[t] *= up;
         }
         {
             float *to = keep_y + (int64_t)n * kC * VP;
@@ -191,19 +181,28 @@ __global__ void __launch_bounds__(W *kWave) delta_walk_back(Delta a, Records rec
             const Split g0 = split(G[0], G[1], p.inv), g1 = split(G[2], G[3], p.inv);
             const float whole = coef->whole;
 #pragma unroll
-            for (int t = 0; t < KT; ++t) {
-                const h8 k0 = left_turned<KP>(kt, tk_at, t, 0), k1 = left_turned<KP>(kt, tk_at, t, 1);
-                const h8 q0 = left_turned<KP>(qt, tk_at, t, 0), q1 = left_turned<KP>(qt, tk_at, t, 1);
-                f4 d = mma(k0, y0.lo, f4{});
-                d = mma(k1, y1.lo, d);
-                d = mma(q0, g0.lo, d);
-                d = mma(q1, g1.lo, d);
-                d = mma(k0, y0.hi, d);
-                d = mma(k1, y1.hi, d);
-                d = mma(q0, g0.hi, d);
-                d = mma(q1, g1.hi, d);
+            for (int t = 0; t < KT; t += 4) {
+                f4 d[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) S[t][i] = __builtin_fmaf(whole, S[t][i], p.back * d[i]);
+                for (int i = 0; i < 4; ++i) d[i] = mma(left_turned<KP>(kt, tk_at, t + i, 0), y0.lo, f4{});
+#pragma unroll
+                for (int i = 0; i < 4; ++i) d[i] = mma(left_turned<KP>(kt, tk_at, t + i, 1), y1.lo, d[i]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) d[i] = mma(left_turned<KP>(qt, tk_at, t + i, 0), g0.lo, d[i]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) d[i] = mma(left_turned<KP>(qt, tk_at, t + i, 1), g1.lo, d[i]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) d[i] = mma(left_turned<KP>(kt, tk_at, t + i, 0), y0.hi, d[i]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) d[i] = mma(left_turned<KP>(kt, tk_at, t + i, 1), y1.hi, d[i]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) d[i] = mma(left_turned<KP>(qt, tk_at, t + i, 0), g0.hi, d[i]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) d[i] = mma(left_turned<KP>(qt, tk_at, t + i, 1), g1.hi, d[i]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) S[t + i][j] = __builtin_fmaf(whole, S[t + i][j], p.back * d[i][j]);
             }
         }
         stage.store(smem + (~n & 1) * kBuf);
@@ -220,23 +219,6 @@ __global__ void __launch_bounds__(W *kWave) delta_walk_back(Delta a, Records rec
     }
     for (int row = chunks * kC + grp; row < a.S; row += 4)  // rows that no chunk covers
         if (mine) w.gv[(((int64_t)row * a.B + b) * a.H + h) * a.V + col] = 0;
-}
-
-// Instructions stay on their side of this: operands are read a few products ahead, and not all of a loop's at once,
-// which would take more registers than there are.
-__device__ static inline void keep_order() { __builtin_amdgcn_sched_barrier(0); }
-
-// The same number, as a new one: what is computed from it is computed where it stands, not ahead of all loops, to
-// be kept in registers that are needed.
-__device__ static inline int anew(int v) {
-    asm volatile("" : "+v"(v));
-    return v;
-}
-__device__ static inline f4 anew(h4 v) {
-    auto u = __builtin_bit_cast(uint2, v);
-    asm volatile("" : "+v"(u.x), "+v"(u.y));
-    v = __builtin_bit_cast(h4, u);
-    return f4{(float)v[0], (float)v[1], (float)v[2], (float)v[3]};
 }
 
 // 8 values of a row from column c, zeros past V and where the row is not there. ROWS8: V is a multiple of 8.
@@ -439,10 +421,9 @@ __global__ void __launch_bounds__(KP / 16 * kWave) delta_grads(Delta a, Records 
                     }
                 }
             }
-            // gO U^T and Y U^T
+            // gO U^T and Y U^T (those above the diagonal too: the waves that have them would wait for the others)
 #pragma unroll
             for (int j = 0; j < NJ; ++j) {
-                if ((j0 + j) / 2 > rt / 2) continue;
                 keep_order();
                 f4 x = {}, y = {};
 #pragma unroll
@@ -484,13 +465,12 @@ __global__ void __launch_bounds__(KP / 16 * kWave) delta_grads(Delta a, Records 
             for (int j = 0; j < NJ; ++j) {
                 keep_order();
                 f4 qk = {}, kk = {};
-                if ((j0 + j) / 2 <= rt / 2)
 #pragma unroll
-                    for (int s = 0; s < KP / 32; ++s) {
-                        const h8 rk = left<KP>(kt, lk_at, j0 + j, s);
-                        qk = mma(left<KP>(qt, lk_at, rt, s), rk, qk);
-                        kk = mma(left<KP>(kt, lk_at, rt, s), rk, kk);
-                    }
+                for (int s = 0; s < KP / 32; ++s) {
+                    const h8 rk = left<KP>(kt, lk_at, j0 + j, s);
+                    qk = mma(left<KP>(qt, lk_at, rt, s), rk, qk);
+                    kk = mma(left<KP>(kt, lk_at, rt, s), rk, kk);
+                }
                 const int c = row_of(j0 + j, m);
                 const double gc = cum[c];
                 const float kc = kr[c];

@@ -55,7 +55,9 @@ struct RowCoef {
 static_assert(sizeof(RowCoef) == 2048, "two of the walks' loads");
 
 constexpr size_t key_bytes(int kp) { return 2 * kC * kp * sizeof(uint16_t) + 4 * kC * sizeof(float); }
-constexpr size_t kXaBytes = 4 * kSquare * sizeof(uint16_t);  // X hi, X lo, A hi, A lo
+// X hi, X lo, A hi, A lo, of each the three 32x32 blocks on and below the diagonal
+constexpr int kTriangle = 3 * 32 * 32;
+constexpr size_t kXaBytes = 4 * kTriangle * sizeof(uint16_t);
 
 // An image row R holds its chunks of 8 values in the order c ^ swizzle(R). The matrix instructions' rows m
 // stand for rows 32 j + 8 (m / 4) + 4 p + m % 4 (below); sixteen of those read one chunk each from
@@ -75,6 +77,23 @@ __device__ static inline int image_at(int row, int chunk) {  // in 16-bit values
 // eight consecutive rows, just what the next product wants of its right operand.
 __device__ static inline int row_of(int tile, int m) { return 32 * (tile >> 1) + 8 * (m >> 2) + 4 * (tile & 1) + (m & 3); }
 
+// Instructions stay on their side of this: operands are read a few products ahead, and not all of a loop's at once,
+// which would take more registers than there are.
+__device__ static inline void keep_order() { __builtin_amdgcn_sched_barrier(0); }
+
+// The same number, as a new one: what is computed from it is computed where it stands, not ahead of all loops, to
+// be kept in registers that are needed.
+__device__ static inline int anew(int v) {
+    asm volatile("" : "+v"(v));
+    return v;
+}
+__device__ static inline f4 anew(h4 v) {
+    auto u = __builtin_bit_cast(uint2, v);
+    asm volatile("" : "+v"(u.x), "+v"(u.y));
+    v = __builtin_bit_cast(h4, u);
+    return f4{(float)v[0], (float)v[1], (float)v[2], (float)v[3]};
+}
+
 // Operands from images. Where a lane reads is a place of its own (left_place and so on, once a kernel) with
 // a step or tile exclusive-or'ed in and constants added: the swizzle does not depend on those.
 typedef short s16x4 __attribute__((ext_vector_type(4)));
@@ -88,6 +107,13 @@ __device__ static inline int left_place(int lane) {
 template <int COLS>
 __device__ static inline h8 left(const uint16_t *image, int place, int tile, int s) {
     return *(const h8 *)(image + (place ^ s << 5) + row_of(tile, 0) * COLS);
+}
+// Of a triangle's blocks, whose rows have four chunks in the order c ^ (row / 8): likewise, step s up to tile / 2.
+__device__ static inline int block_at(int row, int chunk) { return row * 32 + ((chunk ^ (row >> 3)) << 3); }
+__device__ static inline int block_of(int row, int col) { return (row * (row + 1) / 2 + col) * 1024; }
+__device__ static inline int triangle_place(int lane) { return block_at(row_of(0, lane & 15), lane >> 4); }
+__device__ static inline h8 triangle(const uint16_t *image, int place, int tile, int s) {
+    return *(const h8 *)(image + place + block_of(tile >> 1, s) + 4 * (tile & 1) * 32);
 }
 // The transposed image's: its columns as rows (`tile` of them), step s of 32 along its rows.
 // A transposing read gives lane i of 16 column i of the four rows that those lanes read 8 bytes of.
@@ -104,6 +130,13 @@ __device__ static inline h8 turned_at(const uint16_t *__restrict__ p) {
 template <int COLS>
 __device__ static inline h8 left_turned(const uint16_t *image, int place, int tile, int s) {
     return turned_at<COLS>(image + (place ^ (tile >> 1) << 5) + 32 * s * COLS + 4 * (tile & 1));
+}
+// And the transposed triangle's, step s from tile / 2 on.
+__device__ static inline int triangle_turned_place(int lane) {
+    return block_at(8 * (lane >> 4) + (lane >> 2 & 3), lane & 3);
+}
+__device__ static inline h8 triangle_turned(const uint16_t *image, int place, int tile, int s) {
+    return turned_at<32>(image + place + block_of(s, tile >> 1) + 4 * (tile & 1));
 }
 // Right operand: columns 16 tile.. of an image, step s of 32 along its rows.
 template <int COLS>
@@ -123,12 +156,12 @@ __device__ static inline f4 mma(h8 a, h8 b, f4 c) { return __builtin_amdgcn_mfma
 struct Split {
     h8 hi, lo;
 };
-// hi = fp16(v inv), lo = fp16(v inv - hi), which a mixed-precision multiply-add rounds once. (The empty asm, which
+// hi = fp16(v inv), lo = fp16(v inv - hi), each a mixed-precision multiply-add that rounds once. (The empty asm, which
 // has no instruction, keeps the pair hi together: the compiler would round its halves a second time.)
 typedef _Float16 h2 __attribute__((ext_vector_type(2)));
-typedef float f2 __attribute__((ext_vector_type(2)));
 __device__ static inline void split2(float a, float b, float inv, uint32_t &hi, uint32_t &lo) {
-    uint32_t h = __builtin_bit_cast(uint32_t, __builtin_convertvector(f2{a * inv, b * inv}, h2));
+    const h2 first = {(_Float16)__builtin_fmaf(a, inv, 0.0f), (_Float16)__builtin_fmaf(b, inv, 0.0f)};
+    uint32_t h = __builtin_bit_cast(uint32_t, first);
     asm("" : "+v"(h));
     const h2 t = __builtin_bit_cast(h2, h);
     const h2 l = {(_Float16)__builtin_fmaf(a, inv, -(float)t[0]), (_Float16)__builtin_fmaf(b, inv, -(float)t[1])};
@@ -176,8 +209,10 @@ __device__ static inline Power turned_sign(Power p, int lane) {
 
 // The largest magnitude over the four lanes that hold a column.
 __device__ static inline float column_max(float m) {
-    m = __builtin_fmaxf(m, __shfl_xor(m, 16));
-    return __builtin_fmaxf(m, __shfl_xor(m, 32));
+    const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(m), __float_as_uint(m), false, false);
+    m = __builtin_fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+    const auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(m), __float_as_uint(m), false, false);
+    return __builtin_fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
 }
 template <int N>
 __device__ static inline Power column_power(const f4 (&v)[N], int lane) {
@@ -187,6 +222,34 @@ __device__ static inline Power column_power(const f4 (&v)[N], int lane) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) m = __builtin_fmaxf(m, __builtin_fabsf(v[t][i]));
     return turned_sign(power_of(column_max(m)), lane);
+}
+
+// A triangle of two terms (or one, of `hi` alone) times 64 rows of 16 columns, s0 and s1 (one term too); TURNED: the
+// transposed matrix. The terms go by in turns, since a product waits for the last one with the same sum.
+template <bool TURNED, int TERMS>
+__device__ static inline void triangle_times(const uint16_t *hi, const uint16_t *lo, int place, const Split &s0,
+                                             const Split &s1, f4 (&r)[4]) {
+    h8 h[4][2], l[4][2];
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            if (TURNED ? s < t / 2 : s > t / 2) continue;
+            h[t][s] = TURNED ? triangle_turned(hi, place, t, s) : triangle(hi, place, t, s);
+            if (TERMS > 1) l[t][s] = TURNED ? triangle_turned(lo, place, t, s) : triangle(lo, place, t, s);
+        }
+#pragma unroll
+    for (int t = 0; t < 4; ++t) r[t] = f4{};
+#pragma unroll
+    for (int term = TERMS > 1 ? 0 : 2; term < 3; ++term)
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                if (TURNED ? s < t / 2 : s > t / 2) continue;
+                const Split &x = s ? s1 : s0;
+                r[t] = mma(term == 0 ? l[t][s] : h[t][s], term == 1 ? x.lo : x.hi, r[t]);
+            }
 }
 
 // Lane sums and maxima over 16 lanes, by rotations.
@@ -294,13 +357,17 @@ __device__ static inline void load_rows(const Column16 &c, int row0, int rows, i
 // A chunk's operands on their way to LDS: read into registers when the last chunk begins, written when it ends. (Loads
 // straight to LDS need no registers, but while one is under way the compiler has any use of any other load wait
 // for all of them.)
-template <int KP, int W>
+template <int KP, int W, int A_TERMS>
 struct Staged {
-    static constexpr int kThreads = W * kWave, kKeys = 2 * kC * KP * 2, kBytes = kKeys + (int)kXaBytes + (int)sizeof(RowCoef);
-    static constexpr int kOfKeys = kKeys / 16 / kThreads, kOfXa = (int)kXaBytes / 16 / kThreads;
-    static constexpr int kOfCoef = (int)sizeof(RowCoef) / 4 / kThreads;
-    static_assert(kThreads <= 512 && kOfCoef >= 1, "whole loads");
+    static constexpr int kThreads = W * kWave, kKeys = 2 * kC * KP * 2, kXa = (2 + A_TERMS) * kTriangle * 2;
+    static constexpr int kBytes = kKeys + kXa + (int)sizeof(RowCoef);
+    static constexpr int kOfKeys = kKeys / 16 / kThreads, kOfXa = kXa / 16 / kThreads;
+    static constexpr int kRest = (kXa - kOfXa * 16 * kThreads) / 8 / kThreads, kOfCoef = (int)sizeof(RowCoef) / 4 / kThreads;
+    static_assert(kOfXa * 16 * kThreads + kRest * 8 * kThreads == kXa && kOfCoef * 4 * kThreads == (int)sizeof(RowCoef) &&
+                  kOfKeys * 16 * kThreads == kKeys, "whole loads");
+    typedef float f2 __attribute__((ext_vector_type(2)));
     f4 keys[kOfKeys], xa[kOfXa];
+    f2 rest[kRest > 0 ? kRest : 1];
     float coef[kOfCoef];
 
     __device__ void load(const uint8_t *k, const uint8_t *x, const RowCoef *c) {
@@ -308,6 +375,8 @@ struct Staged {
         for (int i = 0; i < kOfKeys; ++i) keys[i] = *lane_at((const f4 *)k + i * kThreads, threadIdx.x);
 #pragma unroll
         for (int i = 0; i < kOfXa; ++i) xa[i] = *lane_at((const f4 *)x + i * kThreads, threadIdx.x);
+#pragma unroll
+        for (int i = 0; i < kRest; ++i) rest[i] = *lane_at((const f2 *)(x + kOfXa * 16 * kThreads) + i * kThreads, threadIdx.x);
 #pragma unroll
         for (int i = 0; i < kOfCoef; ++i) coef[i] = *lane_at((const float *)c + i * kThreads, threadIdx.x);
     }
@@ -317,7 +386,9 @@ struct Staged {
 #pragma unroll
         for (int i = 0; i < kOfXa; ++i) ((f4 *)(to + kKeys))[i * kThreads + threadIdx.x] = xa[i];
 #pragma unroll
-        for (int i = 0; i < kOfCoef; ++i) ((float *)(to + kKeys + kXaBytes))[i * kThreads + threadIdx.x] = coef[i];
+        for (int i = 0; i < kRest; ++i) ((f2 *)(to + kKeys + kOfXa * 16 * kThreads))[i * kThreads + threadIdx.x] = rest[i];
+#pragma unroll
+        for (int i = 0; i < kOfCoef; ++i) ((float *)(to + kKeys + kXa))[i * kThreads + threadIdx.x] = coef[i];
     }
 };
 

@@ -90,7 +90,7 @@ __device__ static inline HVec<8>::t row_chunk(const uint16_t *p, int left) {
 
 // The 64 rows of q or k as an image in LDS and in memory, and the rows' factors.
 template <int DT, int KP>
-__device__ static inline void image_rows(const Delta &a, const uint16_t *base, const int64_t (&st)[3], int b, int g,
+__device__ static __forceinline__ void image_rows(const Delta &a, const uint16_t *base, const int64_t (&st)[3], int b, int g,
                                          int row0, int live, uint16_t *lds, uint16_t *image, float *factor,
                                          float *factor_out, float *power_out) {
     constexpr int kLanes = KP / 8, kRows = kPrepThreads / kLanes;
@@ -128,9 +128,9 @@ __device__ static inline void image_rows(const Delta &a, const uint16_t *base, c
     }
 }
 
-// A 64x64 matrix in LDS as two terms in memory, each an image; returns the power of two taken out.
-__device__ static inline float image_square(const float *m, uint16_t *hi, uint16_t *lo, float *part) {
-    const int row = threadIdx.x / 4, c0 = threadIdx.x % 4 * 16;
+// A triangular 64x64 matrix in LDS as two terms in memory (or the first alone); returns the power of two taken out.
+__device__ static __forceinline__ float image_square(const float *m, uint16_t *hi, uint16_t *lo, float *part, int tid) {
+    const int row = tid / 4, c0 = tid % 4 * 16;
     f4 v[4];
     float big = 0.0f;
 #pragma unroll
@@ -140,17 +140,18 @@ __device__ static inline float image_square(const float *m, uint16_t *hi, uint16
         for (int j = 0; j < 4; ++j) big = __builtin_fmaxf(big, __builtin_fabsf(v[i][j]));
     }
     big = column_max(max16(big));
-    if (threadIdx.x % kWave == 0) part[threadIdx.x / kWave] = big;
+    if (tid % kWave == 0) part[tid / kWave] = big;
     lds_barrier();
     big = __builtin_fmaxf(__builtin_fmaxf(part[0], part[1]), __builtin_fmaxf(part[2], part[3]));
     const Power p = power_of(big);
+    if (c0 / 32 <= row / 32)
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const Split s = split(v[2 * i], v[2 * i + 1], p.inv);
-        const int at = image_at<64>(row, c0 / 8 + i);
-        *(h8 *)(hi + at) = s.hi;
-        *(h8 *)(lo + at) = s.lo;
-    }
+        for (int i = 0; i < 2; ++i) {
+            const Split s = split(v[2 * i], v[2 * i + 1], p.inv);
+            const int at = block_of(row / 32, c0 / 32) + block_at(row % 32, c0 % 32 / 8 + i);
+            *(h8 *)(hi + at) = s.hi;
+            if (lo) *(h8 *)(lo + at) = s.lo;
+        }
     return p.back;
 }
 
@@ -162,7 +163,7 @@ __device__ static inline f4 block_product(const float *l, int r0, int k0, f4 y, 
     for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[i], y[i], c, 0, 0, 0);
     return c;
 }
-__device__ static inline f4 block_at(const float *m, int r0, int c0, int lane) {
+__device__ static inline f4 square_at(const float *m, int r0, int c0, int lane) {
     f4 v;
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = m[(r0 + 4 * (lane >> 4) + i) * kLd + c0 + (lane & 15)];
@@ -175,35 +176,40 @@ __device__ static inline void block_to(float *m, int r0, int c0, f4 v, int lane)
 
 // X = (I + L)^-1 of a strictly lower triangular L: the diagonal blocks of 16 by substitution (a lane each
 // column), then twice the lower left quarter, -X2 L21 X1, on the fp32 matrix units. All of X is written.
-__device__ static inline void invert(const float *L, float *X, int wave, int lane) {
-    for (int i = threadIdx.x; i < kC * kC / 4; i += kPrepThreads) *(f4 *)(X + i / 16 * kLd + i % 16 * 4) = f4{};
+__device__ static __forceinline__ void invert(const float *L, float *X, int wave, int tid) {
+    const int lane = tid % kWave;
+    for (int i = tid; i < kC * kC / 4; i += kPrepThreads) *(f4 *)(X + i / 16 * kLd + i % 16 * 4) = f4{};
     lds_barrier();
     if (wave == 0) {
         const int d0 = 16 * (lane >> 4), c = lane & 15;
         float x[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            x[i] = i == c ? 1.0f : 0.0f;
+        for (int i = 0; i < 16; ++i) x[i] = i == c ? 1.0f : 0.0f;
 #pragma unroll
-            for (int j4 = 0; j4 < i; j4 += 4) {
-                const f4 l = *(const f4 *)(L + (d0 + i) * kLd + d0 + j4);
+        for (int j4 = 0; j4 < 16; j4 += 4) {  // a row that is done goes into all later ones at once
+            f4 l[16];
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (j4 + j < i) x[i] = __builtin_fmaf(-l[j], x[j4 + j], x[i]);
-            }
-            X[(d0 + i) * kLd + d0 + c] = x[i];
+            for (int i = 0; i < 16; ++i)
+                if (i > j4) l[i] = *(const f4 *)(L + (d0 + i) * kLd + d0 + j4);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (i > j4 + j) x[i] = __builtin_fmaf(-l[i][j], x[j4 + j], x[i]);
         }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) X[(d0 + i) * kLd + d0 + c] = x[i];
     }
     lds_barrier();
     if (wave < 2) {
         const int a = 32 * wave, b = a + 16;
-        const f4 y = block_product(L, b, a, block_at(X, a, a, lane), f4{}, lane);
+        const f4 y = block_product(L, b, a, square_at(X, a, a, lane), f4{}, lane);
         block_to(X, b, a, block_product(X, b, b, y, f4{}, lane), lane);
     }
     lds_barrier();
     if (wave < 2) {
         const int c = 16 * wave;
-        const f4 x0 = block_at(X, 0, c, lane), x1 = block_at(X, 16, c, lane);
+        const f4 x0 = square_at(X, 0, c, lane), x1 = square_at(X, 16, c, lane);
         f4 y2 = block_product(L, 32, 0, x0, f4{}, lane), y3 = block_product(L, 48, 0, x0, f4{}, lane);
         y2 = block_product(L, 32, 16, x1, y2, lane), y3 = block_product(L, 48, 16, x1, y3, lane);
         const f4 x2 = block_product(X, 32, 32, y2, f4{}, lane);
@@ -216,7 +222,7 @@ __device__ static inline void invert(const float *L, float *X, int wave, int lan
 }
 
 template <int DT, int KP>
-__global__ void __launch_bounds__(kPrepThreads) delta_prepare(Delta a, Records rec, int n0) {
+__global__ void __launch_bounds__(kPrepThreads, 3) delta_prepare(Delta a, Records rec, int n0, int a_terms) {
     constexpr int kImages = 2 * kC * KP * (int)sizeof(uint16_t), kSquares = 2 * kC * kLd * (int)sizeof(float);
     __shared__ __align__(16) uint8_t smem[kImages > kSquares ? kImages : kSquares];  // rows first, then L, X
     __shared__ float kr[kC], qr[kC], beta[kC], part[4];
@@ -255,6 +261,7 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prepare(Delta a, Records r
     float *P = (float *)smem, *X = P + kC * kLd;
     const int heads = a.H / a.G;
     for (int hh = 0; hh < heads; ++hh) {
+        const int tid = anew(threadIdx.x), lane = tid % kWave, m = lane & 15, grp = lane >> 4;
         const int h = g * heads + hh;
         const int64_t at = (int64_t)(b * a.H + h) * rec.chunks + n;
         RowCoef *coef = rec.coef + at;
@@ -298,10 +305,10 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prepare(Delta a, Records r
             }
         }
         lds_barrier();
-        const float sa = image_square(P, xa + 2 * kSquare, xa + 3 * kSquare, part);
+        const float sa = image_square(P, xa + 2 * kTriangle, a_terms > 1 ? xa + 3 * kTriangle : nullptr, part, tid);
         lds_barrier();
-        invert(X, P, wave, lane);
-        const float sx = image_square(P, xa, xa + kSquare, part);
+        invert(X, P, wave, tid);
+        const float sx = image_square(P, xa, xa + kTriangle, part, tid);
         if (wave == 0) {
             const float ek = exp2_f((float)mine), k1 = kr[lane];
             coef->p[lane] = ek * k1;
@@ -326,17 +333,20 @@ struct Walk {
     int blocks;                     // of columns, a head
 };
 
+// TERMS: those of what only the output is made of, A U and Q~ S0. Its 16 bits are the last rounding (2^-9 of a bf16
+// value), next to which one fp16 term of A, U and S0 (2^-12 each) does not count; fp16 outputs take two.
 // KEEP: the states and U are kept. (Two waves a SIMD would fit: with all of a SIMD's registers the compiler has the
 // products' results in accumulation registers and moves each of them.)
 template <int DT, int KP, int W, bool KEEP, bool WIDE>
 __global__ void __launch_bounds__(W *kWave, 2) delta_walk(Delta a, Records rec, Walk w) {
     constexpr int KT = KP / 16, KS = KP / 32;
-    typedef Staged<KP, W> Stage;
+    constexpr int TERMS = DT == MCCB_BF16 ? 1 : 2;
+    typedef Staged<KP, W, TERMS> Stage;
     constexpr int kBuf = Stage::kBytes, kKeys = Stage::kKeys;
     __shared__ __align__(16) uint8_t smem[2 * kBuf];
     const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int m = lane & 15, grp = lane >> 4;
-    const int lk_at = left_place<KP>(lane), tk_at = turned_place<KP>(lane), ls_at = left_place<64>(lane);
+    const int lk_at = left_place<KP>(lane), tk_at = turned_place<KP>(lane), ls_at = triangle_place(lane);
     const int id = same_die(blockIdx.x, gridDim.x);
     const int bh = id / w.blocks, b = bh / a.H, h = bh % a.H, g = h / (a.H / a.G);
     const int col = (id % w.blocks * W + wave) * 16 + m, VP = padded_v(a.V);
@@ -374,8 +384,8 @@ __global__ void __launch_bounds__(W *kWave, 2) delta_walk(Delta a, Records rec, 
     for (int n = w.n0; n < end; ++n) {
         const uint8_t *buf = smem + (n & 1) * kBuf;
         const uint16_t *kt = (const uint16_t *)buf, *qt = kt + kC * KP;
-        const uint16_t *xh = (const uint16_t *)(buf + kKeys), *xl = xh + kSquare, *ah = xl + kSquare, *al = ah + kSquare;
-        const RowCoef *coef = (const RowCoef *)(buf + kKeys + kXaBytes);
+        const uint16_t *xh = (const uint16_t *)(buf + kKeys), *xl = xh + kTriangle, *ah = xl + kTriangle, *al = ah + kTriangle;
+        const RowCoef *coef = (const RowCoef *)(buf + kKeys + Stage::kXa);
         fetch(n + 1 < end ? n + 1 : n);
         if (KEEP) {
             float *to = keep_s + (int64_t)n * KP * VP;
@@ -390,14 +400,16 @@ __global__ void __launch_bounds__(W *kWave, 2) delta_walk(Delta a, Records rec, 
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
             const Split sp = split(S[2 * s], S[2 * s + 1], ps.inv);
+            h8 lk[4], lq[4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) lk[t] = left<KP>(kt, lk_at, t, s), lq[t] = left<KP>(qt, lk_at, t, s);
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
-                const h8 lk = left<KP>(kt, lk_at, t, s), lq = left<KP>(qt, lk_at, t, s);
-                P[t] = mma(lk, sp.hi, P[t]);
-                O[t] = mma(lq, sp.hi, O[t]);
-                P[t] = mma(lk, sp.lo, P[t]);
-                O[t] = mma(lq, sp.lo, O[t]);
+                P[t] = mma(lk[t], sp.lo, P[t]);
+                if (TERMS > 1) O[t] = mma(lq[t], sp.lo, O[t]);
             }
+#pragma unroll
+            for (int t = 0; t < 4; ++t) P[t] = mma(lk[t], sp.hi, P[t]), O[t] = mma(lq[t], sp.hi, O[t]);
         }
         // beta (V - p K~ S0)
         f4 R[4];
@@ -409,56 +421,36 @@ __global__ void __launch_bounds__(W *kWave, 2) delta_walk(Delta a, Records rec, 
             for (int i = 0; i < 4; ++i) R[t][i] = cb[i] * __builtin_fmaf(-cp[i], P[t][i], to_f32<DT>(v[t][i]));
         }
         load_rows<WIDE>(vcol, (n + 1) * kC, length - (n + 1) * kC, lane, v);
-        // U = X R
+        // U = X R, without the powers of two in `up`
         f4 U[4];
+        float up;
         {
             const Power p = column_power(R, lane);
-            const Split s0 = split(R[0], R[1], p.inv), s1 = split(R[2], R[3], p.inv);
-            const float up = p.back * coef->x;
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                f4 u = {};
-#pragma unroll
-                for (int s = 0; s <= t / 2; ++s) {
-                    const h8 lh = left<64>(xh, ls_at, t, s), ll = left<64>(xl, ls_at, t, s);
-                    const Split &sp = s ? s1 : s0;
-                    u = mma(ll, sp.hi, u);
-                    u = mma(lh, sp.lo, u);
-                    u = mma(lh, sp.hi, u);
-                }
-                U[t] = u * up;
-            }
+            up = p.back * coef->x;
+            triangle_times<false, 2>(xh, xl, ls_at, split(R[0], R[1], p.inv), split(R[2], R[3], p.inv), U);
         }
         if (KEEP) {
             float *to = keep_u + (int64_t)n * kC * VP;
 #pragma unroll
             for (int t = 0; t < 4; ++t)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) to[(row_of(t, 0) + i) * VP] = U[t][i];
+                for (int i = 0; i < 4; ++i) to[(row_of(t, 0) + i) * VP] = up * U[t][i];
         }
         // out = q Q~ S0 + A U
         {
             const Power p = column_power(U, lane);
-            const Split s0 = split(U[0], U[1], p.inv), s1 = split(U[2], U[3], p.inv);
-            const float up = p.back * coef->a;
+            f4 AU[4];
+            triangle_times<false, TERMS>(ah, al, ls_at, split(U[0], U[1], p.inv), split(U[2], U[3], p.inv), AU);
+            const float back = p.back * up * coef->a;
             const int left_rows = a.S - n * kC;
             const Buffer to = buffer_of(w.out + (int64_t)n * kC * (out_row / 2) + (int64_t)b * a.H * a.V,
                                         (left_rows < kC ? left_rows - 1 : kC - 1) * out_row + 2u * a.H * a.V);
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
-                f4 o = {};
-#pragma unroll
-                for (int s = 0; s <= t / 2; ++s) {
-                    const h8 lh = left<64>(ah, ls_at, t, s), ll = left<64>(al, ls_at, t, s);
-                    const Split &sp = s ? s1 : s0;
-                    o = mma(ll, sp.hi, o);
-                    o = mma(lh, sp.lo, o);
-                    o = mma(lh, sp.hi, o);
-                }
                 const f4 cq = *(const f4 *)(coef->q + row_of(t, 4 * grp)) * ps.back;
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    __builtin_amdgcn_raw_buffer_store_b16(from_f32<DT>(__builtin_fmaf(o[i], up, cq[i] * O[t][i])), to,
+                    __builtin_amdgcn_raw_buffer_store_b16(from_f32<DT>(__builtin_fmaf(AU[t][i], back, cq[i] * O[t][i])), to,
                                                           out_at + (row_of(t, 0) + i) * out_row, 0, 0);
             }
         }
@@ -468,16 +460,22 @@ __global__ void __launch_bounds__(W *kWave, 2) delta_walk(Delta a, Records rec, 
             for (int t = 0; t < 4; ++t) U[t] *= *(const f4 *)(coef->u + row_of(t, 4 * grp));
             const Power p = column_power(U, lane);
             const Split s0 = split(U[0], U[1], p.inv), s1 = split(U[2], U[3], p.inv);
-            const float whole = coef->whole;
+            const float whole = coef->whole, back = p.back * up;
 #pragma unroll
-            for (int t = 0; t < KT; ++t) {
-                const h8 l0 = left_turned<KP>(kt, tk_at, t, 0), l1 = left_turned<KP>(kt, tk_at, t, 1);
-                f4 d = mma(l0, s0.lo, f4{});
-                d = mma(l1, s1.lo, d);
-                d = mma(l0, s0.hi, d);
-                d = mma(l1, s1.hi, d);
+            for (int t = 0; t < KT; t += 4) {
+                f4 d[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) S[t][i] = __builtin_fmaf(whole, S[t][i], p.back * d[i]);
+                for (int i = 0; i < 4; ++i) d[i] = mma(left_turned<KP>(kt, tk_at, t + i, 0), s0.lo, f4{});
+#pragma unroll
+                for (int i = 0; i < 4; ++i) d[i] = mma(left_turned<KP>(kt, tk_at, t + i, 1), s1.lo, d[i]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) d[i] = mma(left_turned<KP>(kt, tk_at, t + i, 0), s0.hi, d[i]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) d[i] = mma(left_turned<KP>(kt, tk_at, t + i, 1), s1.hi, d[i]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) S[t + i][j] = __builtin_fmaf(whole, S[t + i][j], back * d[i][j]);
             }
         }
         stage.store(smem + (~n & 1) * kBuf);
@@ -605,9 +603,9 @@ __global__ void __launch_bounds__(kStepThreads) delta_one(Delta a, float *state,
 // Host side.
 // ---------------------------------------------------------------------------------------------
 template <int DT, int KP>
-int prepare(const Delta &d, const Records &rec, int n0, int n1, hipStream_t st) {
+int prepare(const Delta &d, const Records &rec, int n0, int n1, bool keep, hipStream_t st) {
     hipLaunchKernelGGL((delta_prepare<DT, KP>), dim3((unsigned)(n1 - n0), (unsigned)(d.B * d.G)), dim3(kPrepThreads),
-                       0, st, d, rec, n0);
+                       0, st, d, rec, n0, keep || DT == MCCB_FP16 ? 2 : 1);
     return launched();
 }
 template <int DT, int KP, bool KEEP>
@@ -622,7 +620,7 @@ int walk(const Delta &d, const Records &rec, Walk w, hipStream_t st) {
 template <int DT, int KP>
 int all_chunks(const Delta &d, const Records &rec, const Walk &w, hipStream_t st) {
     if (w.n1 > w.n0) {
-        const int rc = prepare<DT, KP>(d, rec, w.n0, w.n1, st);
+        const int rc = prepare<DT, KP>(d, rec, w.n0, w.n1, w.states != nullptr, st);
         if (rc != MCCB_OK) return rc;
     }
     return w.states ? walk<DT, KP, true>(d, rec, w, st) : walk<DT, KP, false>(d, rec, w, st);
