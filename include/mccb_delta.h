@@ -40,7 +40,8 @@ extern "C" {
  *
  * lengths: optional int64 [B] on the device, clamped to [0, S]; NULL = all S. Rows at or past a sequence's
  * length are not computed with, whatever they hold: outputs and gradients there are zero, and states are
- * those after the last row before it. A length of zero hands the initial state on.
+ * those after the last row before it. A length of zero hands the initial state on. A live row that is not
+ * finite makes NaN of what comes after it in its sequence, and of up to 63 rows before it (its chunk's).
  *
  * S in [0, 2^28), B H in [1, 65535], G a divisor of H, K in 1..128, V in 1..256, scale finite.
  * -----------------------------------------------------------------------------------------------*/

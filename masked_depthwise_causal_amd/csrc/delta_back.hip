@@ -407,9 +407,10 @@ __global__ void __launch_bounds__(KP / 16 * kWave) delta_grads(Delta a, Records 
                         z = mma(luh, sg[s].lo, z);
                     }
                     const int r = row_of(t, 4 * grp);
-                    const f4 fo = *(const f4 *)(po + r) * *(const f4 *)(coef + 2 * kC + r) * ps.back;
-                    const f4 fy = *(const f4 *)(py + r) * *(const f4 *)(coef + r) * *(const f4 *)(coef + kC + r) * ps.back;
-                    const f4 fu = *(const f4 *)(pu + r) * *(const f4 *)(coef + 3 * kC + r) * pg.back;
+                    // sizes that cancel first: gradients may be as small as states are large
+                    const f4 fo = *(const f4 *)(po + r) * ps.back * *(const f4 *)(coef + 2 * kC + r);
+                    const f4 fy = *(const f4 *)(py + r) * ps.back * *(const f4 *)(coef + r) * *(const f4 *)(coef + kC + r);
+                    const f4 fu = *(const f4 *)(pu + r) * pg.back * *(const f4 *)(coef + 3 * kC + r);
                     const f4 kf = anew(kd[t]), qf = anew(qd[t]);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {

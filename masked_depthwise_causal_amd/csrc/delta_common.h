@@ -13,9 +13,9 @@
 //
 // Numbers. Products run on the matrix units in fp16, in as many terms as they need to come out as in fp32:
 // rows of q and k are exact in one (with a power of two a row taken out, bf16's 8 bits fit wherever fp16 is
-// normal; smaller values lose less than 2^-25 of the row's largest); everything that is computed is split
+// normal; values below 2^-28 of the row's largest lose 2^-40 of it); everything that is computed is split
 // in two, hi + lo, 22 bits (a power of two a column, or a matrix, taken out, so that no value's size
-// matters; what is lost is below 2^-22 of a value or 2^-25 of the largest). An exact operand with a split
+// matters; what is lost is below 2^-22 of a value or 2^-40 of the largest). An exact operand with a split
 // one takes two products, two split ones three (lo lo is below 2^-22). On this card that is 8 and 5 times
 // the rate of the fp32 matrix instructions; in bf16 terms it would take three and six products.
 #pragma once
@@ -181,17 +181,19 @@ __device__ static inline Split split(const f4 &a, const f4 &b, float inv) {
     return s;
 }
 
-// The power of two at or below m (0 for 0 and subnormal values), and its inverse. Infinities and the largest
-// binade keep 2^126, and stay what they are; NaN is not counted by the maximum that comes in.
+// What brings the largest value m to 2^14..2^15, a power of two, and its inverse. (So high, since the others' last bits
+// are then fp16's smallest, 2^-24: a column of Y may hold rows whose sizes are a chunk's whole decay apart, and the small
+// ones count, where their factors are the large ones.) From 2^-112 on down m counts as 2^-112; infinities stay what
+// they are; NaN is not counted by the maximum that comes in.
 struct Power {
     float back, inv;
 };
 __device__ static inline Power power_of(float m) {
-    uint32_t e = __float_as_uint(m) & 0x7f800000u;
-    e = e > (253u << 23) ? 253u << 23 : e;
+    uint32_t e = __float_as_uint(m) >> 23;
+    e = e < 15 ? 15 : e > 254 ? 254 : e;
     Power p;
-    p.back = __uint_as_float(e);
-    p.inv = __uint_as_float((254u << 23) - e);
+    p.back = __uint_as_float((e - 14) << 23);
+    p.inv = __uint_as_float((268 - e) << 23);
     return p;
 }
 

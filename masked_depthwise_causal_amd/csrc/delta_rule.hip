@@ -101,10 +101,11 @@ __device__ static __forceinline__ void image_rows(const Delta &a, const uint16_t
         float v[8], m = 0.0f, ss = 0.0f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = to_f32<DT>(raw[i]), m = __builtin_fmaxf(m, __builtin_fabsf(v[i]));
-        // the row's largest value is brought to 1..2
+        // the row's largest value is brought to 2^14..2^15
 #pragma unroll
         for (int i = 1; i < kLanes; i *= 2) m = __builtin_fmaxf(m, __shfl_xor(m, i));
-        int e = m > 0.0f ? ((__float_as_uint(m) >> 23) & 255) - 127 : 0;
+        // (a row of zeros, whose factor would be 1000 next to the other rows' 1, has 2^-10 taken out)
+        int e = m > 0.0f ? ((__float_as_uint(m) >> 23) & 255) - 127 - 14 : -10;
         e = e < -100 ? -100 : e > 126 ? 126 : e;
         h8 h;
 #pragma unroll
