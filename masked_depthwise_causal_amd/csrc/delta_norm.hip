@@ -38,9 +38,15 @@ struct Norm {
 // ---------------------------------------------------------------------------------------------
 typedef HVec<kVec>::t vec8;
 
-__device__ static inline vec8 load8(const uint16_t *p, int n) {
+// p is a group's column c, of which n are left. A last vector of fewer is read as the last 8 values and moved down.
+__device__ static inline vec8 load8(const uint16_t *p, int n, int c) {
     if (n >= kVec) return *(const vec8 *)p;
     vec8 v = {};
+    if (n <= 0) return v;
+    if (c >= kVec) {
+        const auto last = __builtin_bit_cast(unsigned __int128, *(const vec8 *)(p - (kVec - n)));
+        return __builtin_bit_cast(vec8, last >> (16 * (kVec - n)));
+    }
 #pragma unroll
     for (int i = 0; i < kVec; ++i)
         if (i < n) v[i] = p[i];
@@ -119,8 +125,8 @@ __global__ void __launch_bounds__(T > kWave ? kMaxTeam : kBlock)
     for (int e = 0; e < E; ++e) {
         const int c = kVec * (p.lane + e * team);
         have[e] = n.D - c;
-        w[e] = load8(n.w + (int64_t)p.g * n.weight_step + c, have[e]);
-        s[e] = n.scale ? load8(n.scale + first + c, have[e]) : vec8{};
+        w[e] = load8(n.w + (int64_t)p.g * n.weight_step + c, have[e], c);
+        s[e] = n.scale ? load8(n.scale + first + c, have[e], c) : vec8{};
     }
     const int64_t end = min(n.R, (blockIdx.y + 1) * t.strip);
     int turn = 0;
@@ -128,10 +134,11 @@ __global__ void __launch_bounds__(T > kWave ? kMaxTeam : kBlock)
         vec8 x[E], res[E], z[E];
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-            const int64_t c = first + kVec * (p.lane + e * team);
-            x[e] = load8(n.x + r * n.x_ld + c, have[e]);
-            res[e] = n.residual ? load8(n.residual + r * n.residual_ld + c, have[e]) : vec8{};
-            z[e] = POST && n.z ? load8(n.z + r * n.z_ld + c, have[e]) : vec8{};
+            const int col = kVec * (p.lane + e * team);
+            const int64_t c = first + col;
+            x[e] = load8(n.x + r * n.x_ld + c, have[e], col);
+            res[e] = n.residual ? load8(n.residual + r * n.residual_ld + c, have[e], col) : vec8{};
+            z[e] = POST && n.z ? load8(n.z + r * n.z_ld + c, have[e], col) : vec8{};
         }
         float a = 0.0f, unused = 0.0f;
         float v[E][kVec];
@@ -175,15 +182,43 @@ struct NormGrads {
     const uint16_t *g, *gsum;       // gsum: prenorm's gradient into the sum
     int64_t g_ld, gsum_ld;
     uint16_t *gx, *gres, *gz;       // gres: prenorm's, where it is not gx
-    float *pw, *ps;                 // [partial rows][H]: sums over a team's rows, of weight and scale
+    float *pw, *ps;                 // sums over a block's rows, of weight and scale
 };
 
+// A row's values as they were read.
+template <int E>
+struct Row {
+    vec8 x[E], g[E], other[E], gsum[E];  // other: residual, or the gate
+};
+template <bool POST, int E>
+__device__ static inline void load_row(const Norm &n, const NormGrads &q, int64_t r, int64_t first, int lane, int team,
+                                       const int (&have)[E], Row<E> &row) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        const int col = kVec * (lane + e * team);
+        const int64_t c = first + col;
+        row.x[e] = load8(n.x + r * n.x_ld + c, have[e], col);
+        row.g[e] = load8(q.g + r * q.g_ld + c, have[e], col);
+        row.other[e] = row.gsum[e] = vec8{};
+        if (POST) {
+            if (n.z) row.other[e] = load8(n.z + r * n.z_ld + c, have[e], col);
+        } else {
+            if (n.residual) row.other[e] = load8(n.residual + r * n.residual_ld + c, have[e], col);
+            if (q.gsum) row.gsum[e] = load8(q.gsum + r * q.gsum_ld + c, have[e], col);
+        }
+    }
+}
+
+// The next row is on its way while one is worked on, where a lane has one vector; with two, in blocks that leave a
+// lane 128 registers, there is no room for it, nor for the weights, which are read again with each row.
 template <int DT, bool POST, int T, int E>
-__global__ void __launch_bounds__(T > kWave ? kMaxTeam : kBlock)
+__global__ void __launch_bounds__(T > kWave ? kMaxTeam : kBlock, T == 16 && E == 1 ? 4 : 1)
     norm_backward(Norm n, Teams t, NormGrads q) {
+    constexpr int kTeams = T > kWave ? 1 : kBlock / T;
+    constexpr bool kAhead = T <= kWave || E == 1;
     __shared__ float part[2][2 * kMaxTeam / kWave];
+    __shared__ float meet[kTeams > 1 ? kTeams : 1][kTeams > 1 ? T * E * kVec : 1];
     const Place p = place<T>(n, t);
-    if (T <= kWave && !p.on) return;
     const int team = T > kWave ? blockDim.x : T;
     const int64_t H = (int64_t)n.D * n.G, first = (int64_t)p.g * n.D;
     vec8 w[E], s[E];
@@ -192,39 +227,42 @@ __global__ void __launch_bounds__(T > kWave ? kMaxTeam : kBlock)
 #pragma unroll
     for (int e = 0; e < E; ++e) {
         const int c = kVec * (p.lane + e * team);
-        have[e] = n.D - c;
-        w[e] = load8(n.w + (int64_t)p.g * n.weight_step + c, have[e]);
-        s[e] = n.scale ? load8(n.scale + first + c, have[e]) : vec8{};
+        have[e] = p.on ? n.D - c : 0;
+        w[e] = load8(n.w + (int64_t)p.g * n.weight_step + c, have[e], c);
+        s[e] = n.scale ? load8(n.scale + first + c, have[e], c) : vec8{};
 #pragma unroll
         for (int i = 0; i < kVec; ++i) sw[e][i] = ss[e][i] = 0.0f;
     }
-    const int64_t end = min(n.R, (blockIdx.y + 1) * t.strip);
+    const int64_t end = p.on ? min(n.R, (blockIdx.y + 1) * t.strip) : 0;
     int turn = 0;
-    for (int64_t r = blockIdx.y * t.strip + p.slot; r < end; r += t.slots, turn ^= 1) {
-        vec8 x[E], g[E], other[E], gsum[E];  // other: residual, or the gate
+    Row<E> next;
+    int64_t r = blockIdx.y * t.strip + p.slot;
+    if (kAhead && r < end) load_row<POST>(n, q, r, first, p.lane, team, have, next);
+    for (; r < end; r += t.slots, turn ^= 1) {
+        Row<E> row;
+        if (kAhead) {
+            row = next;
+            if (r + t.slots < end) load_row<POST>(n, q, r + t.slots, first, p.lane, team, have, next);
+        } else {
+            load_row<POST>(n, q, r, first, p.lane, team, have, row);
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const int64_t c = first + kVec * (p.lane + e * team);
-            x[e] = load8(n.x + r * n.x_ld + c, have[e]);
-            g[e] = load8(q.g + r * q.g_ld + c, have[e]);
-            other[e] = gsum[e] = vec8{};
-            if (POST) {
-                if (n.z) other[e] = load8(n.z + r * n.z_ld + c, have[e]);
-            } else {
-                if (n.residual) other[e] = load8(n.residual + r * n.residual_ld + c, have[e]);
-                if (q.gsum) gsum[e] = load8(q.gsum + r * q.gsum_ld + c, have[e]);
+            for (int e = 0; e < E; ++e) {
+                const int c = kVec * (p.lane + e * team);
+                w[e] = load8(n.w + (int64_t)p.g * n.weight_step + c, have[e], c);
+                if (n.scale) s[e] = load8(n.scale + first + c, have[e], c);
             }
         }
-        // what is normalized, and the gradient at the normalized value
+        // what is normalized, and the gradient at the normalized value; the gate's logistic function is kept
+        float sig[POST ? E : 1][kVec];
         auto at = [&](int e, int i, float &v, float &gn) {
-            v = to_f32<DT>(x[e][i]);
-            gn = to_f32<DT>(g[e][i]) * to_f32<DT>(w[e][i]);
+            v = to_f32<DT>(row.x[e][i]);
+            gn = to_f32<DT>(row.g[e][i]) * to_f32<DT>(w[e][i]);
             if (POST) {
                 if (n.scale) gn *= to_f32<DT>(s[e][i]);
-                if (n.z) gn *= silu_f(to_f32<DT>(other[e][i]));
+                if (n.z) gn *= to_f32<DT>(row.other[e][i]) * sig[e][i];
             } else {
                 if (n.scale) v *= to_f32<DT>(s[e][i]);
-                if (n.residual) v += to_f32<DT>(other[e][i]);
+                if (n.residual) v += to_f32<DT>(row.other[e][i]);
             }
         };
         float a = 0.0f, b = 0.0f;
@@ -233,6 +271,7 @@ __global__ void __launch_bounds__(T > kWave ? kMaxTeam : kBlock)
 #pragma unroll
             for (int i = 0; i < kVec; ++i) {
                 float v, gn;
+                if (POST && n.z) sig[e][i] = sigmoid_f(to_f32<DT>(row.other[e][i]));
                 at(e, i, v, gn);
                 a = __builtin_fmaf(v, v, a);
                 b = __builtin_fmaf(v, gn, b);
@@ -250,18 +289,19 @@ __global__ void __launch_bounds__(T > kWave ? kMaxTeam : kBlock)
                 at(e, i, v, gn);
                 const float nv = v * rstd;
                 float gr = rstd * __builtin_fmaf(-nv, mean, gn);
-                const float gv = to_f32<DT>(g[e][i]);
+                const float gv = to_f32<DT>(row.g[e][i]);
                 if (POST) {
                     const float wv = to_f32<DT>(w[e][i]), sv = n.scale ? to_f32<DT>(s[e][i]) : 1.0f;
-                    const float zv = to_f32<DT>(other[e][i]), gate = n.z ? silu_f(zv) : 1.0f;
+                    const float zv = to_f32<DT>(row.other[e][i]), gate = n.z ? zv * sig[e][i] : 1.0f;
                     const float gy = gv * nv;  // the gradient of every factor behind the norm, save itself
                     sw[e][i] = __builtin_fmaf(gy * sv, gate, sw[e][i]);
                     ss[e][i] = __builtin_fmaf(gy * wv, gate, ss[e][i]);
-                    oz[i] = from_f32<DT>(gy * sv * wv * silu_slope_f(zv));
+                    if (n.z)
+                        oz[i] = from_f32<DT>(gy * sv * wv * sig[e][i] * __builtin_fmaf(bounded(zv), 1.0f - sig[e][i], 1.0f));
                 } else {
                     sw[e][i] = __builtin_fmaf(gv, nv, sw[e][i]);
-                    if (q.gsum) gr += to_f32<DT>(gsum[e][i]);
-                    ss[e][i] = __builtin_fmaf(gr, to_f32<DT>(x[e][i]), ss[e][i]);
+                    if (q.gsum) gr += to_f32<DT>(row.gsum[e][i]);
+                    ss[e][i] = __builtin_fmaf(gr, to_f32<DT>(row.x[e][i]), ss[e][i]);
                     ores[i] = from_f32<DT>(gr);
                     if (n.scale) gr *= to_f32<DT>(s[e][i]);
                 }
@@ -274,16 +314,37 @@ __global__ void __launch_bounds__(T > kWave ? kMaxTeam : kBlock)
             }
         }
     }
-    // a block's slots are partial rows of their own
-    const int64_t at = ((int64_t)blockIdx.y * t.slots + p.slot) * H + first;
+    // A block's sums are one partial row: its slots', and where all groups have one weight, the groups' too.
+    auto meeting = [&](float (&v)[E][kVec], bool all) {
+        if constexpr (kTeams > 1) {
+            const int mine = threadIdx.x / T;
+            lds_barrier();
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+#pragma unroll
+                for (int i = 0; i < kVec; ++i) meet[mine][(e * kVec + i) * T + p.lane] = v[e][i];
+            lds_barrier();
+            const int step = all ? 1 : t.groups, teams = t.groups * t.slots;
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+#pragma unroll
+                for (int i = 0; i < kVec; ++i)
+                    for (int k = mine + step; k < teams; k += step) v[e][i] += meet[k][(e * kVec + i) * T + p.lane];
+        }
+    };
+    const bool shared = n.weight_step == 0 && n.G > 1;
+    meeting(sw, shared);
+    if (q.ps) meeting(ss, false);
+    const int64_t row_w = shared ? ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * n.D : blockIdx.y * H + first;
+    const bool writes = p.on && p.slot == 0, writes_w = shared ? threadIdx.x / (T > kWave ? kMaxTeam : T) == 0 : writes;
 #pragma unroll
     for (int e = 0; e < E; ++e)
 #pragma unroll
         for (int i = 0; i < kVec; ++i)
             if (i < have[e]) {
                 const int c = kVec * (p.lane + e * team) + i;
-                q.pw[at + c] = sw[e][i];
-                if (q.ps) q.ps[at + c] = ss[e][i];
+                if (writes_w) q.pw[row_w + c] = sw[e][i];
+                if (q.ps && writes) q.ps[blockIdx.y * H + first + c] = ss[e][i];
             }
 }
 
@@ -316,21 +377,22 @@ __global__ void __launch_bounds__(kWave *kSumSlots)
 // Host side.
 // ---------------------------------------------------------------------------------------------
 // A team is 16 lanes up to 256 values, a wave up to 1024, and above the smallest block whose lanes
-// have two vectors each at most; one each where there are few rows, since then a row's latency is
-// what counts and not the lanes that a reduction's barrier holds up.
+// have two vectors each at most; `one`: one each, as far as that goes, as the gradients have it (registers), and
+// where there are few rows, since then a row's latency is what counts and not the lanes that a reduction's barrier
+// holds up.
 struct Shape {
     int team, per;                  // lanes (16, 64, or a block's), vectors of a lane
     Teams t;
     unsigned gx, gy, threads;
 };
-Shape shape_of(const mccb_norm_t *a, int64_t blocks_wanted, int64_t least_rows) {
+Shape shape_of(const mccb_norm_t *a, bool one, int64_t blocks_wanted, int64_t least_rows) {
     Shape s;
     const int64_t D = a->H / a->groups, vecs = (D + kVec - 1) / kVec;
     const bool few = a->R * a->groups <= 1024;
     if (vecs <= 32) s.team = 16, s.per = vecs <= 16 ? 1 : 2;
     else if (vecs <= 128) s.team = kWave, s.per = vecs <= 64 ? 1 : 2;
     else {
-        s.per = few && vecs <= kMaxTeam ? 1 : 2;
+        s.per = (few || one) && vecs <= kMaxTeam ? 1 : 2;
         const int64_t lanes = (vecs + s.per - 1) / s.per;
         s.team = (int)((lanes + kWave - 1) / kWave * kWave);
     }
@@ -351,8 +413,8 @@ Shape shape_of(const mccb_norm_t *a, int64_t blocks_wanted, int64_t least_rows) 
     s.gy = (unsigned)(a->R > 0 ? (a->R + s.t.strip - 1) / s.t.strip : 0);
     return s;
 }
-Shape forward_shape(const mccb_norm_t *a) { return shape_of(a, 4096, 1); }
-Shape backward_shape(const mccb_norm_t *a) { return shape_of(a, 1024, 8); }
+Shape forward_shape(const mccb_norm_t *a) { return shape_of(a, false, 4096, 1); }
+Shape backward_shape(const mccb_norm_t *a) { return shape_of(a, true, 1024, 4); }
 
 Norm norm_of(const mccb_norm_t *a) {
     Norm n{};
@@ -441,14 +503,19 @@ int forward(const mccb_norm_t *a, void *out, void *sum, void *stream) {
                       : launch_forward<POST, kMaxTeam, 2>(a, s, po, pt, st);
 }
 
-uint64_t partial_rows(const Shape &s) { return (uint64_t)s.gy * (uint64_t)s.t.slots; }
+// Floats of the partial rows: of a shared weight one a block, else one a strip.
+bool one_weight(const mccb_norm_t *a) { return a->weight_shared && a->groups > 1; }
+uint64_t partial_w(const mccb_norm_t *a, const Shape &s) {
+    return one_weight(a) ? (uint64_t)s.gx * s.gy * (uint64_t)(a->H / a->groups) : (uint64_t)s.gy * (uint64_t)a->H;
+}
 
 template <bool POST>
 int backward_size(const mccb_norm_t *a, uint64_t *size) {
     if (!size) return MCCB_ERR_PARAM_NULLPTR;
     const int rc = check_norm(a, POST);
     if (rc != MCCB_OK) return rc;
-    *size = partial_rows(backward_shape(a)) * (uint64_t)a->H * sizeof(float) * (a->scale ? 2 : 1);
+    const Shape s = backward_shape(a);
+    *size = (partial_w(a, s) + (a->scale ? (uint64_t)s.gy * (uint64_t)a->H : 0)) * sizeof(float);
     return MCCB_OK;
 }
 
@@ -486,9 +553,8 @@ int backward(const mccb_norm_t *a, NormGrads q, void *gw, void *gscale, void *ws
 
     const Shape s = backward_shape(a);
     const hipStream_t st = (hipStream_t)stream;
-    const int64_t rows_p = (int64_t)partial_rows(s);
     q.pw = (float *)ws;
-    q.ps = a->scale ? q.pw + rows_p * a->H : nullptr;
+    q.ps = a->scale ? q.pw + partial_w(a, s) : nullptr;
     if (a->R > 0) {
         if (s.team == 16)
             rc = s.per == 1 ? launch_backward<POST, 16, 1>(a, s, q, st) : launch_backward<POST, 16, 2>(a, s, q, st);
@@ -499,8 +565,7 @@ int backward(const mccb_norm_t *a, NormGrads q, void *gw, void *gscale, void *ws
                             : launch_backward<POST, kMaxTeam, 2>(a, s, q, st);
         if (rc != MCCB_OK) return rc;
     }
-    // a weight that groups share: their columns' sums are partial rows too
-    const int64_t rows_w = a->weight_shared ? rows_p * a->groups : rows_p;
+    const int64_t rows_w = (int64_t)s.gy * (one_weight(a) ? s.gx : 1), rows_p = s.gy;
     const int64_t width_s = a->scale ? a->H : 0;
     const dim3 grid((unsigned)((n_weight + kWave - 1) / kWave + (width_s + kWave - 1) / kWave));
     const dim3 block(kWave * kSumSlots);
