@@ -347,9 +347,7 @@ __global__ void __launch_bounds__(KP / 16 * kWave) delta_grads(Delta a, Records 
                     my = largest(y[2 * j], y[2 * j + 1], my);
                 }
                 auto row_power = [](float x) {
-#pragma unroll
-                    for (int i = 1; i < kPer; i *= 2) x = __builtin_fmaxf(x, __shfl_xor(x, i));
-                    return power_of(x);
+                    return power_of(max_over<kPer>(x));
                 };
                 const Power ro = row_power(mo), ru = row_power(mu), ry = row_power(my);
                 lds_barrier();  // the last block's, or head's, operands have been read
@@ -451,11 +449,9 @@ __global__ void __launch_bounds__(KP / 16 * kWave) delta_grads(Delta a, Records 
         // sums over a row's columns, and of gS1.S0
         lane = anew(threadIdx.x % kWave), m = lane & 15, grp = lane >> 4, kcol = 16 * wave + m;
         lk_at = left_place<KP>(lane);
-#pragma unroll
-        for (int i = 1; i < kPer; i *= 2) dot_u += __shfl_xor(dot_u, i);
+        dot_u = sum_over<kPer>(dot_u);
         if (threadIdx.x % kPer == 0) yu[threadIdx.x / kPer] = dot_u;
-        s0s1 = sum16(s0s1);
-        s0s1 += __shfl_xor(s0s1, 16), s0s1 += __shfl_xor(s0s1, 32);
+        s0s1 = column_sum(sum16(s0s1));
         if (lane == 0) dots[wave] = (double)s0s1;
         // Z, W and the sums of E
         float mz = 0.0f, mw = 0.0f;
@@ -487,14 +483,12 @@ __global__ void __launch_bounds__(KP / 16 * kWave) delta_grads(Delta a, Records 
                     mz = __builtin_fmaxf(mz, __builtin_fabsf(da[j][i]));
                     mw = __builtin_fmaxf(mw, __builtin_fabsf(dl[j][i]));
                 }
-                ec += __shfl_xor(ec, 16);
-                ec += __shfl_xor(ec, 32);
+                ec = column_sum(ec);
                 if (grp == 0) ecol[rt][c] = ec;
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-#pragma unroll
-                for (int o = 1; o < 16; o *= 2) er_[i] += __shfl_xor(er_[i], o);
+                er_[i] = sum_over<16>(er_[i]);
                 if (m == 0) erow[wave % kSide][r + i] = er_[i];
             }
         }
@@ -569,14 +563,9 @@ __global__ void __launch_bounds__(KP / 16 * kWave) delta_grads(Delta a, Records 
             double s = f - e - (ecol[0][r] + ecol[1][r] + ecol[2][r] + ecol[3][r]);
 #pragma unroll
             for (int i = 0; i < kSide; ++i) s += erow[i][r];
-#pragma unroll
-            for (int o = 32; o; o /= 2) e += __shfl_xor(e, o);
-            e += (double)whole * s0;
-#pragma unroll
-            for (int o = 1; o < kC; o *= 2) {
-                const double up = __shfl_down(s, o);
-                if (lane + o < kC) s += up;
-            }
+            e = last_lane(sum_up(e)) + (double)whole * s0;
+            const double up = sum_up(s);
+            s += last_lane(up) - up;
             const double glog = s + e;  // of log a
             double pa = 0.0, pb = 0.0;
             if (r < live) {
@@ -592,8 +581,7 @@ __global__ void __launch_bounds__(KP / 16 * kWave) delta_grads(Delta a, Records 
                 w.gdt[to] = from_f32<DT>((float)pb);
                 w.gb[to] = r < live ? from_f32<DT>((1.0f - beta) * yu[r]) : 0;
             }
-#pragma unroll
-            for (int o = 32; o; o /= 2) pa += __shfl_xor(pa, o), pb += __shfl_xor(pb, o);
+            pa = last_lane(sum_up(pa)), pb = last_lane(sum_up(pb));
             if (lane == 0) {
                 const int64_t to = ((int64_t)n * a.B + b) * a.H + h;
                 w.part[to] = pa, w.part[(int64_t)w.chunks * a.B * a.H + to] = pb;

@@ -209,13 +209,39 @@ __device__ static inline Power turned_sign(Power p, int lane) {
     return p;
 }
 
-// The largest magnitude over the four lanes that hold a column.
-__device__ static inline float column_max(float m) {
-    const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(m), __float_as_uint(m), false, false);
-    m = __builtin_fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
-    const auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(m), __float_as_uint(m), false, false);
-    return __builtin_fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+// Over the four lanes that hold a column, 16 apart: the largest value, and the sum.
+struct Pair {
+    uint32_t a, b;
+};
+template <int LANES>
+__device__ static inline Pair swapped(uint32_t v) {
+    if constexpr (LANES == 32) {
+        const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+        return {r[0], r[1]};
+    } else {
+        const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+        return {r[0], r[1]};
+    }
 }
+__device__ static inline float column_max(float m) {
+    Pair p = swapped<32>(__float_as_uint(m));
+    m = __builtin_fmaxf(__uint_as_float(p.a), __uint_as_float(p.b));
+    p = swapped<16>(__float_as_uint(m));
+    return __builtin_fmaxf(__uint_as_float(p.a), __uint_as_float(p.b));
+}
+__device__ static inline float column_sum(float v) {
+    Pair p = swapped<32>(__float_as_uint(v));
+    v = __uint_as_float(p.a) + __uint_as_float(p.b);
+    p = swapped<16>(__float_as_uint(v));
+    return __uint_as_float(p.a) + __uint_as_float(p.b);
+}
+template <int LANES>
+__device__ static inline double swapped_sum(double v) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const Pair lo = swapped<LANES>((uint32_t)u), hi = swapped<LANES>((uint32_t)(u >> 32));
+    return __builtin_bit_cast(double, (uint64_t)hi.a << 32 | lo.a) + __builtin_bit_cast(double, (uint64_t)hi.b << 32 | lo.b);
+}
+__device__ static inline double column_sum(double v) { return swapped_sum<16>(swapped_sum<32>(v)); }
 template <int N>
 __device__ static inline Power column_power(const f4 (&v)[N], int lane) {
     float m = 0.0f;
@@ -254,22 +280,54 @@ __device__ static inline void triangle_times(const uint16_t *hi, const uint16_t 
             }
 }
 
-// Lane sums and maxima over 16 lanes, by rotations.
+// Sums and maxima over the 8 or 16 lanes of a group, on all of them: across pairs, quads, halves and the row, all within
+// the vector unit (a shuffle by way of LDS is some 100 cycles).
 template <int CTRL>
-__device__ static inline float turn16(float v) {
+__device__ static inline float moved(float v) {
     return __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v), CTRL, 0xf, 0xf, true));
 }
-__device__ static inline float sum16(float v) {
-    v += turn16<0x128>(v);
-    v += turn16<0x124>(v);
-    v += turn16<0x122>(v);
-    return v + turn16<0x121>(v);
+template <int CTRL, int ROWS = 0xf>
+__device__ static inline double moved(double v) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, ROWS, 0xf, false);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, ROWS, 0xf, false);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
-__device__ static inline float max16(float v) {
-    v = __builtin_fmaxf(v, turn16<0x128>(v));
-    v = __builtin_fmaxf(v, turn16<0x124>(v));
-    v = __builtin_fmaxf(v, turn16<0x122>(v));
-    return __builtin_fmaxf(v, turn16<0x121>(v));
+constexpr int kPairs = 0xB1, kQuads = 0x4E, kHalves = 0x141, kRow = 0x140;
+template <int LANES, typename T>
+__device__ static inline T sum_over(T v) {
+    v += moved<kPairs>(v);
+    v += moved<kQuads>(v);
+    if (LANES > 4) v += moved<kHalves>(v);
+    if (LANES > 8) v += moved<kRow>(v);
+    return v;
+}
+template <int LANES>
+__device__ static inline float max_over(float v) {
+    v = __builtin_fmaxf(v, moved<kPairs>(v));
+    v = __builtin_fmaxf(v, moved<kQuads>(v));
+    if (LANES > 4) v = __builtin_fmaxf(v, moved<kHalves>(v));
+    if (LANES > 8) v = __builtin_fmaxf(v, moved<kRow>(v));
+    return v;
+}
+__device__ static inline float sum16(float v) { return sum_over<16>(v); }
+__device__ static inline float max16(float v) { return max_over<16>(v); }
+
+// The sum over lanes 0 to this one, and its value on the last.
+__device__ static inline double sum_up(double v) {
+    v += moved<0x111>(v);       // rows of 16, by 1, 2, 4 and 8 lanes
+    v += moved<0x112>(v);
+    v += moved<0x114>(v);
+    v += moved<0x118>(v);
+    v += moved<0x142, 0xa>(v);  // a row's last to the next row; the second row's to the last two
+    v += moved<0x143, 0xc>(v);
+    return v;
+}
+__device__ static inline double last_lane(double v) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)u, kWave - 1);
+    const uint32_t hi = __builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), kWave - 1);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -359,9 +417,10 @@ __device__ static inline void load_rows(const Column16 &c, int row0, int rows, i
 // A chunk's operands on their way to LDS: read into registers when the last chunk begins, written when it ends. (Loads
 // straight to LDS need no registers, but while one is under way the compiler has any use of any other load wait
 // for all of them.)
+// A_TERMS: of A, 0 with nothing for outputs: neither A nor the image of q.
 template <int KP, int W, int A_TERMS>
 struct Staged {
-    static constexpr int kThreads = W * kWave, kKeys = 2 * kC * KP * 2, kXa = (2 + A_TERMS) * kTriangle * 2;
+    static constexpr int kThreads = W * kWave, kKeys = (A_TERMS > 0 ? 2 : 1) * kC * KP * 2, kXa = (2 + A_TERMS) * kTriangle * 2;
     static constexpr int kBytes = kKeys + kXa + (int)sizeof(RowCoef);
     static constexpr int kOfKeys = kKeys / 16 / kThreads, kOfXa = kXa / 16 / kThreads;
     static constexpr int kRest = (kXa - kOfXa * 16 * kThreads) / 8 / kThreads, kOfCoef = (int)sizeof(RowCoef) / 4 / kThreads;

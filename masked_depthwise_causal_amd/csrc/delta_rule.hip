@@ -88,46 +88,56 @@ __device__ static inline HVec<8>::t row_chunk(const uint16_t *p, int left) {
     return v;
 }
 
-// The 64 rows of q or k as an image in LDS and in memory, and the rows' factors.
+// The 64 rows of q or k: read all at once, then made an image in LDS and in memory, and the rows' factors.
 template <int DT, int KP>
-__device__ static __forceinline__ void image_rows(const Delta &a, const uint16_t *base, const int64_t (&st)[3], int b, int g,
-                                         int row0, int live, uint16_t *lds, uint16_t *image, float *factor,
-                                         float *factor_out, float *power_out) {
-    constexpr int kLanes = KP / 8, kRows = kPrepThreads / kLanes;
-    const int lane = threadIdx.x % kLanes;
-    for (int r = threadIdx.x / kLanes; r < kC; r += kRows) {
-        HVec<8>::t raw = {};
-        if (r < live) raw = row_chunk(base + (int64_t)(row0 + r) * st[0] + b * st[1] + g * st[2] + 8 * lane, a.K - 8 * lane);
-        float v[8], m = 0.0f, ss = 0.0f;
+struct RawRows {
+    static constexpr int kLanes = KP / 8, kRows = kPrepThreads / kLanes, kTurns = kC / kRows;
+    HVec<8>::t raw[kTurns];
+
+    __device__ void load(const Delta &a, const uint16_t *base, const int64_t (&st)[3], int b, int g, int row0, int live) {
+        const int lane = threadIdx.x % kLanes;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = to_f32<DT>(raw[i]), m = __builtin_fmaxf(m, __builtin_fabsf(v[i]));
-        // the row's largest value is brought to 2^14..2^15
-#pragma unroll
-        for (int i = 1; i < kLanes; i *= 2) m = __builtin_fmaxf(m, __shfl_xor(m, i));
-        // (a row of zeros, whose factor would be 1000 next to the other rows' 1, has 2^-10 taken out)
-        int e = m > 0.0f ? ((__float_as_uint(m) >> 23) & 255) - 127 - 14 : -10;
-        e = e < -100 ? -100 : e > 126 ? 126 : e;
-        h8 h;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            v[i] = __builtin_ldexpf(v[i], -e);
-            ss = __builtin_fmaf(v[i], v[i], ss);
-            h[i] = (_Float16)v[i];
-        }
-#pragma unroll
-        for (int i = 1; i < kLanes; i *= 2) ss += __shfl_xor(ss, i);
-        const int at = image_at<KP>(r, lane);
-        *(h8 *)(lds + at) = h;
-        *(h8 *)(image + at) = h;
-        if (lane == 0) {
-            const float f = a.normalize ? 1.0f / __builtin_sqrtf(ss + __builtin_ldexpf(kNormEps, -2 * e))
-                                        : __builtin_ldexpf(1.0f, e);
-            factor[r] = f;
-            factor_out[r] = f;
-            power_out[r] = __builtin_ldexpf(1.0f, -e);
+        for (int i = 0; i < kTurns; ++i) {
+            const int r = threadIdx.x / kLanes + i * kRows;
+            raw[i] = HVec<8>::t{};
+            if (r < live)
+                raw[i] = row_chunk(base + (int64_t)(row0 + r) * st[0] + b * st[1] + g * st[2] + 8 * lane, a.K - 8 * lane);
         }
     }
-}
+    __device__ void image(const Delta &a, uint16_t *lds, uint16_t *to, float *factor, float *factor_out, float *power_out) const {
+        const int lane = threadIdx.x % kLanes;
+#pragma unroll
+        for (int t = 0; t < kTurns; ++t) {
+            const int r = threadIdx.x / kLanes + t * kRows;
+            float v[8], m = 0.0f, ss = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = to_f32<DT>(raw[t][i]), m = __builtin_fmaxf(m, __builtin_fabsf(v[i]));
+            // the row's largest value is brought to 2^14..2^15
+            m = max_over<kLanes>(m);
+            // (a row of zeros, whose factor would be 1000 next to the other rows' 1, has 2^-10 taken out)
+            int e = m > 0.0f ? ((__float_as_uint(m) >> 23) & 255) - 127 - 14 : -10;
+            e = e < -100 ? -100 : e > 126 ? 126 : e;
+            h8 h;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                v[i] = __builtin_ldexpf(v[i], -e);
+                ss = __builtin_fmaf(v[i], v[i], ss);
+                h[i] = (_Float16)v[i];
+            }
+            ss = sum_over<kLanes>(ss);
+            const int at = image_at<KP>(r, lane);
+            *(h8 *)(lds + at) = h;
+            *(h8 *)(to + at) = h;
+            if (lane == 0) {
+                const float f = a.normalize ? 1.0f / __builtin_sqrtf(ss + __builtin_ldexpf(kNormEps, -2 * e))
+                                            : __builtin_ldexpf(1.0f, e);
+                factor[r] = f;
+                factor_out[r] = f;
+                power_out[r] = __builtin_ldexpf(1.0f, -e);
+            }
+        }
+    }
+};
 
 // A triangular 64x64 matrix in LDS as two terms in memory (or the first alone); returns the power of two taken out.
 __device__ static __forceinline__ float image_square(const float *m, uint16_t *hi, uint16_t *lo, float *part, int tid) {
@@ -223,7 +233,7 @@ __device__ static __forceinline__ void invert(const float *L, float *X, int wave
 }
 
 template <int DT, int KP>
-__global__ void __launch_bounds__(kPrepThreads, 3) delta_prepare(Delta a, Records rec, int n0, int a_terms) {
+__global__ void __launch_bounds__(kPrepThreads, 4) delta_prepare(Delta a, Records rec, int n0, int a_terms) {
     constexpr int kImages = 2 * kC * KP * (int)sizeof(uint16_t), kSquares = 2 * kC * kLd * (int)sizeof(float);
     __shared__ __align__(16) uint8_t smem[kImages > kSquares ? kImages : kSquares];  // rows first, then L, X
     __shared__ float kr[kC], qr[kC], beta[kC], part[4];
@@ -232,15 +242,27 @@ __global__ void __launch_bounds__(kPrepThreads, 3) delta_prepare(Delta a, Record
     const int row0 = (n0 + n) * kC, live = length_of(a, b) - row0;
     if (live <= 0) return;
     const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int heads = a.H / a.G;
+    // a head's step sizes and gates, ahead of its turn: a lane each row, the first wave's
+    uint16_t raw = 0, gate = 0;
+    auto read_gates = [&](int h) {
+        const int64_t row = row0 + (int)(threadIdx.x % kWave);
+        if ((int)(threadIdx.x % kWave) < live) {
+            raw = a.dt[row * a.ds[0] + b * a.ds[1] + h * a.ds[2]];
+            gate = a.b[row * a.bs[0] + b * a.bs[1] + h * a.bs[2]];
+        }
+    };
+    if (wave == 0) read_gates(g * heads);
     uint16_t *kt = (uint16_t *)smem, *qt = kt + kC * KP;
     {
         uint8_t *key = rec.key + ((int64_t)(b * a.G + g) * rec.chunks + n) * key_bytes(KP);
         uint16_t *images = (uint16_t *)key;
         float *factors = (float *)(images + 2 * kC * KP);
-        image_rows<DT, KP>(a, a.k, a.ks, b, g, row0, live, kt, images, kr, factors,
-                           factors + 2 * kC);
-        image_rows<DT, KP>(a, a.q, a.qs, b, g, row0, live, qt, images + kC * KP, qr,
-                           factors + kC, factors + 3 * kC);
+        RawRows<DT, KP> k, q;
+        k.load(a, a.k, a.ks, b, g, row0, live);
+        q.load(a, a.q, a.qs, b, g, row0, live);
+        k.image(a, kt, images, kr, factors, factors + 2 * kC);
+        q.image(a, qt, images + kC * KP, qr, factors + kC, factors + 3 * kC);
     }
     lds_barrier();
     // K~ K~^T and Q~ K~^T: wave w has rows 16 w.. of both, up to the diagonal block
@@ -260,7 +282,6 @@ __global__ void __launch_bounds__(kPrepThreads, 3) delta_prepare(Delta a, Record
             }
     }
     float *P = (float *)smem, *X = P + kC * kLd;
-    const int heads = a.H / a.G;
     for (int hh = 0; hh < heads; ++hh) {
         const int tid = anew(threadIdx.x), lane = tid % kWave, m = lane & 15, grp = lane >> 4;
         const int h = g * heads + hh;
@@ -269,19 +290,12 @@ __global__ void __launch_bounds__(kPrepThreads, 3) delta_prepare(Delta a, Record
         uint16_t *xa = (uint16_t *)(rec.xa + at * kXaBytes);
         double total = 0.0, mine = 0.0;
         if (wave == 0) {
-            float bt = 0.0f;
-            if (lane < live) {
-                const int64_t row = row0 + lane;
-                const float raw = to_f32<DT>(a.dt[row * a.ds[0] + b * a.ds[1] + h * a.ds[2]]) + (a.bias ? a.bias[h] : 0.0f);
-                mine = log2_decay(step_size(raw, a.softplus), a.A[h]);
-                bt = sigmoid_f(to_f32<DT>(a.b[row * a.bs[0] + b * a.bs[1] + h * a.bs[2]]));
-            }
-#pragma unroll
-            for (int s = 1; s < kC; s *= 2) {
-                const double o = __shfl_up(mine, s);
-                if (lane >= s) mine += o;
-            }
-            total = __shfl(mine, kC - 1);
+            if (lane < live)
+                mine = log2_decay(step_size(to_f32<DT>(raw) + (a.bias ? a.bias[h] : 0.0f), a.softplus), a.A[h]);
+            const float bt = lane < live ? sigmoid_f(to_f32<DT>(gate)) : 0.0f;
+            if (hh + 1 < heads) read_gates(h + 1);
+            mine = sum_up(mine);
+            total = last_lane(mine);
             cum[lane] = mine, beta[lane] = bt;
         }
         lds_barrier();  // also: the last head's reads of P and X, or the rows' reads above, are done
@@ -330,18 +344,26 @@ struct Walk {
     float *state_out;               // or NULL
     uint16_t *out;                  // [S,B,H,V]
     float *states, *u;              // kept for the backward, padded: [B,H][chunk][K,V] and [B,H][chunk][64,V]; or NULL
-    int n0, n1;                     // chunks
+    float *ends;                    // [segment][B,H][K, V + K], padded: what delta_walk_segments finds
+    float *carry;                   // [segment - 1][B,H][K,V], padded: the state before each segment but the first
+    int chunks, per;                // chunks, and of a segment
+    int segments;
     int blocks;                     // of columns, a head
 };
+
 
 // TERMS: those of what only the output is made of, A U and Q~ S0. Its 16 bits are the last rounding (2^-9 of a bf16
 // value), next to which one fp16 term of A, U and S0 (2^-12 each) does not count; fp16 outputs take two.
 // KEEP: the states and U are kept. (Two waves a SIMD would fit: with all of a SIMD's registers the compiler has the
 // products' results in accumulation registers and moves each of them.)
-template <int DT, int KP, int W, bool KEEP, bool WIDE>
+// SEGMENTS: where there are few heads, the first pass of two over a sequence that is cut into segments, all at once:
+// no outputs, but what a segment makes of the state before it, S -> T S + F. F is what the walk makes of a state of
+// zeros, and T's columns are what it makes of the identity's where there is nothing to write (V = 0): K more columns.
+// delta_carry then finds the states before the segments, and the second pass walks all of them at once with outputs.
+template <int DT, int KP, int W, bool KEEP, bool WIDE, bool SEGMENTS>
 __global__ void __launch_bounds__(W *kWave, 2) delta_walk(Delta a, Records rec, Walk w) {
     constexpr int KT = KP / 16, KS = KP / 32;
-    constexpr int TERMS = DT == MCCB_BF16 ? 1 : 2;
+    constexpr int TERMS = SEGMENTS ? 0 : DT == MCCB_BF16 ? 1 : 2;
     typedef Staged<KP, W, TERMS> Stage;
     constexpr int kBuf = Stage::kBytes, kKeys = Stage::kKeys;
     __shared__ __align__(16) uint8_t smem[2 * kBuf];
@@ -349,10 +371,12 @@ __global__ void __launch_bounds__(W *kWave, 2) delta_walk(Delta a, Records rec, 
     const int m = lane & 15, grp = lane >> 4;
     const int lk_at = left_place<KP>(lane), tk_at = turned_place<KP>(lane), ls_at = triangle_place(lane);
     const int id = same_die(blockIdx.x, gridDim.x);
-    const int bh = id / w.blocks, b = bh / a.H, h = bh % a.H, g = h / (a.H / a.G);
+    const int all = a.B * a.H, segment = id / (w.blocks * all), bh = id / w.blocks % all;
+    const int b = bh / a.H, h = bh % a.H, g = h / (a.H / a.G);
     const int col = (id % w.blocks * W + wave) * 16 + m, VP = padded_v(a.V);
+    const int n0 = segment * w.per, n1 = n0 + w.per < w.chunks ? n0 + w.per : w.chunks;
     const int length = length_of(a, b);
-    const int chunks = (length + kC - 1) / kC, end = chunks < w.n1 ? chunks : w.n1;
+    const int chunks = (length + kC - 1) / kC, end = chunks < n1 ? chunks : n1;
 
     f4 S[KT];
 #pragma unroll
@@ -360,15 +384,16 @@ __global__ void __launch_bounds__(W *kWave, 2) delta_walk(Delta a, Records rec, 
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int k = row_of(t, 4 * grp + i);
-            S[t][i] = w.state_in && k < a.K && col < a.V ? w.state_in[((int64_t)bh * a.K + k) * a.V + col] : 0.0f;
+            if (SEGMENTS) S[t][i] = col == VP + k ? 1.0f : 0.0f;
+            else if (segment > 0) S[t][i] = w.carry[(((int64_t)(segment - 1) * all + bh) * KP + k) * VP + col];
+            else S[t][i] = w.state_in && k < a.K && col < a.V ? w.state_in[((int64_t)bh * a.K + k) * a.V + col] : 0.0f;
         }
     const uint8_t *key = rec.key + (int64_t)(b * a.G + g) * rec.chunks * key_bytes(KP);
     const uint8_t *xa = rec.xa + (int64_t)bh * rec.chunks * kXaBytes;
     const RowCoef *coefs = rec.coef + (int64_t)bh * rec.chunks;
     Stage stage;
     auto fetch = [&](int n) {
-        const int64_t i = n - w.n0;
-        stage.load(key + i * (int64_t)key_bytes(KP), xa + i * (int64_t)kXaBytes, coefs + i);
+        stage.load(key + n * (int64_t)key_bytes(KP), xa + n * (int64_t)kXaBytes, coefs + n);
     };
     const Column16 vcol = {a.v + b * a.vs[1] + h * a.vs[2], a.vs[0], col, a.V};
     const uint32_t out_row = 2u * (uint32_t)(a.B * a.H) * a.V;       // bytes
@@ -376,13 +401,13 @@ __global__ void __launch_bounds__(W *kWave, 2) delta_walk(Delta a, Records rec, 
     float *keep_s = KEEP ? w.states + ((int64_t)bh * rec.chunks * KP + 8 * grp) * VP + col : nullptr;
     float *keep_u = KEEP ? w.u + ((int64_t)bh * rec.chunks * kC + 8 * grp) * VP + col : nullptr;
     uint16_t v[4][4];
-    if (w.n0 < end) {
-        fetch(w.n0);
-        load_rows<WIDE>(vcol, w.n0 * kC, length - w.n0 * kC, lane, v);
-        stage.store(smem + (w.n0 & 1) * kBuf);
+    if (n0 < end) {
+        fetch(n0);
+        load_rows<WIDE>(vcol, n0 * kC, length - n0 * kC, lane, v);
+        stage.store(smem + (n0 & 1) * kBuf);
         lds_barrier();
     }
-    for (int n = w.n0; n < end; ++n) {
+    for (int n = n0; n < end; ++n) {
         const uint8_t *buf = smem + (n & 1) * kBuf;
         const uint16_t *kt = (const uint16_t *)buf, *qt = kt + kC * KP;
         const uint16_t *xh = (const uint16_t *)(buf + kKeys), *xl = xh + kTriangle, *ah = xl + kTriangle, *al = ah + kTriangle;
@@ -403,14 +428,20 @@ __global__ void __launch_bounds__(W *kWave, 2) delta_walk(Delta a, Records rec, 
             const Split sp = split(S[2 * s], S[2 * s + 1], ps.inv);
             h8 lk[4], lq[4];
 #pragma unroll
-            for (int t = 0; t < 4; ++t) lk[t] = left<KP>(kt, lk_at, t, s), lq[t] = left<KP>(qt, lk_at, t, s);
+            for (int t = 0; t < 4; ++t) {
+                lk[t] = left<KP>(kt, lk_at, t, s);
+                if (!SEGMENTS) lq[t] = left<KP>(qt, lk_at, t, s);
+            }
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
                 P[t] = mma(lk[t], sp.lo, P[t]);
                 if (TERMS > 1) O[t] = mma(lq[t], sp.lo, O[t]);
             }
 #pragma unroll
-            for (int t = 0; t < 4; ++t) P[t] = mma(lk[t], sp.hi, P[t]), O[t] = mma(lq[t], sp.hi, O[t]);
+            for (int t = 0; t < 4; ++t) {
+                P[t] = mma(lk[t], sp.hi, P[t]);
+                if (!SEGMENTS) O[t] = mma(lq[t], sp.hi, O[t]);
+            }
         }
         // beta (V - p K~ S0)
         f4 R[4];
@@ -438,7 +469,7 @@ __global__ void __launch_bounds__(W *kWave, 2) delta_walk(Delta a, Records rec, 
                 for (int i = 0; i < 4; ++i) to[(row_of(t, 0) + i) * VP] = up * U[t][i];
         }
         // out = q Q~ S0 + A U
-        {
+        if constexpr (!SEGMENTS) {
             const Power p = column_power(U, lane);
             f4 AU[4];
             triangle_times<false, TERMS>(ah, al, ls_at, split(U[0], U[1], p.inv), split(U[2], U[3], p.inv), AU);
@@ -482,7 +513,16 @@ __global__ void __launch_bounds__(W *kWave, 2) delta_walk(Delta a, Records rec, 
         stage.store(smem + (~n & 1) * kBuf);
         lds_barrier();  // the next chunk's operands are there, and all waves are done with this one's
     }
-    if (w.state_out) {
+    if (SEGMENTS) {
+        const int wide = VP + KP;
+        float *to = w.ends + (((int64_t)segment * all + bh) * KP + 8 * grp) * wide + col;
+#pragma unroll
+        for (int t = 0; t < KT; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) to[(row_of(t, 0) + i) * wide] = S[t][i];
+        return;
+    }
+    if (w.state_out && segment == w.segments - 1) {
 #pragma unroll
         for (int t = 0; t < KT; ++t)
 #pragma unroll
@@ -492,9 +532,90 @@ __global__ void __launch_bounds__(W *kWave, 2) delta_walk(Delta a, Records rec, 
             }
     }
     // rows that no chunk covers are zeros
-    const int from = (end > w.n0 ? end : w.n0) * kC, to = w.n1 * kC < a.S ? w.n1 * kC : a.S;
+    const int from = (end > n0 ? end : n0) * kC, to = n1 * kC < a.S ? n1 * kC : a.S;
     for (int row = from + grp; row < to; row += 4)
         if (col < a.V) w.out[(((int64_t)row * a.B + b) * a.H + h) * a.V + col] = 0;
+}
+
+// The states before the segments, one after the other: S -> T S + F. A block has 16 columns, a wave 32 rows of them;
+// what a segment needs of T and F does not depend on S and is read and split one segment ahead, and S goes from wave to
+// wave in LDS as the products' right operand, with a power of two for each wave's rows of a column.
+template <int KP>
+__global__ void __launch_bounds__(KP / 32 * kWave, 1) delta_carry(Delta a, Walk w) {
+    constexpr int KS = KP / 32;     // steps of a product, and waves
+    __shared__ __align__(16) h8 parts[2][KS][2][kWave];
+    __shared__ float backs[2][KS][16];
+    const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int m = lane & 15, grp = lane >> 4, all = a.B * a.H, VP = padded_v(a.V), wide = VP + KP, blocks = VP / 16;
+    const int bh = blockIdx.x / blocks, col = blockIdx.x % blocks * 16 + m;
+    f4 S[2], F[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int k = row_of(2 * wave + t, 4 * grp + i);
+            S[t][i] = w.state_in && k < a.K && col < a.V ? w.state_in[((int64_t)bh * a.K + k) * a.V + col] : 0.0f;
+        }
+    f4 x[2][KS][2];                 // T's rows
+    auto read = [&](int n) {
+        const float *end = w.ends + ((int64_t)n * all + bh) * KP * wide;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const float *row = end + row_of(2 * wave + t, m) * wide + VP + 8 * grp;
+#pragma unroll
+            for (int s = 0; s < KS; ++s)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) x[t][s][j] = *(const f4 *)(row + 32 * s + 4 * j);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) F[t][i] = end[(row_of(2 * wave + t, 4 * grp) + i) * wide + col];
+        }
+    };
+    read(0);
+    for (int n = 0; n + 1 < w.segments; ++n) {
+        Split T[2][KS];
+        float back[2];
+        f4 next[2] = {F[0], F[1]};
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            float big = 0.0f;
+#pragma unroll
+            for (int s = 0; s < KS; ++s)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    big = __builtin_fmaxf(big, __builtin_fmaxf(__builtin_fabsf(x[t][s][0][i]), __builtin_fabsf(x[t][s][1][i])));
+            const Power p = power_of(column_max(max16(big)));
+            back[t] = p.back;
+#pragma unroll
+            for (int s = 0; s < KS; ++s) T[t][s] = split(x[t][s][0], x[t][s][1], p.inv);
+        }
+        read(n + 2 < w.segments ? n + 1 : n);
+        const Power p = column_power(S, lane);
+        const Split mine = split(S[0], S[1], p.inv);
+        const int buf = n & 1;
+        parts[buf][wave][0][lane] = mine.hi, parts[buf][wave][1][lane] = mine.lo;
+        if (grp == 0) backs[buf][wave][m] = p.back;
+        lds_barrier();
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+            const h8 hi = parts[buf][s][0][lane], lo = parts[buf][s][1][lane];
+            const float up = backs[buf][s][m];
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                f4 d = mma(T[t][s].lo, hi, f4{});
+                d = mma(T[t][s].hi, lo, d);
+                d = mma(T[t][s].hi, hi, d);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) next[t][i] = __builtin_fmaf(d[i], back[t] * up, next[t][i]);
+            }
+        }
+        float *to = w.carry + (((int64_t)n * all + bh) * KP + 8 * grp) * VP + col;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            S[t] = next[t];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) to[(row_of(2 * wave + t, 0) + i) * VP] = S[t][i];
+        }
+    }
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -538,10 +659,8 @@ __global__ void __launch_bounds__(kStepThreads) delta_one(Delta a, float *state,
     const float decay = exp2_f((float)log2_decay(step_size(raw, a.softplus), a.A[h]));
     const float beta = sigmoid_f(to_f32<DT>(a.b[b * a.bs[1] + h * a.bs[2]]));
     if (t < kMaxK) {
-        const float kk = sum16(kv * kv), qq = sum16(qv * qv), kq = sum16(kv * qv);
-        const float x = kk + __shfl_xor(kk, 16), y = qq + __shfl_xor(qq, 16), z = kq + __shfl_xor(kq, 16);
-        const float x2 = x + __shfl_xor(x, 32), y2 = y + __shfl_xor(y, 32), z2 = z + __shfl_xor(z, 32);
-        if (lane == 0) norms[0][wave] = x2, norms[1][wave] = y2, norms[2][wave] = z2;
+        const float kk = column_sum(sum16(kv * kv)), qq = column_sum(sum16(qv * qv)), kq = column_sum(sum16(kv * qv));
+        if (lane == 0) norms[0][wave] = kk, norms[1][wave] = qq, norms[2][wave] = kq;
     }
     __syncthreads();
     const float rk = a.normalize ? 1.0f / __builtin_sqrtf(norms[0][0] + norms[0][1] + kNormEps) : 1.0f;
@@ -564,9 +683,7 @@ __global__ void __launch_bounds__(kStepThreads) delta_one(Delta a, float *state,
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        acc[j] += turn16<0x128>(acc[j]);
-        acc[j] += __shfl_xor(acc[j], 16);
-        acc[j] += __shfl_xor(acc[j], 32);
+        acc[j] = column_sum(acc[j] + moved<0x128>(acc[j]));  // lanes 8, 16 and 32 apart
     }
     if (lane < 8) {
         *(f4 *)part[wave][lane] = f4{acc[0], acc[1], acc[2], acc[3]};
@@ -609,36 +726,79 @@ int prepare(const Delta &d, const Records &rec, int n0, int n1, bool keep, hipSt
                        0, st, d, rec, n0, keep || DT == MCCB_FP16 ? 2 : 1);
     return launched();
 }
-template <int DT, int KP, bool KEEP>
+template <int DT, int KP, bool KEEP, bool SEGMENTS>
 int walk(const Delta &d, const Records &rec, Walk w, hipStream_t st) {
     constexpr int W = 4;
-    w.blocks = padded_v(d.V) / (16 * W);
-    const dim3 grid((unsigned)(d.B * d.H * w.blocks)), block(W * kWave);
-    if (row_buffer(d.vs[0], d.V)) hipLaunchKernelGGL((delta_walk<DT, KP, W, KEEP, false>), grid, block, 0, st, d, rec, w);
-    else hipLaunchKernelGGL((delta_walk<DT, KP, W, KEEP, true>), grid, block, 0, st, d, rec, w);
+    w.blocks = (padded_v(d.V) + (SEGMENTS ? KP : 0)) / (16 * W);
+    const int segments = w.segments - (SEGMENTS ? 1 : 0);  // nothing comes after the last one
+    const dim3 grid((unsigned)(segments * d.B * d.H * w.blocks)), block(W * kWave);
+    if (row_buffer(d.vs[0], d.V))
+        hipLaunchKernelGGL((delta_walk<DT, KP, W, KEEP, false, SEGMENTS>), grid, block, 0, st, d, rec, w);
+    else
+        hipLaunchKernelGGL((delta_walk<DT, KP, W, KEEP, true, SEGMENTS>), grid, block, 0, st, d, rec, w);
     return launched();
 }
 template <int DT, int KP>
 int all_chunks(const Delta &d, const Records &rec, const Walk &w, hipStream_t st) {
-    if (w.n1 > w.n0) {
-        const int rc = prepare<DT, KP>(d, rec, w.n0, w.n1, w.states != nullptr, st);
+    int rc = MCCB_OK;
+    if (w.chunks > 0) rc = prepare<DT, KP>(d, rec, 0, w.chunks, w.states != nullptr, st);
+    if (rc == MCCB_OK && w.segments > 1) {
+        rc = walk<DT, KP, false, true>(d, rec, w, st);
         if (rc != MCCB_OK) return rc;
+        hipLaunchKernelGGL((delta_carry<KP>), dim3((unsigned)(d.B * d.H * (padded_v(d.V) / 16))), dim3(KP / 32 * kWave), 0, st,
+                           d, w);
+        rc = launched();
     }
-    return w.states ? walk<DT, KP, true>(d, rec, w, st) : walk<DT, KP, false>(d, rec, w, st);
+    if (rc != MCCB_OK) return rc;
+    return w.states ? walk<DT, KP, true, false>(d, rec, w, st) : walk<DT, KP, false, false>(d, rec, w, st);
+}
+
+// Segments of a walk, by what it costs: 3.2 us a chunk where a wave has a SIMD to itself, with outputs and also
+// without (two waves a SIMD then, of 1024 SIMDs), 3 us to carry a state over a segment, and 10 us for two more launches
+// and their ends. S=16384 B=1 H=16: 812 us as one segment, 285 as eight; S=777 B=5 H=6: 43 as one, 52 as three.
+struct Cut {
+    int segments, per;
+};
+Cut cut_of(const mccb_delta_t *a) {
+    const int64_t chunks = (int64_t)chunks_of(a), heads = a->B * a->H, VP = padded_v((int)a->V), KP = padded(a->K);
+    Cut best = {1, (int)chunks};
+    int64_t least = 32 * chunks;
+    for (int64_t n = 2; n <= 16 && n <= chunks && n * heads * VP / 16 <= 1024; ++n) {
+        const int64_t per = (chunks + n - 1) / n, rounds = ((n - 1) * heads * (VP + KP) / 16 + 2047) / 2048;
+        const int64_t cost = 32 * per * (1 + rounds) + 30 * (n - 1) + 100;
+        if (cost < least) least = cost, best.per = (int)per, best.segments = (int)((chunks + per - 1) / per);
+    }
+    return best;
+}
+uint64_t ends_floats(const mccb_delta_t *a, const Cut &c) {
+    return (uint64_t)(c.segments - 1) * (uint64_t)(a->B * a->H) * (uint64_t)padded(a->K) * (uint64_t)(padded_v((int)a->V) + padded(a->K));
+}
+uint64_t carry_floats(const mccb_delta_t *a, const Cut &c) {
+    return (uint64_t)(c.segments - 1) * (uint64_t)(a->B * a->H) * (uint64_t)padded(a->K) * (uint64_t)padded_v((int)a->V);
+}
+uint64_t cut_bytes(const mccb_delta_t *a) {
+    const Cut c = cut_of(a);
+    return (ends_floats(a, c) + carry_floats(a, c)) * sizeof(float);
 }
 
 template <int DT>
 int forward(const mccb_delta_t *a, void *out, float *final_state, void *saved, void *ws, hipStream_t st) {
     const Delta d = delta_of(a);
     const uint64_t chunks = chunks_of(a);
-    Records rec = records_at(saved ? saved : ws, (uint64_t)(a->B * a->G), (uint64_t)(a->B * a->H), chunks, padded(a->K));
+    uint8_t *const at = (uint8_t *)(saved ? saved : ws);
+    Records rec = records_at(at, (uint64_t)(a->B * a->G), (uint64_t)(a->B * a->H), chunks, padded(a->K));
     Walk w{};
     w.state_in = a->state, w.state_out = final_state, w.out = (uint16_t *)out;
-    w.n0 = 0, w.n1 = (int)chunks;
+    const Cut c = cut_of(a);
+    w.chunks = (int)chunks, w.segments = c.segments, w.per = c.per;
+    uint64_t used = records_size(a, chunks);
     if (saved) {
-        w.states = (float *)((uint8_t *)saved + records_size(a, chunks));
+        w.states = (float *)(at + used);
         w.u = (float *)((uint8_t *)w.states + chunk_states_bytes(a));
+        used += chunk_states_bytes(a) + chunk_rows_bytes(a);
     }
+    w.ends = (float *)(at + used);
+    w.carry = w.ends + ends_floats(a, c);
     return padded(a->K) == 64 ? all_chunks<DT, 64>(d, rec, w, st) : all_chunks<DT, 128>(d, rec, w, st);
 }
 
@@ -651,7 +811,7 @@ int mccb_delta_saved_size(const mccb_delta_t *a, uint64_t *bytes) {
     const int rc = check_delta(a, false);
     if (rc != MCCB_OK) return rc;
     const uint64_t chunks = chunks_of(a);
-    *bytes = records_size(a, chunks) + chunk_states_bytes(a) + chunk_rows_bytes(a);
+    *bytes = records_size(a, chunks) + chunk_states_bytes(a) + chunk_rows_bytes(a) + cut_bytes(a);
     return MCCB_OK;
 }
 
@@ -659,7 +819,7 @@ int mccb_delta_forward_get_workspace_size(const mccb_delta_t *a, uint64_t *size)
     if (!size) return MCCB_ERR_PARAM_NULLPTR;
     const int rc = check_delta(a, false);
     if (rc != MCCB_OK) return rc;
-    *size = records_size(a, chunks_of(a));
+    *size = records_size(a, chunks_of(a)) + cut_bytes(a);
     return MCCB_OK;
 }
 
