@@ -666,13 +666,17 @@ __global__ void __launch_bounds__(kWave *kSumSlots)
 // ---------------------------------------------------------------------------------------------
 uint64_t part_bytes(const mccb_delta_t *a) { return 2 * chunks_of(a) * (uint64_t)(a->B * a->H) * sizeof(double); }
 
-template <int DT, int KP>
-int launch(const Delta &d, const Records &rec, Back w, hipStream_t st) {
-    constexpr int W = 4;
+template <int DT, int KP, int W>
+void walk_back(const Delta &d, const Records &rec, Back w, hipStream_t st) {
     w.blocks = padded_v(d.V) / (16 * W);
     const dim3 grid((unsigned)(d.B * d.H * w.blocks)), block(W * kWave);
     if (row_buffer(w.gs[0], d.V)) hipLaunchKernelGGL((delta_walk_back<DT, KP, W, false>), grid, block, 0, st, d, rec, w);
     else hipLaunchKernelGGL((delta_walk_back<DT, KP, W, true>), grid, block, 0, st, d, rec, w);
+}
+template <int DT, int KP>
+int launch(const Delta &d, const Records &rec, const Back &w, hipStream_t st) {
+    if (KP == 128 && half_blocks(d, 1)) walk_back<DT, KP, KP == 128 ? 2 : 4>(d, rec, w, st);
+    else walk_back<DT, KP, 4>(d, rec, w, st);
     int rc = launched();
     if (rc != MCCB_OK || w.chunks == 0) return rc;
     const dim3 all((unsigned)w.chunks, (unsigned)(d.B * d.G)), threads(KP / 16 * kWave);

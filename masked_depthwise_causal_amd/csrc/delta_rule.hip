@@ -726,9 +726,8 @@ int prepare(const Delta &d, const Records &rec, int n0, int n1, bool keep, hipSt
                        0, st, d, rec, n0, keep || DT == MCCB_FP16 ? 2 : 1);
     return launched();
 }
-template <int DT, int KP, bool KEEP, bool SEGMENTS>
-int walk(const Delta &d, const Records &rec, Walk w, hipStream_t st) {
-    constexpr int W = 4;
+template <int DT, int KP, int W, bool KEEP, bool SEGMENTS>
+int walk_of(const Delta &d, const Records &rec, Walk w, hipStream_t st) {
     w.blocks = (padded_v(d.V) + (SEGMENTS ? KP : 0)) / (16 * W);
     const int segments = w.segments - (SEGMENTS ? 1 : 0);  // nothing comes after the last one
     const dim3 grid((unsigned)(segments * d.B * d.H * w.blocks)), block(W * kWave);
@@ -737,6 +736,12 @@ int walk(const Delta &d, const Records &rec, Walk w, hipStream_t st) {
     else
         hipLaunchKernelGGL((delta_walk<DT, KP, W, KEEP, true, SEGMENTS>), grid, block, 0, st, d, rec, w);
     return launched();
+}
+template <int DT, int KP, bool KEEP, bool SEGMENTS>
+int walk(const Delta &d, const Records &rec, const Walk &w, hipStream_t st) {
+    if constexpr (KP == 128 && !SEGMENTS)
+        if (half_blocks(d, w.segments)) return walk_of<DT, KP, 2, KEEP, SEGMENTS>(d, rec, w, st);
+    return walk_of<DT, KP, 4, KEEP, SEGMENTS>(d, rec, w, st);
 }
 template <int DT, int KP>
 int all_chunks(const Delta &d, const Records &rec, const Walk &w, hipStream_t st) {
