@@ -97,8 +97,7 @@ int mccb_delta_step(const mccb_delta_t *args, float *state, void *out, void *str
  * its own for every value, or (weight_shared) one of H/groups values for all groups. residual, scale [H]
  * and z may be NULL: then their factor or term is left out. Everything has the dtype, is computed in fp32
  * and rounded once; prenorm's norm is of the sum before its rounding. Gradients of weight and scale add
- * a block's rows in fp32 (8 to R/1024 of them, and one block's at most where there are fewer) and go on in
- * fp64. Rows are contiguous and x_ld, residual_ld, z_ld elements apart; results are contiguous.
+ * a block's rows in fp32 (about R groups/1024 of them, 4 at least, where R is as large) and go on in fp64. Rows are contiguous and x_ld, residual_ld, z_ld elements apart; results are contiguous.
  *
  * R in [0, 2^31), H in [1, 2^24], groups in [1, 65535] and a divisor of H, H/groups up to 16384, eps
  * positive. prenorm has groups = 1 and no z.
