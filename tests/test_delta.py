@@ -128,6 +128,51 @@ def test_many_chunks(S, B, H, G, K, V, dtype, lengths):
     check(S, B, H, G, K, V, dtype, lengths, seed=S)
 
 
+@pytest.mark.parametrize("S,B,H,G,K,V,dtype,lengths,layout", [
+    (1300, 1, 2, 1, 64, 48, "fp16", None, "contig"),
+    (1250, 2, 1, 1, 100, 130, "bf16", [1250, 70], "parts"),
+    (1100, 3, 2, 2, 128, 32, "fp16", [0, 1100, 513], "batch_first"),
+])
+def test_long_sequences_of_few_heads(S, B, H, G, K, V, dtype, lengths, layout):
+    """Cut into segments, whose states before them come from a pass of their own. A state goes through one more
+    product for each of up to 16 segments, of the same error as a chunk's: within the bound of S's chunks."""
+    check(S, B, H, G, K, V, dtype, lengths, layout, seed=S)
+
+
+def test_long_sequences_of_rows_that_overlap():
+    v, go, _ = inputs(1111, 1, 2, 1, 128, 40, "bf16", 6)
+    d = {n: None if t is None else t.cuda() for n, t in v.items()}
+    x = torch.randn(1111 * 8 + 80).bfloat16().cuda().as_strided((1111, 1, 2, 40), (8, 8, 40, 1))
+    got = [mdc.delta_forward(d["q"], d["k"], y, d["dt"], d["b"], d["A"], dt_bias=d["dt_bias"], state=d["state"],
+                             return_state=True) for y in (x, x.contiguous())]
+    assert all(torch.equal(p, q) for p, q in zip(*got))
+
+
+def test_more_heads_than_blocks_of_two_waves():
+    check(130, 35, 2, 1, 128, 128, "bf16", [130] * 30 + [0, 1, 64, 65, 129], "parts", seed=41)
+
+
+def test_tensors_of_more_than_2_31_values():
+    """The last rows, against a call for them alone from the state before them."""
+    S, B, H, G, K, V, tail = 64 * 2190, 1, 64, 1, 16, 256, 192
+    g = torch.Generator(device="cuda").manual_seed(3)
+    r = lambda *s: torch.randn(s, generator=g, device="cuda", dtype=torch.bfloat16)  # noqa: E731
+    q, k, v, dt, b, go = r(S, B, G, K), r(S, B, G, K), r(S, B, H, V), r(S, B, H), r(S, B, H), r(S, B, H, V)
+    assert v.numel() > 1 << 31
+    A = -torch.rand(H, generator=g, device="cuda")
+    announce("delta, more than 2^31 values")
+    _, before = mdc.delta_forward(*(t[:S - tail] for t in (q, k, v, dt, b)), A, return_state=True)
+    out, end, saved = mdc.delta_forward(q, k, v, dt, b, A, return_state=True, return_saved=True)
+    gr = mdc.delta_backward(go, q, k, v, dt, b, A, saved)
+    part = [t[S - tail:].clone() for t in (q, k, v, dt, b)]
+    out2, end2, saved2 = mdc.delta_forward(*part, A, state=before, return_state=True, return_saved=True)
+    gr2 = mdc.delta_backward(go[S - tail:].clone(), *part, A, saved2, state=before)
+    torch.cuda.synchronize()
+    assert torch.equal(out[S - tail:], out2) and torch.equal(end, end2)
+    for name in ("q", "k", "v", "dt", "b"):
+        assert torch.equal(getattr(gr, name)[S - tail:], getattr(gr2, name)), name
+
+
 def test_no_rows():
     s = torch.randn((2, 4, 16, 24), device="cuda")
     dt = torch.bfloat16

@@ -140,3 +140,25 @@ def test_outputs_given_and_same_bits():
     a = mdc.postnorm_backward(z, x, w, z=z, scale=w)
     dirty()
     assert all(torch.equal(p, q) for p, q in zip(a, mdc.postnorm_backward(z, x, w, z=z, scale=w)))
+
+
+def test_tensors_of_more_than_2_31_values():
+    """The last rows, against a call for them alone."""
+    R, H, tail = 530_000, 4100, 2000
+    x = torch.randn((R, H), device="cuda", dtype=torch.bfloat16)
+    z, w = torch.randn((R, H), device="cuda", dtype=torch.bfloat16), torch.randn(H, device="cuda").bfloat16()
+    assert x.numel() > 1 << 31
+    last = lambda t: t[R - tail:].clone()  # noqa: E731
+    announce("norms, more than 2^31 values")
+    out, total = mdc.prenorm_forward(x, w, residual=z, return_sum=True)
+    out2, total2 = mdc.prenorm_forward(last(x), w, residual=last(z), return_sum=True)
+    assert torch.equal(out[R - tail:], out2) and torch.equal(total[R - tail:], total2)
+    del out, total
+    g = mdc.prenorm_backward(z, x, w)
+    assert torch.equal(g.x[R - tail:], mdc.prenorm_backward(last(z), last(x), w).x)
+    out = mdc.postnorm_forward(x, w, z=z, groups=4)
+    assert torch.equal(out[R - tail:], mdc.postnorm_forward(last(x), w, z=last(z), groups=4))
+    del g
+    g = mdc.postnorm_backward(out, x, w, z=z, groups=4)
+    g2 = mdc.postnorm_backward(last(out), last(x), w, z=last(z), groups=4)
+    assert torch.equal(g.x[R - tail:], g2.x) and torch.equal(g.z[R - tail:], g2.z)
