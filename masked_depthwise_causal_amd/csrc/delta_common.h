@@ -456,9 +456,8 @@ struct Staged {
 // Blocks of one head, and heads of one key head, next to each other on one of the 8 dies, which have an L2 each.
 __device__ static inline int same_die(int id, int all) { return all % 8 ? id : id % 8 * (all / 8) + id / 8; }
 
-// A walk's blocks have four waves, or two where those all have a CU to themselves (LDS holds one block of either, for
-// K above 64): more CUs then share what is read and written. Training S=2048 B=4 H=16 K=V=128, 128 blocks of four or
-// 256 of two: 161 and 148 us forward, 197 and 186 back; S=4096 B=4 H=32, 256 or 512: 241 and 400.
+// A walk's blocks have four waves with states, or two where those all have a CU to themselves (for K above 64 LDS holds
+// one block of either): more CUs then share what is read and written, and there are SIMDs left for more.
 __host__ static inline bool half_blocks(const Delta &d, int segments) {
     return (int64_t)segments * d.B * d.H * (padded_v(d.V) / 32) <= 256;
 }

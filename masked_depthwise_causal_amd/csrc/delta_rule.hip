@@ -341,6 +341,15 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prepare(Delta a, Record
 // ---------------------------------------------------------------------------------------------
 // The walk.
 // ---------------------------------------------------------------------------------------------
+constexpr int terms_of(int dt) { return dt == MCCB_BF16 ? 1 : 2; }
+// What a wave with a state hands to the one that makes its outputs.
+template <int KP, int W, int TERMS>
+struct Handed {
+    h8 s[W][KP / 32][TERMS > 0 ? TERMS : 1][kWave];     // S0 as a right operand
+    f4 u[W][4][kWave];
+    float s_back[W][16], u_up[W][16];
+};
+
 struct Walk {
     const float *state_in;          // [B,H,K,V] or NULL
     float *state_out;               // or NULL
@@ -356,8 +365,7 @@ struct Walk {
 
 // Bound by the vector and matrix instructions of one wave a SIMD, issued in 57 % of its cycles, and by what they wait for
 // (one product's largest values, then the next one's operands): S=4096 B=4 H=32 G=16 K=V=128, 241 us, 3.8 a chunk.
-// Training, S=2048 B=4 H=16, 148 us, of which the kept states and U (201 MB) are 30: the blocks are at what a CU of 256
-// has of the memory's rate.
+// Training, S=2048 B=4 H=16, 129 us, of which the kept states and U (201 MB) are some 30.
 // TERMS: those of what only the output is made of, A U and Q~ S0. Its 16 bits are the last rounding (2^-9 of a bf16
 // value), next to which one fp16 term of A, U and S0 (2^-12 each) does not count; fp16 outputs take two.
 // KEEP: the states and U are kept. (Two waves a SIMD would fit: with all of a SIMD's registers the compiler has the
@@ -366,14 +374,22 @@ struct Walk {
 // no outputs, but what a segment makes of the state before it, S -> T S + F. F is what the walk makes of a state of
 // zeros, and T's columns are what it makes of the identity's where there is nothing to write (V = 0): K more columns.
 // delta_carry then finds the states before the segments, and the second pass walks all of them at once with outputs.
+// W: waves with states, four a block; or two where blocks are few (half_blocks), and then each has a second one (PAIRS)
+// that makes the outputs of S0 and U as it finds them in LDS, and brings the operands: neither is on the way from one
+// state to the next. 148 -> 129 us (training, as above), 44 -> 38 (S=777 B=5 H=6 K=96 V=80); with four and their
+// seconds, two a SIMD, 241 and 241 (S=4096 B=4 H=32), 125 and 137 (S=16384 H=16 in segments).
 template <int DT, int KP, int W, bool KEEP, bool WIDE, bool SEGMENTS>
-__global__ void __launch_bounds__(W *kWave, 2) delta_walk(Delta a, Records rec, Walk w) {
+__global__ void __launch_bounds__((W == 2 ? 2 : 1) * W *kWave, 2) delta_walk(Delta a, Records rec, Walk w) {
+    constexpr bool PAIRS = W == 2;
     constexpr int KT = KP / 16, KS = KP / 32;
-    constexpr int TERMS = SEGMENTS ? 0 : DT == MCCB_BF16 ? 1 : 2;
+    constexpr int TERMS = SEGMENTS ? 0 : terms_of(DT);
     typedef Staged<KP, W, TERMS> Stage;
+    typedef Handed<KP, W, TERMS> Pairs;
     constexpr int kBuf = Stage::kBytes, kKeys = Stage::kKeys;
-    __shared__ __align__(16) uint8_t smem[2 * kBuf];
-    const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    __shared__ __align__(16) uint8_t smem[2 * kBuf + (PAIRS ? (int)sizeof(Pairs) : 0)];
+    Pairs *const handed = (Pairs *)(smem + 2 * kBuf);
+    const int lane = threadIdx.x % kWave, all_waves = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int wave = PAIRS ? all_waves % W : all_waves;
     const int m = lane & 15, grp = lane >> 4;
     const int lk_at = left_place<KP>(lane), tk_at = turned_place<KP>(lane), ls_at = triangle_place(lane);
     const int id = same_die(blockIdx.x, gridDim.x);
@@ -384,16 +400,6 @@ __global__ void __launch_bounds__(W *kWave, 2) delta_walk(Delta a, Records rec, 
     const int length = length_of(a, b);
     const int chunks = (length + kC - 1) / kC, end = chunks < n1 ? chunks : n1;
 
-    f4 S[KT];
-#pragma unroll
-    for (int t = 0; t < KT; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int k = row_of(t, 4 * grp + i);
-            if (SEGMENTS) S[t][i] = col == VP + k ? 1.0f : 0.0f;
-            else if (segment > 0) S[t][i] = w.carry[(((int64_t)(segment - 1) * all + bh) * KP + k) * VP + col];
-            else S[t][i] = w.state_in && k < a.K && col < a.V ? w.state_in[((int64_t)bh * a.K + k) * a.V + col] : 0.0f;
-        }
     const uint8_t *key = rec.key + (int64_t)(b * a.G + g) * rec.chunks * key_bytes(KP);
     const uint8_t *xa = rec.xa + (int64_t)bh * rec.chunks * kXaBytes;
     const RowCoef *coefs = rec.coef + (int64_t)bh * rec.chunks;
@@ -404,21 +410,82 @@ __global__ void __launch_bounds__(W *kWave, 2) delta_walk(Delta a, Records rec, 
     const Column16 vcol = {a.v + b * a.vs[1] + h * a.vs[2], a.vs[0], col, a.V};
     const uint32_t out_row = 2u * (uint32_t)(a.B * a.H) * a.V;       // bytes
     const uint32_t out_at = col < a.V ? 8 * grp * out_row + 2 * (h * a.V + col) : kNowhere;
+    // out = q Q~ S0 + A U
+    auto output = [&](int n, const uint8_t *buf, const f4 (&O)[4], float s_back, const f4 (&U)[4], float up) {
+        const uint16_t *ah = (const uint16_t *)(buf + kKeys) + 2 * kTriangle, *al = ah + kTriangle;
+        const RowCoef *coef = (const RowCoef *)(buf + kKeys + Stage::kXa);
+        const Power p = column_power(U, lane);
+        f4 AU[4];
+        triangle_times<false, TERMS>(ah, al, ls_at, split(U[0], U[1], p.inv), split(U[2], U[3], p.inv), AU);
+        const float back = p.back * up * coef->a;
+        const int left_rows = a.S - n * kC;
+        const Buffer to = buffer_of(w.out + (int64_t)n * kC * (out_row / 2) + (int64_t)b * a.H * a.V,
+                                    (left_rows < kC ? left_rows - 1 : kC - 1) * out_row + 2u * a.H * a.V);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const f4 cq = *(const f4 *)(coef->q + row_of(t, 4 * grp)) * s_back;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                __builtin_amdgcn_raw_buffer_store_b16(from_f32<DT>(__builtin_fmaf(AU[t][i], back, cq[i] * O[t][i])), to,
+                                                      out_at + (row_of(t, 0) + i) * out_row, 0, 0);
+        }
+    };
+    if constexpr (PAIRS)
+        if (all_waves < W) {
+            if (n0 < end) {
+                fetch(n0);
+                stage.store(smem + (n0 & 1) * kBuf);
+                lds_barrier();
+            }
+            for (int n = n0; n < end; ++n) {
+                const uint8_t *buf = smem + (n & 1) * kBuf;
+                const uint16_t *qt = (const uint16_t *)buf + kC * KP;
+                fetch(n + 1 < end ? n + 1 : n);
+                lds_barrier();  // S0 is there
+                f4 O[4] = {}, U[4];
+#pragma unroll
+                for (int s = 0; s < KS; ++s)
+#pragma unroll
+                    for (int term = TERMS - 1; term >= 0; --term) {
+                        const h8 x = handed->s[wave][s][term][lane];
+#pragma unroll
+                        for (int t = 0; t < 4; ++t) O[t] = mma(left<KP>(qt, lk_at, t, s), x, O[t]);
+                    }
+                const float s_back = handed->s_back[wave][m];
+                lds_barrier();  // and U
+#pragma unroll
+                for (int t = 0; t < 4; ++t) U[t] = handed->u[wave][t][lane];
+                output(n, buf, O, s_back, U, handed->u_up[wave][m]);
+                stage.store(smem + (~n & 1) * kBuf);
+                lds_barrier();  // as below
+            }
+            return;
+        }
+    f4 S[KT];
+#pragma unroll
+    for (int t = 0; t < KT; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int k = row_of(t, 4 * grp + i);
+            if (SEGMENTS) S[t][i] = col == VP + k ? 1.0f : 0.0f;
+            else if (segment > 0) S[t][i] = w.carry[(((int64_t)(segment - 1) * all + bh) * KP + k) * VP + col];
+            else S[t][i] = w.state_in && k < a.K && col < a.V ? w.state_in[((int64_t)bh * a.K + k) * a.V + col] : 0.0f;
+        }
     float *keep_s = KEEP ? w.states + ((int64_t)bh * rec.chunks * KP + 8 * grp) * VP + col : nullptr;
     float *keep_u = KEEP ? w.u + ((int64_t)bh * rec.chunks * kC + 8 * grp) * VP + col : nullptr;
     uint16_t v[4][4];
     if (n0 < end) {
-        fetch(n0);
+        if (!PAIRS) fetch(n0);
         load_rows<WIDE>(vcol, n0 * kC, length - n0 * kC, lane, v);
-        stage.store(smem + (n0 & 1) * kBuf);
+        if (!PAIRS) stage.store(smem + (n0 & 1) * kBuf);
         lds_barrier();
     }
     for (int n = n0; n < end; ++n) {
         const uint8_t *buf = smem + (n & 1) * kBuf;
         const uint16_t *kt = (const uint16_t *)buf, *qt = kt + kC * KP;
-        const uint16_t *xh = (const uint16_t *)(buf + kKeys), *xl = xh + kTriangle, *ah = xl + kTriangle, *al = ah + kTriangle;
+        const uint16_t *xh = (const uint16_t *)(buf + kKeys), *xl = xh + kTriangle;
         const RowCoef *coef = (const RowCoef *)(buf + kKeys + Stage::kXa);
-        fetch(n + 1 < end ? n + 1 : n);
+        if (!PAIRS) fetch(n + 1 < end ? n + 1 : n);
         if (KEEP) {
             float *to = keep_s + (int64_t)n * KP * VP;
 #pragma unroll
@@ -432,22 +499,30 @@ __global__ void __launch_bounds__(W *kWave, 2) delta_walk(Delta a, Records rec, 
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
             const Split sp = split(S[2 * s], S[2 * s + 1], ps.inv);
+            if constexpr (PAIRS) {
+                handed->s[wave][s][0][lane] = sp.hi;
+                if (TERMS > 1) handed->s[wave][s][TERMS - 1][lane] = sp.lo;
+            }
             h8 lk[4], lq[4];
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
                 lk[t] = left<KP>(kt, lk_at, t, s);
-                if (!SEGMENTS) lq[t] = left<KP>(qt, lk_at, t, s);
+                if (!SEGMENTS && !PAIRS) lq[t] = left<KP>(qt, lk_at, t, s);
             }
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
                 P[t] = mma(lk[t], sp.lo, P[t]);
-                if (TERMS > 1) O[t] = mma(lq[t], sp.lo, O[t]);
+                if (TERMS > 1 && !PAIRS) O[t] = mma(lq[t], sp.lo, O[t]);
             }
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
                 P[t] = mma(lk[t], sp.hi, P[t]);
-                if (!SEGMENTS) O[t] = mma(lq[t], sp.hi, O[t]);
+                if (!SEGMENTS && !PAIRS) O[t] = mma(lq[t], sp.hi, O[t]);
             }
+        }
+        if constexpr (PAIRS) {
+            if (grp == 0) handed->s_back[wave][m] = ps.back;
+            lds_barrier();
         }
         // beta (V - p K~ S0)
         f4 R[4];
@@ -474,23 +549,13 @@ __global__ void __launch_bounds__(W *kWave, 2) delta_walk(Delta a, Records rec, 
 #pragma unroll
                 for (int i = 0; i < 4; ++i) to[(row_of(t, 0) + i) * VP] = up * U[t][i];
         }
-        // out = q Q~ S0 + A U
-        if constexpr (!SEGMENTS) {
-            const Power p = column_power(U, lane);
-            f4 AU[4];
-            triangle_times<false, TERMS>(ah, al, ls_at, split(U[0], U[1], p.inv), split(U[2], U[3], p.inv), AU);
-            const float back = p.back * up * coef->a;
-            const int left_rows = a.S - n * kC;
-            const Buffer to = buffer_of(w.out + (int64_t)n * kC * (out_row / 2) + (int64_t)b * a.H * a.V,
-                                        (left_rows < kC ? left_rows - 1 : kC - 1) * out_row + 2u * a.H * a.V);
+        if constexpr (PAIRS) {
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                const f4 cq = *(const f4 *)(coef->q + row_of(t, 4 * grp)) * ps.back;
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    __builtin_amdgcn_raw_buffer_store_b16(from_f32<DT>(__builtin_fmaf(AU[t][i], back, cq[i] * O[t][i])), to,
-                                                          out_at + (row_of(t, 0) + i) * out_row, 0, 0);
-            }
+            for (int t = 0; t < 4; ++t) handed->u[wave][t][lane] = U[t];
+            if (grp == 0) handed->u_up[wave][m] = up;
+            lds_barrier();
+        } else if constexpr (!SEGMENTS) {
+            output(n, buf, O, ps.back, U, up);
         }
         // S = whole S0 + K~^T u U
         {
@@ -516,7 +581,7 @@ __global__ void __launch_bounds__(W *kWave, 2) delta_walk(Delta a, Records rec, 
                     for (int j = 0; j < 4; ++j) S[t + i][j] = __builtin_fmaf(whole, S[t + i][j], back * d[i][j]);
             }
         }
-        stage.store(smem + (~n & 1) * kBuf);
+        if (!PAIRS) stage.store(smem + (~n & 1) * kBuf);
         lds_barrier();  // the next chunk's operands are there, and all waves are done with this one's
     }
     if (SEGMENTS) {
@@ -738,7 +803,7 @@ template <int DT, int KP, int W, bool KEEP, bool SEGMENTS>
 int walk_of(const Delta &d, const Records &rec, Walk w, hipStream_t st) {
     w.blocks = (padded_v(d.V) + (SEGMENTS ? KP : 0)) / (16 * W);
     const int segments = w.segments - (SEGMENTS ? 1 : 0);  // nothing comes after the last one
-    const dim3 grid((unsigned)(segments * d.B * d.H * w.blocks)), block(W * kWave);
+    const dim3 grid((unsigned)(segments * d.B * d.H * w.blocks)), block((W == 2 ? 2 : 1) * W * kWave);
     if (row_buffer(d.vs[0], d.V))
         hipLaunchKernelGGL((delta_walk<DT, KP, W, KEEP, false, SEGMENTS>), grid, block, 0, st, d, rec, w);
     else
@@ -747,8 +812,8 @@ int walk_of(const Delta &d, const Records &rec, Walk w, hipStream_t st) {
 }
 template <int DT, int KP, bool KEEP, bool SEGMENTS>
 int walk(const Delta &d, const Records &rec, const Walk &w, hipStream_t st) {
-    if constexpr (KP == 128 && !SEGMENTS)
-        if (half_blocks(d, w.segments)) return walk_of<DT, KP, 2, KEEP, SEGMENTS>(d, rec, w, st);
+    if constexpr (!SEGMENTS)
+        if (half_blocks(d, w.segments)) return walk_of<DT, KP, 2, KEEP, false>(d, rec, w, st);
     return walk_of<DT, KP, 4, KEEP, SEGMENTS>(d, rec, w, st);
 }
 template <int DT, int KP>
