@@ -41,15 +41,25 @@ struct Back {
     int blocks;                     // of columns, a head
 };
 
-// As the forward walk it is bound by one wave a SIMD, with a longer chain and twice as many transposed operands: S=2048 B=4
-// H=16 K=V=128, 186 us, 5.8 a chunk, 235 MB written.
+// What second waves make, and hand to those with the state's gradient: all that comes of gO alone.
+template <int KP, int W>
+struct Given {
+    f4 u[W][4][kWave];              // A^T gO
+    f4 s[W][KP / 16][kWave];        // Q~^T (q gO)
+};
+// Bound as the forward walk is, with a longer chain and twice as many transposed operands: S=2048 B=4 H=16 K=V=128, 143
+// us, 4.5 a chunk, 235 MB written. W as there: without second waves 186, in blocks of four 197; S=513 B=2 H=6 K=64 V=128
+// 24 and 38. (Four and their seconds would need more than the LDS for K above 64.)
 template <int DT, int KP, int W, bool WIDE>
-__global__ void __launch_bounds__(W *kWave) delta_walk_back(Delta a, Records rec, Back w) {
+__global__ void __launch_bounds__((W == 2 ? 2 : 1) * W *kWave, 1) delta_walk_back(Delta a, Records rec, Back w) {
+    constexpr bool PAIRS = W == 2;
     constexpr int KT = KP / 16, KS = KP / 32;
     typedef Staged<KP, W, 2> Stage;
     constexpr int kBuf = Stage::kBytes, kKeys = Stage::kKeys;
-    __shared__ __align__(16) uint8_t smem[2 * kBuf];
-    const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    __shared__ __align__(16) uint8_t smem[2 * kBuf + (PAIRS ? (int)sizeof(Given<KP, W>) : 0)];
+    Given<KP, W> *const given = (Given<KP, W> *)(smem + 2 * kBuf);
+    const int lane = threadIdx.x % kWave, all_waves = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int wave = PAIRS ? all_waves % W : all_waves;
     const int m = lane & 15, grp = lane >> 4;
     const int lk_at = left_place<KP>(lane), tk_at = turned_place<KP>(lane), ts_at = triangle_turned_place(lane);
     const int id = same_die(blockIdx.x, gridDim.x);
@@ -58,6 +68,87 @@ __global__ void __launch_bounds__(W *kWave) delta_walk_back(Delta a, Records rec
     const bool mine = col < a.V;
     const int length = length_of(a, b), chunks = (length + kC - 1) / kC;
 
+    const uint8_t *key = rec.key + (int64_t)(b * a.G + g) * rec.chunks * key_bytes(KP);
+    const uint8_t *xa = rec.xa + (int64_t)bh * rec.chunks * kXaBytes;
+    const RowCoef *coefs = rec.coef + (int64_t)bh * rec.chunks;
+    Stage stage;
+    auto fetch = [&](int n) { stage.load(key + n * (int64_t)key_bytes(KP), xa + n * (int64_t)kXaBytes, coefs + n); };
+    const Column16 gcol = {w.gout + b * w.gs[1] + h * w.gs[2], w.gs[0], col, a.V};
+    uint16_t v[4][4];
+    auto begin = [&]() {  // the last chunk's operands
+        const int n = chunks - 1;
+        if (!PAIRS || all_waves < W) {
+            fetch(n);
+            load_rows<WIDE>(gcol, n * kC, length - n * kC, lane, v);
+            stage.store(smem + (n & 1) * kBuf);
+        }
+        lds_barrier();
+    };
+    // A^T gO, whose 16-bit values are exact in one term
+    auto from_outputs = [&](const uint8_t *buf, const f4 (&G)[4], f4 (&D)[4]) {
+        const uint16_t *ah = (const uint16_t *)(buf + kKeys) + 2 * kTriangle, *al = ah + kTriangle;
+        const Power p = column_power(G, lane);
+        h8 one[2];
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) one[s][i] = (_Float16)(G[2 * s + i / 4][i % 4] * p.inv);
+        const float up = p.back * ((const RowCoef *)(buf + kKeys + Stage::kXa))->a;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            f4 d = {};
+#pragma unroll
+            for (int s = t / 2; s < 2; ++s) {
+                d = mma(triangle_turned(al, ts_at, t, s), one[s], d);
+                d = mma(triangle_turned(ah, ts_at, t, s), one[s], d);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) D[t][i] = __builtin_fmaf(d[i], up, D[t][i]);
+        }
+    };
+    if constexpr (PAIRS)
+        if (all_waves < W) {
+            if (chunks > 0) begin();
+            for (int n = chunks - 1; n >= 0; --n) {
+                const uint8_t *buf = smem + (n & 1) * kBuf;
+                const uint16_t *qt = (const uint16_t *)buf + kC * KP;
+                const RowCoef *coef = (const RowCoef *)(buf + kKeys + Stage::kXa);
+                const int next = n > 0 ? n - 1 : 0;
+                fetch(next);
+                f4 G[4], D[4] = {};
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) G[t][i] = to_f32<DT>(v[t][i]);
+                load_rows<WIDE>(gcol, next * kC, length - next * kC, lane, v);
+                from_outputs(buf, G, D);
+#pragma unroll
+                for (int t = 0; t < 4; ++t) given->u[wave][t][lane] = D[t];
+                lds_barrier();  // A^T gO is there
+#pragma unroll
+                for (int t = 0; t < 4; ++t) G[t] *= *(const f4 *)(coef->q + row_of(t, 4 * grp));
+                const Power p = column_power(G, lane);
+                const Split g0 = split(G[0], G[1], p.inv), g1 = split(G[2], G[3], p.inv);
+#pragma unroll
+                for (int t = 0; t < KT; t += 4) {
+                    f4 x[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[i] = mma(left_turned<KP>(qt, tk_at, t + i, 0), g0.lo, f4{});
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[i] = mma(left_turned<KP>(qt, tk_at, t + i, 1), g1.lo, x[i]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[i] = mma(left_turned<KP>(qt, tk_at, t + i, 0), g0.hi, x[i]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[i] = mma(left_turned<KP>(qt, tk_at, t + i, 1), g1.hi, x[i]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) given->s[wave][t + i][lane] = p.back * x[i];
+                }
+                lds_barrier();  // and Q~^T (q gO)
+                stage.store(smem + (~n & 1) * kBuf);
+                lds_barrier();  // as below
+            }
+            return;
+        }
     f4 S[KT];  // the gradient of the state
 #pragma unroll
     for (int t = 0; t < KT; ++t)
@@ -66,31 +157,18 @@ __global__ void __launch_bounds__(W *kWave) delta_walk_back(Delta a, Records rec
             const int k = row_of(t, 4 * grp + i);
             S[t][i] = w.gfinal && k < a.K && mine ? w.gfinal[((int64_t)bh * a.K + k) * a.V + col] : 0.0f;
         }
-    const uint8_t *key = rec.key + (int64_t)(b * a.G + g) * rec.chunks * key_bytes(KP);
-    const uint8_t *xa = rec.xa + (int64_t)bh * rec.chunks * kXaBytes;
-    const RowCoef *coefs = rec.coef + (int64_t)bh * rec.chunks;
-    Stage stage;
-    auto fetch = [&](int n) { stage.load(key + n * (int64_t)key_bytes(KP), xa + n * (int64_t)kXaBytes, coefs + n); };
-    const Column16 gcol = {w.gout + b * w.gs[1] + h * w.gs[2], w.gs[0], col, a.V};
     const uint32_t gv_row = 2u * (uint32_t)(a.B * a.H) * a.V;  // bytes
     const uint32_t gv_at = mine ? 8 * grp * gv_row + 2 * (h * a.V + col) : kNowhere;
     float *keep_s = w.gstates + ((int64_t)bh * rec.chunks * KP + 8 * grp) * VP + col;
     float *keep_y = w.y + ((int64_t)bh * rec.chunks * kC + 8 * grp) * VP + col;
-    uint16_t v[4][4];
-    if (chunks > 0) {
-        const int n = chunks - 1;
-        fetch(n);
-        load_rows<WIDE>(gcol, n * kC, length - n * kC, lane, v);
-        stage.store(smem + (n & 1) * kBuf);
-        lds_barrier();
-    }
+    if (chunks > 0) begin();
     for (int n = chunks - 1; n >= 0; --n) {
         const uint8_t *buf = smem + (n & 1) * kBuf;
         const uint16_t *kt = (const uint16_t *)buf, *qt = kt + kC * KP;
-        const uint16_t *xh = (const uint16_t *)(buf + kKeys), *xl = xh + kTriangle, *ah = xl + kTriangle, *al = ah + kTriangle;
+        const uint16_t *xh = (const uint16_t *)(buf + kKeys), *xl = xh + kTriangle;
         const RowCoef *coef = (const RowCoef *)(buf + kKeys + Stage::kXa);
         const int next = n > 0 ? n - 1 : 0;
-        fetch(next);
+        if (!PAIRS) fetch(next);
         {
             float *to = keep_s + (int64_t)n * KP * VP;
 #pragma unroll
@@ -99,11 +177,13 @@ __global__ void __launch_bounds__(W *kWave) delta_walk_back(Delta a, Records rec
                 for (int i = 0; i < 4; ++i) to[(row_of(t, 0) + i) * VP] = S[t][i];
         }
         f4 G[4], D[4] = {};
+        if constexpr (!PAIRS) {
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
+            for (int t = 0; t < 4; ++t)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) G[t][i] = to_f32<DT>(v[t][i]);
-        load_rows<WIDE>(gcol, next * kC, length - next * kC, lane, v);
+                for (int i = 0; i < 4; ++i) G[t][i] = to_f32<DT>(v[t][i]);
+            load_rows<WIDE>(gcol, next * kC, length - next * kC, lane, v);
+        }
         // u K~ gS1
         {
             const Power p = column_power(S, lane);
@@ -121,26 +201,13 @@ __global__ void __launch_bounds__(W *kWave) delta_walk_back(Delta a, Records rec
 #pragma unroll
             for (int t = 0; t < 4; ++t) D[t] *= *(const f4 *)(coef->u + row_of(t, 4 * grp)) * p.back;
         }
-        // + A^T gO, whose 16-bit values are exact in one term
-        {
-            const Power p = column_power(G, lane);
-            h8 one[2];
+        // + A^T gO
+        if constexpr (PAIRS) {
+            lds_barrier();
 #pragma unroll
-            for (int s = 0; s < 2; ++s)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) one[s][i] = (_Float16)(G[2 * s + i / 4][i % 4] * p.inv);
-            const float up = p.back * coef->a;
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                f4 d = {};
-#pragma unroll
-                for (int s = t / 2; s < 2; ++s) {
-                    d = mma(triangle_turned(al, ts_at, t, s), one[s], d);
-                    d = mma(triangle_turned(ah, ts_at, t, s), one[s], d);
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) D[t][i] = __builtin_fmaf(d[i], up, D[t][i]);
-            }
+            for (int t = 0; t < 4; ++t) D[t] += given->u[wave][t][lane];
+        } else {
+            from_outputs(buf, G, D);
         }
         // Y = X^T gU
         f4 Y[4];
@@ -159,7 +226,7 @@ __global__ void __launch_bounds__(W *kWave) delta_walk_back(Delta a, Records rec
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
                 const int r = row_of(t, 4 * grp);
-                const f4 cp = *(const f4 *)(coef->p + r), cb = *(const f4 *)(coef->beta + r), cq = *(const f4 *)(coef->q + r);
+                const f4 cp = *(const f4 *)(coef->p + r), cb = *(const f4 *)(coef->beta + r);
                 const f4 x = cb * Y[t];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -167,11 +234,34 @@ __global__ void __launch_bounds__(W *kWave) delta_walk_back(Delta a, Records rec
                     __builtin_amdgcn_raw_buffer_store_b16(from_f32<DT>(x[i]), gv, gv_at + (row_of(t, 0) + i) * gv_row, 0, 0);
                 }
                 Y[t] = -cp * x;
-                G[t] *= cq;
+                if (!PAIRS) G[t] *= *(const f4 *)(coef->q + r);
             }
         }
-        // gS0, both products in one sum: their columns have one power of two
-        {
+        if constexpr (PAIRS) {
+            lds_barrier();  // Q~^T (q gO) is there
+            const Power p = column_power(Y, lane);
+            const Split y0 = split(Y[0], Y[1], p.inv), y1 = split(Y[2], Y[3], p.inv);
+            const float whole = coef->whole;
+#pragma unroll
+            for (int t = 0; t < KT; t += 4) {
+                f4 d[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) d[i] = mma(left_turned<KP>(kt, tk_at, t + i, 0), y0.lo, f4{});
+#pragma unroll
+                for (int i = 0; i < 4; ++i) d[i] = mma(left_turned<KP>(kt, tk_at, t + i, 1), y1.lo, d[i]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) d[i] = mma(left_turned<KP>(kt, tk_at, t + i, 0), y0.hi, d[i]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) d[i] = mma(left_turned<KP>(kt, tk_at, t + i, 1), y1.hi, d[i]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const f4 more = given->s[wave][t + i][lane];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        S[t + i][j] = __builtin_fmaf(whole, S[t + i][j], __builtin_fmaf(p.back, d[i][j], more[j]));
+                }
+            }
+        } else {  // both products in one sum: their columns have one power of two
             float big = 0.0f;
 #pragma unroll
             for (int t = 0; t < 4; ++t)
@@ -207,7 +297,7 @@ __global__ void __launch_bounds__(W *kWave) delta_walk_back(Delta a, Records rec
                     for (int j = 0; j < 4; ++j) S[t + i][j] = __builtin_fmaf(whole, S[t + i][j], p.back * d[i][j]);
             }
         }
-        stage.store(smem + (~n & 1) * kBuf);
+        if (!PAIRS) stage.store(smem + (~n & 1) * kBuf);
         lds_barrier();  // the next chunk's operands are there, and all waves are done with this one's
     }
     if (w.gstate) {
@@ -674,13 +764,13 @@ uint64_t part_bytes(const mccb_delta_t *a) { return 2 * chunks_of(a) * (uint64_t
 template <int DT, int KP, int W>
 void walk_back(const Delta &d, const Records &rec, Back w, hipStream_t st) {
     w.blocks = padded_v(d.V) / (16 * W);
-    const dim3 grid((unsigned)(d.B * d.H * w.blocks)), block(W * kWave);
+    const dim3 grid((unsigned)(d.B * d.H * w.blocks)), block((W == 2 ? 2 : 1) * W * kWave);
     if (row_buffer(w.gs[0], d.V)) hipLaunchKernelGGL((delta_walk_back<DT, KP, W, false>), grid, block, 0, st, d, rec, w);
     else hipLaunchKernelGGL((delta_walk_back<DT, KP, W, true>), grid, block, 0, st, d, rec, w);
 }
 template <int DT, int KP>
 int launch(const Delta &d, const Records &rec, const Back &w, hipStream_t st) {
-    if (KP == 128 && half_blocks(d, 1)) walk_back<DT, KP, KP == 128 ? 2 : 4>(d, rec, w, st);
+    if (half_blocks(d, 1)) walk_back<DT, KP, 2>(d, rec, w, st);
     else walk_back<DT, KP, 4>(d, rec, w, st);
     int rc = launched();
     if (rc != MCCB_OK || w.chunks == 0) return rc;

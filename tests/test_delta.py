@@ -148,8 +148,9 @@ def test_long_sequences_of_rows_that_overlap():
     assert all(torch.equal(p, q) for p, q in zip(*got))
 
 
-def test_more_heads_than_blocks_of_two_waves():
-    check(130, 35, 2, 1, 128, 128, "bf16", [130] * 30 + [0, 1, 64, 65, 129], "parts", seed=41)
+@pytest.mark.parametrize("B,K,dtype", [(35, 128, "bf16"), (40, 64, "fp16")])
+def test_more_heads_than_blocks_of_two_waves(B, K, dtype):
+    check(130, B, 2, 1, K, 128, dtype, [130] * (B - 5) + [0, 1, 64, 65, 129], "parts", seed=41)
 
 
 def test_tensors_of_more_than_2_31_values():
