@@ -3,8 +3,8 @@
 //
 // delta_prepare makes what a chunk has without a state: the images of its rows of k and q, X and A. One
 // block a chunk and key head; all chunks at once.
-// delta_walk goes over a head's chunks with the state in registers. A wave owns 16 columns of V
-// and nothing passes between waves: results of one product are the right operand of the next as they stand
+// delta_walk goes over a head's chunks with the state in registers. A wave owns 16 columns of V,
+// and nothing passes between waves (but to second ones that make outputs, where heads are few): results of one product are the right operand of the next as they stand
 // in the registers (row_of in delta_common.h), and the left operands, the same for all of a head's columns,
 // come from LDS, where the next chunk's are written when this one's are done with, from loads that
 // ran meanwhile.
@@ -355,13 +355,12 @@ struct Walk {
     float *state_out;               // or NULL
     uint16_t *out;                  // [S,B,H,V]
     float *states, *u;              // kept for the backward, padded: [B,H][chunk][K,V] and [B,H][chunk][64,V]; or NULL
-    float *ends;                    // [segment][B,H][K, V + K], padded: what delta_walk_segments finds
+    float *ends;                    // [segment][B,H][K, V + K], padded: what a first pass over segments finds
     float *carry;                   // [segment - 1][B,H][K,V], padded: the state before each segment but the first
     int chunks, per;                // chunks, and of a segment
     int segments;
     int blocks;                     // of columns, a head
 };
-
 
 // Bound by the vector and matrix instructions of one wave a SIMD, issued in 57 % of its cycles, and by what they wait for
 // (one product's largest values, then the next one's operands): S=4096 B=4 H=32 G=16 K=V=128, 241 us, 3.8 a chunk.
