@@ -245,3 +245,28 @@ def test_leaves_nothing_behind():
     torch.cuda.synchronize()
     assert torch.cuda.memory_allocated() == before
     assert [sys.getrefcount(o) for o in (v["q"], v["w"], bad)] == counts
+
+
+@pytest.mark.parametrize("S,B,H,G,K,V", [(700, 2, 8, 4, 128, 128), (1300, 1, 4, 4, 40, 70), (200, 20, 8, 8, 128, 128)])
+def test_calls_at_once_give_the_same_bits(S, B, H, G, K, V):
+    """On three streams, each with outputs and workspaces of its own."""
+    g = torch.Generator(device="cuda").manual_seed(S)
+    r = lambda *s: torch.randn(s, generator=g, device="cuda")  # noqa: E731
+    q, k, v, dt, b, go = (r(*s).to(BF) for s in ((S, B, G, K), (S, B, G, K), (S, B, H, V), (S, B, H), (S, B, H), (S, B, H, V)))
+    A, state = -torch.rand(H, generator=g, device="cuda") * 4, r(B, H, K, V)
+
+    def calls():
+        out, end, saved = mdc.delta_forward(q, k, v, dt, b, A, state=state, return_state=True, return_saved=True)
+        gr = mdc.delta_backward(go, q, k, v, dt, b, A, saved, state=state, gradFinalState=state)
+        return [out, end, *(x for x in gr if x is not None)]
+
+    want = calls()
+    torch.cuda.synchronize()
+    announce(f"three streams at once, S={S}")
+    streams, got = [torch.cuda.Stream() for _ in range(3)], []
+    for i in range(9):
+        with torch.cuda.stream(streams[i % 3]):
+            got.append(calls())
+    torch.cuda.synchronize()
+    for one in got:
+        assert all(torch.equal(x, y) for x, y in zip(one, want))
