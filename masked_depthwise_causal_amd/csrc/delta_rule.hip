@@ -832,7 +832,8 @@ int all_chunks(const Delta &d, const Records &rec, const Walk &w, hipStream_t st
 
 // Segments of a walk, by what it costs: 3.2 us a chunk where a wave has a SIMD to itself, with outputs and also
 // without (two waves a SIMD then, of 1024 SIMDs), 3 us to carry a state over a segment, and 10 us for two more launches
-// and their ends. S=16384 B=1 H=16: 812 us as one segment, 285 as eight; S=777 B=5 H=6: 43 as one, 52 as three.
+// and their ends. S=16384 B=1 H=16: 812 us as one segment, 285 as eight; S=777 B=5 H=6: 43 as one
+// (38 with second waves), 52 as three.
 struct Cut {
     int segments, per;
 };
