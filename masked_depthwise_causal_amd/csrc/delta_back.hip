@@ -54,7 +54,7 @@ template <int DT, int KP, int W, bool WIDE>
 __global__ void __launch_bounds__((W == 2 ? 2 : 1) * W *kWave, 1) delta_walk_back(Delta a, Records rec, Back w) {
     constexpr bool PAIRS = W == 2;
     constexpr int KT = KP / 16, KS = KP / 32;
-    typedef Staged<KP, W, 2> Stage;
+    typedef Staged<KP, W, true> Stage;
     constexpr int kBuf = Stage::kBytes, kKeys = Stage::kKeys;
     __shared__ __align__(16) uint8_t smem[2 * kBuf + (PAIRS ? (int)sizeof(Given<KP, W>) : 0)];
     Given<KP, W> *const given = (Given<KP, W> *)(smem + 2 * kBuf);
@@ -214,7 +214,7 @@ __global__ void __launch_bounds__((W == 2 ? 2 : 1) * W *kWave, 1) delta_walk_bac
         {
             const Power p = column_power(D, lane);
             const float up = p.back * coef->x;
-            triangle_times<true, 2>(xh, xl, ts_at, split(D[0], D[1], p.inv), split(D[2], D[3], p.inv), Y);
+            triangle_times<true>(xh, xl, ts_at, split(D[0], D[1], p.inv), split(D[2], D[3], p.inv), Y);
 #pragma unroll
             for (int t = 0; t < 4; ++t) Y[t] *= up;
         }

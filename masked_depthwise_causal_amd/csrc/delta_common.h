@@ -252,9 +252,9 @@ __device__ static inline Power column_power(const f4 (&v)[N], int lane) {
     return turned_sign(power_of(column_max(m)), lane);
 }
 
-// A triangle of two terms (or one, of `hi` alone) times 64 rows of 16 columns, s0 and s1 (one term too); TURNED: the
-// transposed matrix. The terms go by in turns, since a product waits for the last one with the same sum.
-template <bool TURNED, int TERMS>
+// A triangle of two terms times 64 rows of 16 columns, s0 and s1; TURNED: the transposed matrix. The terms go by in
+// turns, since a product waits for the last one with the same sum.
+template <bool TURNED>
 __device__ static inline void triangle_times(const uint16_t *hi, const uint16_t *lo, int place, const Split &s0,
                                              const Split &s1, f4 (&r)[4]) {
     h8 h[4][2], l[4][2];
@@ -264,12 +264,12 @@ __device__ static inline void triangle_times(const uint16_t *hi, const uint16_t 
         for (int s = 0; s < 2; ++s) {
             if (TURNED ? s < t / 2 : s > t / 2) continue;
             h[t][s] = TURNED ? triangle_turned(hi, place, t, s) : triangle(hi, place, t, s);
-            if (TERMS > 1) l[t][s] = TURNED ? triangle_turned(lo, place, t, s) : triangle(lo, place, t, s);
+            l[t][s] = TURNED ? triangle_turned(lo, place, t, s) : triangle(lo, place, t, s);
         }
 #pragma unroll
     for (int t = 0; t < 4; ++t) r[t] = f4{};
 #pragma unroll
-    for (int term = TERMS > 1 ? 0 : 2; term < 3; ++term)
+    for (int term = 0; term < 3; ++term)
 #pragma unroll
         for (int s = 0; s < 2; ++s)
 #pragma unroll
@@ -417,10 +417,10 @@ __device__ static inline void load_rows(const Column16 &c, int row0, int rows, i
 // A chunk's operands on their way to LDS: read into registers when the last chunk begins, written when it ends. (Loads
 // straight to LDS need no registers, but while one is under way the compiler has any use of any other load wait
 // for all of them.)
-// A_TERMS: of A, 0 with nothing for outputs: neither A nor the image of q.
-template <int KP, int W, int A_TERMS>
+// OUTPUTS: false where none are made: neither A nor the image of q then.
+template <int KP, int W, bool OUTPUTS>
 struct Staged {
-    static constexpr int kThreads = W * kWave, kKeys = (A_TERMS > 0 ? 2 : 1) * kC * KP * 2, kXa = (2 + A_TERMS) * kTriangle * 2;
+    static constexpr int kThreads = W * kWave, kKeys = (OUTPUTS ? 2 : 1) * kC * KP * 2, kXa = (OUTPUTS ? 4 : 2) * kTriangle * 2;
     static constexpr int kBytes = kKeys + kXa + (int)sizeof(RowCoef);
     static constexpr int kOfKeys = kKeys / 16 / kThreads, kOfXa = kXa / 16 / kThreads;
     static constexpr int kRest = (kXa - kOfXa * 16 * kThreads) / 8 / kThreads, kOfCoef = (int)sizeof(RowCoef) / 4 / kThreads;

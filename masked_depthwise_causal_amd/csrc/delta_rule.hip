@@ -139,7 +139,7 @@ struct RawRows {
     }
 };
 
-// A triangular 64x64 matrix in LDS as two terms in memory (or the first alone); returns the power of two taken out.
+// A triangular 64x64 matrix in LDS as two terms in memory; returns the power of two taken out.
 __device__ static __forceinline__ float image_square(const float *m, uint16_t *hi, uint16_t *lo, float *part, int tid) {
     const int row = tid / 4, c0 = tid % 4 * 16;
     f4 v[4];
@@ -161,7 +161,7 @@ __device__ static __forceinline__ float image_square(const float *m, uint16_t *h
             const Split s = split(v[2 * i], v[2 * i + 1], p.inv);
             const int at = block_of(row / 32, c0 / 32) + block_at(row % 32, c0 % 32 / 8 + i);
             *(h8 *)(hi + at) = s.hi;
-            if (lo) *(h8 *)(lo + at) = s.lo;
+            *(h8 *)(lo + at) = s.lo;
         }
     return p.back;
 }
@@ -235,7 +235,7 @@ __device__ static __forceinline__ void invert(const float *L, float *X, int wave
 // Bound by what it writes, and by the chain of products in X's blocks where there are few chunks: S=4096 B=4 H=32 G=16
 // K=V=128, 4096 blocks, 122 us for 325 MB written and 138 read (3.8 TB/s); S=513 B=2 H=6 G=3 K=64, 54 blocks, 13 us.
 template <int DT, int KP>
-__global__ void __launch_bounds__(kPrepThreads, 4) delta_prepare(Delta a, Records rec, int n0, int a_terms) {
+__global__ void __launch_bounds__(kPrepThreads, 4) delta_prepare(Delta a, Records rec, int n0) {
     constexpr int kImages = 2 * kC * KP * (int)sizeof(uint16_t), kSquares = 2 * kC * kLd * (int)sizeof(float);
     __shared__ __align__(16) uint8_t smem[kImages > kSquares ? kImages : kSquares];  // rows first, then L, X
     __shared__ float kr[kC], qr[kC], beta[kC], part[4];
@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prepare(Delta a, Record
             }
         }
         lds_barrier();
-        const float sa = image_square(P, xa + 2 * kTriangle, a_terms > 1 ? xa + 3 * kTriangle : nullptr, part, tid);
+        const float sa = image_square(P, xa + 2 * kTriangle, xa + 3 * kTriangle, part, tid);
         lds_barrier();
         invert(X, P, wave, tid);
         const float sx = image_square(P, xa, xa + kTriangle, part, tid);
@@ -341,11 +341,10 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prepare(Delta a, Record
 // ---------------------------------------------------------------------------------------------
 // The walk.
 // ---------------------------------------------------------------------------------------------
-constexpr int terms_of(int dt) { return dt == MCCB_BF16 ? 1 : 2; }
 // What a wave with a state hands to the one that makes its outputs.
-template <int KP, int W, int TERMS>
+template <int KP, int W>
 struct Handed {
-    h8 s[W][KP / 32][TERMS > 0 ? TERMS : 1][kWave];     // S0 as a right operand
+    h8 s[W][KP / 32][2][kWave];     // S0 as a right operand
     f4 u[W][4][kWave];
     float s_back[W][16], u_up[W][16];
 };
@@ -365,8 +364,6 @@ struct Walk {
 // Bound by the vector and matrix instructions of one wave a SIMD, issued in 57 % of its cycles, and by what they wait for
 // (one product's largest values, then the next one's operands): S=4096 B=4 H=32 G=16 K=V=128, 241 us, 3.8 a chunk.
 // Training, S=2048 B=4 H=16, 129 us, of which the kept states and U (201 MB) are some 30.
-// TERMS: those of what only the output is made of, A U and Q~ S0. Its 16 bits are the last rounding (2^-9 of a bf16
-// value), next to which one fp16 term of A, U and S0 (2^-12 each) does not count; fp16 outputs take two.
 // KEEP: the states and U are kept. (Two waves a SIMD would fit: with all of a SIMD's registers the compiler has the
 // products' results in accumulation registers and moves each of them.)
 // SEGMENTS: where there are few heads, the first pass of two over a sequence that is cut into segments, all at once:
@@ -381,9 +378,8 @@ template <int DT, int KP, int W, bool KEEP, bool WIDE, bool SEGMENTS>
 __global__ void __launch_bounds__((W == 2 ? 2 : 1) * W *kWave, 2) delta_walk(Delta a, Records rec, Walk w) {
     constexpr bool PAIRS = W == 2;
     constexpr int KT = KP / 16, KS = KP / 32;
-    constexpr int TERMS = SEGMENTS ? 0 : terms_of(DT);
-    typedef Staged<KP, W, TERMS> Stage;
-    typedef Handed<KP, W, TERMS> Pairs;
+    typedef Staged<KP, W, !SEGMENTS> Stage;
+    typedef Handed<KP, W> Pairs;
     constexpr int kBuf = Stage::kBytes, kKeys = Stage::kKeys;
     __shared__ __align__(16) uint8_t smem[2 * kBuf + (PAIRS ? (int)sizeof(Pairs) : 0)];
     Pairs *const handed = (Pairs *)(smem + 2 * kBuf);
@@ -415,7 +411,7 @@ __global__ void __launch_bounds__((W == 2 ? 2 : 1) * W *kWave, 2) delta_walk(Del
         const RowCoef *coef = (const RowCoef *)(buf + kKeys + Stage::kXa);
         const Power p = column_power(U, lane);
         f4 AU[4];
-        triangle_times<false, TERMS>(ah, al, ls_at, split(U[0], U[1], p.inv), split(U[2], U[3], p.inv), AU);
+        triangle_times<false>(ah, al, ls_at, split(U[0], U[1], p.inv), split(U[2], U[3], p.inv), AU);
         const float back = p.back * up * coef->a;
         const int left_rows = a.S - n * kC;
         const Buffer to = buffer_of(w.out + (int64_t)n * kC * (out_row / 2) + (int64_t)b * a.H * a.V,
@@ -445,7 +441,7 @@ __global__ void __launch_bounds__((W == 2 ? 2 : 1) * W *kWave, 2) delta_walk(Del
 #pragma unroll
                 for (int s = 0; s < KS; ++s)
 #pragma unroll
-                    for (int term = TERMS - 1; term >= 0; --term) {
+                    for (int term = 1; term >= 0; --term) {
                         const h8 x = handed->s[wave][s][term][lane];
 #pragma unroll
                         for (int t = 0; t < 4; ++t) O[t] = mma(left<KP>(qt, lk_at, t, s), x, O[t]);
@@ -500,7 +496,7 @@ __global__ void __launch_bounds__((W == 2 ? 2 : 1) * W *kWave, 2) delta_walk(Del
             const Split sp = split(S[2 * s], S[2 * s + 1], ps.inv);
             if constexpr (PAIRS) {
                 handed->s[wave][s][0][lane] = sp.hi;
-                if (TERMS > 1) handed->s[wave][s][TERMS - 1][lane] = sp.lo;
+                handed->s[wave][s][1][lane] = sp.lo;
             }
             h8 lk[4], lq[4];
 #pragma unroll
@@ -511,7 +507,7 @@ __global__ void __launch_bounds__((W == 2 ? 2 : 1) * W *kWave, 2) delta_walk(Del
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
                 P[t] = mma(lk[t], sp.lo, P[t]);
-                if (TERMS > 1 && !PAIRS) O[t] = mma(lq[t], sp.lo, O[t]);
+                if (!SEGMENTS && !PAIRS) O[t] = mma(lq[t], sp.lo, O[t]);
             }
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
@@ -539,7 +535,7 @@ __global__ void __launch_bounds__((W == 2 ? 2 : 1) * W *kWave, 2) delta_walk(Del
         {
             const Power p = column_power(R, lane);
             up = p.back * coef->x;
-            triangle_times<false, 2>(xh, xl, ls_at, split(R[0], R[1], p.inv), split(R[2], R[3], p.inv), U);
+            triangle_times<false>(xh, xl, ls_at, split(R[0], R[1], p.inv), split(R[2], R[3], p.inv), U);
         }
         if (KEEP) {
             float *to = keep_u + (int64_t)n * kC * VP;
@@ -793,9 +789,9 @@ __global__ void __launch_bounds__(kStepThreads) delta_one(Delta a, float *state,
 // Host side.
 // ---------------------------------------------------------------------------------------------
 template <int DT, int KP>
-int prepare(const Delta &d, const Records &rec, int n0, int n1, bool keep, hipStream_t st) {
+int prepare(const Delta &d, const Records &rec, int n0, int n1, hipStream_t st) {
     hipLaunchKernelGGL((delta_prepare<DT, KP>), dim3((unsigned)(n1 - n0), (unsigned)(d.B * d.G)), dim3(kPrepThreads),
-                       0, st, d, rec, n0, keep || DT == MCCB_FP16 ? 2 : 1);
+                       0, st, d, rec, n0);
     return launched();
 }
 template <int DT, int KP, int W, bool KEEP, bool SEGMENTS>
@@ -818,7 +814,7 @@ int walk(const Delta &d, const Records &rec, const Walk &w, hipStream_t st) {
 template <int DT, int KP>
 int all_chunks(const Delta &d, const Records &rec, const Walk &w, hipStream_t st) {
     int rc = MCCB_OK;
-    if (w.chunks > 0) rc = prepare<DT, KP>(d, rec, 0, w.chunks, w.states != nullptr, st);
+    if (w.chunks > 0) rc = prepare<DT, KP>(d, rec, 0, w.chunks, st);
     if (rc == MCCB_OK && w.segments > 1) {
         rc = walk<DT, KP, false, true>(d, rec, w, st);
         if (rc != MCCB_OK) return rc;
