@@ -21,6 +21,12 @@
 // E is Z o Q~ K~^T + W o K~ K~^T below the diagonal. (The diagonal, whose two sums cancel, is left out, and
 // the sums are in fp64, since most of what they add cancels too: a row that has nothing before it gets
 // exactly 0. The same gradient from gO.out - gV.V, which costs nothing, comes out to 1e-5 only.)
+//
+// A row's kr and qr may be anything: 1/|k~|, 1000 times 2^e for a row whose square is below 1e-6, 2^e where nothing is
+// normalized. Z and W, which are split with one power of two each, would hold the small rows' values next to the
+// others', and gk = 2^-e gK~ would make up for it with nothing left. So kr = s c m: s a power of two for the chunk, c
+// one for the row, 1 for the largest, and m, about the same for all. The rows' images are multiplied by c, what is
+// called gK~ and gQ~ below is without c and s, and Z and W have m only.
 #include "delta_common.h"
 
 using namespace delta;
@@ -336,6 +342,8 @@ __device__ static inline float pick(const f4 (&v)[4], int n) {
     const float x = n & 1 ? r[1] : r[0], y = n & 1 ? r[3] : r[2];
     return n & 2 ? y : x;
 }
+__device__ static inline int exponent(float v) { return (int)(__float_as_uint(v) >> 23 & 255) - 127; }
+__device__ static inline float uniform(float v) { return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(v))); }
 __device__ static inline float largest(const f4 &x, const f4 &y, float m) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) m = __builtin_fmaxf(m, __builtin_fmaxf(__builtin_fabsf(x[i]), __builtin_fabsf(y[i])));
@@ -355,8 +363,8 @@ __global__ void __launch_bounds__(KP / 16 * kWave) delta_grads(Delta a, Records 
     constexpr int kPer = kThreads / kC, kCols = 64 / kPer;  // staging: threads of a row, columns of a thread
     __shared__ __align__(16) uint16_t kt[kC * KP], qt[kC * KP];
     __shared__ __align__(16) uint16_t stage[5 * kSquare];  // gO, U hi, U lo, Y hi, Y lo; then Z and W in two terms
-    __shared__ __align__(16) float po[kC], pu[kC], py[kC], coef[4 * kC], kr[kC], qr[kC];
-    __shared__ float rowf[W][kC], rowe[W][kC], yu[kC], big[2][W];
+    __shared__ __align__(16) float po[kC], pu[kC], py[kC], coef[4 * kC], kr[kC], qr[kC], unit[2][kC];
+    __shared__ float rowf[W][kC], rowe[W][kC], yu[kC], big[2][W], size[2];
     __shared__ double cum[kC], dots[W], erow[kSide][kC], ecol[4][kC];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     int lane = threadIdx.x % kWave, m = lane & 15, grp = lane >> 4;
@@ -382,13 +390,36 @@ __global__ void __launch_bounds__(KP / 16 * kWave) delta_grads(Delta a, Records 
         return;
     }
     const uint8_t *key = rec.key + ((int64_t)(b * a.G + g) * rec.chunks + n) * key_bytes(KP);
-    const float *factors = (const float *)(key + 2 * kC * KP * 2);
-    for (int i = threadIdx.x; i < kC * KP / 8; i += kThreads) {
-        ((h8 *)kt)[i] = ((const h8 *)key)[i];
-        ((h8 *)qt)[i] = ((const h8 *)key)[kC * KP / 8 + i];
+    constexpr int kTurns = kC * KP / 8 / kThreads;
+    h8 kraw[kTurns], qraw[kTurns];
+#pragma unroll
+    for (int i = 0; i < kTurns; ++i) {
+        kraw[i] = ((const h8 *)key)[threadIdx.x + i * kThreads];
+        qraw[i] = ((const h8 *)key)[kC * KP / 8 + threadIdx.x + i * kThreads];
     }
-    if (threadIdx.x < kC) kr[threadIdx.x] = factors[threadIdx.x], qr[threadIdx.x] = factors[kC + threadIdx.x];
+    if (wave < 2) {  // the rows' factors, of k and of q
+        const float *factors = (const float *)(key + 2 * kC * KP * 2);
+        const float f = factors[wave * kC + lane], back = factors[(2 + wave) * kC + lane];
+        const float most = column_max(max16(back > 0.0f ? f : 0.0f));
+        // m is 2^-15..2^-14. s stays where its square is a number; c is above 1 for rows of zeros only
+        int s = most > 0.0f ? exponent(most) + 15 : 0;
+        s = s < -60 ? -60 : s > 60 ? 60 : s;
+        int c = exponent(f) + 15 - s;
+        if (back > 0.0f && c > 0) c = 0;
+        (wave ? qr : kr)[lane] = __builtin_ldexpf(f, -s - c);
+        unit[wave][lane] = __builtin_ldexpf(__builtin_fabsf(back), s + c);
+        coef[wave * kC + lane] = __builtin_ldexpf(1.0f, c < 0 ? c : 0);
+        if (lane == 0) size[wave] = __builtin_ldexpf(1.0f, s);
+    }
     lds_barrier();
+#pragma unroll
+    for (int i = 0; i < kTurns; ++i) {
+        const int at = threadIdx.x + i * kThreads, r = at / (KP / 8);
+        ((h8 *)kt)[at] = kraw[i] * (_Float16)coef[r];
+        ((h8 *)qt)[at] = qraw[i] * (_Float16)coef[kC + r];
+    }
+    lds_barrier();
+    const float sk = uniform(size[0]), sq = uniform(size[1]), sqk = sq / sk;
     // this lane's values of K~ and Q~ in the results' layout
     h4 kd[4], qd[4];
     f4 aq[4] = {}, ak[4] = {};
@@ -406,8 +437,14 @@ __global__ void __launch_bounds__(KP / 16 * kWave) delta_grads(Delta a, Records 
         const RowCoef *rc = rec.coef + at;
         const float whole = rc->whole;
         lds_barrier();  // the last head's reads are done
-        if (threadIdx.x < 4 * kC) coef[threadIdx.x] = ((const float *)rc)[threadIdx.x];
-        if (threadIdx.x < kC) cum[threadIdx.x] = rc->cum[threadIdx.x];
+        if (threadIdx.x < 4 * kC) {  // as RowCoef has them, but for c and s
+            const int r = threadIdx.x % kC, which = threadIdx.x / kC;
+            const double G = rc->cum[r];
+            if (which == 0) cum[r] = G, coef[r] = exp2_f((float)G) * kr[r];
+            if (which == 1) coef[kC + r] = rc->beta[r];
+            if (which == 2) coef[2 * kC + r] = a.scale * exp2_f((float)G) * qr[r];
+            if (which == 3) coef[3 * kC + r] = exp2_f((float)(rc->cum[kC - 1] - G)) * kr[r];
+        }
         f4 da[NJ] = {}, dl[NJ] = {}, er[4] = {}, fr[4] = {};
         float s0s1 = 0.0f, dot_u = 0.0f;
         for (int v0 = 0; v0 < a.V; v0 += 64) {
@@ -504,7 +541,7 @@ __global__ void __launch_bounds__(KP / 16 * kWave) delta_grads(Delta a, Records 
                     const f4 fo = *(const f4 *)(po + r) * ps.back * *(const f4 *)(coef + 2 * kC + r);
                     const f4 fy = *(const f4 *)(py + r) * ps.back * *(const f4 *)(coef + r) * *(const f4 *)(coef + kC + r);
                     const f4 fu = *(const f4 *)(pu + r) * pg.back * *(const f4 *)(coef + 3 * kC + r);
-                    const f4 kf = anew(kd[t]), qf = anew(qd[t]);
+                    const f4 kf = anew(kd[t]), qf = anew(qd[t]) * sqk;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const float e = fu[i] * z[i], o = fo[i] * x[i], l = fy[i] * y[i];
@@ -573,7 +610,7 @@ __global__ void __launch_bounds__(KP / 16 * kWave) delta_grads(Delta a, Records 
                     const float decay = on ? exp2_f((float)(cum[r + i] - gc)) * kc : 0.0f;
                     da[j][i] = on ? a.scale * decay * qr[r + i] * da[j][i] : 0.0f;
                     dl[j][i] = below ? -coef[kC + r + i] * decay * kr[r + i] * dl[j][i] : 0.0f;
-                    const double e = below ? (double)__builtin_fmaf(da[j][i], qk[i], dl[j][i] * kk[i]) : 0.0;
+                    const double e = below ? (double)__builtin_fmaf(da[j][i], sq * sk * qk[i], dl[j][i] * (sk * sk * kk[i])) : 0.0;
                     er_[i] += e, ec += e;
                     mz = __builtin_fmaxf(mz, __builtin_fabsf(da[j][i]));
                     mw = __builtin_fmaxf(mw, __builtin_fabsf(dl[j][i]));
@@ -642,8 +679,8 @@ __global__ void __launch_bounds__(KP / 16 * kWave) delta_grads(Delta a, Records 
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    aq[t][i] = __builtin_fmaf(pz.back, x[i], aq[t][i]);
-                    ak[t][i] = __builtin_fmaf(pz.back, y[i], __builtin_fmaf(pw.back, z[i], ak[t][i]));
+                    aq[t][i] = __builtin_fmaf(pz.back * sk, x[i], aq[t][i]);
+                    ak[t][i] = __builtin_fmaf(pz.back * sq, y[i], __builtin_fmaf(pw.back * sk, z[i], ak[t][i]));
                 }
             }
         }
@@ -654,6 +691,7 @@ __global__ void __launch_bounds__(KP / 16 * kWave) delta_grads(Delta a, Records 
             double e = 0.0, f = 0.0, s0 = 0.0;
 #pragma unroll
             for (int i = 0; i < W; ++i) e += (double)rowe[i][r], f += (double)rowf[i][r], s0 += dots[i];
+            e *= (double)sk, f *= (double)sk;
             // gG, then its sum from a row on
             double s = f - e - (ecol[0][r] + ecol[1][r] + ecol[2][r] + ecol[3][r]);
 #pragma unroll
@@ -684,7 +722,7 @@ __global__ void __launch_bounds__(KP / 16 * kWave) delta_grads(Delta a, Records 
         }
     }
     lane = anew(threadIdx.x % kWave), m = lane & 15, grp = lane >> 4, kcol = 16 * wave + m;
-    // through the norms: gk = 2^-e (gK~ - K~ kr^2 (K~.gK~))
+    // through the norms: gk = 2^-e s c (gK~ - K~ (s m)^2 (K~.gK~))
     f4 qs[4], ks[4];
 #pragma unroll
     for (int t = 0; t < 4; ++t)
@@ -699,10 +737,10 @@ __global__ void __launch_bounds__(KP / 16 * kWave) delta_grads(Delta a, Records 
         float q = 0.0f, k = 0.0f;
 #pragma unroll
         for (int j = 0; j < W; ++j) q += rowf[j][r], k += rowe[j][r];
-        coef[r] = a.normalize ? q * qr[r] * qr[r] : 0.0f;
-        coef[kC + r] = a.normalize ? k * kr[r] * kr[r] : 0.0f;
-        coef[2 * kC + r] = factors[3 * kC + r];
-        coef[3 * kC + r] = factors[2 * kC + r];
+        coef[r] = a.normalize ? q * (sq * qr[r]) * (sq * qr[r]) : 0.0f;
+        coef[kC + r] = a.normalize ? k * (sk * kr[r]) * (sk * kr[r]) : 0.0f;
+        coef[2 * kC + r] = unit[1][r];
+        coef[3 * kC + r] = unit[0][r];
     }
     lds_barrier();
     // by way of LDS, in rows

@@ -38,8 +38,8 @@ typedef float f4 __attribute__((ext_vector_type(4)));
 // ---------------------------------------------------------------------------------------------
 // What one kernel hands to the next for a chunk. A key head's: the images of its rows of k and q, the factors
 // that make them normalized rows, kn = kr k~, qn = qr q~ (without the scale), and those of k~ = k 2^-e and
-// q~ = q 2^-e. A value head's: the
-// images of X and A in two terms each, and what belongs to single rows.
+// q~ = q 2^-e, negative for a row of zeros. A value head's: the images of X and A in two terms each, and what
+// belongs to single rows.
 // ---------------------------------------------------------------------------------------------
 struct RowCoef {
     float p[kC];        // exp(G) kr: V - p (K~ S0)

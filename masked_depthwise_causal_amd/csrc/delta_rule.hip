@@ -114,7 +114,6 @@ struct RawRows {
             for (int i = 0; i < 8; ++i) v[i] = to_f32<DT>(raw[t][i]), m = __builtin_fmaxf(m, __builtin_fabsf(v[i]));
             // the row's largest value is brought to 2^14..2^15
             m = max_over<kLanes>(m);
-            // (a row of zeros, whose factor would be 1000 next to the other rows' 1, has 2^-10 taken out)
             int e = m > 0.0f ? ((__float_as_uint(m) >> 23) & 255) - 127 - 14 : -10;
             e = e < -100 ? -100 : e > 126 ? 126 : e;
             h8 h;
@@ -131,9 +130,11 @@ struct RawRows {
             if (lane == 0) {
                 const float f = a.normalize ? 1.0f / __builtin_sqrtf(ss + __builtin_ldexpf(kNormEps, -2 * e))
                                             : __builtin_ldexpf(1.0f, e);
-                factor[r] = f;
+                // a row of zeros gets zeros from whatever its factor meets here, and must not be the largest of what is
+                // split; its gradient has the factor, and a sign that says so
+                factor[r] = m > 0.0f ? f : 0.0f;
                 factor_out[r] = f;
-                power_out[r] = __builtin_ldexpf(1.0f, -e);
+                power_out[r] = __builtin_ldexpf(m > 0.0f ? 1.0f : -1.0f, -e);
             }
         }
     }

@@ -18,6 +18,34 @@ from .test_delta import inputs, slack
 pytestmark = pytest.mark.gpu
 
 
+def both(v, go, gf=None, lengths=None, **opt):
+    """The 64-bit results, the outputs and the gradients."""
+    r = ref.delta(v["q"], v["k"], v["v"], v["dt"], v["b"], v["A"], v["dt_bias"], normalize=opt.get("normalize", True),
+                  lengths=lengths, state=v["state"], gout=go, gfinal=gf)
+    out, end, g = run(v, go, gf, lengths, **opt)
+    return r, out, end, g
+
+
+def run(v, go, gf=None, lengths=None, **opt):
+    d = {n: None if t is None else t.cuda() for n, t in v.items()}
+    ins = (d["q"], d["k"], d["v"], d["dt"], d["b"], d["A"])
+    opt |= {"dt_bias": d["dt_bias"], "state": d["state"],
+            "lengths": None if lengths is None else torch.tensor(lengths, device="cuda")}
+    out, end, saved = mdc.delta_forward(*ins, **opt, return_state=True, return_saved=True)
+    g = mdc.delta_backward(go.cuda(), *ins, saved, **opt, gradFinalState=None if gf is None else gf.cuda())
+    torch.cuda.synchronize()
+    return out, end, g
+
+
+def row_near(got, want, size, e, name):
+    """One row, or what is compared as one: its rounding, and e of `size`."""
+    half = torch.finfo(got.dtype).eps / 2
+    got = got.detach().cpu().to(F)
+    assert torch.isfinite(got).all(), name
+    off, allowed = float((got - want).norm()), float(half * want.norm() + e * size.norm())
+    assert off <= allowed, f"{name}: {off} of {float(want.norm())}, {allowed} allowed"
+
+
 @pytest.mark.parametrize("S,B,H,G,K,V", [(64, 2, 2, 2, 64, 64), (130, 35, 2, 1, 128, 128), (100, 3, 4, 2, 96, 80)])
 def test_outputs_in_bf16_are_rounded_once(S, B, H, G, K, V):
     """A value within d of the 64-bit one is another bf16 number than that one's for d of each rounding step, up to 2^-7 of
@@ -30,3 +58,41 @@ def test_outputs_in_bf16_are_rounded_once(S, B, H, G, K, V):
     once = r["out"].to(torch.bfloat16).to(F)
     off = float((out.cpu().to(F) - once).norm() / once.norm())
     assert off <= (2.0 ** -7 * slack(S)) ** 0.5, off
+
+
+def small_rows(power, normalize, dtype="bf16"):
+    v, go, gf = inputs(90, 1, 2, 1, 32, 24, dtype, 50, unit=normalize)
+    for name, rows in (("k", (20, 70)), ("q", (33, 34, 80))):
+        for i in rows:
+            v[name][i] *= 2.0 ** power
+    v["k"][10] = v["q"][12] = 0
+    return v, go, gf
+
+
+@pytest.mark.parametrize("power,normalize", [(-30, True), (-44, True), (-52, True), (-44, False), (-70, False)])
+def test_gradients_of_small_rows(power, normalize):
+    """Of q and k, each row next to its own size: they are g / sqrt(1e-6) where normalized, 1000 times the others'."""
+    v, go, gf = small_rows(power, normalize)
+    announce(f"small rows 2^{power}, normalize={normalize}")
+    r, _, _, g = both(v, go, gf, normalize=normalize)
+    for name, got in (("gk", g.k), ("gq", g.q)):
+        for i in range(90):
+            row_near(got[i], r[name][i], r[name + "_before"][i], 16 * slack(90), f"{name} row {i}")
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+def test_rows_of_zeros_beside_others(dtype):
+    """Keys and queries of zeros in one chunk, as padding has them: gradients of the other rows; and states of small keys."""
+    v, go, gf = inputs(90, 1, 2, 1, 32, 24, dtype, 54)
+    v["k"][10:12] = v["q"][11:13] = 0
+    announce(f"rows of zeros {dtype}")
+    r, _, _, g = both(v, go, gf)
+    for name, got in (("gk", g.k), ("gq", g.q)):
+        for i in range(90):
+            row_near(got[i], r[name][i], r[name + "_before"][i], 16 * slack(90), f"{name} row {i}")
+    if dtype == "bf16":
+        v, go, _ = inputs(90, 1, 2, 1, 32, 24, dtype, 55, unit=False, state=False)
+        v["k"] *= 2.0 ** -30
+        v["k"][10:12] = 0
+        r, _, end, _ = both(v, go, normalize=False)
+        ref.norm_close(end, r["state"], slack(90), "state")
