@@ -128,8 +128,11 @@ struct RawRows {
             *(h8 *)(lds + at) = h;
             *(h8 *)(to + at) = h;
             if (lane == 0) {
-                const float f = a.normalize ? 1.0f / __builtin_sqrtf(ss + __builtin_ldexpf(kNormEps, -2 * e))
-                                            : __builtin_ldexpf(1.0f, e);
+                // eps next to the row's square in whichever scale has them both as numbers
+                float f = __builtin_ldexpf(1.0f, e);
+                if (a.normalize)
+                    f = e < 0 ? f / __builtin_sqrtf(__builtin_ldexpf(ss, 2 * e) + kNormEps)
+                              : 1.0f / __builtin_sqrtf(ss + __builtin_ldexpf(kNormEps, -2 * e));
                 // a row of zeros gets zeros from whatever its factor meets here, and must not be the largest of what is
                 // split; its gradient has the factor, and a sign that says so
                 factor[r] = m > 0.0f ? f : 0.0f;

@@ -69,7 +69,7 @@ def small_rows(power, normalize, dtype="bf16"):
     return v, go, gf
 
 
-@pytest.mark.parametrize("power,normalize", [(-30, True), (-44, True), (-52, True), (-44, False), (-70, False)])
+@pytest.mark.parametrize("power,normalize", [(-30, True), (-44, True), (-52, True), (-65, True), (-90, True), (-44, False), (-70, False)])
 def test_gradients_of_small_rows(power, normalize):
     """Of q and k, each row next to its own size: they are g / sqrt(1e-6) where normalized, 1000 times the others'."""
     v, go, gf = small_rows(power, normalize)
