@@ -90,16 +90,19 @@ __global__ void __launch_bounds__((W == 2 ? 2 : 1) * W *kWave, 1) delta_walk_bac
         }
         lds_barrier();
     };
-    // A^T gO, whose 16-bit values are exact in one term
+    // A^T gO, whose 16-bit values, with A's powers of two, are exact in one term
     auto from_outputs = [&](const uint8_t *buf, const f4 (&G)[4], f4 (&D)[4]) {
         const uint16_t *ah = (const uint16_t *)(buf + kKeys) + 2 * kTriangle, *al = ah + kTriangle;
-        const Power p = column_power(G, lane);
+        const RowCoef *coef = (const RowCoef *)(buf + kKeys + Stage::kXa);
+        f4 R[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) R[t] = G[t] * *(const f4 *)(coef->a + row_of(t, 4 * grp));
+        const Power p = column_power(R, lane);
         h8 one[2];
 #pragma unroll
         for (int s = 0; s < 2; ++s)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) one[s][i] = (_Float16)(G[2 * s + i / 4][i % 4] * p.inv);
-        const float up = p.back * ((const RowCoef *)(buf + kKeys + Stage::kXa))->a;
+            for (int i = 0; i < 8; ++i) one[s][i] = (_Float16)(R[2 * s + i / 4][i % 4] * p.inv);
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
             f4 d = {};
@@ -109,7 +112,7 @@ __global__ void __launch_bounds__((W == 2 ? 2 : 1) * W *kWave, 1) delta_walk_bac
                 d = mma(triangle_turned(ah, ts_at, t, s), one[s], d);
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) D[t][i] = __builtin_fmaf(d[i], up, D[t][i]);
+            for (int i = 0; i < 4; ++i) D[t][i] = __builtin_fmaf(d[i], p.back, D[t][i]);
         }
     };
     if constexpr (PAIRS)

@@ -47,10 +47,11 @@ struct RowCoef {
     float q[kC];        // scale exp(G) qr
     float u[kC];        // exp(G[C-1] - G) kr
     float whole;        // exp(G[C-1])
-    float x, a;         // X = x (hi + lo), A = a (hi + lo)
-    float pad[13];
+    float x;            // X = x (hi + lo)
+    float pad[14];
     double cum[kC];     // G in units of log 2
-    float pad2[112];
+    float a[kC];        // A's rows = a (hi + lo): as small as the rows of q, and as what they make
+    float pad2[48];
 };
 static_assert(sizeof(RowCoef) == 2048, "two of the walks' loads");
 

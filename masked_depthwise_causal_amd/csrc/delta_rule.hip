@@ -143,7 +143,9 @@ struct RawRows {
     }
 };
 
-// A triangular 64x64 matrix in LDS as two terms in memory; returns the power of two taken out.
+// A triangular 64x64 matrix in LDS as two terms in memory; returns the power of two taken out, of the whole matrix or
+// (ROWS) of the thread's row, tid / 4.
+template <bool ROWS>
 __device__ static __forceinline__ float image_square(const float *m, uint16_t *hi, uint16_t *lo, float *part, int tid) {
     const int row = tid / 4, c0 = tid % 4 * 16;
     f4 v[4];
@@ -154,10 +156,14 @@ __device__ static __forceinline__ float image_square(const float *m, uint16_t *h
 #pragma unroll
         for (int j = 0; j < 4; ++j) big = __builtin_fmaxf(big, __builtin_fabsf(v[i][j]));
     }
-    big = column_max(max16(big));
-    if (tid % kWave == 0) part[tid / kWave] = big;
-    lds_barrier();
-    big = __builtin_fmaxf(__builtin_fmaxf(part[0], part[1]), __builtin_fmaxf(part[2], part[3]));
+    if (ROWS) {
+        big = max_over<4>(big);
+    } else {
+        big = column_max(max16(big));
+        if (tid % kWave == 0) part[tid / kWave] = big;
+        lds_barrier();
+        big = __builtin_fmaxf(__builtin_fmaxf(part[0], part[1]), __builtin_fmaxf(part[2], part[3]));
+    }
     const Power p = power_of(big);
     if (c0 / 32 <= row / 32)
 #pragma unroll
@@ -326,10 +332,11 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prepare(Delta a, Record
             }
         }
         lds_barrier();
-        const float sa = image_square(P, xa + 2 * kTriangle, xa + 3 * kTriangle, part, tid);
+        const float sa = image_square<true>(P, xa + 2 * kTriangle, xa + 3 * kTriangle, part, tid);
+        if (tid % 4 == 0) coef->a[tid / 4] = sa;
         lds_barrier();
         invert(X, P, wave, tid);
-        const float sx = image_square(P, xa, xa + kTriangle, part, tid);
+        const float sx = image_square<false>(P, xa, xa + kTriangle, part, tid);
         if (wave == 0) {
             const float ek = exp2_f((float)mine), k1 = kr[lane];
             coef->p[lane] = ek * k1;
@@ -337,7 +344,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prepare(Delta a, Record
             coef->q[lane] = a.scale * ek * qr[lane];
             coef->u[lane] = exp2_f((float)(total - mine)) * k1;
             coef->cum[lane] = mine;
-            if (lane == 0) coef->whole = exp2_f((float)total), coef->x = sx, coef->a = sa;
+            if (lane == 0) coef->whole = exp2_f((float)total), coef->x = sx;
         }
     }
 }
@@ -416,16 +423,17 @@ __global__ void __launch_bounds__((W == 2 ? 2 : 1) * W *kWave, 2) delta_walk(Del
         const Power p = column_power(U, lane);
         f4 AU[4];
         triangle_times<false>(ah, al, ls_at, split(U[0], U[1], p.inv), split(U[2], U[3], p.inv), AU);
-        const float back = p.back * up * coef->a;
+        const float back = p.back * up;
         const int left_rows = a.S - n * kC;
         const Buffer to = buffer_of(w.out + (int64_t)n * kC * (out_row / 2) + (int64_t)b * a.H * a.V,
                                     (left_rows < kC ? left_rows - 1 : kC - 1) * out_row + 2u * a.H * a.V);
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
             const f4 cq = *(const f4 *)(coef->q + row_of(t, 4 * grp)) * s_back;
+            const f4 ca = *(const f4 *)(coef->a + row_of(t, 4 * grp)) * back;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                __builtin_amdgcn_raw_buffer_store_b16(from_f32<DT>(__builtin_fmaf(AU[t][i], back, cq[i] * O[t][i])), to,
+                __builtin_amdgcn_raw_buffer_store_b16(from_f32<DT>(__builtin_fmaf(AU[t][i], ca[i], cq[i] * O[t][i])), to,
                                                       out_at + (row_of(t, 0) + i) * out_row, 0, 0);
         }
     };

@@ -96,3 +96,20 @@ def test_rows_of_zeros_beside_others(dtype):
         v["k"][10:12] = 0
         r, _, end, _ = both(v, go, normalize=False)
         ref.norm_close(end, r["state"], slack(90), "state")
+
+
+@pytest.mark.parametrize("power,normalize", [(-30, True), (-44, True), (-65, True), (-90, True), (-44, False), (-70, False)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_outputs_of_small_rows(power, normalize, dtype):
+    """Of queries, each row next to its own size (in fp16 as small as its numbers are)."""
+    if dtype == "fp16":
+        power //= 8
+    v, go, gf = small_rows(power, normalize, dtype)
+    if dtype == "fp16":
+        v["v"] *= 64
+        v["state"] *= 64
+    announce(f"small rows 2^{power} {dtype}, normalize={normalize}")
+    r, out, _, _ = both(v, go, gf, normalize=normalize)
+    for i in range(90):
+        tiny = torch.full_like(r["out"][i], torch.finfo(out.dtype).smallest_normal)  # results below it have fewer bits
+        row_near(out[i], r["out"][i], r["out"][i].abs() + tiny / (16 * slack(90)), 16 * slack(90), f"row {i}")
