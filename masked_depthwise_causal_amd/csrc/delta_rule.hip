@@ -617,7 +617,8 @@ __global__ void __launch_bounds__((W == 2 ? 2 : 1) * W *kWave, 2) delta_walk(Del
 
 // The states before the segments, one after the other: S -> T S + F. A block has 16 columns, a wave 32 rows of them;
 // what a segment needs of T and F does not depend on S and is read and split one segment ahead, and S goes from wave to
-// wave in LDS as the products' right operand, with a power of two for each wave's rows of a column. S=16384 B=1 H=16
+// wave in LDS as the products' right operand, with a power of two for each wave's rows of a column. Segments that begin
+// past the sequence's length hand S on as it is, in all its bits. S=16384 B=1 H=16
 // K=V=128, eight segments: 23 us; with all rows in one wave 63.
 template <int KP>
 __global__ void __launch_bounds__(KP / 32 * kWave, 1) delta_carry(Delta a, Walk w) {
@@ -649,8 +650,17 @@ __global__ void __launch_bounds__(KP / 32 * kWave, 1) delta_carry(Delta a, Walk 
             for (int i = 0; i < 4; ++i) F[t][i] = end[(row_of(2 * wave + t, 4 * grp) + i) * wide + col];
         }
     };
-    read(0);
-    for (int n = 0; n + 1 < w.segments; ++n) {
+    auto write = [&](int n) {
+        float *to = w.carry + (((int64_t)n * all + bh) * KP + 8 * grp) * VP + col;
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) to[(row_of(2 * wave + t, 0) + i) * VP] = S[t][i];
+    };
+    const int chunks = (length_of(a, bh / a.H) + kC - 1) / kC;
+    const int live = (chunks + w.per - 1) / w.per, last = live < w.segments - 1 ? live : w.segments - 1;
+    if (last > 0) read(0);
+    for (int n = 0; n < last; ++n) {
         Split T[2][KS];
         float back[2];
         f4 next[2] = {F[0], F[1]};
@@ -667,7 +677,7 @@ __global__ void __launch_bounds__(KP / 32 * kWave, 1) delta_carry(Delta a, Walk 
 #pragma unroll
             for (int s = 0; s < KS; ++s) T[t][s] = split(x[t][s][0], x[t][s][1], p.inv);
         }
-        read(n + 2 < w.segments ? n + 1 : n);
+        read(n + 1 < last ? n + 1 : n);
         const Power p = column_power(S, lane);
         const Split mine = split(S[0], S[1], p.inv);
         const int buf = n & 1;
@@ -687,14 +697,11 @@ __global__ void __launch_bounds__(KP / 32 * kWave, 1) delta_carry(Delta a, Walk 
                 for (int i = 0; i < 4; ++i) next[t][i] = __builtin_fmaf(d[i], back[t] * up, next[t][i]);
             }
         }
-        float *to = w.carry + (((int64_t)n * all + bh) * KP + 8 * grp) * VP + col;
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            S[t] = next[t];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) to[(row_of(2 * wave + t, 0) + i) * VP] = S[t][i];
-        }
+        for (int t = 0; t < 2; ++t) S[t] = next[t];
+        write(n);
     }
+    for (int n = last; n + 1 < w.segments; ++n) write(n);
 }
 
 // ---------------------------------------------------------------------------------------------

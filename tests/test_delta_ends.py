@@ -113,3 +113,21 @@ def test_outputs_of_small_rows(power, normalize, dtype):
     for i in range(90):
         tiny = torch.full_like(r["out"][i], torch.finfo(out.dtype).smallest_normal)  # results below it have fewer bits
         row_near(out[i], r["out"][i], r["out"][i].abs() + tiny / (16 * slack(90)), 16 * slack(90), f"row {i}")
+
+
+@pytest.mark.parametrize("S,B,H,K,V", [(70, 2, 2, 16, 24), (1100, 3, 2, 32, 24), (1300, 2, 1, 100, 130)])
+def test_state_of_sequences_that_ended(S, B, H, K, V):
+    """No rows: the state that came in, in all its bits, where the sequence is cut into segments too."""
+    v, go, gf = inputs(S, B, H, 1, K, V, "bf16", S)
+    lengths = [0, S, -1][:B]
+    sizes = torch.arange(K)[None, None, :, None] % 61 - 30.0
+    v["state"] *= torch.exp2(sizes)
+    v["state"][0, 0, 3, 2] = float("inf")
+    v["state"][0, 0, 4, 5] = 2.0 ** -126
+    announce(f"ended sequences S={S}")
+    out, end, g = run(v, go, gf, lengths)
+    for b in range(B):
+        if lengths[b] <= 0:
+            assert torch.equal(end[b], v["state"][b].cuda()), b
+            assert torch.equal(g.state[b], gf[b].cuda()), b
+            assert not out[:, b].any()
