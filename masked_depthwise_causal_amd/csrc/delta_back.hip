@@ -229,7 +229,7 @@ __global__ void __launch_bounds__((W == 2 ? 2 : 1) * W *kWave, 1) delta_walk_bac
         }
         {
             float *to = keep_y + (int64_t)n * kC * VP;
-            const int left_rows = a.S - n * kC;
+            const int left_rows = length - n * kC;  // rows past the length are zeros
             const Buffer gv = buffer_of(w.gv + (int64_t)n * kC * (gv_row / 2) + (int64_t)b * a.H * a.V,
                                         (left_rows < kC ? left_rows - 1 : kC - 1) * gv_row + 2u * a.H * a.V);
 #pragma unroll
@@ -318,7 +318,7 @@ __global__ void __launch_bounds__((W == 2 ? 2 : 1) * W *kWave, 1) delta_walk_bac
                 if (k < a.K && mine) w.gstate[((int64_t)bh * a.K + k) * a.V + col] = S[t][i];
             }
     }
-    for (int row = chunks * kC + grp; row < a.S; row += 4)  // rows that no chunk covers
+    for (int row = length + grp; row < a.S; row += 4)  // rows past the length
         if (mine) w.gv[(((int64_t)row * a.B + b) * a.H + h) * a.V + col] = 0;
 }
 

@@ -424,7 +424,7 @@ __global__ void __launch_bounds__((W == 2 ? 2 : 1) * W *kWave, 2) delta_walk(Del
         f4 AU[4];
         triangle_times<false>(ah, al, ls_at, split(U[0], U[1], p.inv), split(U[2], U[3], p.inv), AU);
         const float back = p.back * up;
-        const int left_rows = a.S - n * kC;
+        const int left_rows = length - n * kC;  // rows past the length are zeros, whatever the matrices' zeros meet
         const Buffer to = buffer_of(w.out + (int64_t)n * kC * (out_row / 2) + (int64_t)b * a.H * a.V,
                                     (left_rows < kC ? left_rows - 1 : kC - 1) * out_row + 2u * a.H * a.V);
 #pragma unroll
@@ -609,8 +609,8 @@ __global__ void __launch_bounds__((W == 2 ? 2 : 1) * W *kWave, 2) delta_walk(Del
                 if (k < a.K && col < a.V) w.state_out[((int64_t)bh * a.K + k) * a.V + col] = S[t][i];
             }
     }
-    // rows that no chunk covers are zeros
-    const int from = (end > n0 ? end : n0) * kC, to = n1 * kC < a.S ? n1 * kC : a.S;
+    // rows past the length are zeros
+    const int from = length > n0 * kC ? length : n0 * kC, to = n1 * kC < a.S ? n1 * kC : a.S;
     for (int row = from + grp; row < to; row += 4)
         if (col < a.V) w.out[(((int64_t)row * a.B + b) * a.H + h) * a.V + col] = 0;
 }

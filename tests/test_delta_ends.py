@@ -131,3 +131,16 @@ def test_state_of_sequences_that_ended(S, B, H, K, V):
             assert torch.equal(end[b], v["state"][b].cuda()), b
             assert torch.equal(g.state[b], gf[b].cuda()), b
             assert not out[:, b].any()
+
+
+@pytest.mark.parametrize("B,H,V", [(1, 2, 24), (40, 8, 64)])
+@pytest.mark.parametrize("what", ["v", "k", "q", "go"])
+def test_rows_past_a_length_beside_rows_that_are_not_finite(B, H, V, what):
+    S, n = 130, 70
+    v, go, gf = inputs(S, B, H, 1, 16, V, "bf16", 51)
+    (go if what == "go" else v[what])[66] = float("inf")
+    announce(f"not finite in {what}, B={B}")
+    out, _, g = run(v, go, gf, [n] * B)
+    for name, t in (("out", out), ("gq", g.q), ("gk", g.k), ("gv", g.v), ("gdt", g.dt), ("gb", g.b)):
+        assert not t[n:].any(), name
+    assert not torch.isfinite((g.v if what == "go" else out)[66]).all()
