@@ -11,7 +11,7 @@
 //
 //   gQ~ = q gO S0^T + Z K~                           Z = scale tril(gO U^T) o M o qr kr^T
 //   gK~ = u U gS1^T - p beta Y S0^T + Z^T Q~ + (W + W^T) K~     W = -tril(Y U^T, -1) o beta o M o kr kr^T
-//   gb  = (1 - beta) Y.U  (U holds the factor beta)
+//   gb  = sigmoid(-b) Y.U  (U holds the factor beta, and 1 - beta has nothing left where gates are open)
 //
 // and the log decays, summed over a chunk's rows first (G): with E = tril(gO U^T, -1) o A - tril(Y U^T, -1) o L,
 //
@@ -690,7 +690,6 @@ __global__ void __launch_bounds__(KP / 16 * kWave) delta_grads(Delta a, Records 
         if (wave == W - 1) {
             const int r = lane;
             const int64_t row = row0 + r;
-            const float beta = coef[kC + r];
             double e = 0.0, f = 0.0, s0 = 0.0;
 #pragma unroll
             for (int i = 0; i < W; ++i) e += (double)rowe[i][r], f += (double)rowf[i][r], s0 += dots[i];
@@ -704,7 +703,9 @@ __global__ void __launch_bounds__(KP / 16 * kWave) delta_grads(Delta a, Records 
             s += last_lane(up) - up;
             const double glog = s + e;  // of log a
             double pa = 0.0, pb = 0.0;
+            float shut = 0.0f;
             if (r < live) {
+                shut = sigmoid_f(-to_f32<DT>(a.b[row * a.bs[0] + b * a.bs[1] + h * a.bs[2]]));
                 const float raw = to_f32<DT>(a.dt[row * a.ds[0] + b * a.ds[1] + h * a.ds[2]]) + (a.bias ? a.bias[h] : 0.0f);
                 float slope = 1.0f;
                 const float d = a.softplus ? softplus_f(raw, slope) : raw;
@@ -715,7 +716,7 @@ __global__ void __launch_bounds__(KP / 16 * kWave) delta_grads(Delta a, Records 
             if (r < rows) {
                 const int64_t to = (row * a.B + b) * a.H + h;
                 w.gdt[to] = from_f32<DT>((float)pb);
-                w.gb[to] = r < live ? from_f32<DT>((1.0f - beta) * yu[r]) : 0;
+                w.gb[to] = r < live ? from_f32<DT>(shut * yu[r]) : 0;
             }
             pa = last_lane(sum_up(pa)), pb = last_lane(sum_up(pb));
             if (lane == 0) {

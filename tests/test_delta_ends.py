@@ -13,6 +13,7 @@ import masked_depthwise_causal_amd as mdc
 from . import delta_ref as ref
 from .gpu_util import announce
 from .ssm_ref import F
+from .test_conv_act import DT
 from .test_delta import inputs, slack
 
 pytestmark = pytest.mark.gpu
@@ -144,3 +145,20 @@ def test_rows_past_a_length_beside_rows_that_are_not_finite(B, H, V, what):
     for name, t in (("out", out), ("gq", g.q), ("gk", g.k), ("gv", g.v), ("gdt", g.dt), ("gb", g.b)):
         assert not t[n:].any(), name
     assert not torch.isfinite((g.v if what == "go" else out)[66]).all()
+
+
+@pytest.mark.parametrize("dtype,open_,size", [("bf16", 20, 1.0), ("fp16", 12, 256.0)])
+def test_gradients_of_open_and_shut_gates(dtype, open_, size):
+    """Each gate's next to the slope of its own logistic function."""
+    v, go, gf = inputs(100, 2, 2, 1, 32, 24, dtype, 52)
+    u = torch.rand((100, 2), generator=torch.Generator().manual_seed(1))
+    v["b"][..., 0], v["b"][..., 1] = (6 + (open_ - 6) * u).to(DT[dtype]), -(6 + 6 * u).to(DT[dtype])
+    go, gf = (go.float() * size).to(DT[dtype]), gf * size
+    announce(f"open and shut gates, {dtype}")
+    r, _, _, g = both(v, go, gf)
+    b = v["b"].to(F)
+    slope = torch.sigmoid(b) * torch.sigmoid(-b)
+    half = torch.finfo(g.b.dtype).eps / 2
+    for h in (0, 1):
+        want, got = (r["gb"] / slope)[..., h], (g.b.cpu().to(F) / slope)[..., h]
+        assert float((got - want).norm()) <= float((half + 16 * slack(100)) * want.norm()), h
