@@ -745,13 +745,25 @@ __global__ void __launch_bounds__(kStepThreads) delta_one(Delta a, float *state,
     const float raw = to_f32<DT>(a.dt[b * a.ds[1] + h * a.ds[2]]) + (a.bias ? a.bias[h] : 0.0f);
     const float decay = exp2_f((float)log2_decay(step_size(raw, a.softplus), a.A[h]));
     const float beta = sigmoid_f(to_f32<DT>(a.b[b * a.bs[1] + h * a.bs[2]]));
-    if (t < kMaxK) {
-        const float kk = column_sum(sum16(kv * kv)), qq = column_sum(sum16(qv * qv)), kq = column_sum(sum16(kv * qv));
-        if (lane == 0) norms[0][wave] = kk, norms[1][wave] = qq, norms[2][wave] = kq;
+    auto sums = [&]() {
+        if (t < kMaxK) {
+            const float kk = column_sum(sum16(kv * kv)), qq = column_sum(sum16(qv * qv)), kq = column_sum(sum16(kv * qv));
+            if (lane == 0) norms[0][wave] = kk, norms[1][wave] = qq, norms[2][wave] = kq;
+        }
+        __syncthreads();
+    };
+    sums();
+    float ek = kNormEps, eq = kNormEps;
+    const float most = 3.4e38f;
+    const bool large_k = norms[0][0] + norms[0][1] > most, large_q = norms[1][0] + norms[1][1] > most;
+    if (a.normalize && (large_k || large_q)) {  // squares past fp32's largest: the row as 2^-64 of itself, next to which eps is nothing
+        if (large_k) kv *= 0x1p-64f, ek = 0.0f;
+        if (large_q) qv *= 0x1p-64f, eq = 0.0f;
+        __syncthreads();
+        sums();
     }
-    __syncthreads();
-    const float rk = a.normalize ? 1.0f / __builtin_sqrtf(norms[0][0] + norms[0][1] + kNormEps) : 1.0f;
-    const float rq = a.scale * (a.normalize ? 1.0f / __builtin_sqrtf(norms[1][0] + norms[1][1] + kNormEps) : 1.0f);
+    const float rk = a.normalize ? 1.0f / __builtin_sqrtf(norms[0][0] + norms[0][1] + ek) : 1.0f;
+    const float rq = a.scale * (a.normalize ? 1.0f / __builtin_sqrtf(norms[1][0] + norms[1][1] + eq) : 1.0f);
     const float along = (norms[2][0] + norms[2][1]) * rk * rq;
     if (t < kMaxK) kn[t] = kv * rk, qn[t] = qv * rq;
     __syncthreads();

@@ -162,3 +162,19 @@ def test_gradients_of_open_and_shut_gates(dtype, open_, size):
     for h in (0, 1):
         want, got = (r["gb"] / slope)[..., h], (g.b.cpu().to(F) / slope)[..., h]
         assert float((got - want).norm()) <= float((half + 16 * slack(100)) * want.norm()), h
+
+
+def test_tokens_of_large_rows():
+    """Keys and queries whose squares are past fp32's largest, next to ordinary and small ones."""
+    v, _, _ = inputs(1, 6, 4, 2, 100, 40, "bf16", 53)
+    v["k"][0, 1] *= 2.0 ** 70
+    v["q"][0, 2] *= 2.0 ** 100
+    v["k"][0, 3] *= 2.0 ** 64
+    v["q"][0, 3] *= 2.0 ** -70
+    v["k"][0, 4, 0, 70:] *= 2.0 ** 90
+    r = ref.delta(v["q"], v["k"], v["v"], v["dt"], v["b"], v["A"], v["dt_bias"], state=v["state"])
+    d = {n: t.cuda() for n, t in v.items()}
+    out = mdc.delta_step(d["state"], *(d[n][0] for n in ("q", "k", "v", "dt", "b")), d["A"], dt_bias=d["dt_bias"])
+    for b in range(6):
+        row_near(out[b], r["out"][0, b], r["out"][0, b].abs(), 2.0 ** -18, f"out {b}")
+        ref.norm_close(d["state"][b], r["state"][b], 2.0 ** -18, f"state {b}")
