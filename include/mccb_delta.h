@@ -100,7 +100,7 @@ int mccb_delta_step(const mccb_delta_t *args, float *state, void *out, void *str
  * a block's rows in fp32 (about R groups/1024 of them, 4 at least, where R is as large) and go on in fp64. Rows are contiguous and x_ld, residual_ld, z_ld elements apart; results are contiguous.
  *
  * R in [0, 2^31), H in [1, 2^24], groups in [1, 65535] and a divisor of H, H/groups up to 16384, eps
- * positive. prenorm has groups = 1 and no z.
+ * at least 2^-126. prenorm has groups = 1 and no z.
  * -----------------------------------------------------------------------------------------------*/
 typedef struct {
     int64_t R, H, groups;

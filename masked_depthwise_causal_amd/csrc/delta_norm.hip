@@ -437,7 +437,8 @@ int check_norm(const mccb_norm_t *a, bool post) {
     if (a->R < 0 || a->R > kMaxRows - 1 || a->H < 1 || a->groups < 1 || a->groups > 65535 ||
         a->H % a->groups != 0 || a->H / a->groups > kMaxGroup || a->H > kMaxWidth)
         return MCCB_ERR_SHAPE;
-    if (!(a->eps > 0.0f) || a->eps > 3.0e38f) return MCCB_ERR_PARAM_INVALID;
+    // the hardware's reciprocal root takes subnormal numbers for 0, which would make NaN of a row of zeros
+    if (!(a->eps >= 0x1p-126f) || a->eps > 3.0e38f) return MCCB_ERR_PARAM_INVALID;
     if (!post && (a->z || a->groups != 1)) return MCCB_ERR_PARAM_INVALID;
     return MCCB_OK;
 }
