@@ -367,7 +367,7 @@ __global__ void __launch_bounds__(KP / 16 * kWave) delta_grads(Delta a, Records 
     __shared__ __align__(16) uint16_t kt[kC * KP], qt[kC * KP];
     __shared__ __align__(16) uint16_t stage[5 * kSquare];  // gO, U hi, U lo, Y hi, Y lo; then Z and W in two terms
     __shared__ __align__(16) float po[kC], pu[kC], py[kC], coef[4 * kC], kr[kC], qr[kC], unit[2][kC];
-    __shared__ float rowf[W][kC], rowe[W][kC], yu[kC], big[2][W], size[2];
+    __shared__ float rowf[W][kC], rowe[W][kC], yu[kC], big[2][W], size[3];
     __shared__ double cum[kC], dots[W], erow[kSide][kC], ecol[4][kC];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     int lane = threadIdx.x % kWave, m = lane & 15, grp = lane >> 4;
@@ -415,6 +415,7 @@ __global__ void __launch_bounds__(KP / 16 * kWave) delta_grads(Delta a, Records 
         if (lane == 0) size[wave] = __builtin_ldexpf(1.0f, s);
     }
     lds_barrier();
+    if (threadIdx.x == 0) size[2] = size[1] / size[0];  // kept here: registers are all taken
 #pragma unroll
     for (int i = 0; i < kTurns; ++i) {
         const int at = threadIdx.x + i * kThreads, r = at / (KP / 8);
@@ -422,7 +423,6 @@ __global__ void __launch_bounds__(KP / 16 * kWave) delta_grads(Delta a, Records 
         ((h8 *)qt)[at] = qraw[i] * (_Float16)coef[kC + r];
     }
     lds_barrier();
-    const float sk = uniform(size[0]), sq = uniform(size[1]), sqk = sq / sk;
     // this lane's values of K~ and Q~ in the results' layout
     h4 kd[4], qd[4];
     f4 aq[4] = {}, ak[4] = {};
@@ -441,7 +441,7 @@ __global__ void __launch_bounds__(KP / 16 * kWave) delta_grads(Delta a, Records 
         const float whole = rc->whole;
         lds_barrier();  // the last head's reads are done
         if (threadIdx.x < 4 * kC) {  // as RowCoef has them, but for c and s
-            const int r = threadIdx.x % kC, which = threadIdx.x / kC;
+            const int tid = anew(threadIdx.x), r = tid % kC, which = tid / kC;
             const double G = rc->cum[r];
             if (which == 0) cum[r] = G, coef[r] = exp2_f((float)G) * kr[r];
             if (which == 1) coef[kC + r] = rc->beta[r];
@@ -544,7 +544,7 @@ __global__ void __launch_bounds__(KP / 16 * kWave) delta_grads(Delta a, Records 
                     const f4 fo = *(const f4 *)(po + r) * ps.back * *(const f4 *)(coef + 2 * kC + r);
                     const f4 fy = *(const f4 *)(py + r) * ps.back * *(const f4 *)(coef + r) * *(const f4 *)(coef + kC + r);
                     const f4 fu = *(const f4 *)(pu + r) * pg.back * *(const f4 *)(coef + 3 * kC + r);
-                    const f4 kf = anew(kd[t]), qf = anew(qd[t]) * sqk;
+                    const f4 kf = anew(kd[t]), qf = anew(qd[t]) * uniform(size[2]);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const float e = fu[i] * z[i], o = fo[i] * x[i], l = fy[i] * y[i];
@@ -590,6 +590,7 @@ __global__ void __launch_bounds__(KP / 16 * kWave) delta_grads(Delta a, Records 
         if (lane == 0) dots[wave] = (double)s0s1;
         // Z, W and the sums of E
         float mz = 0.0f, mw = 0.0f;
+        const float sk = uniform(size[0]), sq = uniform(size[1]);
         {
             const int r = row_of(rt, 4 * grp);
             double er_[4] = {};
@@ -741,6 +742,7 @@ __global__ void __launch_bounds__(KP / 16 * kWave) delta_grads(Delta a, Records 
         float q = 0.0f, k = 0.0f;
 #pragma unroll
         for (int j = 0; j < W; ++j) q += rowf[j][r], k += rowe[j][r];
+        const float sk = size[0], sq = size[1];
         coef[r] = a.normalize ? q * (sq * qr[r]) * (sq * qr[r]) : 0.0f;
         coef[kC + r] = a.normalize ? k * (sk * kr[r]) * (sk * kr[r]) : 0.0f;
         coef[2 * kC + r] = unit[1][r];
