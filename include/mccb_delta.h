@@ -33,10 +33,13 @@ extern "C" {
  *   out  = scale S^T qn
  *
  * q, k [S,B,G,K], v and out [S,B,H,V], dt and b [S,B,H] have the dtype; A, dt_bias [H] and the states are
- * fp32. Rows of q, k and v are contiguous; the other axes have element strides (>= 0; 0 repeats). The
- * states are computed with products of two 16-bit terms each, about 22 bits, and fp32 sums; gates and
- * decays in fp32, sums of their logarithms in fp64; results are rounded once. Rates A are negative in
- * ordinary use (decay); A d below -1e5 counts as -1e5, whose decay is 0.
+ * fp32. Rows of q, k and v are contiguous; the other axes have element strides (>= 0; 0 repeats). Gates and
+ * decays are computed in fp32, sums of their logarithms in fp64. delta_step computes in fp32. The other
+ * calls go by chunks of 64 rows, in products of two 16-bit terms for each operand and fp32 sums: what a
+ * product takes of states, U and gradients has 22 bits next to the largest value of its column or row in the
+ * chunk, fewer below 2^-18 of that, and nothing below 2^-40. A small row of k or q, or a row of zeros, takes
+ * none from the others and loses none itself. Outputs and gradients are rounded once to 16 bits. Rates A are negative in ordinary use (decay); A d below -1e5
+ * counts as -1e5, whose decay is 0.
  *
  * lengths: optional int64 [B] on the device, clamped to [0, S]; NULL = all S. Rows at or past a sequence's
  * length are not computed with, whatever they hold: outputs and gradients there are zero, and states are
@@ -59,7 +62,9 @@ typedef struct {
 } mccb_delta_t;
 
 /* out [S,B,H,V]; final_state [B,H,K,V] or NULL; saved: NULL, or mccb_delta_saved_size bytes that the
- * backward reads (the state before every 64th row among them). With saved no workspace is needed. */
+ * backward reads: for every 64 rows of a head the state before them and their U in fp32, K counted as 64 or
+ * 128 and V in steps of 64 (at K = V = 128 and G = H 2.4 KB a row and head with the chunk's matrices; the
+ * backward's workspace is another 1.5 KB). With saved no workspace is needed. */
 int mccb_delta_saved_size(const mccb_delta_t *args, uint64_t *bytes);
 int mccb_delta_forward_get_workspace_size(const mccb_delta_t *args, uint64_t *workspace_size);
 int mccb_delta_forward(const mccb_delta_t *args, void *out, float *final_state, void *saved,
@@ -97,7 +102,8 @@ int mccb_delta_step(const mccb_delta_t *args, float *state, void *out, void *str
  * its own for every value, or (weight_shared) one of H/groups values for all groups. residual, scale [H]
  * and z may be NULL: then their factor or term is left out. Everything has the dtype, is computed in fp32
  * and rounded once; prenorm's norm is of the sum before its rounding. Gradients of weight and scale add
- * a block's rows in fp32 (about R groups/1024 of them, 4 at least, where R is as large) and go on in fp64. Rows are contiguous and x_ld, residual_ld, z_ld elements apart; results are contiguous.
+ * a block's rows in fp32 (about R groups/1024 of them, 4 at least, where R is as large) and go on in fp64.
+ * Rows are contiguous and x_ld, residual_ld, z_ld elements apart; results are contiguous.
  *
  * R in [0, 2^31), H in [1, 2^24], groups in [1, 65535] and a divisor of H, H/groups up to 16384, eps
  * at least 2^-126. prenorm has groups = 1 and no z.

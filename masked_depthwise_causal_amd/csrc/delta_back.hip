@@ -53,9 +53,9 @@ struct Given {
     f4 u[W][4][kWave];              // A^T gO
     f4 s[W][KP / 16][kWave];        // Q~^T (q gO)
 };
-// Bound as the forward walk is, with a longer chain and twice as many transposed operands: S=2048 B=4 H=16 K=V=128, 143
-// us, 4.5 a chunk, 235 MB written. W as there: without second waves 186, in blocks of four 197; S=513 B=2 H=6 K=64 V=128
-// 24 and 38. (Four and their seconds would need more than the LDS for K above 64.)
+// Bound as the forward walk is, with a longer chain and twice as many transposed operands: S=2048 B=4 H=16 K=V=128, 141
+// us, 4.4 a chunk, 235 MB written. W as there: a whole backward of that size 371 us, and 432 in blocks of four; S=513 B=2
+// H=6 K=64 V=128 69 and 84; B H = 80 of V=128, where two waves have no CU each, 544 and 500. (Four and their seconds would need more than the LDS for K above 64.)
 template <int DT, int KP, int W, bool WIDE>
 __global__ void __launch_bounds__((W == 2 ? 2 : 1) * W *kWave, 1) delta_walk_back(Delta a, Records rec, Back w) {
     constexpr bool PAIRS = W == 2;
@@ -357,8 +357,10 @@ __device__ static inline float largest(const f4 &x, const f4 &y, float m) {
 // (a power of two a row taken out), the states' rows are the waves' right operands straight from memory, each
 // wave with 16 rows of K. Of the 64x64 matrices a wave has a part of a row of tiles. Bound by latency: all of a SIMD's
 // registers go to two waves, one block a CU, whose loads, staging and products wait for each other (vector
-// instructions in 40 % of the cycles): S=2048 B=4 H=16 K=V=128, 249 us for 530 MB read and 89 written. The next block of
-// columns read ahead spills 47 registers: 300 us.
+// instructions in 40 % of the cycles): S=2048 B=4 H=16 K=V=128, 252 us for 539 MB read and 98 written. 7 registers are
+// spilled (none where V is no multiple of 8); the next block of columns read ahead spills 47: 300 us. 16.4e6 of 42.4e6
+// LDS cycles are bank conflicts, most of them (9.4e6) of 16-byte reads of operands with 64 columns, whose rows are half of
+// the banks long; 1.6e6 each of those with 128 columns and of transposing reads, 1e6 each of the scattered Z, W and results.
 template <int DT, int KP, bool ROWS8>
 __global__ void __launch_bounds__(KP / 16 * kWave) delta_grads(Delta a, Records rec, Back w) {
     constexpr int W = KP / 16, kThreads = W * kWave;

@@ -14,8 +14,9 @@
 // Numbers. Products run on the matrix units in fp16, in as many terms as they need to come out as in fp32:
 // rows of q and k are exact in one (with a power of two a row taken out, bf16's 8 bits fit wherever fp16 is
 // normal; values below 2^-28 of the row's largest lose 2^-40 of it); everything that is computed is split
-// in two, hi + lo, 22 bits (a power of two a column, or a matrix, taken out, so that no value's size
-// matters; what is lost is below 2^-22 of a value or 2^-40 of the largest). An exact operand with a split
+// in two, hi + lo, 22 bits (a power of two a column, a row of A, or a matrix, taken out; what is lost is below
+// 2^-22 of a value or 2^-40 of the largest that it shares a power with, so that factors which make up for a
+// value's size stay out of what is split). An exact operand with a split
 // one takes two products, two split ones three (lo lo is below 2^-22). On this card that is 8 and 5 times
 // the rate of the fp32 matrix instructions; in bf16 terms it would take three and six products.
 #pragma once

@@ -111,8 +111,9 @@ __device__ static inline Place place(const Norm &n, const Teams &t) {
 
 // T: lanes of a team (over a wave: the block, of any number of waves). E: vectors of a lane.
 // T lanes' vectors lie next to each other: vector e of a lane starts at column 8 (lane + e team).
-// 16384 rows of bf16: prenorm of 4096 with residual, scale and sum 95 us (537 MB, 5.7 TB/s), postnorm in 32 groups with a
-// gate 79 us (403 MB, 5.1 TB/s), of 5120 with gate, scale and residual 134 us (671 MB, 5.0 TB/s).
+// 16384 rows of bf16: prenorm of 4096 with residual, scale and sum 96 us (537 MB, 5.6 TB/s), postnorm in 32 groups with a
+// gate 79 us (403 MB, 5.1 TB/s), of 5120 with gate, scale and residual 135 us (671 MB, 5.0 TB/s). Narrow groups leave lanes of
+// a team idle: 64 groups of 64 84 us, 256 of 16 288.
 template <int DT, bool POST, int T, int E>
 __global__ void __launch_bounds__(T > kWave ? kMaxTeam : kBlock)
     norm_forward(Norm n, Teams t, uint16_t *__restrict__ out, uint16_t *__restrict__ sum) {
@@ -212,9 +213,11 @@ __device__ static inline void load_row(const Norm &n, const NormGrads &q, int64_
 }
 
 // The next row is on its way while one is worked on, where a lane has one vector; with two, in blocks that leave a
-// lane 128 registers, there is no room for it, nor for the weights, which are read again with each row.
-// 16384 rows of bf16: prenorm of 4096 with residual, scale and the sum's gradient 181 us (805 MB, 4.5 TB/s),
-// postnorm of 5120 with gate and scale 223 us (839 MB, 3.8 TB/s).
+// lane 128 registers, there is no room for it, nor for the weights, which are read again with each row, and 68 to 198
+// registers are spilled all the same: groups above 8192 values, of which there is no other form, run at 0.8 to 1.5 TB/s
+// (8192 rows of 8200: prenorm 551 us, postnorm 852). 16-lane teams with a gate spill 7 and 14.
+// 16384 rows of bf16: prenorm of 4096 with residual, scale and the sum's gradient 182 us (805 MB, 4.4 TB/s),
+// postnorm of 5120 with gate and scale 223 to 235 us (839 MB, 3.6 to 3.8 TB/s).
 template <int DT, bool POST, int T, int E>
 __global__ void __launch_bounds__(T > kWave ? kMaxTeam : kBlock, T == 16 && E == 1 ? 4 : 1)
     norm_backward(Norm n, Teams t, NormGrads q) {

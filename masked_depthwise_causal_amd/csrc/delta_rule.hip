@@ -243,7 +243,8 @@ __device__ static __forceinline__ void invert(const float *L, float *X, int wave
 }
 
 // Bound by what it writes, and by the chain of products in X's blocks where there are few chunks: S=4096 B=4 H=32 G=16
-// K=V=128, 4096 blocks, 122 us for 325 MB written and 138 read (3.8 TB/s); S=513 B=2 H=6 G=3 K=64, 54 blocks, 13 us.
+// K=V=128, 4096 blocks, 144 us for 373 MB written and 141 read (3.6 TB/s; 4 registers are spilled); S=513 B=2 H=6 G=3 K=64, 54
+// blocks, 13 us.
 template <int DT, int KP>
 __global__ void __launch_bounds__(kPrepThreads, 4) delta_prepare(Delta a, Records rec, int n0) {
     constexpr int kImages = 2 * kC * KP * (int)sizeof(uint16_t), kSquares = 2 * kC * kLd * (int)sizeof(float);
@@ -372,9 +373,9 @@ struct Walk {
     int blocks;                     // of columns, a head
 };
 
-// Bound by the vector and matrix instructions of one wave a SIMD, issued in 57 % of its cycles, and by what they wait for
-// (one product's largest values, then the next one's operands): S=4096 B=4 H=32 G=16 K=V=128, 241 us, 3.8 a chunk.
-// Training, S=2048 B=4 H=16, 129 us, of which the kept states and U (201 MB) are some 30.
+// Bound by the vector and matrix instructions of one wave a SIMD, issued in 50 % of its cycles, and by what they wait for
+// (one product's largest values, then the next one's operands): S=4096 B=4 H=32 G=16 K=V=128, 318 us, 5.0 a chunk.
+// Training, S=2048 B=4 H=16, 143 us, of which the kept states and U (201 MB) are some 30.
 // KEEP: the states and U are kept. (Two waves a SIMD would fit: with all of a SIMD's registers the compiler has the
 // products' results in accumulation registers and moves each of them.)
 // SEGMENTS: where there are few heads, the first pass of two over a sequence that is cut into segments, all at once:
@@ -383,8 +384,8 @@ struct Walk {
 // delta_carry then finds the states before the segments, and the second pass walks all of them at once with outputs.
 // W: waves with states, four a block; or two where blocks are few (half_blocks), and then each has a second one (PAIRS)
 // that makes the outputs of S0 and U as it finds them in LDS, and brings the operands: neither is on the way from one
-// state to the next. 148 -> 129 us (training, as above), 44 -> 38 (S=777 B=5 H=6 K=96 V=80); with four and their
-// seconds, two a SIMD, 241 and 241 (S=4096 B=4 H=32), 125 and 137 (S=16384 H=16 in segments).
+// state to the next. Whole forwards: training, as above, 235 -> 187 us, S=777 B=5 H=6 K=96 V=80 75 -> 65; where they have no
+// CU each 384 -> 488 (S=4096 B=4 H=32), 378 -> 416 (S=16384 H=16 in segments).
 template <int DT, int KP, int W, bool KEEP, bool WIDE, bool SEGMENTS>
 __global__ void __launch_bounds__((W == 2 ? 2 : 1) * W *kWave, 2) delta_walk(Delta a, Records rec, Walk w) {
     constexpr bool PAIRS = W == 2;
@@ -619,7 +620,7 @@ __global__ void __launch_bounds__((W == 2 ? 2 : 1) * W *kWave, 2) delta_walk(Del
 // what a segment needs of T and F does not depend on S and is read and split one segment ahead, and S goes from wave to
 // wave in LDS as the products' right operand, with a power of two for each wave's rows of a column. Segments that begin
 // past the sequence's length hand S on as it is, in all its bits. S=16384 B=1 H=16
-// K=V=128, eight segments: 23 us; with all rows in one wave 63.
+// K=V=128, eight segments: 25 us; with all rows in one wave 63.
 template <int KP>
 __global__ void __launch_bounds__(KP / 32 * kWave, 1) delta_carry(Delta a, Walk w) {
     constexpr int KS = KP / 32;     // steps of a product, and waves
@@ -708,7 +709,7 @@ __global__ void __launch_bounds__(KP / 32 * kWave, 1) delta_carry(Delta a, Walk 
 // One token. A block has 32 columns of a head's state, a thread four of them in every 32nd row. With
 // a = decay, p = a Kn^T S and o = a Qn^T S from one pass over the state: u = beta (v - p),
 // out = o + (qn . kn) u, S = a S + kn u^T. Bound by the state's bytes, once in and once out: B=32 H=16 K=V=128, 67 MB in
-// 13.9 us (4.9 TB/s); B=1 H=6 K=V=64 4.6 us, a launch.
+// 13.6 us (4.9 TB/s); B=1 H=6 K=V=64 4.6 us, a launch.
 // ---------------------------------------------------------------------------------------------
 constexpr int kStepCols = 32, kStepThreads = 256;
 constexpr int kStepRows = kMaxK / 32;
@@ -857,10 +858,11 @@ int all_chunks(const Delta &d, const Records &rec, const Walk &w, hipStream_t st
     return w.states ? walk<DT, KP, true, false>(d, rec, w, st) : walk<DT, KP, false, false>(d, rec, w, st);
 }
 
-// Segments of a walk, by what it costs: 3.2 us a chunk where a wave has a SIMD to itself, with outputs and also
-// without (two waves a SIMD then, of 1024 SIMDs), 3 us to carry a state over a segment, and 10 us for two more launches
-// and their ends. S=16384 B=1 H=16: 812 us as one segment, 285 as eight; S=777 B=5 H=6: 43 as one
-// (38 with second waves), 52 as three.
+// Segments of a walk, by what it costs: 3.2 us a chunk where a wave has a SIMD to itself, with outputs (2.8 with second
+// waves, 3.9 in segments) and also without (two waves a SIMD then, of 1024 SIMDs), 3 us to carry a state over a segment,
+// and 10 us for two more launches and their ends. Of 1 to 16 segments, at each of 11 sizes, it takes the fastest or one
+// within 2 % of it. Whole forwards: S=16384 B=1 H=16 799 us as one segment, 357 as eight; S=4096 B=2 H=16 225 and 188
+// (four); S=1300 B=1 H=2 K=64 60 and 39; S=2048 B=4 H=16 139 as one, 168 as two; S=777 B=5 H=6 64 and 76 (three).
 struct Cut {
     int segments, per;
 };

@@ -115,7 +115,7 @@ def delta_forward(q, k, v, dt, b, A, dt_bias=None, softplus=True, normalize=True
     `state` [B,H,K,V] fp32 is the state before the first row (zeros if None). The result is out, or a tuple
     of it with the state after each sequence's last row (`return_state`) and what delta_backward needs
     (`return_saved`). Rows at or past `lengths` (int64 [B] on the device) give zeros and leave the state
-    alone."""
+    alone. Computed in chunks of 64 rows with products of about 22 bits and fp32 sums (mccb_delta.h)."""
     return _call("delta_forward", stream, q, k, v, dt, b, A, dt_bias, bool(softplus), bool(normalize),
                  None if scale is None else float(scale), lengths, state, bool(return_state),
                  bool(return_saved), out, final_state)
